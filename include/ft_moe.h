@@ -49,7 +49,7 @@ typedef enum {
   FT_ERR_MISALIGNED = 3,        /* a pointer breaks the alignment stated below          */
   FT_ERR_WORKSPACE_TOO_SMALL = 4,
   FT_ERR_CUDA = 5,              /* a CUDA runtime call or launch failed                 */
-  FT_ERR_DEVICE_FLAG = 6,       /* a kernel saw an expert id outside [0, E)             */
+  FT_ERR_DEVICE_FLAG = 6,       /* a kernel saw an id outside its range (expert, page)  */
   FT_ERR_TIMEOUT = 7            /* reserved: a bounded device-side wait gave up         */
 } ft_status;
 
@@ -302,6 +302,161 @@ ft_status ft_moe_fp8block_decode(const uint16_t* x, int32_t T, const int32_t* to
                                  const ft_fp8block_shared_expert* sh, float swiglu_limit,
                                  uint16_t* out, void* workspace, size_t workspace_bytes,
                                  void* stream);
+
+/*
+ * The decode block around the layer: what a serving engine runs between two MoE calls (the pages
+ * place the layer in decoder blocks with attention over a paged cache, but define none of it; the
+ * readings are stated at each call). Dense NVFP4 products, rotary embedding and cache append,
+ * attention of one new token per sequence, and the norms around the gated residual sum with their
+ * gradient. The conventions at the top of this file hold.
+ */
+
+/* A dense NVFP4 matrix W [N, K] in the layout of the experts' matrices without the E dimension:
+ *   codes uint8 [N, K/2] (16-byte aligned), scales uint8 [N, K/16] (2-byte aligned), gscale one
+ *   device float (4-byte aligned). N >= 1, K a multiple of 32, 32 <= K <= 32768. */
+typedef struct {
+  int32_t N, K;
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const float* gscale;
+} ft_nvfp4_matrix;
+
+/*
+ * ft_nvfp4_linear — y_t = W x_t for 0 <= T <= 64 tokens (T = 0 is a no-op), one launch.
+ *   x        bf16, token t at x + t * x_stride (16-byte aligned; x_stride a multiple of 8, >= K)
+ *   out      [T, N], bf16 (out_f32 = 0, 2-byte aligned) or float (out_f32 = 1, 4-byte aligned),
+ *            fully overwritten; float32 sums, the matrix's scale last, rounded once
+ *   A NaN block scale gives NaN; x is used as it is (infinities and NaN propagate).
+ */
+ft_status ft_nvfp4_linear(const uint16_t* x, int32_t T, int64_t x_stride,
+                          const ft_nvfp4_matrix* w, void* out, int32_t out_f32, void* stream);
+
+/* Element type of a key-value cache. */
+#define FT_KV_BF16 0
+#define FT_KV_E4M3 1
+
+/*
+ * A paged key-value cache: num_pages pages of page_size tokens, Hkv heads of D elements each for
+ * keys and for values. Element d of head h of slot s of page p is at
+ * p * page_stride + s * slot_stride + h * head_stride + d (strides in elements), so both
+ * [page, slot, head, d] and [page, head, slot, d] orders are accepted. Base pointers 16-byte
+ * aligned and strides multiples of 16 bytes. D is 64, 128 or 256; page_size >= 1.
+ * E4M3 caches stand for code * k_scale and code * v_scale (positive, finite; bf16 caches too are
+ * multiplied by their scales, 1 as a rule).
+ */
+typedef struct {
+  void* k;
+  void* v;
+  int32_t num_pages, page_size, Hkv, D;
+  int64_t k_page_stride, k_slot_stride, k_head_stride;
+  int64_t v_page_stride, v_slot_stride, v_head_stride;
+  int32_t dtype;               /* FT_KV_BF16 or FT_KV_E4M3 */
+  float k_scale, v_scale;
+} ft_paged_kv;
+
+/*
+ * ft_kv_append — rotary embedding of the new tokens' q and k, and k and v into the cache: one
+ * launch for the next tokens of a decode batch, or for the tokens of prompts.
+ *   k, v       bf16, heads of token t at k + t * k_stride [Hkv, D] (16-byte aligned, strides
+ *              multiples of 8): slices of one fused projection are accepted
+ *   q, q_out   bf16, q like k with Hq heads, q_out [T, Hq, D] contiguous: the rotated queries. Both
+ *              NULL (Hq = 0) when there is nothing to rotate. q_out must not overlap q.
+ *   positions  int32 [T]: the token's place in its sequence; negative: a padding token, which
+ *              stores nothing and gives a zero query
+ *   seq_ids    int32 [T], the row of block_table of each token; NULL: token t is sequence t
+ *   block_table int32 [B, table_width]: the page of slots [i * page_size, (i + 1) * page_size)
+ *   rope       float [rope_rows, rope_dim] (16-byte aligned): cos in the first half of a row, sin
+ *              in the second; element i and i + rope_dim/2 of a head turn together, elements past
+ *              rope_dim are left alone. rope_dim a multiple of 16, <= D; 0 (rope NULL): none
+ *   E4M3 caches store e4m3(value * (1 / scale)) rounded to nearest, saturated at +-448.
+ *   workspace  at least FT_MOE_WORKSPACE_HEAD_BYTES, its error word collects
+ *              FT_ERR_DEVICE_FLAG, or NULL. A page, sequence or position outside its table stores
+ *              nothing and flags. No two tokens of a call may share a slot.
+ *   T <= 1048576, Hq and Hkv <= 1024.
+ */
+ft_status ft_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                       const uint16_t* q, int64_t q_stride, uint16_t* q_out, int32_t T, int32_t Hq,
+                       const ft_paged_kv* cache, const int32_t* block_table, int32_t B,
+                       int32_t table_width, const int32_t* seq_ids, const int32_t* positions,
+                       const float* rope, int32_t rope_rows, int32_t rope_dim, void* workspace,
+                       void* stream);
+
+/* Workspace bytes of ft_paged_decode_attention for B sequences and heads of D elements on the
+ * current device (0 for invalid sizes or without a device). */
+size_t ft_paged_attention_workspace_bytes(int32_t B, int32_t D);
+
+/*
+ * ft_paged_decode_attention — attention of one new token per sequence over its cached keys and
+ * values (the new token's own among them, once appended):
+ *   s_j = scale * (q . k_j) for max(0, len - window) <= j < len (window 0: all of them)
+ *   out = sum_j softmax(s)_j v_j,   lse = ln sum_j exp(s_j)
+ *   q            bf16, heads of sequence b at q + b * q_stride [Hq, D] (16-byte aligned, q_stride a
+ *                multiple of 8); query head h reads key head h / (Hq / Hkv); Hkv divides Hq <= 1024
+ *   seq_lens     int32 [B] on the device (not read by the host); a length of zero or less gives
+ *                out = 0 and lse = -inf, as does a row whose scores are all -inf
+ *   block_table  int32 [B, table_width] as for ft_kv_append; entries past a sequence's last page
+ *                are not read. A page outside [0, num_pages), or a length past the table, flags
+ *                FT_ERR_DEVICE_FLAG in the workspace, and its keys and values read as zeros.
+ *   out          bf16 [B, Hq, D], lse float [B, Hq] or NULL, fully overwritten
+ *   workspace    ft_paged_attention_workspace_bytes(B, D) bytes, 256-byte aligned, its first
+ *                FT_MOE_WORKSPACE_HEAD_BYTES zeroed once (ft_moe_workspace_init); calls that
+ *                share it must be ordered on one stream. It may be shared with the layer calls.
+ *   0 <= B <= 4096. Whatever masked slots hold does not reach the output. Float32 scores,
+ *   statistics and sums; the work is split over the cache's length and joined in a fixed order
+ *   (two launches), deterministic.
+ */
+ft_status ft_paged_decode_attention(const uint16_t* q, int64_t q_stride, int32_t B, int32_t Hq,
+                                    const ft_paged_kv* cache, const int32_t* block_table,
+                                    int32_t table_width, const int32_t* seq_lens, float scale,
+                                    int32_t window, uint16_t* out, float* lse, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* What a gate of ft_residual_norm multiplies: nothing (no gate), bf16 [H], [T] or [T, H]. */
+#define FT_GATE_NONE 0
+#define FT_GATE_CHANNEL 1
+#define FT_GATE_TOKEN 2
+#define FT_GATE_ELEMENT 3
+
+/*
+ * ft_residual_norm — the norm after a block, the gated residual sum and the norm before the next
+ * block in one launch. Root-mean-square norms over rows of H:
+ *   z  = y / sqrt(mean(y^2) + eps) * w_post        (w_post NULL: z = y)
+ *   r' = residual + scale * gate * z               (residual NULL: 0; gate as gate_kind says)
+ *   x' = r' / sqrt(mean(r'^2) + eps) * w_pre       (w_pre NULL: x_out is not written)
+ *   y bf16 [T, H]; residual, r_out bf16 or float (res_f32) [T, H]; w_post, w_pre bf16 [H]; gate
+ *   bf16; x_out bf16 [T, H]; all 16-byte aligned (a token gate 2-byte) and contiguous. r_out may
+ *   be NULL when only x' is wanted, and may be the residual itself; x_out may be y itself.
+ *   H a multiple of 8, 8 <= H <= 16384; T >= 0; eps >= 0, scale finite. float32 inside; x' is
+ *   taken from r' before its rounding.
+ */
+ft_status ft_residual_norm(const uint16_t* y, const void* residual, const uint16_t* w_post,
+                           const uint16_t* w_pre, const uint16_t* gate, int32_t gate_kind,
+                           int32_t T, int32_t H, int32_t res_f32, float scale, float eps,
+                           void* r_out, uint16_t* x_out, void* stream);
+
+/* Workspace bytes of ft_residual_norm_backward on the current device (0 for invalid sizes). */
+size_t ft_residual_norm_backward_workspace_bytes(int32_t T, int32_t H);
+
+/*
+ * ft_residual_norm_backward — the gradient of ft_residual_norm in every input (statistics are
+ * taken from y and residual again; nothing is kept from the forward call).
+ *   d_r    like the residual, the gradient of r' (NULL: zero); d_x bf16 [T, H], of x' (required
+ *          with w_pre, ignored without)
+ *   dy     bf16 [T, H]; dresidual like the residual's type [T, H] (written with residual NULL too)
+ *   dw_post, dw_pre  float [H], required with their weights
+ *   dgate  float [H] (channel), float [T] (token), bf16 [T, H] (element); required with a gate
+ *   workspace of ft_residual_norm_backward_workspace_bytes(T, H) bytes, 256-byte aligned, any
+ *   contents past its first FT_MOE_WORKSPACE_HEAD_BYTES. T = 0 zeroes the weights' and channel
+ *   gate's gradients. Column sums run in a fixed order (deterministic), two launches.
+ *   dresidual may be d_r itself, dy may be y or d_x itself.
+ */
+ft_status ft_residual_norm_backward(const uint16_t* y, const void* residual,
+                                    const uint16_t* w_post, const uint16_t* w_pre,
+                                    const uint16_t* gate, int32_t gate_kind, const void* d_r,
+                                    const uint16_t* d_x, int32_t T, int32_t H, int32_t res_f32,
+                                    float scale, float eps, uint16_t* dy, void* dresidual,
+                                    float* dw_post, float* dw_pre, void* dgate, void* workspace,
+                                    size_t workspace_bytes, void* stream);
 
 /* Text of the last CUDA runtime error seen by this thread inside the library (the cause
  * behind an FT_ERR_CUDA); static storage, never NULL. */

@@ -46,6 +46,8 @@ ft_status cuda_status(cudaError_t e) {
   return FT_ERR_CUDA;
 }
 
+int device_sms() { return sm_count(); }
+
 unsigned wait_limit(unsigned dflt) {
   const long long v = g_wait_limit.load(std::memory_order_relaxed);
   return v < 0 ? dflt : (unsigned)v;
@@ -126,7 +128,7 @@ const char* ft_status_string(ft_status s) {
     case FT_ERR_MISALIGNED: return "FT_ERR_MISALIGNED: pointer alignment";
     case FT_ERR_WORKSPACE_TOO_SMALL: return "FT_ERR_WORKSPACE_TOO_SMALL: workspace too small";
     case FT_ERR_CUDA: return "FT_ERR_CUDA: CUDA runtime error";
-    case FT_ERR_DEVICE_FLAG: return "FT_ERR_DEVICE_FLAG: expert id outside [0, E) or repeated in a token";
+    case FT_ERR_DEVICE_FLAG: return "FT_ERR_DEVICE_FLAG: expert id outside [0, E) or repeated in a token, or a page, sequence or position outside its table";
     case FT_ERR_TIMEOUT: return "FT_ERR_TIMEOUT: bounded device wait expired";
   }
   return "unknown ft_status";
@@ -407,7 +409,7 @@ ft_status ft_moe_get_error(void* workspace, void* stream) {
     st = cuda_status(cudaMemcpy(workspace, &zero, sizeof(int), cudaMemcpyHostToDevice));
     if (st != FT_OK) return st;
   }
-  if (word & kErrBadExpert) return FT_ERR_DEVICE_FLAG;
+  if (word & (kErrBadExpert | kErrBadPage)) return FT_ERR_DEVICE_FLAG;
   if (word & kErrTimeout) return FT_ERR_TIMEOUT;
   return FT_OK;
 }

@@ -96,4 +96,89 @@ cudaError_t launch_f8_decode(const uint16_t* x, int T, const int* topk_idx, cons
                              int k, const F8Ptrs& ex, float limit, uint16_t* out, void* ws,
                              int num_sms, cudaStream_t stream);
 
+// Dense NVFP4 matrix times 1 to 64 tokens (linear.cu).
+struct LinearArgs {
+  const uint16_t* x;       // [T][x_stride] bf16
+  int64_t x_stride;
+  int T, N, K;
+  const uint8_t *codes, *scales;
+  const float* gscale;
+  void* out;               // [T][N] bf16 or float
+  int out_f32;
+  int split;               // blocks of a cluster that share K (set by the launch)
+};
+cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream);
+
+// Rotary embedding and cache append (kv.cu). err: error word or null.
+struct AppendArgs {
+  const uint16_t *k, *v, *q;
+  int64_t k_stride, v_stride, q_stride;   // elements between tokens
+  uint16_t* q_out;
+  int T, Hq;
+  ft_paged_kv kv;
+  float inv_k, inv_v;
+  const int *block_table, *seq_ids, *positions;
+  int B, table_width;
+  const float* rope;
+  int rope_rows, rope_dim;
+  int* err;
+};
+cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
+
+// Paged attention of one new token per sequence (attention.cu).
+struct AttendArgs {
+  const uint16_t* q;
+  int64_t q_stride;
+  int B, Hq;
+  ft_paged_kv kv;
+  const int *block_table, *seq_lens;
+  int table_width;
+  float scale;
+  int window;
+  uint16_t* out;
+  float* lse;
+  int* err;                // workspace: error word, plan [B + 1], pieces' (max, sum) and sums
+  int* plan;
+  float *part_ml, *part_o;
+  int group, gt;           // query heads per key head, 16-head parts of them (set by the launch)
+  int div_mul, div_shift;  // division by the page size (set by the launch)
+};
+// Workspace regions (byte offsets, 256-byte aligned).
+struct AttendLayout {
+  size_t plan = 0, ml = 0, o = 0, total = 0;
+  AttendLayout(int B, int D, int num_sms) {
+    plan = 1024;
+    ml = align_up(plan + (size_t)(B + 1) * 4, 256);
+    o = align_up(ml + (size_t)num_sms * 2 * 16 * 2 * 4, 256);
+    total = align_up(o + (size_t)num_sms * 2 * 16 * D * 4, 256);
+  }
+};
+cudaError_t launch_attend(const AttendArgs& a, int num_sms, cudaStream_t stream);
+
+// Norms around a gated residual sum, and the gradient (norm.cu).
+struct NormArgs {
+  const uint16_t* y;
+  const void* r;           // bf16 or float (res_f32), or null
+  const uint16_t *w_post, *w_pre, *gate;
+  int T, H, gate_kind, res_f32;
+  float scale, eps;
+  void* r_out;             // forward
+  uint16_t* x_out;
+  const void* dr;          // backward
+  const uint16_t* dx;
+  uint16_t* dy;
+  void* dres;
+  float *dw_post, *dw_pre;
+  void* dgate;             // float [H] / [T], bf16 [T][H]
+  float* part;             // workspace: column sums [group][nq][H]
+  int nq;
+};
+// Row groups (rows of the workspace's partial sums) of the backward pass.
+int norm_bwd_groups(int T, int H, int num_sms);
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream);
+cudaError_t launch_norm_bwd(const NormArgs& a, int num_sms, cudaStream_t stream);
+
+// SM count of the current device (0: no device).
+int device_sms();
+
 }  // namespace ftmoe

@@ -45,6 +45,7 @@ D1Geom d1_geom(int H, int I, int grid);
 // Error word bits (workspace offset 0).
 constexpr int kErrBadExpert = 1;
 constexpr int kErrTimeout = 2;
+constexpr int kErrBadPage = 4;   // a page, sequence or rotary position outside its table
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
@@ -28,7 +29,10 @@ EXPORTED = ["ft_moe_abi_version", "ft_status_string", "ft_moe_route", "ft_moe_wo
             "ft_moe_nvfp4_decode_routed", "ft_moe_decode_smem_bytes",
             "ft_moe_debug_set_wait_limit", "ft_moe_layer_from_host",
             "ft_moe_fp8block_workspace_bytes", "ft_moe_fp8block_decode",
-            "ft_moe_router_logits", "ft_moe_router_route"]
+            "ft_moe_router_logits", "ft_moe_router_route",
+            "ft_nvfp4_linear", "ft_kv_append", "ft_paged_attention_workspace_bytes",
+            "ft_paged_decode_attention", "ft_residual_norm",
+            "ft_residual_norm_backward_workspace_bytes", "ft_residual_norm_backward"]
 
 # Leading bytes of a workspace that must be zero before a call (FT_MOE_WORKSPACE_HEAD_BYTES);
 # the rest is scratch whose contents never reach an output.
@@ -66,6 +70,21 @@ class _F8Shared(ctypes.Structure):
     _fields_ = [("w13", ctypes.c_void_p), ("w13_scale", ctypes.c_void_p),
                 ("w2", ctypes.c_void_p), ("w2_scale", ctypes.c_void_p),
                 ("gate", ctypes.c_void_p)]
+
+
+class _Matrix(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int32), ("K", ctypes.c_int32), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("gscale", ctypes.c_void_p)]
+
+
+class _PagedKV(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("k_page_stride", ctypes.c_int64), ("k_slot_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64),
+                ("v_slot_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("k_scale", ctypes.c_float),
+                ("v_scale", ctypes.c_float)]
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -112,6 +131,24 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ft_moe_fp8block_decode.restype = ctypes.c_int
     lib.ft_moe_fp8block_decode.argtypes = [vp, i32, vp, vp, i32, ctypes.POINTER(_F8Experts),
                                            ctypes.POINTER(_F8Shared), f32, vp, vp, sz, vp]
+    i64 = ctypes.c_int64
+    lib.ft_nvfp4_linear.restype = ctypes.c_int
+    lib.ft_nvfp4_linear.argtypes = [vp, i32, i64, ctypes.POINTER(_Matrix), vp, i32, vp]
+    lib.ft_kv_append.restype = ctypes.c_int
+    lib.ft_kv_append.argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, i32, ctypes.POINTER(_PagedKV),
+                                 vp, i32, i32, vp, vp, vp, i32, i32, vp, vp]
+    lib.ft_paged_attention_workspace_bytes.restype = sz
+    lib.ft_paged_attention_workspace_bytes.argtypes = [i32, i32]
+    lib.ft_paged_decode_attention.restype = ctypes.c_int
+    lib.ft_paged_decode_attention.argtypes = [vp, i64, i32, i32, ctypes.POINTER(_PagedKV), vp, i32,
+                                              vp, f32, i32, vp, vp, vp, sz, vp]
+    lib.ft_residual_norm.restype = ctypes.c_int
+    lib.ft_residual_norm.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, f32, vp, vp, vp]
+    lib.ft_residual_norm_backward_workspace_bytes.restype = sz
+    lib.ft_residual_norm_backward_workspace_bytes.argtypes = [i32, i32]
+    lib.ft_residual_norm_backward.restype = ctypes.c_int
+    lib.ft_residual_norm_backward.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, f32,
+                                              f32, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.ft_moe_debug_set_wait_limit.restype = ctypes.c_int
     lib.ft_moe_debug_set_wait_limit.argtypes = [ctypes.c_int64]
     return lib
@@ -631,6 +668,335 @@ def fp8block_decode(x, topk_idx, topk_w, experts: Fp8BlockExperts, shared=None, 
                                      _stream(stream, dev))
     _check(st, "ft_moe_fp8block_decode")
     return out
+
+
+# ---------------------------------------------------------------- the decode block
+# The operators between two layer calls: dense NVFP4 products, cache append, attention of one new
+# token per sequence and the norms around the gated residual sum. Sizes come from the tensors;
+# what the kernels require beyond them (multiples, ranges) is refused by the library with its
+# status, what they would read out of bounds is refused here.
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_ELEMENT = range(4)
+_RES = (torch.bfloat16, torch.float32)
+
+
+def _need_rows(t, name, dev, inner):
+    """t on cuda:dev, bf16 bits [T, *inner] whose rows are contiguous: the distance between rows
+    may be larger than a row (a slice of a wider tensor). Returns it, in elements."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a tensor on cuda:{dev}, got one on {t.device}")
+    if t.dtype not in BF16_BITS:
+        raise TypeError(f"{name}: element type {t.dtype} is not accepted here")
+    if tuple(t.shape[1:]) != inner:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [T, {', '.join(map(str, inner))}]")
+    at = 1
+    for size, stride in zip(reversed(inner), reversed(t.stride()[1:])):
+        if stride != at and size != 1:
+            raise ValueError(f"{name}: the elements of a row must be contiguous")
+        at *= size
+    if t.shape[0] > 1 and t.stride(0) < at:
+        raise ValueError(f"{name}: the rows must not overlap")
+    return t.stride(0) if t.shape[0] > 1 else at
+
+
+def _scratch(n, dev, stream):
+    """n bytes of the workspace that calls without one share per (device, stream)."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    key = (dev, stream.cuda_stream)
+    ws = _DEFAULT_WS.get(key)
+    if ws is None or ws.numel() < n:
+        ws = _new_scratch(n, dev, stream)
+        _DEFAULT_WS[key] = ws
+    return ws
+
+
+def _new_scratch(n, dev, stream):
+    ws = torch.empty(n + 256, dtype=torch.uint8, device=torch.device("cuda", dev))
+    off = (-ws.data_ptr()) % 256
+    ws = ws[off:off + n]
+    _check(_LIB.ft_moe_workspace_init(_ptr(ws), n, _stream(stream, dev)), "ft_moe_workspace_init")
+    return ws
+
+
+@dataclass(frozen=True)
+class NvFP4Linear:
+    """A dense NVFP4 matrix on the device: codes u8 [N,K/2], scales u8 [N,K/16] (any 1-byte type),
+    gscale a 1-element f32 tensor. Checked when built."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    gscale: torch.Tensor
+
+    def __post_init__(self):
+        dev = _device_of(self.codes, "NvFP4Linear")
+        if self.codes.dim() != 2:
+            raise ValueError("NvFP4Linear: codes [N,K/2] are 2-D")
+        N, K = self.codes.shape[0], self.codes.shape[1] * 2
+        if K % 32 != 0 or K == 0 or N == 0:
+            raise ValueError("NvFP4Linear: K is a multiple of 32, and N is not 0")
+        _need(self.codes, "codes", dev, None, (N, K // 2))
+        _need(self.scales, "scales", dev, None, (N, K // 16))
+        _need_scalar(self.gscale, "gscale", dev)
+        object.__setattr__(self, "device_index", dev)
+        object.__setattr__(self, "N", N)
+        object.__setattr__(self, "K", K)
+        object.__setattr__(self, "_cs", _Matrix(N, K, _ptr(self.codes), _ptr(self.scales),
+                                                _ptr(self.gscale)))
+        object.__setattr__(self, "_ref", ctypes.byref(self._cs))
+
+
+def nvfp4_linear(x, weight: NvFP4Linear, out=None, out_dtype=torch.bfloat16, stream=None):
+    """ft_nvfp4_linear: x bf16 [T,K] (T <= 64; rows may be slices of a wider tensor) -> W x_t,
+    [T,N] in bf16, or in float32 (out_dtype, or the type of `out`)."""
+    dev = weight.device_index
+    if x.dim() != 2:
+        raise ValueError("x: [T, K] expected")
+    stride = _need_rows(x, "x", dev, (weight.K,))
+    T = x.shape[0]
+    if out is None:
+        if out_dtype not in _RES:
+            raise TypeError(f"out_dtype: {out_dtype} is not accepted here")
+        out = torch.empty((T, weight.N), dtype=out_dtype, device=x.device)
+    else:
+        _need(out, "out", dev, _RES, (T, weight.N))
+    st = _LIB.ft_nvfp4_linear(x.data_ptr(), T, stride, weight._ref, out.data_ptr(),
+                              out.dtype is torch.float32, _stream(stream, dev))
+    _check(st, "ft_nvfp4_linear")
+    return out
+
+
+@dataclass(frozen=True)
+class PagedKVCache:
+    """A paged key-value cache on the device: k and v [num_pages, page_size, Hkv, D], bf16 or
+    float8_e4m3fn (values are code * scale), elements of a head contiguous and the other strides
+    free (a permuted view of [page, head, slot, d] storage is fine). Checked when built."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: float = 1.0
+    v_scale: float = 1.0
+
+    def __post_init__(self):
+        dev = _device_of(self.k, "PagedKVCache")
+        if self.k.dim() != 4 or self.k.shape != self.v.shape:
+            raise ValueError("PagedKVCache: k and v [num_pages, page_size, Hkv, D] of one shape")
+        if self.v.get_device() != dev:
+            raise ValueError("PagedKVCache: k and v must be on one device")
+        if self.k.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or self.k.dtype != self.v.dtype:
+            raise TypeError("PagedKVCache: k and v are both bfloat16 or both float8_e4m3fn")
+        if self.k.stride(3) != 1 or self.v.stride(3) != 1:
+            raise ValueError("PagedKVCache: the elements of a head must be contiguous")
+        f8 = self.k.dtype == torch.float8_e4m3fn
+        object.__setattr__(self, "device_index", dev)
+        object.__setattr__(self, "_cs", _PagedKV(
+            _ptr(self.k), _ptr(self.v), *self.k.shape, *self.k.stride()[:3], *self.v.stride()[:3],
+            int(f8), float(self.k_scale), float(self.v_scale)))
+        object.__setattr__(self, "_ref", ctypes.byref(self._cs))
+
+    @property
+    def page_size(self):
+        return self._cs.page_size
+
+    @property
+    def Hkv(self):
+        return self._cs.Hkv
+
+    @property
+    def D(self):
+        return self._cs.D
+
+
+def kv_append(k, v, cache: PagedKVCache, block_table, positions, seq_ids=None, q=None, rope=None,
+              q_out=None, workspace=None, stream=None):
+    """ft_kv_append: k, v bf16 [T,Hkv,D] into the cache's slots of `positions` int32 [T] (of the
+    sequences seq_ids int32 [T], or 0..T-1) through block_table int32 [B,width], k rotated by rope
+    f32 [rows, R] (cos | sin; None: not at all). Returns the rotated q bf16 [T,Hq,D], or None
+    without q. Rows of k, v and q may be slices of one projection's output."""
+    dev = cache.device_index
+    cs = cache._cs
+    if k.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("k [T, Hkv, D] and block_table [B, width] expected")
+    T, inner = k.shape[0], (cs.Hkv, cs.D)
+    ks, vs = _need_rows(k, "k", dev, inner), _need_rows(v, "v", dev, inner)
+    if v.shape[0] != T:
+        raise ValueError("v: as many tokens as k expected")
+    _need(block_table, "block_table", dev, _I32, None)
+    _need(positions, "positions", dev, _I32, (T,))
+    B = block_table.shape[0]
+    if seq_ids is not None:
+        _need(seq_ids, "seq_ids", dev, _I32, (T,))
+    elif T > B:
+        raise ValueError("seq_ids: required for more tokens than block_table has rows")
+    Hq, qs = 0, 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != T:
+            raise ValueError("q: [T, Hq, D] expected")
+        Hq = q.shape[1]
+        qs = _need_rows(q, "q", dev, (Hq, cs.D))
+        if q_out is None:
+            q_out = torch.empty((T, Hq, cs.D), dtype=torch.bfloat16, device=q.device)
+        else:
+            _need(q_out, "q_out", dev, BF16_BITS, (T, Hq, cs.D))
+    rows, dim = 0, 0
+    if rope is not None:
+        if rope.dim() != 2:
+            raise ValueError("rope: [rows, R] expected")
+        _need(rope, "rope", dev, _F32, None)
+        rows, dim = rope.shape
+    if workspace is not None:
+        _need(workspace, "workspace", dev, None, None)
+        if workspace.numel() < WORKSPACE_HEAD_BYTES:
+            raise ValueError("workspace: at least WORKSPACE_HEAD_BYTES expected")
+    st = _LIB.ft_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q), qs,
+                           _ptr(q_out) if q is not None else 0, T, Hq, cache._ref,
+                           block_table.data_ptr(), B, block_table.shape[1], _ptr(seq_ids),
+                           positions.data_ptr(), _ptr(rope), rows, dim, _ptr(workspace),
+                           _stream(stream, dev))
+    _check(st, "ft_kv_append")
+    return q_out if q is not None else None
+
+
+def paged_attention_workspace_bytes(B, D) -> int:
+    return _LIB.ft_paged_attention_workspace_bytes(B, D)
+
+
+def paged_decode_attention(q, cache: PagedKVCache, block_table, seq_lens, scale=None, window=0,
+                           out=None, lse=None, workspace=None, stream=None):
+    """ft_paged_decode_attention: q bf16 [B,Hq,D], one new token per sequence, over the first
+    seq_lens int32 [B] slots of each (the last `window` of them if window > 0) through block_table
+    int32 [B,width]. scale: 1/sqrt(D) by default. Returns (out bf16 [B,Hq,D], lse f32 [B,Hq])."""
+    dev = cache.device_index
+    D = cache._cs.D
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q [B, Hq, D] and block_table [B, width] expected")
+    B, Hq = q.shape[0], q.shape[1]
+    qs = _need_rows(q, "q", dev, (Hq, D))
+    _need(block_table, "block_table", dev, _I32, None)
+    if block_table.shape[0] != B:
+        raise ValueError(f"block_table: {block_table.shape[0]} rows for {B} sequences")
+    _need(seq_lens, "seq_lens", dev, _I32, (B,))
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=q.device)
+    else:
+        _need(out, "out", dev, BF16_BITS, (B, Hq, D))
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    else:
+        _need(lse, "lse", dev, _F32, (B, Hq))
+    if workspace is not None:
+        _need(workspace, "workspace", dev, None, None)
+    elif B > 0:
+        n = _LIB.ft_paged_attention_workspace_bytes(B, D)
+        if n == 0:
+            raise FtError(2, "ft_paged_attention_workspace_bytes")
+        workspace = _scratch(n, dev, stream)
+    st = _LIB.ft_paged_decode_attention(
+        q.data_ptr(), qs, B, Hq, cache._ref, block_table.data_ptr(), block_table.shape[1],
+        seq_lens.data_ptr(), D ** -0.5 if scale is None else scale, window, out.data_ptr(),
+        lse.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+        _stream(stream, dev))
+    _check(st, "ft_paged_decode_attention")
+    return out, lse
+
+
+def _norm_inputs(y, residual, w_post, w_pre, gate):
+    """Checks shared by the norm and its gradient. Returns (device, T, H, gate kind, stream type)."""
+    dev = _device_of(y, "ft_residual_norm")
+    if y.dim() != 2:
+        raise ValueError("y: [T, H] expected")
+    T, H = y.shape
+    _need(y, "y", dev, BF16_BITS, (T, H))
+    res = torch.bfloat16
+    if residual is not None:
+        _need(residual, "residual", dev, _RES, (T, H))
+        res = residual.dtype
+    if w_post is not None:
+        _need(w_post, "w_post", dev, BF16_BITS, (H,))
+    if w_pre is not None:
+        _need(w_pre, "w_pre", dev, BF16_BITS, (H,))
+    kind = GATE_NONE
+    if gate is not None:
+        shape = tuple(gate.shape)
+        if shape == (H,):
+            kind = GATE_CHANNEL
+        elif shape == (T, 1):
+            kind = GATE_TOKEN
+        elif shape == (T, H):
+            kind = GATE_ELEMENT
+        else:
+            raise ValueError(f"gate: shape {shape}, expected ({H},), ({T}, 1) or ({T}, {H})")
+        _need(gate, "gate", dev, BF16_BITS, None)
+    return dev, T, H, kind, res
+
+
+def residual_norm(y, residual=None, w_post=None, w_pre=None, gate=None, scale=1.0, eps=1e-6,
+                  res_out=None, x_out=None, stream=None):
+    """ft_residual_norm: r' = residual + scale * gate * norm(y, w_post) and x' = norm(r', w_pre) for
+    y bf16 [T,H]; a weight that is None leaves its norm out. gate bf16 [H], [T,1] or [T,H].
+    Returns (r' in the residual's type, x' bf16 or None without w_pre)."""
+    dev, T, H, kind, res = _norm_inputs(y, residual, w_post, w_pre, gate)
+    if res_out is None:
+        res_out = torch.empty((T, H), dtype=res, device=y.device)
+    else:
+        _need(res_out, "res_out", dev, _RES if residual is None else (res,), (T, H))
+        res = res_out.dtype
+    if w_pre is None:
+        x_out = None
+    elif x_out is None:
+        x_out = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
+    else:
+        _need(x_out, "x_out", dev, BF16_BITS, (T, H))
+    st = _LIB.ft_residual_norm(y.data_ptr(), _ptr(residual), _ptr(w_post), _ptr(w_pre), _ptr(gate),
+                               kind, T, H, res is torch.float32, scale, eps, res_out.data_ptr(),
+                               _ptr(x_out), _stream(stream, dev))
+    _check(st, "ft_residual_norm")
+    return res_out, x_out
+
+
+class NormGradients(NamedTuple):
+    """What residual_norm_backward returns; None for inputs that were None."""
+    dy: torch.Tensor
+    dresidual: torch.Tensor
+    dw_post: torch.Tensor | None
+    dw_pre: torch.Tensor | None
+    dgate: torch.Tensor | None
+
+
+def residual_norm_backward(y, residual, d_r, d_x=None, w_post=None, w_pre=None, gate=None,
+                           scale=1.0, eps=1e-6, workspace=None, stream=None) -> NormGradients:
+    """ft_residual_norm_backward: the gradient of residual_norm for d_r (of r', its type; None: zero)
+    and d_x (of x', bf16; required with w_pre): dy bf16, dresidual in the stream's type (the
+    residual's, or d_r's without one), dw_post and dw_pre f32 [H], dgate f32 [H] or [T,1], or bf16
+    [T,H]."""
+    dev, T, H, kind, res = _norm_inputs(y, residual, w_post, w_pre, gate)
+    if d_r is not None:
+        _need(d_r, "d_r", dev, _RES if residual is None else (res,), (T, H))
+        res = d_r.dtype
+    if w_pre is not None:
+        if d_x is None:
+            raise ValueError("d_x: required with w_pre")
+        _need(d_x, "d_x", dev, BF16_BITS, (T, H))
+    cuda, f32 = y.device, torch.float32
+    dy = torch.empty((T, H), dtype=torch.bfloat16, device=cuda)
+    dres = torch.empty((T, H), dtype=res, device=cuda)
+    dw_post = torch.empty(H, dtype=f32, device=cuda) if w_post is not None else None
+    dw_pre = torch.empty(H, dtype=f32, device=cuda) if w_pre is not None else None
+    dgate = None
+    if gate is not None:
+        dgate = torch.empty(gate.shape, dtype=torch.bfloat16 if kind == GATE_ELEMENT else f32,
+                            device=cuda)
+    if workspace is not None:
+        _need(workspace, "workspace", dev, None, None)
+    elif T > 0:
+        n = _LIB.ft_residual_norm_backward_workspace_bytes(T, H)
+        if n == 0:
+            raise FtError(2, "ft_residual_norm_backward_workspace_bytes")
+        workspace = _scratch(n, dev, stream)
+    st = _LIB.ft_residual_norm_backward(
+        y.data_ptr(), _ptr(residual), _ptr(w_post), _ptr(w_pre), _ptr(gate), kind, _ptr(d_r),
+        _ptr(d_x) if w_pre is not None else 0, T, H, res is torch.float32, scale, eps,
+        dy.data_ptr(), dres.data_ptr(), _ptr(dw_post), _ptr(dw_pre), _ptr(dgate), _ptr(workspace),
+        0 if workspace is None else workspace.numel(), _stream(stream, dev))
+    _check(st, "ft_residual_norm_backward")
+    return NormGradients(dy, dres, dw_post, dw_pre, dgate)
 
 
 def get_error(workspace, stream=None) -> int:

@@ -10,10 +10,12 @@ Modules
 * ``oracle.fp8block`` — block-FP8 dequantisation (E4M3 elements, float32 tile scales).
 * ``oracle.moe``   — route (softmax, top-k, renormalise), clamped SwiGLU experts, the
   router-weighted sum and the gated shared expert.
+* ``oracle.block`` — dense NVFP4 products, rotary embedding, attention over cached keys and
+  the norms around the gated residual sum with their gradient (float64).
 
 Every function is pinned by tests/test_oracle_*.py against values fixed outside the
 oracle: the printed E2M1 value table, the library float8 type, hand-derived closed
 forms stored under tests/golden/, brute force on tiny inputs, and invariants (weights sum
 to one, a zero expert contributes nothing, linearity in W2, the k = E dense reduction).
 """
-from . import fp8block, moe, nvfp4  # noqa: F401
+from . import block, fp8block, moe, nvfp4  # noqa: F401
