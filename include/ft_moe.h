@@ -313,7 +313,7 @@ ft_status ft_moe_fp8block_decode(const uint16_t* x, int32_t T, const int32_t* to
 
 /* A dense NVFP4 matrix W [N, K] in the layout of the experts' matrices without the E dimension:
  *   codes uint8 [N, K/2] (16-byte aligned), scales uint8 [N, K/16] (2-byte aligned), gscale one
- *   device float (4-byte aligned). N >= 1, K a multiple of 32, 32 <= K <= 32768. */
+ *   device float (4-byte aligned). 1 <= N <= 2^30, K a multiple of 32, 32 <= K <= 32768. */
 typedef struct {
   int32_t N, K;
   const uint8_t* codes;
@@ -321,15 +321,22 @@ typedef struct {
   const float* gscale;
 } ft_nvfp4_matrix;
 
+/* Workspace bytes of ft_nvfp4_linear: 0 for up to 8 tokens (and for invalid sizes). */
+size_t ft_nvfp4_linear_workspace_bytes(int32_t T, int32_t K);
+
 /*
- * ft_nvfp4_linear — y_t = W x_t for 0 <= T <= 64 tokens (T = 0 is a no-op), one launch.
+ * ft_nvfp4_linear — y_t = W x_t for 0 <= T <= 64 tokens (T = 0 is a no-op): one launch for up to 8
+ * tokens, two (x's layout first) for more.
  *   x        bf16, token t at x + t * x_stride (16-byte aligned; x_stride a multiple of 8, >= K)
  *   out      [T, N], bf16 (out_f32 = 0, 2-byte aligned) or float (out_f32 = 1, 4-byte aligned),
  *            fully overwritten; float32 sums, the matrix's scale last, rounded once
+ *   workspace ft_nvfp4_linear_workspace_bytes(T, K) bytes, 256-byte aligned (NULL when that is 0);
+ *            any contents past the error word; calls that share it must be ordered on one stream
  *   A NaN block scale gives NaN; x is used as it is (infinities and NaN propagate).
  */
 ft_status ft_nvfp4_linear(const uint16_t* x, int32_t T, int64_t x_stride,
-                          const ft_nvfp4_matrix* w, void* out, int32_t out_f32, void* stream);
+                          const ft_nvfp4_matrix* w, void* out, int32_t out_f32, void* workspace,
+                          size_t workspace_bytes, void* stream);
 
 /* Element type of a key-value cache. */
 #define FT_KV_BF16 0

@@ -13,6 +13,7 @@ using namespace ftmoe;
 namespace {
 
 constexpr int kMaxLinearK = 32768;
+constexpr int kMaxLinearN = 1 << 30;
 constexpr int kMaxSeqs = 4096;
 constexpr int kMaxHeads = 1024;
 constexpr int kMaxAppend = 1 << 20;
@@ -60,10 +61,19 @@ ft_status check_norm(const uint16_t* y, const void* residual, const uint16_t* w_
 
 extern "C" {
 
+size_t ft_nvfp4_linear_workspace_bytes(int32_t T, int32_t K) {
+  if (T < 1 || T > kMaxDecodeT || K < 32 || K % 32 != 0 || K > kMaxLinearK) return 0;
+  if (T <= kLinearFew) return 0;
+  const int sms = device_sms();
+  return sms > 0 ? LinearLayout(T, K, sms).total : 0;
+}
+
 ft_status ft_nvfp4_linear(const uint16_t* x, int32_t T, int64_t x_stride,
-                          const ft_nvfp4_matrix* w, void* out, int32_t out_f32, void* stream) {
+                          const ft_nvfp4_matrix* w, void* out, int32_t out_f32, void* workspace,
+                          size_t workspace_bytes, void* stream) {
   if (!w || T < 0 || w->N < 1 || w->K < 1) return FT_ERR_INVALID_ARG;
-  if (T > kMaxDecodeT || w->K % 32 != 0 || w->K > kMaxLinearK) return FT_ERR_UNSUPPORTED_SHAPE;
+  if (T > kMaxDecodeT || w->K % 32 != 0 || w->K > kMaxLinearK || w->N > kMaxLinearN)
+    return FT_ERR_UNSUPPORTED_SHAPE;
   if (!w->codes || !w->scales || !w->gscale) return FT_ERR_INVALID_ARG;
   if (!aligned(w->codes, 16) || !aligned(w->scales, 2) || !aligned(w->gscale, 4))
     return FT_ERR_MISALIGNED;
@@ -71,9 +81,23 @@ ft_status ft_nvfp4_linear(const uint16_t* x, int32_t T, int64_t x_stride,
   if (!x || !out || (T > 1 && x_stride < w->K)) return FT_ERR_INVALID_ARG;
   if (!aligned(x, 16) || x_stride % 8 != 0 || !aligned(out, out_f32 ? 4 : 2))
     return FT_ERR_MISALIGNED;
+  if (T > kLinearFew) {
+    if (!workspace) return FT_ERR_INVALID_ARG;
+    if (!aligned(workspace, 256)) return FT_ERR_MISALIGNED;
+    if (workspace_bytes < LinearLayout(T, w->K, 1).total) return FT_ERR_WORKSPACE_TOO_SMALL;
+  }
   const int sms = device_sms();
   if (sms <= 0) return FT_ERR_CUDA;
+  const LinearLayout L(T, w->K, sms);
+  if (workspace_bytes < L.total) return FT_ERR_WORKSPACE_TOO_SMALL;
   LinearArgs a = {};
+  if (L.total > 0) {
+    char* ws = static_cast<char*>(workspace);
+    a.err = reinterpret_cast<int*>(ws);
+    a.xdown = reinterpret_cast<float*>(ws + L.xdown);
+    a.xh = reinterpret_cast<uint16_t*>(ws + L.xh);
+    a.part = reinterpret_cast<float*>(ws + L.part);
+  }
   a.x = x; a.x_stride = x_stride; a.T = T; a.N = w->N; a.K = w->K;
   a.codes = w->codes; a.scales = w->scales; a.gscale = w->gscale;
   a.out = out; a.out_f32 = out_f32 ? 1 : 0;

@@ -105,7 +105,24 @@ struct LinearArgs {
   const float* gscale;
   void* out;               // [T][N] bf16 or float
   int out_f32;
+  int* err;                // workspace: error word, x's powers of two [T], x as f16, partial tiles
+  float* xdown;
+  uint16_t* xh;
+  float* part;
   int split;               // blocks of a cluster that share K (set by the launch)
+};
+// Workspace regions (byte offsets, 256-byte aligned): none for the calls that lay x out themselves.
+constexpr int kLinearFew = 8;   // tokens up to which they do
+struct LinearLayout {
+  size_t xdown = 0, xh = 0, part = 0, total = 0;
+  LinearLayout(int T, int K, int num_sms) {
+    if (T <= kLinearFew) return;
+    const size_t width = (T + 15) / 16 * 16;
+    xdown = 1024;
+    xh = xdown + 256;   // 64 floats
+    part = xh + width * (align_up(K, 256) * 2);
+    total = part + (size_t)num_sms * 4 * width * 256 * 4;   // two blocks an SM, two pieces each
+  }
 };
 cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream);
 

@@ -9,9 +9,29 @@
 // f16 after a scaling per token by a power of two (exact but for elements under 2^-29 of the
 // largest), the sums are float32, and the matrix's scale multiplies them at the end.
 //
-// The block's warps are WM groups of 16 rows times 8 / WM slices of K; a cluster of S blocks splits
-// K further when there are fewer row groups than SMs or x does not fit. Partial sums are added in a
-// fixed order (warps in shared memory, blocks through the cluster's shared memory).
+// k_linear_few (up to 8 tokens): the block's eight warps each hold an eighth of K and go down the
+// block's row tiles, some pieces of 128 elements ahead in registers across tile ends, so the stream of
+// weights does not stop; x is laid out once per block. A cluster of S blocks splits K when there are
+// fewer row tiles than SMs or x does not fit one block. Partial sums are added in a fixed order (warps
+// in shared memory, blocks through the cluster's).
+//
+// k_linear_mid (9 to 32 tokens, few rows): the same in one launch with tiles of 128 rows and K over a
+// cluster, each of whose blocks lays its own slice of x out.
+//
+// k_linear_more (9 to 64 tokens, many rows): a launch of its own lays x out (k_linear_x). The work is
+// the list of (256-row tile, 256 elements of K); each block takes an equal run of it. Every warp has 32
+// rows of the tile, so that a piece of x read from shared memory meets 32 rows; the blocks' x comes by
+// bulk copies into a ring. A tile that two runs share leaves float32 sums for k_linear_join, which adds
+// them in order.
+//
+// What bounds it: a weight costs half a conversion, half a multiply and 1/256 of a product per eight
+// tokens on the warp schedulers. At 100003 x 4096 (34 us of memory time): 1 token 42 us, 81 % of the
+// measured copy rate; 5 tokens 44; 16 tokens 56; 32 and 64 tokens 92 and 144 us, where the m16n8k16 rate
+// (1024 products per clock and SM: 44 and 88 us) is the larger bound. The same tiles through tcgen05 with
+// the converted weights in tensor memory took 103 us at 16 tokens and 118 at 64: its rate per 128 x 16
+// block does not depend on the tokens, but the hand-over through tensor memory and barriers costs 1.2 us
+// per 128 x 256 weights. Small matrices are bound by latency: 1 x 4096 x 4096 takes 6.3 us for 1.4 us of
+// memory time, a chain of launch, load, conversion, sum and store.
 #include <cmath>
 #include <cuda_runtime.h>
 
@@ -24,8 +44,8 @@ namespace ftmoe {
 namespace {
 
 constexpr int kLinWarps = 8;
-constexpr int kLinAhead = 4;               // 128-element pieces whose loads are in flight per warp
-constexpr size_t kLinXMax = 96 * 1024;     // x of one block in shared memory
+constexpr int kLinUnit = 256;              // elements of K in a unit of work
+constexpr size_t kLinXMax = 200 * 1024;    // x of one block in shared memory
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -45,6 +65,15 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
                : "memory");
   return v;
 }
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t rank) {
+  float4 v;
+  asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+               "ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [a];\n\t}"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr), "r"(rank)
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ uint4 ld_once(const uint8_t* p) {   // weights: read once
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -53,216 +82,634 @@ __device__ __forceinline__ uint4 ld_once(const uint8_t* p) {   // weights: read 
   return v;
 }
 
-struct Piece {   // 128 elements of 16 rows: this lane's 32 of two rows
-  uint4 w0, w1;
-  uint32_t s0, s1;
+// 128 elements of 16 MT rows: this lane's 32 of rows l / 4, l / 4 + 8, ...
+template <int MT>
+struct Piece {
+  uint4 w[2 * MT];
+  uint32_t s[2 * MT];
 };
 
-template <int NT, int WM>
-__global__ void __launch_bounds__(kLinWarps * 32) k_linear(const LinearArgs a) {
-  constexpr int WK = kLinWarps / WM;   // slices of K in the block
-  constexpr int TOK = NT * 8;
-  extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float down[WK][TOK];
-  griddep_launch_dependents();
-  griddep_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int wm = warp / WK, wk = warp % WK;
-  const int q = lane & 3, r = lane >> 2;
-  const uint32_t rank = a.split > 1 ? cluster_rank() : 0;
-  const int t0 = blockIdx.y * TOK;
-  const int T = min(a.T - t0, TOK);
-  const int row0 = (blockIdx.x / a.split) * (16 * WM) + wm * 16;
-
-  // this warp's pieces of K: [p0, p1) of ceil(K / 128), the block's and the warp's share
-  const int pieces = (a.K + 127) >> 7;
-  const int bp = (pieces + a.split - 1) / a.split;
-  const int bp0 = min((int)rank * bp, pieces), bp1 = min(bp0 + bp, pieces);
-  const int wp = (bp + WK - 1) / WK;
-  const int p0 = min(bp0 + wk * wp, bp1), p1 = min(p0 + wp, bp1);
-
-  const int ra = min(row0 + r, a.N - 1), rb = min(row0 + r + 8, a.N - 1);
-  const uint8_t* wa = a.codes + (size_t)ra * (a.K >> 1);
-  const uint8_t* wb = a.codes + (size_t)rb * (a.K >> 1);
-  const uint8_t* sa = a.scales + (size_t)ra * (a.K >> 4);
-  const uint8_t* sb = a.scales + (size_t)rb * (a.K >> 4);
-  auto load = [&](int p, Piece& w) {
-    const int k = p * 128 + q * 32;
-    if (p < p1 && k < a.K) {
-      w.w0 = ld_once(wa + (k >> 1));
-      w.w1 = ld_once(wb + (k >> 1));
-      w.s0 = *reinterpret_cast<const uint16_t*>(sa + (k >> 4));
-      w.s1 = *reinterpret_cast<const uint16_t*>(sb + (k >> 4));
+// This lane's place in 16 MT rows of the matrix (rows past the last read the last one again).
+template <int MT>
+struct Rows {
+  const uint8_t *codes, *scales;    // row0 + l / 4, element k0
+  uint32_t to_row[2 * MT];          // from there to rows l / 4 + 8 i, in codes; an eighth in scales
+  __device__ __forceinline__ void set(const LinearArgs& a, int row0, int r, int k0) {
+    const int row = min(row0 + r, a.N - 1);
+    codes = a.codes + (size_t)row * (a.K >> 1) + (k0 >> 1);
+    scales = a.scales + (size_t)row * (a.K >> 4) + (k0 >> 4);
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i)
+      to_row[i] = (uint32_t)(min(row0 + r + 8 * i, a.N - 1) - row) * (uint32_t)(a.K >> 1);
+  }
+  // piece p's lines towards L2: no data is taken, so this may run ahead of the launches before
+  __device__ __forceinline__ void prefetch(int p) const {
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(codes + to_row[i] + p * 64));
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(scales + p * 8));
+  }
+  // piece p from k0 on; off: scales of zero, so that nothing counts
+  __device__ __forceinline__ void load(Piece<MT>& w, int p, bool on) const {
+    if (on) {
+#pragma unroll
+      for (int i = 0; i < 2 * MT; ++i) w.w[i] = ld_once(codes + to_row[i] + p * 64);
+#pragma unroll
+      for (int i = 0; i < 2 * MT; ++i)
+        w.s[i] = *reinterpret_cast<const uint16_t*>(scales + (to_row[i] >> 3) + p * 8);
     } else {
-      w.w0 = w.w1 = make_uint4(0, 0, 0, 0);
-      w.s0 = w.s1 = 0;
-    }
-  };
-  Piece buf[kLinAhead];
 #pragma unroll
-  for (int i = 0; i < kLinAhead; ++i) load(p0 + i, buf[i]);
+      for (int i = 0; i < 2 * MT; ++i) w.s[i] = 0;
+    }
+  }
+};
 
-  // x of the block's K to shared memory as f16, in the B operand's order: 16-byte unit
-  // ((piece * 4 + j) * TOK + token) * 4 + q = elements 32 q + 8 j .. + 7 of the piece
-  uint4* xs = reinterpret_cast<uint4*>(smem);
-  for (int job = warp; job < T * WK; job += kLinWarps) {   // (token, slice)
-    // with one row group a warp stages its own slice only
-    const int n = WM == 1 ? job / WK : job % T, s = WM == 1 ? warp : job / T;
-    const int c0 = min(bp0 + s * wp, bp1), c1 = min(c0 + wp, bp1);
-    const uint16_t* x = a.x + (size_t)(t0 + n) * a.x_stride;
-    float top = 0.f;
-    for (int k = c0 * 128 + lane * 8; k < c1 * 128; k += 256) {
-      if (k < a.K) {
-        const uint4 v = *reinterpret_cast<const uint4*>(x + k);
-        top = fmaxf(top, fmaxf(finite_top(v.x, v.y), finite_top(v.z, v.w)));
-      }
-    }
-    top = warp_max(top);
-    float up, dn;
-    f16_scale(top, up, dn);
-    if (lane == 0) down[s][n] = dn;
-    for (int k = c0 * 128 + lane * 8; k < c1 * 128; k += 256) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (k < a.K) v = *reinterpret_cast<const uint4*>(x + k);
-      const uint4 h = make_uint4(pack_f16(bf16_lo(v.x) * up, bf16_hi(v.x) * up),
-                                 pack_f16(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
-                                 pack_f16(bf16_lo(v.z) * up, bf16_hi(v.z) * up),
-                                 pack_f16(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
-      const int k8 = (k >> 3) & 15;
-      xs[(((k >> 7) - bp0) * 4 + (k8 & 3)) * (TOK * 4) + n * 4 + (k8 >> 2)] = h;
-    }
-  }
-  if constexpr (WM == 1) __syncwarp();
-  else __syncthreads();
+// Eight codes (a word) times a splat scale: four f16x2.
+__device__ __forceinline__ void dequant8(uint32_t w, uint32_t s, uint32_t (&h)[4]) {
+  e2m1x8_to_f16x2x4(w, h[0], h[1], h[2], h[3]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = hmul2(h[i], s);
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int j) {
+  return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
+}
 
-  float acc[NT][4];
+// acc += the piece's products with x, NT groups of eight tokens; xp: this lane's first unit of x, the
+// next eight elements' units xj further, the next eight tokens' 32
+template <int MT, int NT>
+__device__ __forceinline__ void products(float (&acc)[MT][NT][4], const Piece<MT>& w, const uint4* xp,
+                                         int xj) {
+  uint32_t lo[2 * MT], hi[2 * MT];   // scales of elements 0-15 and 16-31, splat
 #pragma unroll
-  for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-  for (int p = p0; p < p1; p += kLinAhead) {
-#pragma unroll
-    for (int i = 0; i < kLinAhead; ++i) {
-      if (p + i >= p1) break;   // uniform over the warp
-      const Piece w = buf[i];
-      load(p + i + kLinAhead, buf[i]);
-      uint32_t ca[16], cb[16];
-      dequant32(w.w0, w.s0, ca);
-      dequant32(w.w1, w.s1, cb);
-      const uint4* xp = xs + (size_t)(p + i - bp0) * (TOK * 16);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          uint4 b = make_uint4(0, 0, 0, 0);
-          if (n * 8 + r < T) b = xp[j * (TOK * 4) + n * 32 + lane];
-          mma_f16(acc[n], ca[4 * j], cb[4 * j], ca[4 * j + 1], cb[4 * j + 1], b.x, b.y);
-          mma_f16(acc[n], ca[4 * j + 2], cb[4 * j + 2], ca[4 * j + 3], cb[4 * j + 3], b.z, b.w);
-        }
-    }
+  for (int i = 0; i < 2 * MT; ++i) {
+    const uint32_t s = e4m3x2_to_f16x2(w.s[i]);
+    lo[i] = splat_lo(s);
+    hi[i] = splat_hi(s);
   }
-  // lane: rows r, r + 8, tokens 8 n + 2 q, + 1
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const float d0 = n * 8 + 2 * q < T ? down[wk][n * 8 + 2 * q] : 0.f;
-    const float d1 = n * 8 + 2 * q + 1 < T ? down[wk][n * 8 + 2 * q + 1] : 0.f;
-    acc[n][0] *= d0; acc[n][1] *= d1;
-    acc[n][2] *= d0; acc[n][3] *= d1;
-  }
-
-  // add the slices: sums [slice][token][row] over x's memory
-  constexpr int ROWS = 16 * WM;
-  __syncthreads();
-  float* sums = reinterpret_cast<float*>(smem);
+  for (int j = 0; j < 4; ++j) {
+    uint32_t h[2 * MT][4];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int t = n * 8 + 2 * q, row = wm * 16 + r;
-    float* at = sums + (size_t)(wk * TOK + t) * ROWS + row;
-    at[0] = acc[n][0];
-    at[ROWS] = acc[n][1];
-    at[8] = acc[n][2];
-    at[ROWS + 8] = acc[n][3];
-  }
-  __syncthreads();
-  const float g = *a.gscale;
-  if (a.split > 1) {
-    // the block's own sum over its slices, then the cluster's, each block an equal part
-    for (int x = threadIdx.x; x < T * ROWS; x += kLinWarps * 32) {
-      float v = sums[x];
+    for (int i = 0; i < 2 * MT; ++i) dequant8(word(w.w[i], j), j < 2 ? lo[i] : hi[i], h[i]);
 #pragma unroll
-      for (int s = 1; s < WK; ++s) v += sums[s * TOK * ROWS + x];
-      sums[x] = v;
-    }
-    cluster_sync();
-    const int share = (T * ROWS + a.split - 1) / a.split;
-    const int x0 = (int)rank * share, x1 = min(x0 + share, T * ROWS);
-    for (int x = x0 + threadIdx.x; x < x1; x += kLinWarps * 32) {
-      float v = 0.f;
-      for (int s = 0; s < a.split; ++s) v += ld_cluster(smem_addr(sums + x), s);
-      const int t = x / ROWS, row = (blockIdx.x / a.split) * ROWS + x % ROWS;
-      if (row < a.N) {
-        const size_t at = (size_t)(t0 + t) * a.N + row;
-        if (a.out_f32) static_cast<float*>(a.out)[at] = v * g;
-        else static_cast<uint16_t*>(a.out)[at] = (uint16_t)(pack_bf16(v * g, 0.f) & 0xFFFFu);
-      }
-    }
-    cluster_sync();   // no block leaves while its sums are read
-  } else {
-    for (int x = threadIdx.x; x < T * ROWS; x += kLinWarps * 32) {
-      float v = sums[x];
+    for (int n = 0; n < NT; ++n) {
+      const uint4 b = xp[j * xj + n * 32];
 #pragma unroll
-      for (int s = 1; s < WK; ++s) v += sums[s * TOK * ROWS + x];
-      const int t = x / ROWS, row = blockIdx.x * ROWS + x % ROWS;
-      if (row < a.N) {
-        const size_t at = (size_t)(t0 + t) * a.N + row;
-        if (a.out_f32) static_cast<float*>(a.out)[at] = v * g;
-        else static_cast<uint16_t*>(a.out)[at] = (uint16_t)(pack_bf16(v * g, 0.f) & 0xFFFFu);
+      for (int m = 0; m < MT; ++m) {
+        mma_f16(acc[m][n], h[2 * m][0], h[2 * m + 1][0], h[2 * m][1], h[2 * m + 1][1], b.x, b.y);
+        mma_f16(acc[m][n], h[2 * m][2], h[2 * m + 1][2], h[2 * m][3], h[2 * m + 1][3], b.z, b.w);
       }
     }
   }
 }
 
-template <int NT, int WM>
-cudaError_t launch(LinearArgs a, int num_sms, cudaStream_t stream) {
-  constexpr int ROWS = 16 * WM, TOK = NT * 8, WK = kLinWarps / WM;
-  const int groups = (a.N + ROWS - 1) / ROWS, pieces = (a.K + 127) / 128;
-  auto x_bytes = [&](int split) { return (size_t)((pieces + split - 1) / split) * 128 * TOK * 2; };
-  // K is split over a cluster while x does not fit, or while there are fewer blocks than SMs and
-  // every warp keeps at least two pieces
-  int split = 1;
-  while (split < 8 && (x_bytes(split) > kLinXMax ||
-                       (groups * split < num_sms && pieces >= 2 * split * WK * 2)))
-    split *= 2;
-  a.split = split;
-  const size_t sums = (size_t)WK * TOK * ROWS * 4;
-  const size_t smem = x_bytes(split) > sums ? x_bytes(split) : sums;
+__device__ __forceinline__ uint4 to_f16(uint4 v, float up) {   // 8 bf16 times a power of two
+  return make_uint4(pack_f16(bf16_lo(v.x) * up, bf16_hi(v.x) * up),
+                    pack_f16(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
+                    pack_f16(bf16_lo(v.z) * up, bf16_hi(v.z) * up),
+                    pack_f16(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
+}
+
+// 16-byte unit of elements k .. k + 7 of token n in the B operand's order, `tok` tokens wide: unit
+// ((piece * 4 + j) * tok + n) * 4 + q holds elements 32 q + 8 j .. of the 128-element piece.
+__device__ __forceinline__ int x_unit(int k, int n, int tok) {
+  const int k8 = (k >> 3) & 15;
+  return (((k >> 7) * 4 + (k8 & 3)) * tok + n) * 4 + (k8 >> 2);
+}
+
+// x of tokens n0 .. n0 + 3 (of T), elements [ka, kb), to f16 at dst (units of the block's slice, which
+// begins at element k0), with a power of two per token in down[]. One warp; up to 512 elements stay in
+// registers between the search for the largest and the conversion, four tokens' loads at a time.
+__device__ __forceinline__ void stage_x(const LinearArgs& a, int t0, int n0, int T, int ka, int kb, int k0,
+                                        int tok, uint4* dst, float* down) {
+  const int lane = threadIdx.x & 31;
+  const uint16_t* x = a.x + (size_t)(t0 + n0) * a.x_stride;
+  const int cnt = min(T - n0, 4);
+  uint4 v[4][2];
+  float top[4] = {};
+  auto get = [&](int j, int k) {
+    return j < cnt && k < kb && k < a.K
+               ? *reinterpret_cast<const uint4*>(x + (size_t)j * a.x_stride + k)
+               : make_uint4(0, 0, 0, 0);
+  };
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j][i] = get(j, ka + lane * 8 + i * 256);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      top[j] = fmaxf(top[j], fmaxf(finite_top(v[j][i].x, v[j][i].y), finite_top(v[j][i].z, v[j][i].w)));
+  for (int k = ka + lane * 8 + 512; k < kb; k += 256)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint4 w = get(j, k);
+      top[j] = fmaxf(top[j], fmaxf(finite_top(w.x, w.y), finite_top(w.z, w.w)));
+    }
+  float up[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float dn;
+    f16_scale(warp_max(top[j]), up[j], dn);
+    if (lane == 0 && j < cnt) down[n0 + j] = dn;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = ka + lane * 8 + i * 256;
+      if (j < cnt && k < kb) dst[x_unit(k - k0, n0 + j, tok)] = to_f16(v[j][i], up[j]);
+    }
+  for (int k = ka + lane * 8 + 512; k < kb; k += 256)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < cnt) dst[x_unit(k - k0, n0 + j, tok)] = to_f16(get(j, k), up[j]);
+}
+
+__device__ __forceinline__ void store_out(const LinearArgs& a, int t, int row, float v) {
+  const size_t at = (size_t)t * a.N + row;
+  if (a.out_f32) static_cast<float*>(a.out)[at] = v;
+  else static_cast<uint16_t*>(a.out)[at] = (uint16_t)(pack_bf16(v, 0.f) & 0xFFFFu);
+}
+
+// Up to 8 tokens: tiles of 16 MT rows, AHEAD pieces in flight per warp.
+template <int MT, int AHEAD>
+__global__ void __launch_bounds__(kLinWarps * 32, 2) k_linear_few(const LinearArgs a) {
+  constexpr int W = kLinWarps, ROWS = 16 * MT;
+  extern __shared__ __align__(128) unsigned char few_smem[];   // x [piece][j][token][q]
+  __shared__ float down[W][8];
+  __shared__ float sums[2][W][8][ROWS + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q = lane & 3, r = lane >> 2;
+  const int rank = a.split > 1 ? (int)cluster_rank() : 0;
+  const int T = a.T;
+  const int tiles = (a.N + ROWS - 1) / ROWS, step = gridDim.x / a.split;
+  const int tile0 = blockIdx.x / a.split;
+  // pieces of K: the block's [b0, b1), this warp's [p0, p0 + np), those past p1 are zeros
+  const int pieces = (a.K + 127) >> 7;
+  const int bp = (pieces + a.split - 1) / a.split;
+  const int b0 = min(rank * bp, pieces), b1 = min(b0 + bp, pieces);
+  const int np = (bp + W - 1) / W;
+  const int p0 = min(b0 + warp * np, b1), p1 = min(p0 + np, b1);
+  const int k0 = p0 * 128 + q * 32;
+  const int mine = min(p1 - p0, (a.K - k0 + 127) >> 7);   // pieces in which this lane has elements
+  griddep_launch_dependents();
+
+  // the cursor of the loads, AHEAD pieces before that of the products
+  Piece<MT> buf[AHEAD];
+  Rows<MT> rows;
+  int lt = tile0, lp = 0, limit = mine;
+  rows.set(a, lt * ROWS, r, k0);
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i)
+    if (i < mine && i < np) rows.prefetch(i);
+  griddep_wait();
+  const float g = *a.gscale;
+  auto advance = [&](Piece<MT>& w) {
+    rows.load(w, lp, lp < limit);
+    if (++lp == np) {
+      lp = 0;
+      lt += step;
+      if (lt < tiles) rows.set(a, lt * ROWS, r, k0);
+      else limit = 0;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) advance(buf[i]);
+
+  // this warp's slice of x
+  uint4* xs = reinterpret_cast<uint4*>(few_smem);
+  for (int n = 0; n < T; n += 4)
+    stage_x(a, 0, n, T, p0 * 128, p1 * 128, b0 * 128, T, xs, down[warp]);
+  __syncwarp();
+  const float d0 = 2 * q < T ? down[warp][2 * q] : 0.f;
+  const float d1 = 2 * q + 1 < T ? down[warp][2 * q + 1] : 0.f;
+  // columns past T repeat the last token's (nobody reads them)
+  const uint4* const xw = xs + (size_t)(p0 - b0) * (T * 16) + min(r, T - 1) * 4 + q;
+
+  float acc[MT][1][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) acc[m][0][0] = acc[m][0][1] = acc[m][0][2] = acc[m][0][3] = 0.f;
+  int p = 0, flip = 0;
+  for (int tile = tile0; tile < tiles;) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (tile >= tiles) break;   // uniform over the block
+      if (p0 + p < p1) products<MT, 1>(acc, buf[i], xw + p * (T * 16), T * 4);
+      advance(buf[i]);
+      if (++p < np) continue;
+      // the tile's end: lane has rows r + 8 i of tokens 2 q, 2 q + 1
+      float (*part)[8][ROWS + 1] = sums[flip];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        part[warp][2 * q][16 * m + r] = acc[m][0][0] * d0;
+        part[warp][2 * q + 1][16 * m + r] = acc[m][0][1] * d1;
+        part[warp][2 * q][16 * m + r + 8] = acc[m][0][2] * d0;
+        part[warp][2 * q + 1][16 * m + r + 8] = acc[m][0][3] * d1;
+        acc[m][0][0] = acc[m][0][1] = acc[m][0][2] = acc[m][0][3] = 0.f;
+      }
+      p = 0;
+      __syncthreads();   // one per tile: the other copy of sums is free again after the next one
+      const int x = threadIdx.x, t = x / ROWS, row = tile * ROWS + x % ROWS;
+      float v = 0.f;
+      if (t < T) {
+#pragma unroll
+        for (int s = 0; s < W; ++s) v += part[s][t][x % ROWS];
+      }
+      if (a.split > 1) {
+        __syncthreads();
+        if (t < T) part[0][t][x % ROWS] = v;
+        cluster_sync();
+        // the tile's outputs go round the cluster's blocks
+        if (t < T && x % a.split == rank) {
+          v = 0.f;
+          for (int s = 0; s < a.split; ++s) v += ld_cluster(smem_addr(&part[0][t][x % ROWS]), s);
+          if (row < a.N) store_out(a, t, row, v * g);
+        }
+        cluster_sync();   // no block goes on (or leaves) while its sums are read
+      } else if (t < T && row < a.N) {
+        store_out(a, t, row, v * g);
+      }
+      flip ^= 1;
+      tile += step;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- 9 to 64 tokens, few rows
+// One launch: tiles of 128 rows (four groups of 32 rows x two slices of K in a block), K over a cluster
+// of S blocks, each of which lays its own slice of x out. Up to 8 NT tokens per grid row.
+constexpr int kMidRows = 128;
+template <int NT>
+__global__ void __launch_bounds__(kLinWarps * 32, NT <= 4 ? 2 : 1) k_linear_mid(const LinearArgs a) {
+  constexpr int WK = 2, TOK = NT * 8, ROWS = kMidRows, AHEAD = 2;
+  extern __shared__ __align__(128) unsigned char mid_smem[];   // x, then sums [token][row]
+  __shared__ float down[WK][TOK];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wm = warp >> 1, wk = warp & 1;
+  const int q = lane & 3, r = lane >> 2;
+  const int rank = a.split > 1 ? (int)cluster_rank() : 0;
+  const int t0 = blockIdx.y * TOK, T = min(a.T - t0, TOK);
+  const int tile = blockIdx.x / a.split;
+  const int pieces = (a.K + 127) >> 7;
+  const int bp = (pieces + a.split - 1) / a.split;
+  const int b0 = min(rank * bp, pieces), b1 = min(b0 + bp, pieces);
+  const int np = (bp + WK - 1) / WK;
+  const int p0 = min(b0 + wk * np, b1), p1 = min(p0 + np, b1);
+  const int k0 = p0 * 128 + q * 32;
+  const int mine = min(p1 - p0, (a.K - k0 + 127) >> 7);
+  griddep_launch_dependents();
+  Rows<2> rows;
+  rows.set(a, tile * ROWS + wm * 32, r, k0);
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i)
+    if (i < mine) rows.prefetch(i);
+  griddep_wait();
+  Piece<2> buf[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) rows.load(buf[i], i, i < mine);
+  const float g = *a.gscale;
+  uint4* xs = reinterpret_cast<uint4*>(mid_smem);
+  // (four tokens, slice) pairs go round the warps
+  for (int job = warp; job < (T + 3) / 4 * WK; job += kLinWarps) {
+    const int s = job & 1, n = (job >> 1) * 4;
+    const int c0 = min(b0 + s * np, b1), c1 = min(c0 + np, b1);
+    stage_x(a, t0, n, T, c0 * 128, c1 * 128, b0 * 128, TOK, xs, down[s]);
+  }
+  __syncthreads();
+  float acc[2][NT][4];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
+  const uint4* xw = xs + (size_t)(p0 - b0) * (TOK * 16) + lane;
+  for (int p = 0; p < p1 - p0; p += AHEAD) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (p + i >= p1 - p0) break;   // uniform over the warp
+      products<2, NT>(acc, buf[i], xw + (p + i) * (TOK * 16), TOK * 4);
+      rows.load(buf[i], p + i + AHEAD, p + i + AHEAD < mine);
+    }
+  }
+  // the block's sums [token][row]: the second slice adds to the first
+  constexpr int LD = ROWS + 4;
+  float* sums = reinterpret_cast<float*>(mid_smem);
+  __syncthreads();
+#pragma unroll
+  for (int s = 0; s < WK; ++s) {
+    if (wk == s) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int t = n * 8 + 2 * q + e;
+          const float d = t < T ? down[wk][t] : 0.f;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            float* at = sums + t * LD + wm * 32 + 8 * x + r;
+            const float v = acc[x >> 1][n][(x & 1) * 2 + e] * d;
+            *at = s == 0 ? v : *at + v;
+          }
+        }
+    }
+    __syncthreads();
+  }
+  // the cluster's sums, four rows at a time: the tokens' rows go round the blocks
+  if (a.split > 1) cluster_sync();
+  const int items = T * (ROWS / 4);
+  for (int x = rank * kLinWarps * 32 + threadIdx.x; x < items; x += a.split * kLinWarps * 32) {
+    const int t = x / (ROWS / 4), in = x % (ROWS / 4) * 4, row = tile * ROWS + in;
+    const uint32_t at = smem_addr(sums + t * LD + in);
+    float4 v[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s)   // all in flight, added in order
+      v[s] = s < a.split ? ld_cluster4(at, s) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      y[0] += v[s].x; y[1] += v[s].y; y[2] += v[s].z; y[3] += v[s].w;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (row + j < a.N) store_out(a, t0 + t, row + j, y[j] * g);
+  }
+  if (a.split > 1) cluster_sync();   // no block leaves while its sums are read
+}
+
+// ---------------------------------------------------------------- 9 to 64 tokens, many rows
+constexpr int kMoreRows = 32 * kLinWarps;   // rows of a tile
+constexpr int kMoreStages = 4;              // units of x in shared memory
+
+// x in f16 with a power of two per token, in the B operand's order (x_unit) `width` tokens wide. A
+// block per token; the tokens past T stay unwritten (they only reach sums that nobody reads), elements
+// past K are zeros.
+constexpr int kPrepThreads = 256;
+constexpr int kPrepKeep = 4;   // 8-element pieces a thread keeps between the two passes
+__global__ void __launch_bounds__(kPrepThreads) k_linear_x(const LinearArgs a, int width) {
+  __shared__ float red[kPrepThreads / 32];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int t = blockIdx.x, lane = threadIdx.x & 31;
+  const uint16_t* x = a.x + (size_t)t * a.x_stride;
+  const int Kp = (a.K + kLinUnit - 1) / kLinUnit * kLinUnit;
+  auto get = [&](int k) {
+    return k < a.K ? *reinterpret_cast<const uint4*>(x + k) : make_uint4(0, 0, 0, 0);
+  };
+  uint4 v[kPrepKeep];
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPrepKeep; ++i) v[i] = get((i * kPrepThreads + (int)threadIdx.x) * 8);
+#pragma unroll
+  for (int i = 0; i < kPrepKeep; ++i)
+    top = fmaxf(top, fmaxf(finite_top(v[i].x, v[i].y), finite_top(v[i].z, v[i].w)));
+  for (int k = (kPrepKeep * kPrepThreads + (int)threadIdx.x) * 8; k < a.K; k += kPrepThreads * 8) {
+    const uint4 w = get(k);
+    top = fmaxf(top, fmaxf(finite_top(w.x, w.y), finite_top(w.z, w.w)));
+  }
+  top = warp_max(top);
+  if (lane == 0) red[threadIdx.x >> 5] = top;
+  __syncthreads();
+  top = warp_max(lane < kPrepThreads / 32 ? red[lane] : 0.f);
+  float up, down;
+  f16_scale(top, up, down);
+  if (threadIdx.x == 0) a.xdown[t] = down;
+  uint4* xh = reinterpret_cast<uint4*>(a.xh);
+#pragma unroll
+  for (int i = 0; i < kPrepKeep; ++i) {
+    const int k = (i * kPrepThreads + (int)threadIdx.x) * 8;
+    if (k < Kp) xh[x_unit(k, t, width)] = to_f16(v[i], up);
+  }
+  for (int k = (kPrepKeep * kPrepThreads + (int)threadIdx.x) * 8; k < Kp; k += kPrepThreads * 8)
+    xh[x_unit(k, t, width)] = to_f16(get(k), up);
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kLinWarps * 32, NT <= 4 ? 2 : 1)
+    k_linear_more(const LinearArgs a, int uk, int quota) {
+  constexpr int TOK = NT * 8, ST = kMoreStages, AHEAD = 2, PU = kLinUnit / 128;
+  constexpr uint32_t kX = TOK * kLinUnit * 2;   // bytes of a unit of x
+  extern __shared__ __align__(128) unsigned char more_smem[];   // x [stage][unit]
+  __shared__ __align__(8) uint64_t full[ST], empty[ST];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q = lane & 3, r = lane >> 2;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kLinWarps);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  griddep_launch_dependents();
+  griddep_wait();
+  const int total = ((a.N + kMoreRows - 1) / kMoreRows) * uk;
+  const int u0 = min((int)blockIdx.x * quota, total), u1 = min(u0 + quota, total);
+  const float g = *a.gscale;
+
+  auto send = [&](int i) {   // x of unit u0 + i (one thread)
+    const int st = i % ST;
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::
+                     "r"(smem_addr(&full[st])), "r"(kX) : "memory");
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
+                 "[%0], [%1], %2, [%3];" ::"r"(smem_addr(more_smem) + st * kX),
+                 "l"(reinterpret_cast<const char*>(a.xh) + (size_t)((u0 + i) % uk) * kX), "r"(kX),
+                 "r"(smem_addr(&full[st])) : "memory");
+  };
+  if (threadIdx.x == 0)
+    for (int i = 0; i < ST && u0 + i < u1; ++i) send(i);
+
+  // the cursor of the loads: units from u0 on, PU pieces each
+  Piece<2> buf[AHEAD];
+  Rows<2> rows;
+  int lu = u0, lp = 0, limit = 0;
+  auto enter = [&]() {   // the rows and this lane's pieces of unit lu
+    limit = 0;
+    if (lu < u1) {
+      const int tile = lu / uk, k0 = (lu - tile * uk) * kLinUnit + q * 32;
+      rows.set(a, tile * kMoreRows + warp * 32, r, k0);
+      limit = min(PU, (a.K - k0 + 127) >> 7);
+    }
+  };
+  auto advance = [&](Piece<2>& w) {
+    rows.load(w, lp, lp < limit);
+    if (++lp == PU) {
+      lp = 0;
+      ++lu;
+      enter();
+    }
+  };
+  enter();
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) advance(buf[i]);
+
+  float acc[2][NT][4];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
+  for (int u = u0; u < u1; ++u) {
+    const int i = u - u0, st = i % ST;
+    if (!mbar_wait(&full[st], (uint32_t)(i / ST) & 1u, a.err, kErrTimeout)) break;
+    __syncwarp();
+    const uint4* xu = reinterpret_cast<const uint4*>(more_smem + st * kX) + lane;
+#pragma unroll
+    for (int p = 0; p < PU; ++p) {
+      products<2, NT>(acc, buf[p % AHEAD], xu + p * (TOK * 16), TOK * 4);
+      advance(buf[p % AHEAD]);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[st]);
+    // the stage before this one again, once every warp has read it
+    if (threadIdx.x == 0 && i > 0 && u - 1 + ST < u1 &&
+        mbar_wait(&empty[(i - 1) % ST], (uint32_t)((i - 1) / ST) & 1u, a.err, kErrTimeout))
+      send(i - 1 + ST);
+    const int tile = u / uk;
+    if (u + 1 < u1 && (u + 1) % uk != 0) continue;
+    // the end of the tile or of the run: lane has rows r + 8 i of tokens 8 n + 2 q, + 1
+    const bool whole = (u + 1) % uk == 0 && u - uk + 1 >= u0;
+    float* part = a.part + (size_t)(2 * blockIdx.x + (tile * uk <= u0 ? 0 : 1)) * TOK * kMoreRows;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int t = n * 8 + 2 * q + e;
+        if (t < a.T) {
+          const float d = whole ? a.xdown[t] * g : 1.f;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int in = warp * 32 + 8 * x + r, row = tile * kMoreRows + in;
+            const float v = acc[x >> 1][n][(x & 1) * 2 + e] * d;
+            if (!whole) part[(size_t)t * kMoreRows + in] = v;
+            else if (row < a.N) store_out(a, t, row, v);
+          }
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
+    }
+  }
+}
+
+// Tiles that several runs share: their sums in order, four rows of a token per thread. Grid (tile, 4
+// tokens).
+__global__ void __launch_bounds__(kMoreRows) k_linear_join(const LinearArgs a, int width, int uk,
+                                                           int quota) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int tile = blockIdx.x, t = blockIdx.y * 4 + (threadIdx.x >> 6), in = (threadIdx.x & 63) * 4;
+  const int s0 = tile * uk, s1 = s0 + uk;
+  const int first = s0 / quota, last = (s1 - 1) / quota;
+  const int row = tile * kMoreRows + in;
+  if (first == last || t >= a.T || row >= a.N) return;
+  const float d = a.xdown[t] * *a.gscale;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int b = first; b <= last; ++b) {
+    const float4 u = *reinterpret_cast<const float4*>(
+        a.part + ((size_t)(2 * b + (b * quota >= s0 ? 0 : 1)) * width + t) * kMoreRows + in);
+    v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+  }
+  const float y[4] = {v.x * d, v.y * d, v.z * d, v.w * d};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (row + j < a.N) store_out(a, t, row + j, y[j]);
+}
+
+template <typename K, typename... Args>
+cudaError_t start(K kernel, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,
+                  Args... args) {
   cudaError_t e;
-  if ((e = cudaFuncSetAttribute(k_linear<NT, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)smem)) != cudaSuccess)
+  if (smem > 32 * 1024 &&   // with the static part past 48 KB; per device and host-side only: set on every call that needs it
+      (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
+          cudaSuccess)
     return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(groups * split), (unsigned)((a.T + TOK - 1) / TOK));
-  cfg.blockDim = dim3(kLinWarps * 32);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = (unsigned)split;
+  at[1].val.clusterDim.x = (unsigned)cluster;
   at[1].val.clusterDim.y = 1;
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_linear<NT, WM>, a);
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int MT, int AHEAD>
+cudaError_t launch_few(LinearArgs a, int num_sms, cudaStream_t stream) {
+  const int tiles = (a.N + 16 * MT - 1) / (16 * MT), pieces = (a.K + 127) / 128;
+  auto x_bytes = [&](int split) { return (size_t)((pieces + split - 1) / split) * 256 * a.T; };
+  // K is split over a cluster while x does not fit, or while there are fewer blocks than SMs and
+  // every warp keeps a piece
+  int split = 1;
+  while (split < 8 && (x_bytes(split) > kLinXMax ||
+                       (tiles * split < num_sms && pieces >= 2 * split * kLinWarps)))
+    split *= 2;
+  a.split = split;
+  // resident blocks: two an SM, one when x takes more than half of the shared memory
+  const int most = (x_bytes(split) > kLinXMax / 2 ? 1 : 2) * num_sms / split;
+  const int blocks = tiles < most ? tiles : most;
+  return start(k_linear_few<MT, AHEAD>, dim3((unsigned)(blocks * split)), kLinWarps * 32, x_bytes(split),
+               split, stream, a);
+}
+
+template <int NT>
+cudaError_t launch_mid(LinearArgs a, int num_sms, cudaStream_t stream) {
+  constexpr int TOK = NT * 8;
+  const int tiles = (a.N + kMidRows - 1) / kMidRows, pieces = (a.K + 127) / 128;
+  auto x_bytes = [&](int split) { return (size_t)((pieces + split - 1) / split) * 256 * TOK; };
+  // K over a cluster while there are fewer than two blocks an SM and every warp keeps two pieces, and
+  // while x does not fit
+  int split = 1;
+  while (split < 8 && (x_bytes(split) > kLinXMax / 2 ||
+                       (tiles * split < 2 * num_sms && pieces >= 8 * split)))
+    split *= 2;
+  a.split = split;
+  const size_t sums = (size_t)TOK * (kMidRows + 4) * 4;
+  const size_t smem = x_bytes(split) > sums ? x_bytes(split) : sums;
+  return start(k_linear_mid<NT>, dim3((unsigned)(tiles * split), (unsigned)((a.T + TOK - 1) / TOK)),
+               kLinWarps * 32, smem, split, stream, a);
+}
+
+template <int NT>
+cudaError_t launch_more(const LinearArgs& a, int num_sms, cudaStream_t stream) {
+  constexpr int TOK = NT * 8;
+  const int uk = (a.K + kLinUnit - 1) / kLinUnit;
+  const int tiles = (a.N + kMoreRows - 1) / kMoreRows, total = tiles * uk;
+  const int most = (NT <= 4 ? 2 : 1) * num_sms;   // resident blocks
+  const int quota = (total + most - 1) / most;
+  const int blocks = (total + quota - 1) / quota;
+  cudaError_t e = start(k_linear_x, dim3((unsigned)a.T), kPrepThreads, 0, 1, stream, a, TOK);
+  if (e != cudaSuccess) return e;
+  e = start(k_linear_more<NT>, dim3((unsigned)blocks), kLinWarps * 32,
+            (size_t)kMoreStages * TOK * kLinUnit * 2, 1, stream, a, uk, quota);
+  if (e != cudaSuccess || quota % uk == 0) return e;   // every run ends with a tile
+  return start(k_linear_join, dim3((unsigned)tiles, (unsigned)((a.T + 3) / 4)), kMoreRows, 0, 1, stream,
+               a, TOK, uk, quota);
 }
 
 }  // namespace
 
 cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream) {
-  // K <= 32768 in eight blocks: 4096 elements of x for each of 8, 16 or (K <= 16384) 32 tokens is
-  // at most 128 KB; more tokens than that are a second dimension of the grid
-  if (a.T <= 8) return launch<1, 1>(a, num_sms, stream);
-  if (a.T <= 16 || a.K > 16384) return launch<2, 4>(a, num_sms, stream);
-  return launch<4, 4>(a, num_sms, stream);
+  // From 64 rows per SM on the wider forms win (us, K = 4096): one token, 16- or 32-row tiles: 6.3 or
+  // 6.8 at 4096 rows, 48 or 42 at 100003; 32 tokens, one launch or three: 12.3 or 14.5 at 4096 rows, 37
+  // or 29 at 20000. Past 32 tokens one launch would read the matrix twice: 23 or 16 us at 64 tokens.
+  const bool wide = a.N >= 64 * num_sms;
+  if (a.T <= kLinearFew)
+    return wide ? launch_few<2, 2>(a, num_sms, stream) : launch_few<1, 4>(a, num_sms, stream);
+  const int nt = (a.T + 7) / 8;
+  if (!wide && nt <= 4)
+    return nt <= 2 || a.K > 16384 ? launch_mid<2>(a, num_sms, stream) : launch_mid<4>(a, num_sms, stream);
+  if (nt <= 2) return launch_more<2>(a, num_sms, stream);
+  if (nt <= 4) return launch_more<4>(a, num_sms, stream);
+  if (nt <= 6) return launch_more<6>(a, num_sms, stream);
+  return launch_more<8>(a, num_sms, stream);
 }
 
 }  // namespace ftmoe

@@ -30,7 +30,7 @@ EXPORTED = ["ft_moe_abi_version", "ft_status_string", "ft_moe_route", "ft_moe_wo
             "ft_moe_debug_set_wait_limit", "ft_moe_layer_from_host",
             "ft_moe_fp8block_workspace_bytes", "ft_moe_fp8block_decode",
             "ft_moe_router_logits", "ft_moe_router_route",
-            "ft_nvfp4_linear", "ft_kv_append", "ft_paged_attention_workspace_bytes",
+            "ft_nvfp4_linear_workspace_bytes", "ft_nvfp4_linear", "ft_kv_append", "ft_paged_attention_workspace_bytes",
             "ft_paged_decode_attention", "ft_residual_norm",
             "ft_residual_norm_backward_workspace_bytes", "ft_residual_norm_backward"]
 
@@ -132,8 +132,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ft_moe_fp8block_decode.argtypes = [vp, i32, vp, vp, i32, ctypes.POINTER(_F8Experts),
                                            ctypes.POINTER(_F8Shared), f32, vp, vp, sz, vp]
     i64 = ctypes.c_int64
+    lib.ft_nvfp4_linear_workspace_bytes.restype = sz
+    lib.ft_nvfp4_linear_workspace_bytes.argtypes = [i32, i32]
     lib.ft_nvfp4_linear.restype = ctypes.c_int
-    lib.ft_nvfp4_linear.argtypes = [vp, i32, i64, ctypes.POINTER(_Matrix), vp, i32, vp]
+    lib.ft_nvfp4_linear.argtypes = [vp, i32, i64, ctypes.POINTER(_Matrix), vp, i32, vp, sz, vp]
     lib.ft_kv_append.restype = ctypes.c_int
     lib.ft_kv_append.argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, i32, ctypes.POINTER(_PagedKV),
                                  vp, i32, i32, vp, vp, vp, i32, i32, vp, vp]
@@ -167,6 +169,8 @@ def _ptr(t) -> int:
 
 def _stream(stream, dev=None) -> int:
     if stream is None:
+        if dev is not None and torch._C._cuda_getDevice() == dev:
+            return torch._C._cuda_getCurrentRawStream(dev)
         stream = torch.cuda.current_stream()
     if dev is not None and stream.device_index != dev:
         raise ValueError(f"the tensors are on cuda:{dev}, the stream on cuda:{stream.device_index} "
@@ -700,9 +704,7 @@ def _need_rows(t, name, dev, inner):
 
 def _scratch(n, dev, stream):
     """n bytes of the workspace that calls without one share per (device, stream)."""
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    key = (dev, stream.cuda_stream)
+    key = (dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     ws = _DEFAULT_WS.get(key)
     if ws is None or ws.numel() < n:
         ws = _new_scratch(n, dev, stream)
@@ -744,7 +746,12 @@ class NvFP4Linear:
         object.__setattr__(self, "_ref", ctypes.byref(self._cs))
 
 
-def nvfp4_linear(x, weight: NvFP4Linear, out=None, out_dtype=torch.bfloat16, stream=None):
+def nvfp4_linear_workspace_bytes(T, K) -> int:
+    return _LIB.ft_nvfp4_linear_workspace_bytes(T, K)
+
+
+def nvfp4_linear(x, weight: NvFP4Linear, out=None, out_dtype=torch.bfloat16, workspace=None,
+                 stream=None):
     """ft_nvfp4_linear: x bf16 [T,K] (T <= 64; rows may be slices of a wider tensor) -> W x_t,
     [T,N] in bf16, or in float32 (out_dtype, or the type of `out`)."""
     dev = weight.device_index
@@ -758,8 +765,17 @@ def nvfp4_linear(x, weight: NvFP4Linear, out=None, out_dtype=torch.bfloat16, str
         out = torch.empty((T, weight.N), dtype=out_dtype, device=x.device)
     else:
         _need(out, "out", dev, _RES, (T, weight.N))
+    ws, ws_bytes = 0, 0
+    if workspace is not None:
+        _need(workspace, "workspace", dev, None, None)
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel()
+    elif T > 8:   # fewer tokens need none
+        n = _LIB.ft_nvfp4_linear_workspace_bytes(T, weight.K)
+        if n > 0:
+            workspace = _scratch(n, dev, stream)
+            ws, ws_bytes = workspace.data_ptr(), workspace.numel()
     st = _LIB.ft_nvfp4_linear(x.data_ptr(), T, stride, weight._ref, out.data_ptr(),
-                              out.dtype is torch.float32, _stream(stream, dev))
+                              out.dtype is torch.float32, ws, ws_bytes, _stream(stream, dev))
     _check(st, "ft_nvfp4_linear")
     return out
 

@@ -26,16 +26,17 @@ NAN, INF = float("nan"), float("inf")
 
 @pytest.mark.parametrize("over,expect", [
     (dict(T=-1), 1), (dict(T=65), 2), (dict(N=0), 1), (dict(K=0), 1), (dict(K=48), 2),
-    (dict(K=32800), 2), (dict(codes=0), 1), (dict(gscale=0), 1), (dict(codes=0x10008), 3),
+    (dict(K=32800), 2), (dict(N=(1 << 30) + 1), 2), (dict(codes=0), 1), (dict(gscale=0), 1), (dict(codes=0x10008), 3),
     (dict(scales=0x20001), 3), (dict(gscale=0x30002), 3), (dict(x=0), 1), (dict(out=0), 1),
     (dict(T=2, stride=56), 1), (dict(stride=68), 3), (dict(x=0x40008), 3), (dict(out=0x50001), 3),
-    (dict(out=0x50002, f32=1), 3), (dict(T=0, x=0, out=0), 0)])
+    (dict(out=0x50002, f32=1), 3), (dict(T=0, x=0, out=0), 0), (dict(T=9, ws=0), 1),
+    (dict(T=9, ws=0x60010), 3), (dict(T=9, bytes=4096), 4)])
 def test_linear(m, over, expect):
     a = dict(T=1, N=8, K=64, codes=0x10000, scales=0x20000, gscale=0x30000, x=0x40000, out=0x50000,
-             stride=64, f32=0) | over
+             stride=64, f32=0, ws=0x60000, bytes=1 << 30) | over
     w = m._Matrix(a["N"], a["K"], a["codes"], a["scales"], a["gscale"])
     assert m.lib().ft_nvfp4_linear(a["x"], a["T"], a["stride"], ctypes.byref(w), a["out"], a["f32"],
-                                   None) == expect
+                                   a["ws"], a["bytes"], None) == expect
 
 
 def _cache(m, over):
