@@ -42,6 +42,10 @@ ft_status check_cache(const ft_paged_kv* c) {
   return FT_OK;
 }
 
+size_t norm_bwd_workspace(int T, int H, int sms) {
+  return 1024 + align_up((size_t)norm_bwd_groups(T, H, sms) * 3 * H * sizeof(float), 256);
+}
+
 ft_status check_norm(const uint16_t* y, const void* residual, const uint16_t* w_post,
                      const uint16_t* w_pre, const uint16_t* gate, int32_t gate_kind, int32_t T,
                      int32_t H, float scale, float eps) {
@@ -195,7 +199,7 @@ size_t ft_residual_norm_backward_workspace_bytes(int32_t T, int32_t H) {
   if (T < 0 || H < 8 || H % 8 != 0 || H > kMaxNormH) return 0;
   const int sms = device_sms();
   if (sms <= 0) return 0;
-  return 1024 + align_up((size_t)norm_bwd_groups(T, H, sms) * 3 * H * sizeof(float), 256);
+  return norm_bwd_workspace(T, H, sms);
 }
 
 ft_status ft_residual_norm_backward(const uint16_t* y, const void* residual,
@@ -221,22 +225,19 @@ ft_status ft_residual_norm_backward(const uint16_t* y, const void* residual,
     if (gate_kind == FT_GATE_CHANNEL) return cuda_status(cudaMemsetAsync(dgate, 0, n, s));
     return FT_OK;
   }
-  if (!dy || !dresidual || (w_pre && !d_x) || (gate_kind != FT_GATE_NONE && !dgate))
+  if (!dy || !dresidual || (w_pre && !d_x) || (gate_kind != FT_GATE_NONE && !dgate) || !workspace)
     return FT_ERR_INVALID_ARG;
-  if (!aligned(dy, 16) || !aligned(dresidual, 16) || !aligned(d_r, 16) ||
+  if (!aligned(workspace, 256) || !aligned(dy, 16) || !aligned(dresidual, 16) || !aligned(d_r, 16) ||
       (w_pre && !aligned(d_x, 16)))
     return FT_ERR_MISALIGNED;
+  if (workspace_bytes < norm_bwd_workspace(T, H, 1)) return FT_ERR_WORKSPACE_TOO_SMALL;
   NormArgs a = {};
   a.nq = (w_post ? 1 : 0) + (w_pre ? 1 : 0) + (gate_kind == FT_GATE_CHANNEL ? 1 : 0);
   const int sms = device_sms();
   if (sms <= 0) return FT_ERR_CUDA;
-  if (a.nq > 0) {
-    if (!workspace) return FT_ERR_INVALID_ARG;
-    if (!aligned(workspace, 256)) return FT_ERR_MISALIGNED;
-    if (workspace_bytes < ft_residual_norm_backward_workspace_bytes(T, H))
-      return FT_ERR_WORKSPACE_TOO_SMALL;
-    a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + 1024);
-  }
+  if (workspace_bytes < norm_bwd_workspace(T, H, sms)) return FT_ERR_WORKSPACE_TOO_SMALL;
+  a.err = static_cast<int*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + 1024);
   a.y = y; a.r = residual; a.w_post = w_post; a.w_pre = w_pre; a.gate = gate;
   a.gate_kind = gate_kind; a.T = T; a.H = H; a.res_f32 = res_f32 ? 1 : 0;
   a.scale = scale; a.eps = eps; a.dr = d_r; a.dx = d_x; a.dy = dy; a.dres = dresidual;

@@ -187,10 +187,11 @@ struct NormArgs {
   void* dres;
   float *dw_post, *dw_pre;
   void* dgate;             // float [H] / [T], bf16 [T][H]
-  float* part;             // workspace: column sums [group][nq][H]
+  int* err;                // workspace: error word, column sums [block][nq][H]
+  float* part;
   int nq;
 };
-// Row groups (rows of the workspace's partial sums) of the backward pass.
+// Blocks (rows of the workspace's partial sums) of the backward pass.
 int norm_bwd_groups(int T, int H, int num_sms);
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream);
 cudaError_t launch_norm_bwd(const NormArgs& a, int num_sms, cudaStream_t stream);

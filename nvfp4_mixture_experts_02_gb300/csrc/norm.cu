@@ -17,6 +17,7 @@
 
 #include "ftmoe_internal.h"
 #include "ftmoe_mma.cuh"
+#include "ftmoe_tc.cuh"
 
 namespace ftmoe {
 
@@ -24,6 +25,30 @@ namespace {
 
 constexpr int kWarpRowMax = 512;    // elements of a row that one warp holds
 constexpr int kRowWarps = 8;        // rows (warps) per block in that form
+
+// 1 / sqrt(v) to within a unit in the last place: r' cancels where r and z are opposite, and keeps what
+// error its factors have.
+__device__ __forceinline__ float inv_root(float v) { return __frcp_rn(__fsqrt_rn(v)); }
+
+// scale * gate / sqrt(sum / n + eps) as a float and what it lacks: where r and the block's output nearly
+// cancel, r' keeps the error of this factor many times over.
+struct Factor {
+  float hi, lo;
+};
+__device__ __forceinline__ Factor row_factor(float sum, float n, float eps, float scale, float gate,
+                                             bool norm) {
+  const float tg = scale * gate, tg_lo = fmaf(scale, gate, -tg);
+  if (!norm) return {tg, tg_lo};
+  const float mean = __fdiv_rn(sum, n), mean_lo = fmaf(-mean, n, sum) / n;
+  const float v = mean + eps, from = v - mean;
+  const float v_lo = (mean - (v - from)) + (eps - from) + mean_lo;
+  const float s = inv_root(v), t = v * s;
+  float left = fmaf(-t, s, 1.f);   // 1 - (v + v_lo) s^2
+  left = fmaf(-fmaf(v, s, -t), s, left);
+  left = fmaf(-v_lo * s, s, left);
+  const float s_lo = 0.5f * s * left, hi = tg * s;
+  return {hi, fmaf(tg, s, -hi) + fmaf(tg, s_lo, tg_lo * s)};
+}
 
 // Sum over the row's threads: the warp, or the whole block through red[] (one array per call
 // site, so that one barrier per sum is enough).
@@ -85,18 +110,18 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 1024) k_norm(const Nor
     for (int j = 0; j < 8; ++j) ss = fmaf(y[i][j], y[i][j], ss);
   }
   float s1 = 1.f;
-  if (a.w_post) s1 = rsqrtf(row_sum<WARP>(ss, red[0]) * inv_h + a.eps);
-  const float tg = a.scale * (a.gate_kind == FT_GATE_TOKEN ? one_bf16(a.gate + t) : 1.f);
+  if (a.w_post) s1 = inv_root(row_sum<WARP>(ss, red[0]) * inv_h + a.eps);
+  const float ts = a.scale * (a.gate_kind == FT_GATE_TOKEN ? one_bf16(a.gate + t) : 1.f) * s1;
   ss = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = tid + i * nth;
     if (c >= chunks) continue;
     float w[8], g[8];
-    if (a.w_post) {
+    if (a.w_post) {   // y times the weight and the gate, all bf16, is exact in float32
       cached8(a.w_post + 8 * c, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[i][j] *= s1 * w[j];
+      for (int j = 0; j < 8; ++j) y[i][j] *= w[j];
     }
     if (a.gate_kind == FT_GATE_CHANNEL || a.gate_kind == FT_GATE_ELEMENT) {
       if (a.gate_kind == FT_GATE_CHANNEL) cached8(a.gate + 8 * c, g);
@@ -106,13 +131,13 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 1024) k_norm(const Nor
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      r[i][j] = fmaf(tg, y[i][j], r[i][j]);
+      r[i][j] = fmaf(ts, y[i][j], r[i][j]);
       ss = fmaf(r[i][j], r[i][j], ss);
     }
     if (a.r_out) store8(static_cast<RT*>(a.r_out) + row + 8 * c, r[i]);
   }
   if (!a.w_pre) return;
-  const float s2 = rsqrtf(row_sum<WARP>(ss, red[1]) * inv_h + a.eps);
+  const float s2 = inv_root(row_sum<WARP>(ss, red[1]) * inv_h + a.eps);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = tid + i * nth;
@@ -125,15 +150,17 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 1024) k_norm(const Nor
   }
 }
 
-template <int NV, typename RT, bool WARP>
-__global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 1024) k_norm_bwd(const NormArgs a) {
-  __shared__ float red[4][32];
+// Gradient for rows that one warp holds: eight rows at a time in a block, column sums in registers,
+// joined by the block at the end.
+template <typename RT>
+__global__ void __launch_bounds__(kRowWarps * 32) k_norm_bwd_warp(const NormArgs a) {
+  constexpr int NV = 2;
   griddep_launch_dependents();
   griddep_wait();
-  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const int nth = WARP ? 32 : blockDim.x;
-  const int group = WARP ? blockIdx.x * kRowWarps + (threadIdx.x >> 5) : blockIdx.x;
-  const int groups = WARP ? gridDim.x * kRowWarps : gridDim.x;
+  const int tid = threadIdx.x & 31;
+  const int nth = 32;
+  const int group = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  const int groups = gridDim.x * kRowWarps;
   const int chunks = a.H >> 3;
   const float inv_h = 1.0f / (float)a.H;
   const bool channel = a.gate_kind == FT_GATE_CHANNEL;
@@ -162,9 +189,13 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 1024) k_norm_bwd(const
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = fmaf(y[i][j], y[i][j], ss);
     }
+    ss = warp_sum(ss);
     float s1 = 1.f;
-    if (a.w_post) s1 = rsqrtf(row_sum<WARP>(ss, red[0]) * inv_h + a.eps);
+    if (a.w_post) s1 = inv_root(ss * inv_h + a.eps);
     const float tg = a.scale * (a.gate_kind == FT_GATE_TOKEN ? one_bf16(a.gate + t) : 1.f);
+    const Factor factor = row_factor(ss, (float)a.H, a.eps, a.scale,
+                                     a.gate_kind == FT_GATE_TOKEN ? one_bf16(a.gate + t) : 1.f,
+                                     a.w_post != nullptr);
     // r <- r'
     float rr = 0.f, dot = 0.f;
 #pragma unroll
@@ -178,7 +209,10 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 1024) k_norm_bwd(const
       if (channel) cached8(a.gate + 8 * c, g);
       else if (a.gate_kind == FT_GATE_ELEMENT) cached8(a.gate + row + 8 * c, g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) r[i][j] = fmaf(tg * g[j], y[i][j] * (s1 * w[j]), r[i][j]);
+      for (int j = 0; j < 8; ++j) {
+        const float yu = y[i][j] * w[j] * g[j];
+        r[i][j] = fmaf(yu, factor.lo, fmaf(yu, factor.hi, r[i][j]));
+      }
       if (a.w_pre) {
         cached8(a.w_pre + 8 * c, w);
 #pragma unroll
@@ -190,9 +224,9 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 1024) k_norm_bwd(const
     }
     float s2 = 0.f, cr = 0.f;
     if (a.w_pre) {
-      rr = row_sum<WARP>(rr, red[1]);
-      dot = row_sum<WARP>(dot, red[2]);
-      s2 = rsqrtf(rr * inv_h + a.eps);
+      rr = warp_sum(rr);
+      dot = warp_sum(dot);
+      s2 = inv_root(rr * inv_h + a.eps);
       cr = s2 * s2 * (dot * inv_h);
     }
     float hy = 0.f, dgt = 0.f;
@@ -232,11 +266,9 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 1024) k_norm_bwd(const
         store8(static_cast<uint16_t*>(a.dgate) + row + 8 * c, dg);
     }
     float cy = 0.f;
-    if (a.w_post) cy = s1 * s1 * (row_sum<WARP>(hy, red[3]) * inv_h);
+    if (a.w_post) cy = s1 * s1 * (warp_sum(hy) * inv_h);
     if (a.gate_kind == FT_GATE_TOKEN) {
-      __syncwarp();
-      if constexpr (!WARP) __syncthreads();   // red[0] is free: every thread has passed red[3]
-      dgt = row_sum<WARP>(dgt, red[0]);
+      dgt = warp_sum(dgt);
       if (tid == 0) static_cast<float*>(a.dgate)[t] = dgt;
     }
 #pragma unroll
@@ -249,26 +281,11 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 1024) k_norm_bwd(const
       }
       store8(a.dy + row + 8 * c, dx[i]);
     }
-    if constexpr (!WARP) __syncthreads();   // before the next row writes red[]
   }
 
   // the group's column sums: [block][quantity][H]
   float* part = a.part + (size_t)blockIdx.x * a.nq * a.H;
-  if constexpr (!WARP) {
-    int q = 0;
-#pragma unroll
-    for (int which = 0; which < 3; ++which) {
-      if (which == 0 ? !a.w_post : which == 1 ? !a.w_pre : !channel) continue;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = tid + i * nth;
-        if (c < chunks)
-          store8(part + (size_t)q * a.H + 8 * c,
-                 which == 0 ? acc_post[i] : which == 1 ? acc_pre[i] : acc_gate[i]);
-      }
-      ++q;
-    }
-  } else {
+  {
     __shared__ float cols[kRowWarps][kWarpRowMax];
     int q = 0;
 #pragma unroll
@@ -290,6 +307,357 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 1024) k_norm_bwd(const
       }
       ++q;
     }
+  }
+}
+
+
+// Gradient for longer rows. A block of 512 threads is RG row groups of GT threads, 8 NV columns per
+// thread; a group's rows come whole by bulk copies into its ring of stages, so that the next rows
+// travel while one is worked on. A row's values are read from shared memory where they are used; r', h
+// and the column sums stay in registers. Two barriers a row: the sum that y needs is taken for the next
+// row together with the last sums of this one.
+constexpr int kBwdThreads = 512;
+constexpr size_t kBwdRing = 224 * 1024;   // one stage of the widest rows: 16384, float32, every input
+
+struct BwdRing {   // a stage: y | r | dr | dx | gate rows
+  int stage = 0, off_r = 0, off_dr = 0, off_dx = 0, off_gate = 0, stages = 0;
+  BwdRing() = default;
+  BwdRing(const NormArgs& a, int groups) {
+    const int res = a.H * (a.res_f32 ? 4 : 2);
+    off_r = 2 * a.H;
+    off_dr = off_r + (a.r ? res : 0);
+    off_dx = off_dr + (a.dr ? res : 0);
+    off_gate = off_dx + (a.w_pre ? 2 * a.H : 0);
+    stage = off_gate + (a.gate_kind == FT_GATE_ELEMENT ? 2 * a.H : 0);
+    stages = (int)(kBwdRing / ((size_t)groups * stage));
+    if (stages > 8) stages = 8;
+  }
+};
+
+// Two float32 in one 64-bit register pair: half the arithmetic instructions (packed operations round
+// each half as the scalar ones do).
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 make2(float lo, float hi) {
+  f2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ f2 both(float v) { return make2(v, v); }
+__device__ __forceinline__ float2 split2(f2 v) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+  return d;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float sum_of(f2 v) {
+  const float2 x = split2(v);
+  return x.x + x.y;
+}
+__device__ __forceinline__ void open8(const uint4& v, f2 (&f)[4]) {
+  f[0] = make2(bf16_lo(v.x), bf16_hi(v.x));
+  f[1] = make2(bf16_lo(v.y), bf16_hi(v.y));
+  f[2] = make2(bf16_lo(v.z), bf16_hi(v.z));
+  f[3] = make2(bf16_lo(v.w), bf16_hi(v.w));
+}
+// Eight values of column piece c from a row in shared memory.
+__device__ __forceinline__ void get8(const unsigned char* row, int c, const uint16_t*, f2 (&f)[4]) {
+  open8(reinterpret_cast<const uint4*>(row)[c], f);
+}
+__device__ __forceinline__ void get8(const unsigned char* row, int c, const float*, f2 (&f)[4]) {
+  const ulonglong2* p = reinterpret_cast<const ulonglong2*>(row) + 2 * c;
+  const ulonglong2 u = p[0], v = p[1];
+  f[0] = u.x; f[1] = u.y; f[2] = v.x; f[3] = v.y;
+}
+__device__ __forceinline__ void put8(uint16_t* p, const f2 (&f)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 v = split2(f[j]);
+    w[j] = pack_bf16(v.x, v.y);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void put8(float* p, const f2 (&f)[4]) {
+  reinterpret_cast<ulonglong2*>(p)[0] = make_ulonglong2(f[0], f[1]);
+  reinterpret_cast<ulonglong2*>(p)[1] = make_ulonglong2(f[2], f[3]);
+}
+
+// With u = w_post * (channel gate), tg = scale * (token gate) and e the elementwise gate:
+//   r' = r + (tg s1) y u e     h = tg dr' u e     dy = s1 h - y s1^3 mean(h y)
+//   A = sum_t tg s1 y dr' e    dw_post = A * (channel gate), dgate = A * w_post (channel: tg = scale)
+//   dgate = scale s1 sum_h y u dr' (token),  scale s1 y u dr' (element)
+// so one column sum serves both the weight and the channel's gate.
+template <int GT, int NV, typename RT>
+__global__ void __launch_bounds__(kBwdThreads, 1) k_norm_bwd(const NormArgs a, const BwdRing ring) {
+  constexpr int RG = kBwdThreads / GT, W = GT / 32;
+  extern __shared__ __align__(128) unsigned char bwd_smem[];
+  __shared__ __align__(8) uint64_t full[RG][8];
+  __shared__ float4 red[RG][2][W];
+  const int g = threadIdx.x / GT, tid = threadIdx.x % GT, warp = tid >> 5, lane = tid & 31;
+  const int chunks = a.H >> 3, ST = ring.stages;
+  const bool ahead = ST >= 3;   // stages enough to look at the next row's y within this one
+  const float inv_h = 1.0f / (float)a.H;
+  const bool channel = a.gate_kind == FT_GATE_CHANNEL, element = a.gate_kind == FT_GATE_ELEMENT;
+  const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr;
+  const RT* const kind = nullptr;
+  if (tid < ST) mbar_init(&full[g][tid], 1);
+  if (tid == 0) asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  __syncthreads();
+  griddep_launch_dependents();
+  griddep_wait();
+  unsigned char* const mine = bwd_smem + (size_t)g * ST * ring.stage;
+  // rows of this group: t0, t0 + dt, ...
+  const int t0 = blockIdx.x + g * gridDim.x, dt = RG * gridDim.x;
+  const int n_rows = t0 < a.T ? (a.T - t0 + dt - 1) / dt : 0;
+  auto send = [&](int i) {   // one thread: the copies of row i into stage i % ST
+    uint64_t* bar = &full[g][i % ST];
+    unsigned char* st = mine + (size_t)(i % ST) * ring.stage;
+    const size_t row = (size_t)(t0 + i * dt) * a.H;
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::
+                     "r"(smem_addr(bar)), "r"(ring.stage) : "memory");
+    auto copy = [&](int off, const void* src, size_t bytes_per) {
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
+                   "[%0], [%1], %2, [%3];" ::"r"(smem_addr(st + off)),
+                   "l"(static_cast<const char*>(src) + row * bytes_per),
+                   "r"((uint32_t)(a.H * bytes_per)), "r"(smem_addr(bar)) : "memory");
+    };
+    copy(0, a.y, 2);
+    if (a.r) copy(ring.off_r, a.r, sizeof(RT));
+    if (a.dr) copy(ring.off_dr, a.dr, sizeof(RT));
+    if (pre) copy(ring.off_dx, a.dx, 2);
+    if (element) copy(ring.off_gate, a.gate, 2);
+  };
+  auto barrier = [&]() {
+    asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "n"(GT) : "memory");
+  };
+  // sums over the group's threads (two arrays in turn: one barrier each)
+  auto sum3 = [&](int which, float x, float y, float z) -> float4 {
+    x = warp_sum(x);
+    y = warp_sum(y);
+    z = warp_sum(z);
+    if (lane == 0) red[g][which][warp] = make_float4(x, y, z, 0.f);
+    barrier();
+    float4 v = red[g][which][lane % W];
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) {
+      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+      v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
+    }
+    return v;
+  };
+  // this thread's columns: u in float32, w_pre packed
+  f2 u[NV][4], acc_post[NV][4], acc_pre[NV][4];
+  uint4 wpre[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = tid + v * GT;
+    const uint4 one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+    f2 gt[4];
+    open8(post && c < chunks ? *reinterpret_cast<const uint4*>(a.w_post + 8 * c) : one, u[v]);
+    open8(channel && c < chunks ? *reinterpret_cast<const uint4*>(a.gate + 8 * c) : one, gt);
+    wpre[v] = pre && c < chunks ? *reinterpret_cast<const uint4*>(a.w_pre + 8 * c) : one;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      u[v][j] = mul2(u[v][j], gt[j]);
+      acc_post[v][j] = acc_pre[v][j] = 0ull;
+    }
+  }
+  auto square_sum = [&](const unsigned char* st) -> float {   // of this thread's part of y
+    f2 ss = 0ull;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = tid + v * GT;
+      if (c >= chunks) continue;
+      f2 y[4];
+      get8(st, c, a.y, y);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ss = fma2(y[j], y[j], ss);
+    }
+    return sum_of(ss);
+  };
+  auto arrived = [&](int i) {
+    mbar_wait(&full[g][i % ST], (uint32_t)(i / ST) & 1u, a.err, kErrTimeout);
+  };
+
+  if (tid == 0)
+    for (int i = 0; i < ST && i < n_rows; ++i) send(i);
+  float ss = 0.f;   // of the coming row's y, already summed
+  if (n_rows > 0 && ahead) {
+    arrived(0);
+    ss = sum3(0, square_sum(mine), 0.f, 0.f).x;
+    barrier();   // red[] is written again within the first row
+  }
+  for (int i = 0; i < n_rows; ++i) {
+    const int t = t0 + i * dt;
+    const size_t row = (size_t)t * a.H;
+    const unsigned char* st = mine + (size_t)(i % ST) * ring.stage;
+    // once every thread is past the row before this one its stage takes a new row
+    auto refill = [&]() {
+      if (ST > 1 && tid == 0 && i > 0 && i - 1 + ST < n_rows) send(i - 1 + ST);
+    };
+    if (!ahead) {
+      arrived(i);
+      ss = sum3(0, square_sum(st), 0.f, 0.f).x;
+      refill();
+      barrier();
+    }
+    const float s1 = post ? inv_root(ss * inv_h + a.eps) : 1.f;
+    const float tg = a.scale * (a.gate_kind == FT_GATE_TOKEN ? one_bf16(a.gate + t) : 1.f);
+    const Factor factor = row_factor(ss, (float)a.H, a.eps, a.scale,
+                                     a.gate_kind == FT_GATE_TOKEN ? one_bf16(a.gate + t) : 1.f, post);
+    const f2 ts = both(factor.hi), ts_lo = both(factor.lo);
+    // r' and the sums that x' needs
+    f2 r[NV][4], rr = 0ull, dot = 0ull;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = tid + v * GT;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r[v][j] = 0ull;
+      if (c >= chunks) continue;
+      f2 y[4], w[4], d[4];
+      get8(st, c, a.y, y);
+      if (a.r) get8(st + ring.off_r, c, kind, r[v]);
+      if (element) {
+        get8(st + ring.off_gate, c, a.gate, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = mul2(y[j], w[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {   // y u is exact
+        const f2 yu = mul2(y[j], u[v][j]);
+        r[v][j] = fma2(yu, ts_lo, fma2(yu, ts, r[v][j]));
+      }
+      if (pre) {
+        get8(st + ring.off_dx, c, a.dx, d);
+        open8(wpre[v], w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          rr = fma2(r[v][j], r[v][j], rr);
+          dot = fma2(mul2(d[j], w[j]), r[v][j], dot);
+        }
+      }
+    }
+    f2 s2 = 0ull, cr = 0ull;
+    if (pre) {
+      const float4 v = sum3(1, sum_of(rr), sum_of(dot), 0.f);
+      const float s = inv_root(v.x * inv_h + a.eps);
+      s2 = both(s);
+      cr = both(-(s * s * (v.y * inv_h)));
+      if (ahead) refill();
+    }
+    f2 h[NV][4], hy = 0ull;   // h without tg
+    const f2 gs = both(a.scale * s1);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = tid + v * GT;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[v][j] = 0ull;
+      if (c >= chunks) continue;
+      f2 dr[4] = {0ull, 0ull, 0ull, 0ull}, d[4], w[4], y[4];
+      if (a.dr) get8(st + ring.off_dr, c, kind, dr);
+      if (pre) {
+        get8(st + ring.off_dx, c, a.dx, d);
+        open8(wpre[v], w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc_pre[v][j] = fma2(mul2(d[j], r[v][j]), s2, acc_pre[v][j]);
+          dr[j] = fma2(s2, fma2(r[v][j], cr, mul2(d[j], w[j])), dr[j]);
+        }
+      }
+      put8(static_cast<RT*>(a.dres) + row + 8 * c, dr);
+      get8(st, c, a.y, y);
+      if (element) {
+        f2 dg[4];
+        get8(st + ring.off_gate, c, a.gate, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          dg[j] = mul2(mul2(mul2(y[j], dr[j]), u[v][j]), gs);
+          dr[j] = mul2(dr[j], w[j]);
+        }
+        put8(static_cast<uint16_t*>(a.dgate) + row + 8 * c, dg);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f2 yd = mul2(y[j], dr[j]);
+        acc_post[v][j] = fma2(yd, ts, acc_post[v][j]);
+        hy = fma2(yd, u[v][j], hy);
+        h[v][j] = mul2(dr[j], u[v][j]);
+      }
+    }
+    float next = 0.f;
+    if (ahead && i + 1 < n_rows) {
+      arrived(i + 1);
+      if (post) next = square_sum(mine + (size_t)((i + 1) % ST) * ring.stage);
+    }
+    const float4 sums = sum3(0, sum_of(hy), next, 0.f);
+    ss = sums.y;
+    if (ahead && !pre) refill();
+    if (a.gate_kind == FT_GATE_TOKEN && tid == 0)
+      static_cast<float*>(a.dgate)[t] = a.scale * s1 * sums.x;
+    const f2 k1 = both(post ? tg * s1 : tg), k2 = both(post ? -(tg * s1 * s1 * s1 * (sums.x * inv_h)) : 0.f);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = tid + v * GT;
+      if (c >= chunks) continue;
+      if (post) {
+        f2 y[4];
+        get8(st, c, a.y, y);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[v][j] = fma2(y[j], k2, mul2(h[v][j], k1));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[v][j] = mul2(h[v][j], k1);
+      }
+      put8(a.dy + row + 8 * c, h[v]);
+    }
+    if (ST == 1) {
+      barrier();
+      if (tid == 0 && i + 1 < n_rows) send(i + 1);
+    } else if (!pre || !ahead) {
+      barrier();   // red[0] is written again before another barrier of the next row
+    }
+  }
+
+  // the block's column sums, its groups added in order: [block][quantity][H]
+  float* part = a.part + (size_t)blockIdx.x * a.nq * a.H;
+  float* cols = reinterpret_cast<float*>(bwd_smem);   // [group][H], over the rings
+  int q = 0;
+#pragma unroll
+  for (int which = 0; which < 3; ++which) {
+    if (which == 0 ? !post : which == 1 ? !pre : !channel) continue;
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = tid + v * GT;
+      if (c >= chunks) continue;
+      f2 sum[4], w[4];
+      const uint4 one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+      open8(which == 0 ? (channel ? *reinterpret_cast<const uint4*>(a.gate + 8 * c) : one)
+            : which == 2 && post ? *reinterpret_cast<const uint4*>(a.w_post + 8 * c) : one, w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[j] = which == 1 ? acc_pre[v][j] : mul2(acc_post[v][j], w[j]);
+      put8((RG > 1 ? cols + (size_t)g * a.H : part + (size_t)q * a.H) + 8 * c, sum);
+    }
+    if constexpr (RG > 1) {
+      __syncthreads();
+      for (int x = threadIdx.x; x < a.H; x += kBwdThreads) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < RG; ++w) v += cols[(size_t)w * a.H + x];
+        part[(size_t)q * a.H + x] = v;
+      }
+    }
+    ++q;
   }
 }
 
@@ -346,11 +714,41 @@ cudaError_t launch(K kernel, int grid, int threads, cudaStream_t stream, const N
 // Threads of a block that holds rows of `chunks` 8-element pieces, nv per thread.
 int row_threads(int chunks, int nv) { return ((chunks + nv - 1) / nv + 31) / 32 * 32; }
 
+template <int GT, int NV, typename RT>
+cudaError_t launch_bwd_t(const NormArgs& a, int grid, cudaStream_t stream) {
+  const BwdRing ring(a, kBwdThreads / GT);
+  const size_t sums = (size_t)kBwdThreads / GT * a.H * 4;
+  size_t smem = (size_t)kBwdThreads / GT * ring.stages * ring.stage;
+  if (GT < kBwdThreads && smem < sums) smem = sums;
+  cudaError_t e;
+  // per device and host-side only: set on every call
+  if ((e = cudaFuncSetAttribute(k_norm_bwd<GT, NV, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)smem)) != cudaSuccess)
+    return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kBwdThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_norm_bwd<GT, NV, RT>, a, ring);
+}
+
+template <int GT, int NV>
+cudaError_t launch_bwd(const NormArgs& a, int grid, cudaStream_t stream) {
+  return a.res_f32 ? launch_bwd_t<GT, NV, float>(a, grid, stream)
+                   : launch_bwd_t<GT, NV, uint16_t>(a, grid, stream);
+}
+
 }  // namespace
 
 int norm_bwd_groups(int T, int H, int num_sms) {
   const int rows = H <= kWarpRowMax ? (T + kRowWarps - 1) / kRowWarps : T;
-  const int most = 2 * num_sms;
+  const int most = H <= kWarpRowMax ? 2 * num_sms : num_sms;
   return rows < most ? rows : most;
 }
 
@@ -371,12 +769,18 @@ cudaError_t launch_norm_bwd(const NormArgs& a, int num_sms, cudaStream_t stream)
   const int grid = norm_bwd_groups(a.T, a.H, num_sms);
   cudaError_t e;
   if (a.H <= kWarpRowMax) {
-    e = a.res_f32 ? launch(k_norm_bwd<2, float, true>, grid, kRowWarps * 32, stream, a)
-                  : launch(k_norm_bwd<2, uint16_t, true>, grid, kRowWarps * 32, stream, a);
+    e = a.res_f32 ? launch(k_norm_bwd_warp<float>, grid, kRowWarps * 32, stream, a)
+                  : launch(k_norm_bwd_warp<uint16_t>, grid, kRowWarps * 32, stream, a);
+  } else if (chunks <= 128) {
+    e = launch_bwd<64, 2>(a, grid, stream);
+  } else if (chunks <= 256) {
+    e = launch_bwd<128, 2>(a, grid, stream);
+  } else if (chunks <= 512) {
+    e = launch_bwd<256, 2>(a, grid, stream);
+  } else if (chunks <= 1024) {
+    e = launch_bwd<512, 2>(a, grid, stream);
   } else {
-    const int th = row_threads(chunks, 2);
-    e = a.res_f32 ? launch(k_norm_bwd<2, float, false>, grid, th, stream, a)
-                  : launch(k_norm_bwd<2, uint16_t, false>, grid, th, stream, a);
+    e = launch_bwd<512, 4>(a, grid, stream);
   }
   if (e != cudaSuccess || a.nq == 0) return e;
   cudaLaunchConfig_t cfg = {};

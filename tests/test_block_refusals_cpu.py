@@ -109,7 +109,8 @@ def test_norm(m, over, expect):
 @pytest.mark.parametrize("over,expect", NORM + [
     (dict(dw_post=0), 1), (dict(dw_pre=0), 1), (dict(dgate=0), 1), (dict(dx=0), 1), (dict(dy=0), 1),
     (dict(dres=0), 1), (dict(dw_pre=0x90004), 3), (dict(dgate=0xa0002), 3), (dict(kind=1, gate=0x50000, dgate=0xa0004), 3),
-    (dict(dy=0xb0004), 3), (dict(dr=0xc0002), 3)])
+    (dict(dy=0xb0004), 3), (dict(dr=0xc0002), 3), (dict(ws=0), 1), (dict(ws=0xf0010), 3),
+    (dict(bytes=512), 4)])
 def test_norm_backward(m, over, expect):
     a = dict(dr=0xc0000, dx=0xd0000, dy=0xb0000, dres=0xe0000, dw_post=0x80000, dw_pre=0x90000, dgate=0xa0000,
              ws=0xf0000, bytes=1 << 30) | _norm(over)

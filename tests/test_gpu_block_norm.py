@@ -91,6 +91,15 @@ def test_row_counts(T, H):
     check(T, H, torch.float32, True, True, "token", T)
 
 
+@pytest.mark.parametrize("T,H,res,gate", [(1500, 4096, torch.float32, "token"), (700, 8192, torch.bfloat16, "element"),
+                                          (2000, 1032, torch.float32, "element"), (400, 16384, torch.bfloat16, "none"),
+                                          (500, 8192, torch.bfloat16, "channel")])
+@pytest.mark.parametrize("post,pre", [(True, True), (True, False), (False, True)])
+def test_several_rows_per_block(T, H, res, gate, post, pre):
+    """One, two and three rows in flight per row group."""
+    check(T, H, res, post, pre, gate, T)
+
+
 def test_no_residual_in_place_and_no_gradient_of_r():
     m = ftmoe()
     rng = np.random.default_rng(1)
