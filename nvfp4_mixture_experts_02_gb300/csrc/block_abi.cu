@@ -43,7 +43,7 @@ ft_status check_cache(const ft_paged_kv* c) {
 }
 
 size_t norm_bwd_workspace(int T, int H, int sms) {
-  return 1024 + align_up((size_t)norm_bwd_groups(T, H, sms) * 3 * H * sizeof(float), 256);
+  return 1024 + align_up((size_t)norm_bwd_groups(T, sms) * 3 * H * sizeof(float), 256);
 }
 
 ft_status check_norm(const uint16_t* y, const void* residual, const uint16_t* w_post,

@@ -192,7 +192,7 @@ struct NormArgs {
   int nq;
 };
 // Blocks (rows of the workspace's partial sums) of the backward pass.
-int norm_bwd_groups(int T, int H, int num_sms);
+int norm_bwd_groups(int T, int num_sms);
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream);
 cudaError_t launch_norm_bwd(const NormArgs& a, int num_sms, cudaStream_t stream);
 

@@ -26,28 +26,25 @@ namespace {
 constexpr int kWarpRowMax = 512;    // elements of a row that one warp holds
 constexpr int kRowWarps = 8;        // rows (warps) per block in that form
 
-// 1 / sqrt(v) to within a unit in the last place: r' cancels where r and z are opposite, and keeps what
-// error its factors have.
-__device__ __forceinline__ float inv_root(float v) { return __frcp_rn(__fsqrt_rn(v)); }
-
-// scale * gate / sqrt(sum / n + eps) as a float and what it lacks: where r and the block's output nearly
-// cancel, r' keeps the error of this factor many times over.
+// 1 / sqrt(sum / n + eps) and scale * gate times it, as a float and what it lacks: where r and the
+// block's output nearly cancel, r' keeps the error of this factor many times over. inv_n + inv_n_lo is
+// 1 / n.
 struct Factor {
-  float hi, lo;
+  float hi, lo, root;
 };
-__device__ __forceinline__ Factor row_factor(float sum, float n, float eps, float scale, float gate,
-                                             bool norm) {
+__device__ __forceinline__ Factor row_factor(float sum, float inv_n, float inv_n_lo, float eps,
+                                             float scale, float gate, bool norm) {
   const float tg = scale * gate, tg_lo = fmaf(scale, gate, -tg);
-  if (!norm) return {tg, tg_lo};
-  const float mean = __fdiv_rn(sum, n), mean_lo = fmaf(-mean, n, sum) / n;
+  if (!norm) return {tg, tg_lo, 1.f};
+  const float mean = sum * inv_n, mean_lo = fmaf(sum, inv_n_lo, fmaf(sum, inv_n, -mean));
   const float v = mean + eps, from = v - mean;
   const float v_lo = (mean - (v - from)) + (eps - from) + mean_lo;
-  const float s = inv_root(v), t = v * s;
+  const float s = rsqrtf(v), t = v * s;
   float left = fmaf(-t, s, 1.f);   // 1 - (v + v_lo) s^2
   left = fmaf(-fmaf(v, s, -t), s, left);
   left = fmaf(-v_lo * s, s, left);
   const float s_lo = 0.5f * s * left, hi = tg * s;
-  return {hi, fmaf(tg, s, -hi) + fmaf(tg, s_lo, tg_lo * s)};
+  return {hi, fmaf(tg, s, -hi) + fmaf(tg, s_lo, tg_lo * s), s + s_lo};
 }
 
 // Sum over the row's threads: the warp, or the whole block through red[] (one array per call
@@ -110,7 +107,7 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 1024) k_norm(const Nor
     for (int j = 0; j < 8; ++j) ss = fmaf(y[i][j], y[i][j], ss);
   }
   float s1 = 1.f;
-  if (a.w_post) s1 = inv_root(row_sum<WARP>(ss, red[0]) * inv_h + a.eps);
+  if (a.w_post) s1 = rsqrtf(row_sum<WARP>(ss, red[0]) * inv_h + a.eps);
   const float ts = a.scale * (a.gate_kind == FT_GATE_TOKEN ? one_bf16(a.gate + t) : 1.f) * s1;
   ss = 0.f;
 #pragma unroll
@@ -137,7 +134,7 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 1024) k_norm(const Nor
     if (a.r_out) store8(static_cast<RT*>(a.r_out) + row + 8 * c, r[i]);
   }
   if (!a.w_pre) return;
-  const float s2 = inv_root(row_sum<WARP>(ss, red[1]) * inv_h + a.eps);
+  const float s2 = rsqrtf(row_sum<WARP>(ss, red[1]) * inv_h + a.eps);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = tid + i * nth;
@@ -150,169 +147,7 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 1024) k_norm(const Nor
   }
 }
 
-// Gradient for rows that one warp holds: eight rows at a time in a block, column sums in registers,
-// joined by the block at the end.
-template <typename RT>
-__global__ void __launch_bounds__(kRowWarps * 32) k_norm_bwd_warp(const NormArgs a) {
-  constexpr int NV = 2;
-  griddep_launch_dependents();
-  griddep_wait();
-  const int tid = threadIdx.x & 31;
-  const int nth = 32;
-  const int group = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-  const int groups = gridDim.x * kRowWarps;
-  const int chunks = a.H >> 3;
-  const float inv_h = 1.0f / (float)a.H;
-  const bool channel = a.gate_kind == FT_GATE_CHANNEL;
-
-  float acc_post[NV][8], acc_pre[NV][8], acc_gate[NV][8];   // this group's column sums
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc_post[i][j] = acc_pre[i][j] = acc_gate[i][j] = 0.f;
-
-  for (int t = group; t < a.T; t += groups) {
-    const size_t row = (size_t)t * a.H;
-    float y[NV][8], r[NV][8], dr[NV][8], dx[NV][8];
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = tid + i * nth;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[i][j] = r[i][j] = dr[i][j] = dx[i][j] = 0.f;
-      if (c < chunks) {
-        load8(a.y + row + 8 * c, y[i]);
-        if (a.r) load8(static_cast<const RT*>(a.r) + row + 8 * c, r[i]);
-        if (a.dr) load8(static_cast<const RT*>(a.dr) + row + 8 * c, dr[i]);
-        if (a.w_pre) load8(a.dx + row + 8 * c, dx[i]);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(y[i][j], y[i][j], ss);
-    }
-    ss = warp_sum(ss);
-    float s1 = 1.f;
-    if (a.w_post) s1 = inv_root(ss * inv_h + a.eps);
-    const float tg = a.scale * (a.gate_kind == FT_GATE_TOKEN ? one_bf16(a.gate + t) : 1.f);
-    const Factor factor = row_factor(ss, (float)a.H, a.eps, a.scale,
-                                     a.gate_kind == FT_GATE_TOKEN ? one_bf16(a.gate + t) : 1.f,
-                                     a.w_post != nullptr);
-    // r <- r'
-    float rr = 0.f, dot = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = tid + i * nth;
-      if (c >= chunks) continue;
-      float w[8], g[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = g[j] = 1.f;
-      if (a.w_post) cached8(a.w_post + 8 * c, w);
-      if (channel) cached8(a.gate + 8 * c, g);
-      else if (a.gate_kind == FT_GATE_ELEMENT) cached8(a.gate + row + 8 * c, g);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float yu = y[i][j] * w[j] * g[j];
-        r[i][j] = fmaf(yu, factor.lo, fmaf(yu, factor.hi, r[i][j]));
-      }
-      if (a.w_pre) {
-        cached8(a.w_pre + 8 * c, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          rr = fmaf(r[i][j], r[i][j], rr);
-          dot = fmaf(dx[i][j] * w[j], r[i][j], dot);
-        }
-      }
-    }
-    float s2 = 0.f, cr = 0.f;
-    if (a.w_pre) {
-      rr = warp_sum(rr);
-      dot = warp_sum(dot);
-      s2 = inv_root(rr * inv_h + a.eps);
-      cr = s2 * s2 * (dot * inv_h);
-    }
-    float hy = 0.f, dgt = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = tid + i * nth;
-      if (c >= chunks) continue;
-      float w[8], g[8], dg[8];
-      if (a.w_pre) {
-        cached8(a.w_pre + 8 * c, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          acc_pre[i][j] = fmaf(dx[i][j], r[i][j] * s2, acc_pre[i][j]);
-          dr[i][j] = fmaf(s2, dx[i][j] * w[j] - r[i][j] * cr, dr[i][j]);
-        }
-      }
-      store8(static_cast<RT*>(a.dres) + row + 8 * c, dr[i]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = g[j] = 1.f;
-      if (a.w_post) cached8(a.w_post + 8 * c, w);
-      if (channel) cached8(a.gate + 8 * c, g);
-      else if (a.gate_kind == FT_GATE_ELEMENT) cached8(a.gate + row + 8 * c, g);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float yn = y[i][j] * s1;
-        dg[j] = a.scale * (yn * w[j]) * dr[i][j];
-        const float dz = tg * g[j] * dr[i][j];
-        if (channel) acc_gate[i][j] += dg[j];
-        dgt += dg[j];
-        if (a.w_post) {
-          acc_post[i][j] = fmaf(dz, yn, acc_post[i][j]);
-          hy = fmaf(dz * w[j], y[i][j], hy);
-        }
-        dx[i][j] = dz * w[j];   // h, or dy itself
-      }
-      if (a.gate_kind == FT_GATE_ELEMENT)
-        store8(static_cast<uint16_t*>(a.dgate) + row + 8 * c, dg);
-    }
-    float cy = 0.f;
-    if (a.w_post) cy = s1 * s1 * (warp_sum(hy) * inv_h);
-    if (a.gate_kind == FT_GATE_TOKEN) {
-      dgt = warp_sum(dgt);
-      if (tid == 0) static_cast<float*>(a.dgate)[t] = dgt;
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = tid + i * nth;
-      if (c >= chunks) continue;
-      if (a.w_post) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dx[i][j] = s1 * (dx[i][j] - y[i][j] * cy);
-      }
-      store8(a.dy + row + 8 * c, dx[i]);
-    }
-  }
-
-  // the group's column sums: [block][quantity][H]
-  float* part = a.part + (size_t)blockIdx.x * a.nq * a.H;
-  {
-    __shared__ float cols[kRowWarps][kWarpRowMax];
-    int q = 0;
-#pragma unroll
-    for (int which = 0; which < 3; ++which) {
-      if (which == 0 ? !a.w_post : which == 1 ? !a.w_pre : !channel) continue;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = tid + i * nth;
-        if (c < chunks)
-          store8(&cols[threadIdx.x >> 5][8 * c],
-                 which == 0 ? acc_post[i] : which == 1 ? acc_pre[i] : acc_gate[i]);
-      }
-      __syncthreads();
-      for (int h = threadIdx.x; h < a.H; h += kRowWarps * 32) {
-        float v = 0.f;
-        for (int w = 0; w < kRowWarps; ++w) v += cols[w][h];
-        part[(size_t)q * a.H + h] = v;
-      }
-      ++q;
-    }
-  }
-}
-
-
-// Gradient for longer rows. A block of 512 threads is RG row groups of GT threads, 8 NV columns per
-// thread; a group's rows come whole by bulk copies into its ring of stages, so that the next rows
+// The gradient. A block of 512 threads is RG row groups of GT threads, 8 NV columns per thread; a group's rows come whole by bulk copies into its ring of stages, so that the next rows
 // travel while one is worked on. A row's values are read from shared memory where they are used; r', h
 // and the column sums stay in registers. Two barriers a row: the sum that y needs is taken for the next
 // row together with the last sums of this one.
@@ -405,7 +240,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_norm_bwd(const NormArgs a, c
   const int g = threadIdx.x / GT, tid = threadIdx.x % GT, warp = tid >> 5, lane = tid & 31;
   const int chunks = a.H >> 3, ST = ring.stages;
   const bool ahead = ST >= 3;   // stages enough to look at the next row's y within this one
-  const float inv_h = 1.0f / (float)a.H;
+  const float inv_h = 1.0f / (float)a.H, inv_h_lo = fmaf(-inv_h, (float)a.H, 1.f) * inv_h;
   const bool channel = a.gate_kind == FT_GATE_CHANNEL, element = a.gate_kind == FT_GATE_ELEMENT;
   const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr;
   const RT* const kind = nullptr;
@@ -437,23 +272,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_norm_bwd(const NormArgs a, c
     if (element) copy(ring.off_gate, a.gate, 2);
   };
   auto barrier = [&]() {
-    asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "n"(GT) : "memory");
+    if constexpr (GT == 32) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "n"(GT) : "memory");
   };
-  // sums over the group's threads (two arrays in turn: one barrier each)
-  auto sum3 = [&](int which, float x, float y, float z) -> float4 {
+  // two sums over the group's threads (two arrays in turn: one barrier each)
+  auto sum2 = [&](int which, float x, float y) -> float2 {
     x = warp_sum(x);
     y = warp_sum(y);
-    z = warp_sum(z);
-    if (lane == 0) red[g][which][warp] = make_float4(x, y, z, 0.f);
+    if (lane == 0) red[g][which][warp] = make_float4(x, y, 0.f, 0.f);
     barrier();
     float4 v = red[g][which][lane % W];
 #pragma unroll
     for (int o = W / 2; o > 0; o >>= 1) {
       v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
       v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-      v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
     }
-    return v;
+    return make_float2(v.x, v.y);
   };
   // this thread's columns: u in float32, w_pre packed
   f2 u[NV][4], acc_post[NV][4], acc_pre[NV][4];
@@ -494,7 +328,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_norm_bwd(const NormArgs a, c
   float ss = 0.f;   // of the coming row's y, already summed
   if (n_rows > 0 && ahead) {
     arrived(0);
-    ss = sum3(0, square_sum(mine), 0.f, 0.f).x;
+    ss = sum2(0, square_sum(mine), 0.f).x;
     barrier();   // red[] is written again within the first row
   }
   for (int i = 0; i < n_rows; ++i) {
@@ -507,14 +341,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_norm_bwd(const NormArgs a, c
     };
     if (!ahead) {
       arrived(i);
-      ss = sum3(0, square_sum(st), 0.f, 0.f).x;
+      ss = sum2(0, square_sum(st), 0.f).x;
       refill();
       barrier();
     }
-    const float s1 = post ? inv_root(ss * inv_h + a.eps) : 1.f;
-    const float tg = a.scale * (a.gate_kind == FT_GATE_TOKEN ? one_bf16(a.gate + t) : 1.f);
-    const Factor factor = row_factor(ss, (float)a.H, a.eps, a.scale,
-                                     a.gate_kind == FT_GATE_TOKEN ? one_bf16(a.gate + t) : 1.f, post);
+    const float tgate = a.gate_kind == FT_GATE_TOKEN ? one_bf16(a.gate + t) : 1.f, tg = a.scale * tgate;
+    const Factor factor = row_factor(ss, inv_h, inv_h_lo, a.eps, a.scale, tgate, post);
+    const float s1 = factor.root;
     const f2 ts = both(factor.hi), ts_lo = both(factor.lo);
     // r' and the sums that x' needs
     f2 r[NV][4], rr = 0ull, dot = 0ull;
@@ -549,10 +382,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_norm_bwd(const NormArgs a, c
     }
     f2 s2 = 0ull, cr = 0ull;
     if (pre) {
-      const float4 v = sum3(1, sum_of(rr), sum_of(dot), 0.f);
-      const float s = inv_root(v.x * inv_h + a.eps);
+      const float2 v = sum2(1, sum_of(rr), sum_of(dot));
+      const float s = rsqrtf(v.x * inv_h + a.eps);
       s2 = both(s);
-      cr = both(-(s * s * (v.y * inv_h)));
+      cr = both(-(s * (s * s * (v.y * inv_h))));
       if (ahead) refill();
     }
     f2 h[NV][4], hy = 0ull;   // h without tg
@@ -570,8 +403,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_norm_bwd(const NormArgs a, c
         open8(wpre[v], w);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          acc_pre[v][j] = fma2(mul2(d[j], r[v][j]), s2, acc_pre[v][j]);
-          dr[j] = fma2(s2, fma2(r[v][j], cr, mul2(d[j], w[j])), dr[j]);
+          const f2 ds = mul2(d[j], s2);
+          acc_pre[v][j] = fma2(ds, r[v][j], acc_pre[v][j]);
+          dr[j] = fma2(ds, w[j], fma2(r[v][j], cr, dr[j]));
         }
       }
       put8(static_cast<RT*>(a.dres) + row + 8 * c, dr);
@@ -599,7 +433,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_norm_bwd(const NormArgs a, c
       arrived(i + 1);
       if (post) next = square_sum(mine + (size_t)((i + 1) % ST) * ring.stage);
     }
-    const float4 sums = sum3(0, sum_of(hy), next, 0.f);
+    const float2 sums = sum2(0, sum_of(hy), next);
     ss = sums.y;
     if (ahead && !pre) refill();
     if (a.gate_kind == FT_GATE_TOKEN && tid == 0)
@@ -673,7 +507,7 @@ __global__ void __launch_bounds__(kColWarps * 32) k_norm_cols(const NormArgs a, 
   const int width = a.nq * a.H;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (col < width) {
-#pragma unroll 4
+#pragma unroll 5
     for (int p = warp; p < parts; p += kColWarps) {
       const float4 u = *reinterpret_cast<const float4*>(a.part + (size_t)p * width + col);
       v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
@@ -746,11 +580,7 @@ cudaError_t launch_bwd(const NormArgs& a, int grid, cudaStream_t stream) {
 
 }  // namespace
 
-int norm_bwd_groups(int T, int H, int num_sms) {
-  const int rows = H <= kWarpRowMax ? (T + kRowWarps - 1) / kRowWarps : T;
-  const int most = H <= kWarpRowMax ? 2 * num_sms : num_sms;
-  return rows < most ? rows : most;
-}
+int norm_bwd_groups(int T, int num_sms) { return T < num_sms ? T : num_sms; }
 
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream) {
   const int chunks = a.H / 8;
@@ -766,11 +596,10 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_norm_bwd(const NormArgs& a, int num_sms, cudaStream_t stream) {
   const int chunks = a.H / 8;
-  const int grid = norm_bwd_groups(a.T, a.H, num_sms);
+  const int grid = norm_bwd_groups(a.T, num_sms);
   cudaError_t e;
-  if (a.H <= kWarpRowMax) {
-    e = a.res_f32 ? launch(k_norm_bwd_warp<float>, grid, kRowWarps * 32, stream, a)
-                  : launch(k_norm_bwd_warp<uint16_t>, grid, kRowWarps * 32, stream, a);
+  if (chunks <= 64) {
+    e = launch_bwd<32, 2>(a, grid, stream);
   } else if (chunks <= 128) {
     e = launch_bwd<64, 2>(a, grid, stream);
   } else if (chunks <= 256) {
