@@ -17,11 +17,13 @@
 // pieces in order. Masked and missing keys are not read: their rows are zeros in shared memory, so
 // that whatever the pages hold there (NaN, stale values) cannot reach a sum.
 //
-// Products: q k^T and p v as m16n8k16 with the 16 rows as query heads, float32 sums. bf16 caches:
-// bf16 operands; p, in (0, 1], is split into two bf16 (16 significant bits, so that p is not rounded
-// to 8); up to eight heads the second part rides in the idle rows 8 to 15. E4M3 caches: keys and values
-// become f16 exactly, q is f16 after a scaling of its row by a power of two (exact but for elements
-// under 2^-29 of the row's largest), p rounds to f16 (11 bits). Statistics and sums are float32.
+// Products, m16n8k16 with float32 sums, the query heads as the eight columns (two groups of columns for
+// nine to sixteen heads): s^T = k q^T and o^T = v^T p^T, so that all 16 rows are keys, then dims, and
+// the operands read from shared memory serve every head. The weights p leave s^T's register layout for
+// the other operand's by movmatrix. bf16 caches: bf16 operands; p, in (0, 1], is split into two bf16
+// (16 significant bits, so that p is not rounded to 8). E4M3 caches: keys and values become f16
+// exactly, q is f16 after a scaling of its row by a power of two (exact but for elements under 2^-29
+// of the row's largest), p rounds to f16 (11 bits). Statistics and sums are float32.
 #include <cmath>
 #include <cuda_runtime.h>
 
@@ -37,10 +39,11 @@ template <int D, bool F8>
 struct AttnShape {
   static constexpr int kRow = D * (F8 ? 1 : 2);       // bytes of a key or value
   static constexpr int kCpr = kRow / 16;              // 16-byte pieces of it
-  static constexpr int kWarps = !F8 && D == 256 ? 4 : 8;
   static constexpr int kStageBytes = 2 * 16 * kRow;   // 16 keys and 16 values
+  // warps: enough to hide each other's latencies, three stages or more each
+  static constexpr int kWarps = kRow >= 512 ? 4 : kRow >= 256 ? 8 : 16;
   static constexpr int kFit = 192 * 1024 / (kWarps * kStageBytes);
-  static constexpr int kStages = kFit < 8 ? kFit : 8;
+  static constexpr int kStages = kFit < 6 ? kFit : 6;
   static constexpr int kUnit = 16 * kWarps;           // keys of a unit
   static constexpr int kRing = kWarps * kStages * kStageBytes;
 };
@@ -56,6 +59,12 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
   else return (uint32_t)(r * CPR + (c ^ ((r >> 1) & 3))) * 16;
 }
 
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {   // an 8 x 8 matrix of 16-bit elements
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -68,22 +77,39 @@ __device__ __forceinline__ void span(int len, int window, int unit, int& first, 
   units = len > 0 ? (len + unit - 1) / unit - first / unit : 0;
 }
 
-template <int D, bool F8, int GM>
+template <int D, bool F8, int NG>
 __global__ void __launch_bounds__(AttnShape<D, F8>::kWarps * 32, 1) k_attend(const AttendArgs a) {
   using S = AttnShape<D, F8>;
-  constexpr int W = S::kWarps, ST = S::kStages, CPR = S::kCpr, NT = D / 8, KS = D / 16;
+  constexpr int W = S::kWarps, ST = S::kStages, CPR = S::kCpr, KS = D / 16, MT = D / 16;
+  constexpr int LD = D + 4;   // floats between heads where the warps' sums are joined
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ float wm[W][16], wl[W][16];
   __shared__ int scan[W];
-  int* cum = reinterpret_cast<int*>(smem + S::kRing);   // [B + 1] units before each sequence
+  int* cum = reinterpret_cast<int*>(smem + S::kRing);   // [B + 1] units before each sequence (B > 32)
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = lane & 3, r = lane >> 2;
   const int HS = a.kv.Hkv * a.gt;   // segments of a sequence
 
-  // units before each sequence
-  {
+  // units before each sequence: in every warp's lanes, or in shared memory past 32 sequences
+  int inc = 0;       // B <= 32: units up to and with sequence `lane`
+  int all;
+  if (a.B <= 32) {
+    int first, n = 0;
+    if (lane < a.B) span(a.seq_lens[lane], a.window, S::kUnit, first, n);
+    inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    all = __shfl_sync(0xffffffffu, inc, 31);
+    if (blockIdx.x == 0 && warp == 0) {   // the plan, for k_join
+      if (lane < a.B) a.plan[lane + 1] = inc;
+      if (lane == 0) a.plan[0] = 0;
+    }
+  } else {
     const int per = (a.B + W * 32 - 1) / (W * 32);
     const int b0 = threadIdx.x * per;
     int mine = 0;
@@ -92,15 +118,15 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kWarps * 32, 1) k_attend(con
       span(a.seq_lens[b], a.window, S::kUnit, first, n);
       mine += n;
     }
-    int inc = mine;
+    int upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
     }
-    if (lane == 31) scan[warp] = inc;
+    if (lane == 31) scan[warp] = upto;
     __syncthreads();
-    int at = inc - mine;
+    int at = upto - mine;
     for (int w = 0; w < warp; ++w) at += scan[w];
     for (int b = b0; b < min(b0 + per, a.B); ++b) {
       int first, n;
@@ -110,29 +136,37 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kWarps * 32, 1) k_attend(con
     }
     if (b0 < a.B && b0 + per >= a.B) cum[a.B] = at;
     __syncthreads();
+    all = cum[a.B];
+    if (blockIdx.x == 0)
+      for (int b = threadIdx.x; b <= a.B; b += W * 32) a.plan[b] = cum[b];
   }
-  const int64_t total = (int64_t)cum[a.B] * HS;
+  const int64_t total = (int64_t)all * HS;
   const int64_t quota = (total + gridDim.x - 1) / gridDim.x;
-  if (blockIdx.x == 0) {   // the plan, for k_join
-    for (int b = threadIdx.x; b <= a.B; b += W * 32) a.plan[b] = cum[b];
-  }
   int64_t u = quota * blockIdx.x;
   const int64_t u_end = min(u + quota, total);
   const uint32_t ring = smem_addr(smem) + (uint32_t)(warp * ST * S::kStageBytes);
 
   while (u < u_end) {
-    // the piece that begins at u
-    int lo = 0, hi = a.B;   // cum[lo] * HS <= u < cum[hi] * HS
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if ((int64_t)cum[mid] * HS <= u) lo = mid;
-      else hi = mid;
+    // the piece that begins at u: sequence b, with `before` units ahead of it
+    int b, before;
+    if (a.B <= 32) {
+      b = __ffs(__ballot_sync(0xffffffffu, (int64_t)inc * HS > u)) - 1;
+      before = __shfl_sync(0xffffffffu, inc, b > 0 ? b - 1 : 0);
+      if (b == 0) before = 0;
+    } else {
+      int lo = 0, hi = a.B;   // cum[lo] * HS <= u < cum[hi] * HS
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((int64_t)cum[mid] * HS <= u) lo = mid;
+        else hi = mid;
+      }
+      b = lo;
+      before = cum[b];
     }
-    const int b = lo;
     const int len = a.seq_lens[b];
     int first, units;
     span(len, a.window, S::kUnit, first, units);
-    const int64_t local = u - (int64_t)cum[b] * HS;
+    const int64_t local = u - (int64_t)before * HS;
     const int hs = (int)(local / units);
     const int u0 = (int)(local - (int64_t)hs * units);
     const int n_units = (int)min((int64_t)(units - u0), u_end - u);
@@ -142,8 +176,8 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kWarps * 32, 1) k_attend(con
     const int key1 = min(len, key0 + n_units * S::kUnit);   // keys of the piece: [key0, key1)
 
     // ---- the ring: sub-tile i of this warp = keys key0 + (i * W + warp) * 16 ..
-    const int subs = (key1 - key0 - warp * 16 + W * 16 - 1) / (W * 16);   // may be <= 0
-    const int n_sub = key1 - key0 > warp * 16 ? subs : 0;
+    const int left = key1 - key0 - warp * 16;
+    const int n_sub = left > 0 ? (left + W * 16 - 1) / (W * 16) : 0;
     const int32_t* table = a.block_table + (int64_t)b * a.table_width;
     int page = -1, slot = 0;
     auto look_up = [&](int i) {   // lane l < 16: the page and slot of key l of sub-tile i
@@ -156,28 +190,30 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kWarps * 32, 1) k_attend(con
       }
     };
     auto fetch = [&](int i) {     // the copies of sub-tile i, whose pages look_up has found
-      int64_t ko = -1, vo = -1;
-      if (page >= 0 && page < a.kv.num_pages) {
-        ko = ((int64_t)page * a.kv.k_page_stride + (int64_t)slot * a.kv.k_slot_stride +
-              (int64_t)kvh * a.kv.k_head_stride) * (F8 ? 1 : 2);
-        vo = ((int64_t)page * a.kv.v_page_stride + (int64_t)slot * a.kv.v_slot_stride +
-              (int64_t)kvh * a.kv.v_head_stride) * (F8 ? 1 : 2);
-      } else if (i < n_sub && lane < 16) {
-        const int j = key0 + (i * W + warp) * 16 + lane;
-        if (j >= first && j < key1) atomicOr(a.err, kErrBadPage);   // no such page: read as zeros
-      }
       if (i < n_sub) {
+        int64_t ko = -1, vo = -1;
+        if (page >= 0 && page < a.kv.num_pages) {
+          ko = ((int64_t)page * a.kv.k_page_stride + (int64_t)slot * a.kv.k_slot_stride +
+                (int64_t)kvh * a.kv.k_head_stride) * (F8 ? 1 : 2);
+          if (!a.same_strides)
+            vo = ((int64_t)page * a.kv.v_page_stride + (int64_t)slot * a.kv.v_slot_stride +
+                  (int64_t)kvh * a.kv.v_head_stride) * (F8 ? 1 : 2);
+        } else if (lane < 16) {
+          const int j = key0 + (i * W + warp) * 16 + lane;
+          if (j >= first && j < key1) atomicOr(a.err, kErrBadPage);   // no such page: read as zeros
+        }
         const uint32_t st = ring + (uint32_t)((i % ST) * S::kStageBytes);
         constexpr int RPI = 32 / CPR;   // rows of one warp-wide copy
 #pragma unroll
         for (int p = 0; p < 16 / RPI; ++p) {
           const int row = p * RPI + lane / CPR, ch = lane % CPR;
           const int64_t k_at = __shfl_sync(0xffffffffu, ko, row);
-          const int64_t v_at = __shfl_sync(0xffffffffu, vo, row);
+          const int64_t v_at = a.same_strides ? k_at : __shfl_sync(0xffffffffu, vo, row);
+          const bool on = k_at >= 0;
           cp_async16(st + swz<CPR>(row, ch),
-                     static_cast<const char*>(a.kv.k) + (k_at < 0 ? 0 : k_at) + ch * 16, k_at >= 0);
+                     static_cast<const char*>(a.kv.k) + (on ? k_at + ch * 16 : 0), on);
           cp_async16(st + 16 * S::kRow + swz<CPR>(row, ch),
-                     static_cast<const char*>(a.kv.v) + (v_at < 0 ? 0 : v_at) + ch * 16, v_at >= 0);
+                     static_cast<const char*>(a.kv.v) + (on ? v_at + ch * 16 : 0), on);
         }
       }
       cp_async_commit();
@@ -189,232 +225,212 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kWarps * 32, 1) k_attend(con
       look_up(i + 1);
     }
 
-    // ---- q: the A operand, 16 heads x D
-    uint32_t q[KS][4];
-    float sl0, sl1;   // log2 units per unit of the raw product, rows r and r + 8
+    // ---- q as the column operand: column l / 4 of group g is head 8 g + l / 4
+    uint32_t q[NG][KS][2];
+    float sl[NG][2];   // log2 units per unit of the raw product, heads 8 g + 2 c, + 1
     {
       const uint16_t* qb = a.q + (int64_t)b * a.q_stride + (int64_t)(kvh * a.group + g0) * D;
-      const bool on0 = r < G, on1 = GM == 16 && r + 8 < G;
-      sl0 = sl1 = a.scale * a.kv.k_scale * kLog2e;
-      if constexpr (!F8) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const int d = 16 * ks + 2 * c;
-          q[ks][0] = on0 ? *reinterpret_cast<const uint32_t*>(qb + r * D + d) : 0u;
-          q[ks][2] = on0 ? *reinterpret_cast<const uint32_t*>(qb + r * D + d + 8) : 0u;
-          q[ks][1] = on1 ? *reinterpret_cast<const uint32_t*>(qb + (r + 8) * D + d) : 0u;
-          q[ks][3] = on1 ? *reinterpret_cast<const uint32_t*>(qb + (r + 8) * D + d + 8) : 0u;
-        }
-      } else {
-        float top0 = 0.f, top1 = 0.f;
+      for (int g = 0; g < NG; ++g) {
+        const bool on = 8 * g + r < G;
+        const uint16_t* qh = qb + (8 * g + r) * D;
+        sl[g][0] = sl[g][1] = a.scale * a.kv.k_scale * kLog2e;
+        if constexpr (!F8) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const int d = 16 * ks + 4 * c;   // E4M3 keys come four elements to a lane
-          uint2 v0 = make_uint2(0, 0), v1 = make_uint2(0, 0);
-          if (on0) v0 = *reinterpret_cast<const uint2*>(qb + r * D + d);
-          if (on1) v1 = *reinterpret_cast<const uint2*>(qb + (r + 8) * D + d);
-          q[ks][0] = v0.x; q[ks][2] = v0.y; q[ks][1] = v1.x; q[ks][3] = v1.y;
-          top0 = fmaxf(top0, finite_top(v0.x, v0.y));
-          top1 = fmaxf(top1, finite_top(v1.x, v1.y));
-        }
+          for (int ks = 0; ks < KS; ++ks) {
+            q[g][ks][0] = on ? *reinterpret_cast<const uint32_t*>(qh + 16 * ks + 2 * c) : 0u;
+            q[g][ks][1] = on ? *reinterpret_cast<const uint32_t*>(qh + 16 * ks + 2 * c + 8) : 0u;
+          }
+        } else {
+          float top = 0.f;
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, o));
-          top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, o));
-        }
-        float up0, up1, down0, down1;
-        f16_scale(top0, up0, down0);
-        f16_scale(top1, up1, down1);
-        sl0 *= down0;
-        sl1 *= down1;
+          for (int ks = 0; ks < KS; ++ks) {   // E4M3 keys come four elements to a lane
+            uint2 v = make_uint2(0, 0);
+            if (on) v = *reinterpret_cast<const uint2*>(qh + 16 * ks + 4 * c);
+            q[g][ks][0] = v.x;
+            q[g][ks][1] = v.y;
+            top = fmaxf(top, finite_top(v.x, v.y));
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          float up, down;
+          f16_scale(top, up, down);
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          q[ks][0] = pack_f16(bf16_lo(q[ks][0]) * up0, bf16_hi(q[ks][0]) * up0);
-          q[ks][2] = pack_f16(bf16_lo(q[ks][2]) * up0, bf16_hi(q[ks][2]) * up0);
-          q[ks][1] = pack_f16(bf16_lo(q[ks][1]) * up1, bf16_hi(q[ks][1]) * up1);
-          q[ks][3] = pack_f16(bf16_lo(q[ks][3]) * up1, bf16_hi(q[ks][3]) * up1);
+          for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              q[g][ks][e] = pack_f16(bf16_lo(q[g][ks][e]) * up, bf16_hi(q[g][ks][e]) * up);
+          sl[g][0] *= __shfl_sync(0xffffffffu, down, 8 * c);       // head 2 c: lanes 8 c ..
+          sl[g][1] *= __shfl_sync(0xffffffffu, down, 8 * c + 4);
         }
       }
     }
 
-    float o[NT][4];
+    float o[NG][MT][4], m[NG][2], l[NG][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    for (int g = 0; g < NG; ++g) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t) o[g][t][0] = o[g][t][1] = o[g][t][2] = o[g][t][3] = 0.f;
+      m[g][0] = m[g][1] = -INFINITY;
+      l[g][0] = l[g][1] = 0.f;
+    }
+    const int krow = ((lane >> 3) & 1) * 8 + (lane & 7), half = lane >> 4;
 
     for (int i = 0; i < n_sub; ++i) {
       cp_async_wait<ST - 2>();
       __syncwarp();
       const uint32_t st = ring + (uint32_t)((i % ST) * S::kStageBytes);
-      // s = q k^T, two tiles of eight keys
-      float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-      {
-        const int key = (lane >> 4) * 8 + (lane & 7), half = (lane >> 3) & 1;
-        if constexpr (!F8) {
+      // s^T = k q^T: 16 keys
+      float s[NG][4];
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            uint32_t k[4];
-            ldmatrix4(k, st + swz<CPR>(key, 2 * ks + half));
-            mma_bf16(s0, q[ks][0], q[ks][1], q[ks][2], q[ks][3], k[0], k[1]);
-            mma_bf16(s1, q[ks][0], q[ks][1], q[ks][2], q[ks][3], k[2], k[3]);
-          }
-        } else {
+      for (int g = 0; g < NG; ++g) s[g][0] = s[g][1] = s[g][2] = s[g][3] = 0.f;
+      if constexpr (!F8) {
 #pragma unroll
-          for (int ks = 0; ks < KS; ks += 2) {
-            uint32_t k[4];
-            ldmatrix4(k, st + swz<CPR>(key, ks + half));
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t k[4];   // keys 0-7 and 8-15 of dims 0-7, then of dims 8-15
+          ldmatrix4(k, st + swz<CPR>(krow, 2 * ks + half));
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              mma_f16(s0, q[ks + e][0], q[ks + e][1], q[ks + e][2], q[ks + e][3],
-                      e4m3x2_to_f16x2(k[e]), e4m3x2_to_f16x2(k[e] >> 16));
-              mma_f16(s1, q[ks + e][0], q[ks + e][1], q[ks + e][2], q[ks + e][3],
-                      e4m3x2_to_f16x2(k[2 + e]), e4m3x2_to_f16x2(k[2 + e] >> 16));
-            }
+          for (int g = 0; g < NG; ++g)
+            mma_bf16(s[g], k[0], k[1], k[2], k[3], q[g][ks][0], q[g][ks][1]);
+        }
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < KS; ks += 2) {
+          uint32_t k[4];   // keys 0-7 and 8-15 of 16 dims, then of the next 16
+          ldmatrix4(k, st + swz<CPR>(krow, ks + half));
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t a0 = e4m3x2_to_f16x2(k[2 * e]), a1 = e4m3x2_to_f16x2(k[2 * e + 1]);
+            const uint32_t a2 = e4m3x2_to_f16x2(k[2 * e] >> 16), a3 = e4m3x2_to_f16x2(k[2 * e + 1] >> 16);
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+              mma_f16(s[g], a0, a1, a2, a3, q[g][ks + e][0], q[g][ks + e][1]);
           }
         }
       }
       // the next copies go into the stage that the previous sub-tile has left
       fetch(i + ST - 1);
       look_up(i + ST);
-      // scores in log2 units; keys outside [first, key1) do not count
+      // scores in log2 units: key j0 + r (elements 0, 1) and j0 + r + 8; keys outside [first, key1)
+      // do not count
       const int j0 = key0 + (i * W + warp) * 16;
+      bool up = false;
+      float top[NG][2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        s0[e] *= sl0; s1[e] *= sl0;
-        s0[2 + e] *= sl1; s1[2 + e] *= sl1;
-      }
-      if (j0 < first || j0 + 16 > key1) {
+      for (int g = 0; g < NG; ++g) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = j0 + 2 * c + (e & 1);
-          if (j < first || j >= key1) s0[e] = -INFINITY;
-          if (j + 8 < first || j + 8 >= key1) s1[e] = -INFINITY;
+        for (int e = 0; e < 4; ++e) s[g][e] *= sl[g][e & 1];
+        if (j0 < first || j0 + 16 > key1) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = j0 + r + (e >> 1) * 8;
+            if (j < first || j >= key1) s[g][e] = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float t = fmaxf(s[g][e], s[g][2 + e]);
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
+          top[g][e] = t;
+          up |= t > m[g][e];
         }
       }
-      float t0 = fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s1[0], s1[1]));
-      float t1 = fmaxf(fmaxf(s0[2], s0[3]), fmaxf(s1[2], s1[3]));
-#pragma unroll
-      for (int x = 1; x < 4; x <<= 1) {
-        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, x));
-        if (GM == 16) t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, x));
-      }
-      const bool up = t0 > m0 || (GM == 16 && t1 > m1);
       if (__any_sync(0xffffffffu, up)) {   // a new maximum: what is summed shrinks
-        const float n0 = fmaxf(m0, t0), n1 = GM == 16 ? fmaxf(m1, t1) : n0;
-        const float f0 = m0 == -INFINITY ? 0.f : exp2_fast(m0 - n0);
-        const float f1 = GM == 16 ? (m1 == -INFINITY ? 0.f : exp2_fast(m1 - n1)) : f0;
-        m0 = n0;
-        m1 = n1;
-        l0 *= f0;
-        l1 *= f1;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          o[n][0] *= f0; o[n][1] *= f0;
-          o[n][2] *= f1; o[n][3] *= f1;
+        for (int g = 0; g < NG; ++g) {
+          float f[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float n = fmaxf(m[g][e], top[g][e]);
+            f[e] = m[g][e] == -INFINITY ? 0.f : exp2_fast(m[g][e] - n);
+            m[g][e] = n;
+            l[g][e] *= f[e];
+          }
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            o[g][t][0] *= f[0]; o[g][t][1] *= f[1];
+            o[g][t][2] *= f[0]; o[g][t][3] *= f[1];
+          }
         }
       }
-      const float b0 = m0 == -INFINITY ? 0.f : m0;   // no key yet: every p is 0
-      const float b1 = m1 == -INFINITY ? 0.f : m1;
+      uint32_t p[NG][2], rest[NG][2];   // p^T: columns heads, rows keys 0-7 and 8-15
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        s0[e] = exp2_fast(s0[e] - b0);
-        s1[e] = exp2_fast(s1[e] - b0);
-        l0 += s0[e] + s1[e];
-        if (GM == 16) {
-          s0[2 + e] = exp2_fast(s0[2 + e] - b1);
-          s1[2 + e] = exp2_fast(s1[2 + e] - b1);
-          l1 += s0[2 + e] + s1[2 + e];
+      for (int g = 0; g < NG; ++g) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float base = m[g][e] == -INFINITY ? 0.f : m[g][e];   // no key yet: every p is 0
+          s[g][e] = exp2_fast(s[g][e] - base);
+          s[g][2 + e] = exp2_fast(s[g][2 + e] - base);
+          l[g][e] += s[g][e] + s[g][2 + e];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (F8) {
+            p[g][h] = transpose8(pack_f16(s[g][2 * h], s[g][2 * h + 1]));
+          } else {
+            const uint32_t v = pack_bf16(s[g][2 * h], s[g][2 * h + 1]);
+            p[g][h] = transpose8(v);
+            rest[g][h] = transpose8(pack_bf16(s[g][2 * h] - bf16_lo(v), s[g][2 * h + 1] - bf16_hi(v)));
+          }
         }
       }
-      // o += p v
-      const int key = ((lane >> 3) & 1) * 8 + (lane & 7), half = lane >> 4;
+      // o^T += v^T p^T: 16 dims at a time
       const uint32_t vs = st + 16 * S::kRow;
       if constexpr (!F8) {
-        uint32_t p[4], pl[4];
-        p[0] = pack_bf16(s0[0], s0[1]);
-        p[2] = pack_bf16(s1[0], s1[1]);
-        const uint32_t rest0 = pack_bf16(s0[0] - bf16_lo(p[0]), s0[1] - bf16_hi(p[0]));
-        const uint32_t rest2 = pack_bf16(s1[0] - bf16_lo(p[2]), s1[1] - bf16_hi(p[2]));
-        if (GM == 16) {
-          p[1] = pack_bf16(s0[2], s0[3]);
-          p[3] = pack_bf16(s1[2], s1[3]);
-          pl[0] = rest0;
-          pl[2] = rest2;
-          pl[1] = pack_bf16(s0[2] - bf16_lo(p[1]), s0[3] - bf16_hi(p[1]));
-          pl[3] = pack_bf16(s1[2] - bf16_lo(p[3]), s1[3] - bf16_hi(p[3]));
-        } else {   // rows 8 to 15 carry what rows 0 to 7 lose by rounding
-          p[1] = rest0;
-          p[3] = rest2;
-        }
+        const int vrow = half * 8 + (lane & 7), vch = (lane >> 3) & 1;
 #pragma unroll
-        for (int n = 0; n < NT; n += 2) {
-          uint32_t v[4];
-          ldmatrix4_trans(v, vs + swz<CPR>(key, n + half));
-          mma_bf16(o[n], p[0], p[1], p[2], p[3], v[0], v[1]);
-          mma_bf16(o[n + 1], p[0], p[1], p[2], p[3], v[2], v[3]);
-          if (GM == 16) {
-            mma_bf16(o[n], pl[0], pl[1], pl[2], pl[3], v[0], v[1]);
-            mma_bf16(o[n + 1], pl[0], pl[1], pl[2], pl[3], v[2], v[3]);
+        for (int t = 0; t < MT; ++t) {
+          uint32_t v[4];   // dims 0-7 and 8-15 of keys 0-7, then of keys 8-15
+          ldmatrix4_trans(v, vs + swz<CPR>(vrow, 2 * t + vch));
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            mma_bf16(o[g][t], v[0], v[1], v[2], v[3], p[g][0], p[g][1]);
+            mma_bf16(o[g][t], v[0], v[1], v[2], v[3], rest[g][0], rest[g][1]);
           }
         }
       } else {
-        uint32_t p[4];
-        p[0] = pack_f16(s0[0], s0[1]);
-        p[2] = pack_f16(s1[0], s1[1]);
-        p[1] = GM == 16 ? pack_f16(s0[2], s0[3]) : 0u;
-        p[3] = GM == 16 ? pack_f16(s1[2], s1[3]) : 0u;
 #pragma unroll
-        for (int n = 0; n < NT; n += 4) {   // two 16-byte pieces: dims 8 n .. 8 n + 31
-          uint32_t v[4];
-          ldmatrix4_trans(v, vs + swz<CPR>(key, n / 2 + half));
-          // a register holds (key, dim d), (key, d + 1), (key + 1, d), (key + 1, d + 1)
+        for (int t = 0; t < MT; t += 2) {
+          uint32_t v[4];   // keys 0-7 and 8-15 of 16 dims, then of the next 16
+          ldmatrix4_trans(v, vs + swz<CPR>(krow, t + half));
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t x = __byte_perm(v[2 * h], 0, 0x3120);
-            const uint32_t y = __byte_perm(v[2 * h + 1], 0, 0x3120);
-            mma_f16(o[n + 2 * h], p[0], p[1], p[2], p[3], e4m3x2_to_f16x2(x),
-                    e4m3x2_to_f16x2(y));            // even dims
-            mma_f16(o[n + 2 * h + 1], p[0], p[1], p[2], p[3], e4m3x2_to_f16x2(x >> 16),
-                    e4m3x2_to_f16x2(y >> 16));      // odd dims
+          for (int e = 0; e < 2; ++e) {
+            // (key, dim d), (key, d + 1), (key + 1, d), (key + 1, d + 1): rows 0-7 take the even dims
+            const uint32_t x = __byte_perm(v[2 * e], 0, 0x3120), y = __byte_perm(v[2 * e + 1], 0, 0x3120);
+            const uint32_t a0 = e4m3x2_to_f16x2(x), a1 = e4m3x2_to_f16x2(x >> 16);
+            const uint32_t a2 = e4m3x2_to_f16x2(y), a3 = e4m3x2_to_f16x2(y >> 16);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) mma_f16(o[g][t + e], a0, a1, a2, a3, p[g][0], p[g][1]);
           }
         }
       }
       __syncwarp();   // every lane has read the stage before it is filled again
     }
     cp_async_wait<0>();
-#pragma unroll
-    for (int x = 1; x < 4; x <<= 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, x);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, x);
-    }
 
-    // ---- join the warps: sums [warp][head][D] in the ring's memory
+    // ---- join the warps: sums [warp][head][LD] in the ring's memory
     __syncthreads();
-    float* sums = reinterpret_cast<float*>(smem) + (size_t)warp * 16 * D;
-    if (c == 0) {
-      wm[warp][r] = m0;
-      wl[warp][r] = l0;
-      if (GM == 16) {
-        wm[warp][r + 8] = m1;
-        wl[warp][r + 8] = l1;
-      }
-    }
+    float* sums = reinterpret_cast<float*>(smem) + (size_t)warp * (8 * NG) * LD;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if (GM == 8) {
-        o[n][0] += o[n][2];
-        o[n][1] += o[n][3];
-      }
-      // dims of this lane's two columns
-      const int d0 = F8 ? 16 * (n / 2) + 4 * c + (n & 1) : 8 * n + 2 * c;
-      const int d1 = F8 ? d0 + 2 : d0 + 1;
-      if (r < G) {
-        sums[r * D + d0] = o[n][0];
-        sums[r * D + d1] = o[n][1];
-      }
-      if (GM == 16 && r + 8 < G) {
-        sums[(r + 8) * D + d0] = o[n][2];
-        sums[(r + 8) * D + d1] = o[n][3];
+    for (int g = 0; g < NG; ++g) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[g][e] += __shfl_xor_sync(0xffffffffu, l[g][e], x);
+        const int h = 8 * g + 2 * c + e;
+        if (r == 0) {
+          wm[warp][h] = m[g][e];
+          wl[warp][h] = l[g][e];
+        }
+        if (h < G) {
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            const int d0 = F8 ? 16 * t + 2 * r : 16 * t + r, d1 = F8 ? d0 + 1 : d0 + 8;
+            sums[h * LD + d0] = o[g][t][e];
+            sums[h * LD + d1] = o[g][t][2 + e];
+          }
+        }
       }
     }
     __syncthreads();
@@ -422,27 +438,27 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kWarps * 32, 1) k_attend(con
     const int64_t part = 2 * (int64_t)blockIdx.x + (u == quota * blockIdx.x ? 0 : 1);
     for (int x = threadIdx.x; x < G * D; x += W * 32) {
       const int g = x / D, d = x - g * D;
-      float m = -INFINITY;
+      float top = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < W; ++w) m = fmaxf(m, wm[w][g]);
-      const float base = m == -INFINITY ? 0.f : m;
-      float l = 0.f, v = 0.f;
+      for (int w = 0; w < W; ++w) top = fmaxf(top, wm[w][g]);
+      const float base = top == -INFINITY ? 0.f : top;
+      float sum = 0.f, v = 0.f;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         const float f = exp2_fast(wm[w][g] - base);
-        l = fmaf(f, wl[w][g], l);
-        v = fmaf(f, reinterpret_cast<const float*>(smem)[(size_t)w * 16 * D + x], v);
+        sum = fmaf(f, wl[w][g], sum);
+        v = fmaf(f, reinterpret_cast<const float*>(smem)[(size_t)(w * (8 * NG) + g) * LD + d], v);
       }
       const int64_t row = (int64_t)b * a.Hq + kvh * a.group + g0 + g;
       if (whole) {
-        const float y = l == 0.f ? 0.f : v / l * a.kv.v_scale;   // no weight at all: zeros
+        const float y = sum == 0.f ? 0.f : v / sum * a.kv.v_scale;   // no weight at all: zeros
         a.out[row * D + d] = (uint16_t)(pack_bf16(y, 0.f) & 0xFFFFu);
-        if (d == 0 && a.lse) a.lse[row] = (m + log2f(l)) * kLn2;
+        if (d == 0 && a.lse) a.lse[row] = (top + log2f(sum)) * kLn2;
       } else {
         a.part_o[(part * 16 + g) * D + d] = v;
         if (d == 0) {
-          a.part_ml[(part * 16 + g) * 2] = m;
-          a.part_ml[(part * 16 + g) * 2 + 1] = l;
+          a.part_ml[(part * 16 + g) * 2] = top;
+          a.part_ml[(part * 16 + g) * 2 + 1] = sum;
         }
       }
     }
@@ -505,13 +521,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_join(const AttendArgs a, in
   if (lane == 0 && a.lse) a.lse[row] = (m + log2f(l)) * kLn2;
 }
 
-template <int D, bool F8, int GM>
+template <int D, bool F8, int NG>
 cudaError_t launch_d(const AttendArgs& a, int num_sms, cudaStream_t stream) {
   using S = AttnShape<D, F8>;
-  const size_t smem = S::kRing + (size_t)(a.B + 1) * 4;
+  const size_t smem = S::kRing + (a.B > 32 ? (size_t)(a.B + 1) * 4 : 0);
   cudaError_t e;
   // set on every call: the attribute is per device and the call is host-side only
-  if ((e = cudaFuncSetAttribute(k_attend<D, F8, GM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if ((e = cudaFuncSetAttribute(k_attend<D, F8, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)smem)) != cudaSuccess)
     return e;
   cudaLaunchConfig_t cfg = {};
@@ -524,7 +540,7 @@ cudaError_t launch_d(const AttendArgs& a, int num_sms, cudaStream_t stream) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, k_attend<D, F8, GM>, a)) != cudaSuccess) return e;
+  if ((e = cudaLaunchKernelEx(&cfg, k_attend<D, F8, NG>, a)) != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)(((int64_t)a.B * a.Hq + kJoinWarps - 1) / kJoinWarps));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
@@ -535,8 +551,8 @@ template <int D>
 cudaError_t launch_g(const AttendArgs& a, int num_sms, cudaStream_t stream) {
   const bool f8 = a.kv.dtype == FT_KV_E4M3;
   if (a.group <= 8)
-    return f8 ? launch_d<D, true, 8>(a, num_sms, stream) : launch_d<D, false, 8>(a, num_sms, stream);
-  return f8 ? launch_d<D, true, 16>(a, num_sms, stream) : launch_d<D, false, 16>(a, num_sms, stream);
+    return f8 ? launch_d<D, true, 1>(a, num_sms, stream) : launch_d<D, false, 1>(a, num_sms, stream);
+  return f8 ? launch_d<D, true, 2>(a, num_sms, stream) : launch_d<D, false, 2>(a, num_sms, stream);
 }
 
 }  // namespace
@@ -545,6 +561,8 @@ cudaError_t launch_attend(const AttendArgs& args, int num_sms, cudaStream_t stre
   AttendArgs a = args;
   a.group = a.Hq / a.kv.Hkv;
   a.gt = (a.group + 15) / 16;
+  a.same_strides = a.kv.k_page_stride == a.kv.v_page_stride && a.kv.k_slot_stride == a.kv.v_slot_stride &&
+                   a.kv.k_head_stride == a.kv.v_head_stride;
   // j / page_size for 0 <= j < 2^31 as (umulhi(mul, j) + j) >> shift
   int shift = 0;
   while ((1ll << shift) < a.kv.page_size) ++shift;

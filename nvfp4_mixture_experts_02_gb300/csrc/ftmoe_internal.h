@@ -158,6 +158,7 @@ struct AttendArgs {
   int* plan;
   float *part_ml, *part_o;
   int group, gt;           // query heads per key head, 16-head parts of them (set by the launch)
+  int same_strides;        // keys and values lie alike (set by the launch)
   int div_mul, div_shift;  // division by the page size (set by the launch)
 };
 // Workspace regions (byte offsets, 256-byte aligned).
