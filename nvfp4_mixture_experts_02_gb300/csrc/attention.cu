@@ -39,12 +39,12 @@ template <int D, bool F8>
 struct AttnShape {
   static constexpr int kRow = D * (F8 ? 1 : 2);       // bytes of a key or value
   static constexpr int kCpr = kRow / 16;              // 16-byte pieces of it
-  static constexpr int kStageBytes = 2 * 16 * kRow;   // 16 keys and 16 values
-  // warps: enough to hide each other's latencies, three stages or more each
-  static constexpr int kWarps = kRow >= 512 ? 4 : kRow >= 256 ? 8 : 16;
-  static constexpr int kFit = 192 * 1024 / (kWarps * kStageBytes);
-  static constexpr int kStages = kFit < 6 ? kFit : 6;
-  static constexpr int kUnit = 16 * kWarps;           // keys of a unit
+  static constexpr int kKeys = kRow <= 128 ? 32 : 16; // keys of a warp's step
+  static constexpr int kStageBytes = 2 * kKeys * kRow;   // those keys and values
+  // warps: enough to hide each other's latencies, three stages each
+  static constexpr int kWarps = kRow >= 512 ? 4 : kRow >= 128 ? 8 : 16;
+  static constexpr int kStages = 192 * 1024 / (kWarps * kStageBytes);
+  static constexpr int kUnit = kKeys * kWarps;        // keys of a unit
   static constexpr int kRing = kWarps * kStages * kStageBytes;
 };
 
@@ -65,10 +65,27 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {   // an 8 x 8 matri
   return d;
 }
 
+// Four E4M3 bytes -> f16x2 of the lower two and of the upper two, exact.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(v));
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Four values of an output row, divided by the weights' sum (no weight at all: zeros).
+__device__ __forceinline__ void store_row(const AttendArgs& a, int64_t at, float4 v, float sum) {
+  uint2 y = make_uint2(0, 0);
+  if (!(sum == 0.f)) {
+    const float s = a.kv.v_scale;
+    y = make_uint2(pack_bf16(v.x / sum * s, v.y / sum * s), pack_bf16(v.z / sum * s, v.w / sum * s));
+  }
+  *reinterpret_cast<uint2*>(a.out + at) = y;
 }
 
 // First key and number of units of a sequence.
@@ -81,9 +98,11 @@ template <int D, bool F8, int NG>
 __global__ void __launch_bounds__(AttnShape<D, F8>::kWarps * 32, 1) k_attend(const AttendArgs a) {
   using S = AttnShape<D, F8>;
   constexpr int W = S::kWarps, ST = S::kStages, CPR = S::kCpr, KS = D / 16, MT = D / 16;
+  constexpr int KT = S::kKeys, NH = KT / 16;   // keys of a step, in 16-row tiles
   constexpr int LD = D + 4;   // floats between heads where the warps' sums are joined
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ float wm[W][16], wl[W][16];
+  __shared__ float2 joined[16];
   __shared__ int scan[W];
   int* cum = reinterpret_cast<int*>(smem + S::kRing);   // [B + 1] units before each sequence (B > 32)
   griddep_launch_dependents();
@@ -175,13 +194,13 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kWarps * 32, 1) k_attend(con
     const int key0 = (first / S::kUnit + u0) * S::kUnit;
     const int key1 = min(len, key0 + n_units * S::kUnit);   // keys of the piece: [key0, key1)
 
-    // ---- the ring: sub-tile i of this warp = keys key0 + (i * W + warp) * 16 ..
-    const int left = key1 - key0 - warp * 16;
-    const int n_sub = left > 0 ? (left + W * 16 - 1) / (W * 16) : 0;
+    // ---- the ring: step i of this warp = keys key0 + (i * W + warp) * KT ..
+    const int left = key1 - key0 - warp * KT;
+    const int n_sub = left > 0 ? (left + W * KT - 1) / (W * KT) : 0;
     const int32_t* table = a.block_table + (int64_t)b * a.table_width;
     int page = -1, slot = 0;
-    auto look_up = [&](int i) {   // lane l < 16: the page and slot of key l of sub-tile i
-      const int j = key0 + (i * W + warp) * 16 + (lane & 15);
+    auto look_up = [&](int i) {   // lane l < KT: the page and slot of key l of step i
+      const int j = key0 + (i * W + warp) * KT + lane % KT;
       page = -1;
       if (i < n_sub && j >= first && j < key1) {
         const int col = (int)((__umulhi((uint32_t)a.div_mul, (uint32_t)j) + (uint32_t)j) >> a.div_shift);
@@ -189,7 +208,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kWarps * 32, 1) k_attend(con
         page = col < a.table_width ? table[col] : a.kv.num_pages;
       }
     };
-    auto fetch = [&](int i) {     // the copies of sub-tile i, whose pages look_up has found
+    auto fetch = [&](int i) {     // the copies of step i, whose pages look_up has found
       if (i < n_sub) {
         int64_t ko = -1, vo = -1;
         if (page >= 0 && page < a.kv.num_pages) {
@@ -198,21 +217,21 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kWarps * 32, 1) k_attend(con
           if (!a.same_strides)
             vo = ((int64_t)page * a.kv.v_page_stride + (int64_t)slot * a.kv.v_slot_stride +
                   (int64_t)kvh * a.kv.v_head_stride) * (F8 ? 1 : 2);
-        } else if (lane < 16) {
-          const int j = key0 + (i * W + warp) * 16 + lane;
+        } else if (lane < KT) {
+          const int j = key0 + (i * W + warp) * KT + lane;
           if (j >= first && j < key1) atomicOr(a.err, kErrBadPage);   // no such page: read as zeros
         }
         const uint32_t st = ring + (uint32_t)((i % ST) * S::kStageBytes);
         constexpr int RPI = 32 / CPR;   // rows of one warp-wide copy
 #pragma unroll
-        for (int p = 0; p < 16 / RPI; ++p) {
+        for (int p = 0; p < KT / RPI; ++p) {
           const int row = p * RPI + lane / CPR, ch = lane % CPR;
           const int64_t k_at = __shfl_sync(0xffffffffu, ko, row);
           const int64_t v_at = a.same_strides ? k_at : __shfl_sync(0xffffffffu, vo, row);
           const bool on = k_at >= 0;
           cp_async16(st + swz<CPR>(row, ch),
                      static_cast<const char*>(a.kv.k) + (on ? k_at + ch * 16 : 0), on);
-          cp_async16(st + 16 * S::kRow + swz<CPR>(row, ch),
+          cp_async16(st + KT * S::kRow + swz<CPR>(row, ch),
                      static_cast<const char*>(a.kv.v) + (on ? v_at + ch * 16 : 0), on);
         }
       }
@@ -280,56 +299,69 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kWarps * 32, 1) k_attend(con
       cp_async_wait<ST - 2>();
       __syncwarp();
       const uint32_t st = ring + (uint32_t)((i % ST) * S::kStageBytes);
-      // s^T = k q^T: 16 keys
-      float s[NG][4];
+      // s^T = k q^T: 16 keys a tile
+      float s[NG][NH][4];
 #pragma unroll
-      for (int g = 0; g < NG; ++g) s[g][0] = s[g][1] = s[g][2] = s[g][3] = 0.f;
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int h = 0; h < NH; ++h) s[g][h][0] = s[g][h][1] = s[g][h][2] = s[g][h][3] = 0.f;
       if constexpr (!F8) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          uint32_t k[4];   // keys 0-7 and 8-15 of dims 0-7, then of dims 8-15
-          ldmatrix4(k, st + swz<CPR>(krow, 2 * ks + half));
+        for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-          for (int g = 0; g < NG; ++g)
-            mma_bf16(s[g], k[0], k[1], k[2], k[3], q[g][ks][0], q[g][ks][1]);
-        }
-      } else {
-#pragma unroll
-        for (int ks = 0; ks < KS; ks += 2) {
-          uint32_t k[4];   // keys 0-7 and 8-15 of 16 dims, then of the next 16
-          ldmatrix4(k, st + swz<CPR>(krow, ks + half));
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t a0 = e4m3x2_to_f16x2(k[2 * e]), a1 = e4m3x2_to_f16x2(k[2 * e + 1]);
-            const uint32_t a2 = e4m3x2_to_f16x2(k[2 * e] >> 16), a3 = e4m3x2_to_f16x2(k[2 * e + 1] >> 16);
+          for (int h = 0; h < NH; ++h) {
+            uint32_t k[4];   // keys 0-7 and 8-15 of dims 0-7, then of dims 8-15
+            ldmatrix4(k, st + swz<CPR>(16 * h + krow, 2 * ks + half));
 #pragma unroll
             for (int g = 0; g < NG; ++g)
-              mma_f16(s[g], a0, a1, a2, a3, q[g][ks + e][0], q[g][ks + e][1]);
+              mma_bf16(s[g][h], k[0], k[1], k[2], k[3], q[g][ks][0], q[g][ks][1]);
           }
-        }
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < KS; ks += 2)
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            uint32_t k[4];   // keys 0-7 and 8-15 of 16 dims, then of the next 16
+            ldmatrix4(k, st + swz<CPR>(16 * h + krow, ks + half));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_to_f16(k[2 * e], a0, a2);
+              e4m3x4_to_f16(k[2 * e + 1], a1, a3);
+#pragma unroll
+              for (int g = 0; g < NG; ++g)
+                mma_f16(s[g][h], a0, a1, a2, a3, q[g][ks + e][0], q[g][ks + e][1]);
+            }
+          }
       }
-      // the next copies go into the stage that the previous sub-tile has left
+      // the next copies go into the stage that the previous step has left
       fetch(i + ST - 1);
       look_up(i + ST);
-      // scores in log2 units: key j0 + r (elements 0, 1) and j0 + r + 8; keys outside [first, key1)
+      // scores in log2 units: key j0 + 16 h + r (elements 0, 1) and + 8; keys outside [first, key1)
       // do not count
-      const int j0 = key0 + (i * W + warp) * 16;
+      const int j0 = key0 + (i * W + warp) * KT;
       bool up = false;
       float top[NG][2];
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[g][e] *= sl[g][e & 1];
-        if (j0 < first || j0 + 16 > key1) {
+        for (int h = 0; h < NH; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = j0 + r + (e >> 1) * 8;
-            if (j < first || j >= key1) s[g][e] = -INFINITY;
-          }
+          for (int e = 0; e < 4; ++e) s[g][h][e] *= sl[g][e & 1];
+        if (j0 < first || j0 + KT > key1) {
+#pragma unroll
+          for (int h = 0; h < NH; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = j0 + 16 * h + r + (e >> 1) * 8;
+              if (j < first || j >= key1) s[g][h][e] = -INFINITY;
+            }
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float t = fmaxf(s[g][e], s[g][2 + e]);
+          float t = fmaxf(s[g][0][e], s[g][0][2 + e]);
+#pragma unroll
+          for (int h = 1; h < NH; ++h) t = fmaxf(t, fmaxf(s[g][h][e], s[g][h][2 + e]));
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
           top[g][e] = t;
@@ -354,56 +386,66 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kWarps * 32, 1) k_attend(con
           }
         }
       }
-      uint32_t p[NG][2], rest[NG][2];   // p^T: columns heads, rows keys 0-7 and 8-15
+      uint32_t p[NG][NH][2], rest[NG][NH][2];   // p^T: columns heads, rows keys 0-7 and 8-15 of a tile
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float base = m[g][e] == -INFINITY ? 0.f : m[g][e];   // no key yet: every p is 0
-          s[g][e] = exp2_fast(s[g][e] - base);
-          s[g][2 + e] = exp2_fast(s[g][2 + e] - base);
-          l[g][e] += s[g][e] + s[g][2 + e];
-        }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if constexpr (F8) {
-            p[g][h] = transpose8(pack_f16(s[g][2 * h], s[g][2 * h + 1]));
-          } else {
-            const uint32_t v = pack_bf16(s[g][2 * h], s[g][2 * h + 1]);
-            p[g][h] = transpose8(v);
-            rest[g][h] = transpose8(pack_bf16(s[g][2 * h] - bf16_lo(v), s[g][2 * h + 1] - bf16_hi(v)));
+          for (int h = 0; h < NH; ++h) {
+            s[g][h][e] = exp2_fast(s[g][h][e] - base);
+            s[g][h][2 + e] = exp2_fast(s[g][h][2 + e] - base);
+            l[g][e] += s[g][h][e] + s[g][h][2 + e];
           }
         }
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float p0 = s[g][h][2 * x], p1 = s[g][h][2 * x + 1];
+            if constexpr (F8) {
+              p[g][h][x] = transpose8(pack_f16(p0, p1));
+            } else {
+              const uint32_t v = pack_bf16(p0, p1);
+              p[g][h][x] = transpose8(v);
+              rest[g][h][x] = transpose8(pack_bf16(p0 - bf16_lo(v), p1 - bf16_hi(v)));
+            }
+          }
       }
       // o^T += v^T p^T: 16 dims at a time
-      const uint32_t vs = st + 16 * S::kRow;
+      const uint32_t vs = st + KT * S::kRow;
       if constexpr (!F8) {
         const int vrow = half * 8 + (lane & 7), vch = (lane >> 3) & 1;
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          uint32_t v[4];   // dims 0-7 and 8-15 of keys 0-7, then of keys 8-15
-          ldmatrix4_trans(v, vs + swz<CPR>(vrow, 2 * t + vch));
+        for (int t = 0; t < MT; ++t)
 #pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            mma_bf16(o[g][t], v[0], v[1], v[2], v[3], p[g][0], p[g][1]);
-            mma_bf16(o[g][t], v[0], v[1], v[2], v[3], rest[g][0], rest[g][1]);
+          for (int h = 0; h < NH; ++h) {
+            uint32_t v[4];   // dims 0-7 and 8-15 of keys 0-7, then of keys 8-15
+            ldmatrix4_trans(v, vs + swz<CPR>(16 * h + vrow, 2 * t + vch));
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+              mma_bf16(o[g][t], v[0], v[1], v[2], v[3], p[g][h][0], p[g][h][1]);
+              mma_bf16(o[g][t], v[0], v[1], v[2], v[3], rest[g][h][0], rest[g][h][1]);
+            }
           }
-        }
       } else {
 #pragma unroll
-        for (int t = 0; t < MT; t += 2) {
-          uint32_t v[4];   // keys 0-7 and 8-15 of 16 dims, then of the next 16
-          ldmatrix4_trans(v, vs + swz<CPR>(krow, t + half));
+        for (int t = 0; t < MT; t += 2)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            // (key, dim d), (key, d + 1), (key + 1, d), (key + 1, d + 1): rows 0-7 take the even dims
-            const uint32_t x = __byte_perm(v[2 * e], 0, 0x3120), y = __byte_perm(v[2 * e + 1], 0, 0x3120);
-            const uint32_t a0 = e4m3x2_to_f16x2(x), a1 = e4m3x2_to_f16x2(x >> 16);
-            const uint32_t a2 = e4m3x2_to_f16x2(y), a3 = e4m3x2_to_f16x2(y >> 16);
+          for (int h = 0; h < NH; ++h) {
+            uint32_t v[4];   // keys 0-7 and 8-15 of 16 dims, then of the next 16
+            ldmatrix4_trans(v, vs + swz<CPR>(16 * h + krow, t + half));
 #pragma unroll
-            for (int g = 0; g < NG; ++g) mma_f16(o[g][t + e], a0, a1, a2, a3, p[g][0], p[g][1]);
+            for (int e = 0; e < 2; ++e) {
+              // (key, dim d), (key, d + 1), (key + 1, d), (key + 1, d + 1): rows 0-7 take the even dims
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_to_f16(__byte_perm(v[2 * e], 0, 0x3120), a0, a1);
+              e4m3x4_to_f16(__byte_perm(v[2 * e + 1], 0, 0x3120), a2, a3);
+#pragma unroll
+              for (int g = 0; g < NG; ++g) mma_f16(o[g][t + e], a0, a1, a2, a3, p[g][h][0], p[g][h][1]);
+            }
           }
-        }
       }
       __syncwarp();   // every lane has read the stage before it is filled again
     }
@@ -434,32 +476,43 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kWarps * 32, 1) k_attend(con
       }
     }
     __syncthreads();
-    const bool whole = n_units == units;
-    const int64_t part = 2 * (int64_t)blockIdx.x + (u == quota * blockIdx.x ? 0 : 1);
-    for (int x = threadIdx.x; x < G * D; x += W * 32) {
-      const int g = x / D, d = x - g * D;
-      float top = -INFINITY;
+    // the warps' factors and the joined maximum and sum of each head
+    if (threadIdx.x < 16) {
+      const int g = threadIdx.x;
+      float top = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < W; ++w) top = fmaxf(top, wm[w][g]);
+      for (int w = 0; w < W; ++w) top = fmaxf(top, g < G ? wm[w][g] : -INFINITY);
       const float base = top == -INFINITY ? 0.f : top;
-      float sum = 0.f, v = 0.f;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        const float f = exp2_fast(wm[w][g] - base);
-        sum = fmaf(f, wl[w][g], sum);
-        v = fmaf(f, reinterpret_cast<const float*>(smem)[(size_t)(w * (8 * NG) + g) * LD + d], v);
+        const float f = g < G ? exp2_fast(wm[w][g] - base) : 0.f;
+        wm[w][g] = f;
+        sum = fmaf(f, g < G ? wl[w][g] : 0.f, sum);
       }
+      joined[g] = make_float2(top, sum);
+    }
+    __syncthreads();
+    const bool whole = n_units == units;
+    const int64_t part = 2 * (int64_t)blockIdx.x + (u == quota * blockIdx.x ? 0 : 1);
+    for (int x = threadIdx.x; x < G * (D / 4); x += W * 32) {   // four dims of a head
+      const int g = x / (D / 4), d = (x - g * (D / 4)) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float f = wm[w][g];
+        const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem) +
+                                                          (size_t)(w * (8 * NG) + g) * LD + d);
+        v.x = fmaf(f, y.x, v.x); v.y = fmaf(f, y.y, v.y);
+        v.z = fmaf(f, y.z, v.z); v.w = fmaf(f, y.w, v.w);
+      }
+      const float2 ms = joined[g];
       const int64_t row = (int64_t)b * a.Hq + kvh * a.group + g0 + g;
       if (whole) {
-        const float y = sum == 0.f ? 0.f : v / sum * a.kv.v_scale;   // no weight at all: zeros
-        a.out[row * D + d] = (uint16_t)(pack_bf16(y, 0.f) & 0xFFFFu);
-        if (d == 0 && a.lse) a.lse[row] = (top + log2f(sum)) * kLn2;
+        store_row(a, row * D + d, v, ms.y);
+        if (d == 0 && a.lse) a.lse[row] = (ms.x + log2f(ms.y)) * kLn2;
       } else {
-        a.part_o[(part * 16 + g) * D + d] = v;
-        if (d == 0) {
-          a.part_ml[(part * 16 + g) * 2] = top;
-          a.part_ml[(part * 16 + g) * 2 + 1] = sum;
-        }
+        *reinterpret_cast<float4*>(a.part_o + (part * 16 + g) * D + d) = v;
+        if (d == 0) *reinterpret_cast<float2*>(a.part_ml + (part * 16 + g) * 2) = ms;
       }
     }
     __syncthreads();   // before the ring is filled again
@@ -467,58 +520,88 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kWarps * 32, 1) k_attend(con
   }
 }
 
-// One warp per (sequence, query head) that k_attend has not finished: its pieces in order, or
-// zeros for an empty sequence.
-constexpr int kJoinWarps = 4;
+// Segments that several runs share, and empty sequences. Block (i, g): head g of the segment that the
+// beginning of run i falls inside, if no earlier run begins inside it; its pieces in order, eight warps
+// a share of them each. The blocks also zero the heads of empty sequences.
+constexpr int kJoinWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) k_join(const AttendArgs a, int grid) {
+__global__ void __launch_bounds__(kJoinWarps * 32) k_join(const AttendArgs a) {
+  constexpr int E = D / 32;
+  __shared__ __align__(16) float sums[kJoinWarps][D];
+  __shared__ float wm[kJoinWarps], wl[kJoinWarps];
   griddep_launch_dependents();
   griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-  if (row >= (int64_t)a.B * a.Hq) return;
-  const int b = (int)(row / a.Hq), head = (int)(row - (int64_t)b * a.Hq);
-  constexpr int E = D / 32;
-  const int units = a.plan[b + 1] - a.plan[b];
-  if (units == 0) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) a.out[row * D + lane + 32 * e] = 0;
-    if (lane == 0 && a.lse) a.lse[row] = -INFINITY;
-    return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (blockIdx.y == 0) {
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+      if (a.seq_lens[b] > 0) continue;
+      for (int x = threadIdx.x; x < a.Hq * D / 8; x += kJoinWarps * 32)
+        reinterpret_cast<uint4*>(a.out + (int64_t)b * a.Hq * D)[x] = make_uint4(0, 0, 0, 0);
+      if (a.lse)
+        for (int x = threadIdx.x; x < a.Hq; x += kJoinWarps * 32)
+          a.lse[(int64_t)b * a.Hq + x] = -INFINITY;
+    }
   }
   const int HS = a.kv.Hkv * a.gt;
   const int64_t total = (int64_t)a.plan[a.B] * HS;
-  const int64_t quota = (total + grid - 1) / grid;
-  const int kvh = head / a.group, in = head - kvh * a.group;
-  const int hs = kvh * a.gt + in / 16, g = in % 16;
-  const int64_t s0 = (int64_t)a.plan[b] * HS + (int64_t)hs * units, s1 = s0 + units;
-  const int64_t first = s0 / quota, last = (s1 - 1) / quota;   // blocks with a piece of it
-  if (first == last) return;   // one piece: k_attend has finished it
-  float m = -INFINITY;
-  for (int64_t p = first + lane; p <= last; p += 32) {
-    const int64_t part = 2 * p + (p * quota >= s0 ? 0 : 1);
-    m = fmaxf(m, a.part_ml[(part * 16 + g) * 2]);
+  const int64_t quota = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t u = quota * blockIdx.x;
+  if (blockIdx.x == 0 || u >= total) return;
+  int lo = 0, hi = a.B;   // plan[lo] * HS <= u < plan[hi] * HS
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((int64_t)a.plan[mid] * HS <= u) lo = mid;
+    else hi = mid;
   }
-  m = warp_max(m);
-  const float base = m == -INFINITY ? 0.f : m;
+  const int b = lo;
+  const int64_t before = (int64_t)a.plan[b] * HS;
+  const int units = a.plan[b + 1] - a.plan[b];
+  const int hs = (int)((u - before) / units);
+  const int64_t s0 = before + (int64_t)hs * units, s1 = s0 + units;
+  if (s0 == u || u - quota > s0) return;   // no run ends inside it, or an earlier block has it
+  const int kvh = hs / a.gt, g0 = (hs - kvh * a.gt) * 16, g = blockIdx.y;
+  if (g0 + g >= a.group) return;
+  const int first = (int)(s0 / quota), last = (int)((s1 - 1) / quota);   // runs with a piece of it
+  auto part = [&](int p) { return (2 * (int64_t)p + ((int64_t)p * quota >= s0 ? 0 : 1)) * 16 + g; };
+  float m = -INFINITY;
+  for (int p = first + warp; p <= last; p += kJoinWarps) m = fmaxf(m, a.part_ml[part(p) * 2]);
   float l = 0.f, v[E];
+  const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
   for (int e = 0; e < E; ++e) v[e] = 0.f;
 #pragma unroll 4
-  for (int64_t p = first; p <= last; ++p) {
-    const int64_t part = 2 * p + (p * quota >= s0 ? 0 : 1);
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (part * 16 + g) * 2);
+  for (int p = first + warp; p <= last; p += kJoinWarps) {
+    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + part(p) * 2);
     const float f = exp2_fast(ml.x - base);
     l = fmaf(f, ml.y, l);
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      v[e] = fmaf(f, a.part_o[(part * 16 + g) * D + lane + 32 * e], v[e]);
+    for (int e = 0; e < E; ++e) v[e] = fmaf(f, a.part_o[part(p) * D + lane + 32 * e], v[e]);
   }
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    a.out[row * D + lane + 32 * e] =
-        (uint16_t)(pack_bf16(l == 0.f ? 0.f : v[e] / l * a.kv.v_scale, 0.f) & 0xFFFFu);
-  if (lane == 0 && a.lse) a.lse[row] = (m + log2f(l)) * kLn2;
+  for (int e = 0; e < E; ++e) sums[warp][lane + 32 * e] = v[e];
+  if (lane == 0) {
+    wm[warp] = m;
+    wl[warp] = l;
+  }
+  __syncthreads();
+  if (threadIdx.x >= D / 4) return;
+  const int d = threadIdx.x * 4;
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, wm[w]);
+  const float from = top == -INFINITY ? 0.f : top;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const float f = exp2_fast(wm[w] - from);
+    sum = fmaf(f, wl[w], sum);
+    const float4 x = *reinterpret_cast<const float4*>(&sums[w][d]);
+    y.x = fmaf(f, x.x, y.x); y.y = fmaf(f, x.y, y.y);
+    y.z = fmaf(f, x.z, y.z); y.w = fmaf(f, x.w, y.w);
+  }
+  const int64_t row = (int64_t)b * a.Hq + kvh * a.group + g0 + g;
+  store_row(a, row * D + d, y, sum);
+  if (d == 0 && a.lse) a.lse[row] = (top + log2f(sum)) * kLn2;
 }
 
 template <int D, bool F8, int NG>
@@ -541,10 +624,10 @@ cudaError_t launch_d(const AttendArgs& a, int num_sms, cudaStream_t stream) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, k_attend<D, F8, NG>, a)) != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)(((int64_t)a.B * a.Hq + kJoinWarps - 1) / kJoinWarps));
+  cfg.gridDim = dim3((unsigned)num_sms, (unsigned)(a.group < 16 ? a.group : 16));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, k_join<D>, a, num_sms);
+  return cudaLaunchKernelEx(&cfg, k_join<D>, a);
 }
 
 template <int D>
