@@ -41,9 +41,10 @@ struct AttnShape {
   static constexpr int kCpr = kRow / 16;              // 16-byte pieces of it
   static constexpr int kKeys = kRow <= 128 ? 32 : 16; // keys of a warp's step
   static constexpr int kStageBytes = 2 * kKeys * kRow;   // those keys and values
-  // warps: enough to hide each other's latencies, three stages each
-  static constexpr int kWarps = kRow >= 512 ? 4 : kRow >= 128 ? 8 : 16;
-  static constexpr int kStages = 192 * 1024 / (kWarps * kStageBytes);
+  // two blocks an SM where their rings fit: one streams while the other joins a piece's warps
+  static constexpr int kBlocks = kRow >= 512 ? 1 : 2;
+  static constexpr int kWarps = kRow >= 128 ? 4 : 8;
+  static constexpr int kStages = 192 * 1024 / (kBlocks * kWarps * kStageBytes);
   static constexpr int kUnit = kKeys * kWarps;        // keys of a unit
   static constexpr int kRing = kWarps * kStages * kStageBytes;
 };
@@ -95,7 +96,7 @@ __device__ __forceinline__ void span(int len, int window, int unit, int& first, 
 }
 
 template <int D, bool F8, int NG>
-__global__ void __launch_bounds__(AttnShape<D, F8>::kWarps * 32, 1) k_attend(const AttendArgs a) {
+__global__ void __launch_bounds__(AttnShape<D, F8>::kWarps * 32, AttnShape<D, F8>::kBlocks) k_attend(const AttendArgs a) {
   using S = AttnShape<D, F8>;
   constexpr int W = S::kWarps, ST = S::kStages, CPR = S::kCpr, KS = D / 16, MT = D / 16;
   constexpr int KT = S::kKeys, NH = KT / 16;   // keys of a step, in 16-row tiles
@@ -124,10 +125,6 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kWarps * 32, 1) k_attend(con
       if (lane >= o) inc += v;
     }
     all = __shfl_sync(0xffffffffu, inc, 31);
-    if (blockIdx.x == 0 && warp == 0) {   // the plan, for k_join
-      if (lane < a.B) a.plan[lane + 1] = inc;
-      if (lane == 0) a.plan[0] = 0;
-    }
   } else {
     const int per = (a.B + W * 32 - 1) / (W * 32);
     const int b0 = threadIdx.x * per;
@@ -156,14 +153,13 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kWarps * 32, 1) k_attend(con
     if (b0 < a.B && b0 + per >= a.B) cum[a.B] = at;
     __syncthreads();
     all = cum[a.B];
-    if (blockIdx.x == 0)
-      for (int b = threadIdx.x; b <= a.B; b += W * 32) a.plan[b] = cum[b];
   }
   const int64_t total = (int64_t)all * HS;
   const int64_t quota = (total + gridDim.x - 1) / gridDim.x;
   int64_t u = quota * blockIdx.x;
   const int64_t u_end = min(u + quota, total);
   const uint32_t ring = smem_addr(smem) + (uint32_t)(warp * ST * S::kStageBytes);
+  if (u >= u_end && threadIdx.x == 0) a.shared_segs[blockIdx.x] = make_int4(-1, 0, 0, 0);
 
   while (u < u_end) {
     // the piece that begins at u: sequence b, with `before` units ahead of it
@@ -191,6 +187,13 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kWarps * 32, 1) k_attend(con
     const int n_units = (int)min((int64_t)(units - u0), u_end - u);
     const int kvh = hs / a.gt, g0 = (hs - kvh * a.gt) * 16;
     const int G = min(a.group - g0, 16);
+    if (u == quota * blockIdx.x && threadIdx.x == 0) {
+      // for k_join: a segment that runs share belongs to the first run that begins inside it
+      const int64_t s0 = u - u0, s1 = s0 + units;
+      const bool mine = u0 > 0 && u - quota <= s0;
+      a.shared_segs[blockIdx.x] =
+          make_int4(mine ? b : -1, hs, (int)(s0 / quota) * 2 + (s0 % quota != 0), (int)((s1 - 1) / quota));
+    }
     const int key0 = (first / S::kUnit + u0) * S::kUnit;
     const int key1 = min(len, key0 + n_units * S::kUnit);   // keys of the piece: [key0, key1)
 
@@ -520,19 +523,20 @@ __global__ void __launch_bounds__(AttnShape<D, F8>::kWarps * 32, 1) k_attend(con
   }
 }
 
-// Segments that several runs share, and empty sequences. Block (i, g): head g of the segment that the
-// beginning of run i falls inside, if no earlier run begins inside it; its pieces in order, eight warps
-// a share of them each. The blocks also zero the heads of empty sequences.
+// Segments that several runs share, and empty sequences. Block (i, g): head g of the segment that run i
+// has left for it, if any; its pieces in order, eight warps a share of them each, joined in order. The
+// blocks also zero the heads of empty sequences.
 constexpr int kJoinWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_join(const AttendArgs a) {
-  constexpr int E = D / 32;
   __shared__ __align__(16) float sums[kJoinWarps][D];
   __shared__ float wm[kJoinWarps], wl[kJoinWarps];
   griddep_launch_dependents();
   griddep_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (blockIdx.y == 0) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = blockIdx.y;
+  // sequence or -1, part of its heads, first run (* 2, + 1 where it begins inside that run), last run
+  const int4 seg = a.shared_segs[blockIdx.x];
+  if (g == 0) {
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
       if (a.seq_lens[b] > 0) continue;
       for (int x = threadIdx.x; x < a.Hq * D / 8; x += kJoinWarps * 32)
@@ -542,40 +546,27 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_join(const AttendArgs a) {
           a.lse[(int64_t)b * a.Hq + x] = -INFINITY;
     }
   }
-  const int HS = a.kv.Hkv * a.gt;
-  const int64_t total = (int64_t)a.plan[a.B] * HS;
-  const int64_t quota = (total + gridDim.x - 1) / gridDim.x;
-  const int64_t u = quota * blockIdx.x;
-  if (blockIdx.x == 0 || u >= total) return;
-  int lo = 0, hi = a.B;   // plan[lo] * HS <= u < plan[hi] * HS
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if ((int64_t)a.plan[mid] * HS <= u) lo = mid;
-    else hi = mid;
-  }
-  const int b = lo;
-  const int64_t before = (int64_t)a.plan[b] * HS;
-  const int units = a.plan[b + 1] - a.plan[b];
-  const int hs = (int)((u - before) / units);
-  const int64_t s0 = before + (int64_t)hs * units, s1 = s0 + units;
-  if (s0 == u || u - quota > s0) return;   // no run ends inside it, or an earlier block has it
-  const int kvh = hs / a.gt, g0 = (hs - kvh * a.gt) * 16, g = blockIdx.y;
+  if (seg.x < 0) return;
+  const int kvh = seg.y / a.gt, g0 = (seg.y - kvh * a.gt) * 16;
   if (g0 + g >= a.group) return;
-  const int first = (int)(s0 / quota), last = (int)((s1 - 1) / quota);   // runs with a piece of it
-  auto part = [&](int p) { return (2 * (int64_t)p + ((int64_t)p * quota >= s0 ? 0 : 1)) * 16 + g; };
-  float m = -INFINITY;
-  for (int p = first + warp; p <= last; p += kJoinWarps) m = fmaxf(m, a.part_ml[part(p) * 2]);
-  float l = 0.f, v[E];
-  const float base = m == -INFINITY ? 0.f : m;
+  constexpr int E = D / 32;
+  float m = -INFINITY, l = 0.f, v[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) v[e] = 0.f;
-#pragma unroll 4
-  for (int p = first + warp; p <= last; p += kJoinWarps) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + part(p) * 2);
-    const float f = exp2_fast(ml.x - base);
-    l = fmaf(f, ml.y, l);
+#pragma unroll 2
+  for (int p = (seg.z >> 1) + warp; p <= seg.w; p += kJoinWarps) {
+    // a run's first piece, but for a segment that begins inside its first run
+    const int64_t at = (2 * (int64_t)p + (p == seg.z >> 1 ? seg.z & 1 : 0)) * 16 + g;
+    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+    float y[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = fmaf(f, a.part_o[part(p) * D + lane + 32 * e], v[e]);
+    for (int e = 0; e < E; ++e) y[e] = a.part_o[at * D + lane + 32 * e];
+    const float n = fmaxf(m, ml.x), base = n == -INFINITY ? 0.f : n;
+    const float f0 = exp2_fast(m - base), f1 = exp2_fast(ml.x - base);
+    m = n;
+    l = fmaf(l, f0, ml.y * f1);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = fmaf(v[e], f0, y[e] * f1);
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) sums[warp][lane + 32 * e] = v[e];
@@ -599,7 +590,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_join(const AttendArgs a) {
     y.x = fmaf(f, x.x, y.x); y.y = fmaf(f, x.y, y.y);
     y.z = fmaf(f, x.z, y.z); y.w = fmaf(f, x.w, y.w);
   }
-  const int64_t row = (int64_t)b * a.Hq + kvh * a.group + g0 + g;
+  const int64_t row = (int64_t)seg.x * a.Hq + kvh * a.group + g0 + g;
   store_row(a, row * D + d, y, sum);
   if (d == 0 && a.lse) a.lse[row] = (top + log2f(sum)) * kLn2;
 }
@@ -614,7 +605,8 @@ cudaError_t launch_d(const AttendArgs& a, int num_sms, cudaStream_t stream) {
                                 (int)smem)) != cudaSuccess)
     return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)num_sms);
+  const int grid = S::kBlocks * num_sms;
+  cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(S::kWarps * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -624,7 +616,7 @@ cudaError_t launch_d(const AttendArgs& a, int num_sms, cudaStream_t stream) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, k_attend<D, F8, NG>, a)) != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)num_sms, (unsigned)(a.group < 16 ? a.group : 16));
+  cfg.gridDim = dim3((unsigned)grid, (unsigned)(a.group < 16 ? a.group : 16));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, k_join<D>, a);

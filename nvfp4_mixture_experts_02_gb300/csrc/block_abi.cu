@@ -144,7 +144,7 @@ ft_status ft_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, i
 size_t ft_paged_attention_workspace_bytes(int32_t B, int32_t D) {
   if (B < 1 || B > kMaxSeqs || (D != 64 && D != 128 && D != 256)) return 0;
   const int sms = device_sms();
-  return sms > 0 ? AttendLayout(B, D, sms).total : 0;
+  return sms > 0 ? AttendLayout(D, sms).total : 0;
 }
 
 ft_status ft_paged_decode_attention(const uint16_t* q, int64_t q_stride, int32_t B, int32_t Hq,
@@ -163,10 +163,10 @@ ft_status ft_paged_decode_attention(const uint16_t* q, int64_t q_stride, int32_t
   if (!aligned(q, 16) || q_stride % 8 != 0 || !aligned(out, 16) || !aligned(lse, 4) ||
       !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(workspace, 256))
     return FT_ERR_MISALIGNED;
-  if (workspace_bytes < AttendLayout(B, cache->D, 1).total) return FT_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < AttendLayout(cache->D, 1).total) return FT_ERR_WORKSPACE_TOO_SMALL;
   const int sms = device_sms();
   if (sms <= 0) return FT_ERR_CUDA;
-  const AttendLayout L(B, cache->D, sms);
+  const AttendLayout L(cache->D, sms);
   if (workspace_bytes < L.total) return FT_ERR_WORKSPACE_TOO_SMALL;
   char* ws = static_cast<char*>(workspace);
   AttendArgs a = {};
@@ -174,7 +174,7 @@ ft_status ft_paged_decode_attention(const uint16_t* q, int64_t q_stride, int32_t
   a.block_table = block_table; a.seq_lens = seq_lens; a.table_width = table_width;
   a.scale = scale; a.window = window; a.out = out; a.lse = lse;
   a.err = reinterpret_cast<int*>(ws);
-  a.plan = reinterpret_cast<int*>(ws + L.plan);
+  a.shared_segs = reinterpret_cast<int4*>(ws + L.segs);
   a.part_ml = reinterpret_cast<float*>(ws + L.ml);
   a.part_o = reinterpret_cast<float*>(ws + L.o);
   return cuda_status(launch_attend(a, sms, static_cast<cudaStream_t>(stream)));

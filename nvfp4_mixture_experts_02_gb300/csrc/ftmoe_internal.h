@@ -154,8 +154,8 @@ struct AttendArgs {
   int window;
   uint16_t* out;
   float* lse;
-  int* err;                // workspace: error word, plan [B + 1], pieces' (max, sum) and sums
-  int* plan;
+  int* err;                // workspace: error word, shared segments [run], pieces' (max, sum) and sums
+  int4* shared_segs;
   float *part_ml, *part_o;
   int group, gt;           // query heads per key head, 16-head parts of them (set by the launch)
   int same_strides;        // keys and values lie alike (set by the launch)
@@ -163,12 +163,12 @@ struct AttendArgs {
 };
 // Workspace regions (byte offsets, 256-byte aligned).
 struct AttendLayout {
-  size_t plan = 0, ml = 0, o = 0, total = 0;
-  AttendLayout(int B, int D, int num_sms) {
-    plan = 1024;
-    ml = align_up(plan + (size_t)(B + 1) * 4, 256);
-    o = align_up(ml + (size_t)num_sms * 2 * 16 * 2 * 4, 256);
-    total = align_up(o + (size_t)num_sms * 2 * 16 * D * 4, 256);
+  size_t segs = 0, ml = 0, o = 0, total = 0;
+  AttendLayout(int D, int num_sms) {
+    segs = 1024;
+    ml = align_up(segs + (size_t)num_sms * 2 * 16, 256);
+    o = align_up(ml + (size_t)num_sms * 4 * 16 * 2 * 4, 256);   // two blocks an SM, two pieces each
+    total = align_up(o + (size_t)num_sms * 4 * 16 * D * 4, 256);
   }
 };
 cudaError_t launch_attend(const AttendArgs& a, int num_sms, cudaStream_t stream);

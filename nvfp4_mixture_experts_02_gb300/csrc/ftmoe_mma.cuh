@@ -85,12 +85,16 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return d;
 }
 
-__device__ __forceinline__ void load8(const uint16_t* p, float (&f)[8]) {   // 8 bf16, read once
+__device__ __forceinline__ uint4 ld16(const void* p) {   // 16 bytes, read once
   uint4 v;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-      : "l"(p)
-      : "memory");
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void load8(const uint16_t* p, float (&f)[8]) {   // 8 bf16, read once
+  const uint4 v = ld16(p);
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {

@@ -5,10 +5,11 @@
 //   cache    page = block_table[seq][position / page_size], slot = position % page_size;
 //            bf16, or E4M3 of the value times 1 / scale, saturated at +-448
 //
-// One thread takes two 8-element pieces of one head: a pair of pieces R/2 apart, which rotate into
-// each other, or two neighbours past R. Products and sums are rounded one by one (no fused
-// multiply-add), so that a value on the edge between two E4M3 codes falls as plain float32
-// arithmetic lets it fall.
+// One block takes a token, one thread two 8-element pieces of one head at a time: a pair of pieces R/2
+// apart, which rotate into each other, or two neighbours past R; the values of four such items are on
+// their way before the token's page is known. Products and sums are rounded one by one (no fused
+// multiply-add), so that a value on the edge between two E4M3 codes falls as plain float32 arithmetic
+// lets it fall. Bound by memory: every value is read once and written once.
 #include <cuda_runtime.h>
 
 #include "ftmoe_internal.h"
@@ -18,7 +19,8 @@ namespace ftmoe {
 
 namespace {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
+constexpr int kAppendItems = 4;   // items of a thread whose loads are in flight together
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   uint16_t lo, hi;
@@ -40,94 +42,121 @@ __device__ __forceinline__ void store_cache(void* base, int64_t at, bool f8, flo
   }
 }
 
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = bf16_lo(w[j]);
+    f[2 * j + 1] = bf16_hi(w[j]);
+  }
+}
+
+struct Item {   // a head of q, k or v (kind 0, 1, 2) and its two pieces
+  int kind, head, c0, c1;
+  bool turn;
+  __device__ __forceinline__ Item(const AppendArgs& a, int id) {
+    const int per_head = a.kv.D / 16;
+    const int row = id / per_head, item = id - row * per_head;
+    kind = row < a.Hq ? 0 : row < a.Hq + a.kv.Hkv ? 1 : 2;
+    head = kind == 0 ? row : kind == 1 ? row - a.Hq : row - a.Hq - a.kv.Hkv;
+    const int pairs = kind == 2 ? 0 : a.rope_dim / 16;
+    turn = item < pairs;
+    c0 = turn ? 8 * item : kind == 2 ? 16 * item : a.rope_dim + 16 * (item - pairs);
+    c1 = turn ? c0 + a.rope_dim / 2 : c0 + 8;
+  }
+};
+
 __global__ void __launch_bounds__(kAppendThreads) k_kv_append(const AppendArgs a) {
   griddep_launch_dependents();
   griddep_wait();
-  const int per_head = a.kv.D / 16;
-  const int heads = a.Hq + 2 * a.kv.Hkv;
-  const int64_t id = (int64_t)blockIdx.x * kAppendThreads + threadIdx.x;
-  const int64_t per_token = (int64_t)heads * per_head;
-  if (id >= per_token * a.T) return;
-  const int t = (int)(id / per_token);
-  const int rest = (int)(id - t * per_token);
-  const int head = rest / per_head, item = rest - head * per_head;
-  const int kind = head < a.Hq ? 0 : head < a.Hq + a.kv.Hkv ? 1 : 2;   // q, k, v
-  const int h = kind == 0 ? head : kind == 1 ? head - a.Hq : head - a.Hq - a.kv.Hkv;
-  const int pairs = kind == 2 ? 0 : a.rope_dim / 16;
-  const bool turn = item < pairs;
-  const int c0 = turn ? 8 * item : kind == 2 ? 16 * item : a.rope_dim + 16 * (item - pairs);
-  const int c1 = turn ? c0 + a.rope_dim / 2 : c0 + 8;
-
+  const int64_t t = blockIdx.x;
+  const int items = (a.Hq + 2 * a.kv.Hkv) * (a.kv.D / 16);
   const int pos = a.positions[t];
-  bool ok = pos >= 0;   // a negative position: a padding token, neither stored nor an error
-  if (ok && a.rope_dim > 0 && pos >= a.rope_rows) {
-    ok = false;
-    if (a.err) atomicOr(a.err, kErrBadPage);
-  }
+  const int seq = a.seq_ids ? a.seq_ids[t] : (int)t;
+  bool placed = pos >= 0;   // a negative position: a padding token, neither stored nor an error
+  bool found = false;
   int64_t page = 0;
-  if (ok && kind != 0) {
-    const int seq = a.seq_ids ? a.seq_ids[t] : t;
-    const int col = pos / a.kv.page_size;
-    ok = seq >= 0 && seq < a.B && col < a.table_width;
-    if (ok) {
-      page = a.block_table[(int64_t)seq * a.table_width + col];
-      ok = page >= 0 && page < a.kv.num_pages;
-    }
-    if (!ok && a.err) atomicOr(a.err, kErrBadPage);
-  }
-  uint16_t* qo = kind == 0 ? a.q_out + ((int64_t)t * a.Hq + h) * a.kv.D : nullptr;
-  if (!ok) {
-    if (kind == 0) {   // the query of a token without a position: zeros
-      *reinterpret_cast<uint4*>(qo + c0) = make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4*>(qo + c1) = make_uint4(0, 0, 0, 0);
-    }
-    return;
-  }
-  const uint16_t* src = (kind == 0 ? a.q + t * a.q_stride : kind == 1 ? a.k + t * a.k_stride
-                                                                      : a.v + t * a.v_stride) +
-                        (int64_t)h * a.kv.D;
-  float u[8], w[8];
-  load8(src + c0, u);
-  load8(src + c1, w);
-  if (turn) {
-    const float* rp = a.rope + (int64_t)pos * a.rope_dim + c0;
-    const int half = a.rope_dim / 2;
+  int slot = 0;
+  for (int id0 = threadIdx.x; id0 < items; id0 += kAppendThreads * kAppendItems) {
+    uint4 x[kAppendItems], y[kAppendItems];
 #pragma unroll
-    for (int j = 0; j < 8; j += 4) {
-      const float4 c = *reinterpret_cast<const float4*>(rp + j);
-      const float4 s = *reinterpret_cast<const float4*>(rp + half + j);
-      const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x = u[j + i], y = w[j + i];
-        u[j + i] = __fsub_rn(__fmul_rn(x, cc[i]), __fmul_rn(y, sn[i]));
-        w[j + i] = __fadd_rn(__fmul_rn(y, cc[i]), __fmul_rn(x, sn[i]));
+    for (int i = 0; i < kAppendItems; ++i) {
+      const int id = id0 + i * kAppendThreads;
+      if (id >= items) continue;
+      const Item it(a, id);
+      const uint16_t* src = (it.kind == 0 ? a.q + t * a.q_stride
+                             : it.kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride) +
+                            (int64_t)it.head * a.kv.D;
+      x[i] = ld16(src + it.c0);
+      y[i] = ld16(src + it.c1);
+    }
+    if (id0 == threadIdx.x) {   // the token's place, while the first values travel
+      if (placed && a.rope_dim > 0 && pos >= a.rope_rows) {
+        placed = false;
+        if (a.err && threadIdx.x == 0) atomicOr(a.err, kErrBadPage);
+      }
+      if (placed) {
+        const int col = pos / a.kv.page_size;
+        slot = pos - col * a.kv.page_size;
+        found = seq >= 0 && seq < a.B && col < a.table_width;
+        if (found) {
+          page = a.block_table[(int64_t)seq * a.table_width + col];
+          found = page >= 0 && page < a.kv.num_pages;
+        }
+        if (!found && a.err && threadIdx.x == 0) atomicOr(a.err, kErrBadPage);
       }
     }
-  }
-  if (kind == 0) {
-    store8(qo + c0, u);
-    store8(qo + c1, w);
-    return;
-  }
-  const int slot = pos % a.kv.page_size;
-  if (kind == 1) {
-    const int64_t at = page * a.kv.k_page_stride + slot * a.kv.k_slot_stride + h * a.kv.k_head_stride;
-    store_cache(a.kv.k, at + c0, a.kv.dtype == FT_KV_E4M3, a.inv_k, u);
-    store_cache(a.kv.k, at + c1, a.kv.dtype == FT_KV_E4M3, a.inv_k, w);
-  } else {
-    const int64_t at = page * a.kv.v_page_stride + slot * a.kv.v_slot_stride + h * a.kv.v_head_stride;
-    store_cache(a.kv.v, at + c0, a.kv.dtype == FT_KV_E4M3, a.inv_v, u);
-    store_cache(a.kv.v, at + c1, a.kv.dtype == FT_KV_E4M3, a.inv_v, w);
+#pragma unroll
+    for (int i = 0; i < kAppendItems; ++i) {
+      const int id = id0 + i * kAppendThreads;
+      if (id >= items) continue;
+      const Item it(a, id);
+      float u[8], w[8];
+      unpack8(x[i], u);
+      unpack8(y[i], w);
+      if (it.turn && placed) {
+        const float* rp = a.rope + (int64_t)pos * a.rope_dim + it.c0;
+        const int half = a.rope_dim / 2;
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+          const float4 c = *reinterpret_cast<const float4*>(rp + j);
+          const float4 s = *reinterpret_cast<const float4*>(rp + half + j);
+          const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float p = u[j + e], r = w[j + e];
+            u[j + e] = __fsub_rn(__fmul_rn(p, cc[e]), __fmul_rn(r, sn[e]));
+            w[j + e] = __fadd_rn(__fmul_rn(r, cc[e]), __fmul_rn(p, sn[e]));
+          }
+        }
+      }
+      if (it.kind == 0) {
+        uint16_t* to = a.q_out + (t * a.Hq + it.head) * a.kv.D;
+        if (!placed) {   // the query of a token without a position: zeros
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[j] = w[j] = 0.f;
+        }
+        store8(to + it.c0, u);
+        store8(to + it.c1, w);
+      } else if (found) {
+        const bool key = it.kind == 1;
+        const int64_t at =
+            key ? page * a.kv.k_page_stride + slot * a.kv.k_slot_stride + it.head * a.kv.k_head_stride
+                : page * a.kv.v_page_stride + slot * a.kv.v_slot_stride + it.head * a.kv.v_head_stride;
+        void* to = key ? a.kv.k : a.kv.v;
+        const float inv = key ? a.inv_k : a.inv_v;
+        store_cache(to, at + it.c0, a.kv.dtype == FT_KV_E4M3, inv, u);
+        store_cache(to, at + it.c1, a.kv.dtype == FT_KV_E4M3, inv, w);
+      }
+    }
   }
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
-  const int64_t items = (int64_t)a.T * (a.Hq + 2 * a.kv.Hkv) * (a.kv.D / 16);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((items + kAppendThreads - 1) / kAppendThreads));
+  cfg.gridDim = dim3((unsigned)a.T);
   cfg.blockDim = dim3(kAppendThreads);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
