@@ -686,20 +686,22 @@ _RES = (torch.bfloat16, torch.float32)
 def _need_rows(t, name, dev, inner):
     """t on cuda:dev, bf16 bits [T, *inner] whose rows are contiguous: the distance between rows
     may be larger than a row (a slice of a wider tensor). Returns it, in elements."""
+    shape = t.shape
     if t.get_device() != dev:
         raise ValueError(f"{name}: expected a tensor on cuda:{dev}, got one on {t.device}")
     if t.dtype not in BF16_BITS:
         raise TypeError(f"{name}: element type {t.dtype} is not accepted here")
-    if tuple(t.shape[1:]) != inner:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [T, {', '.join(map(str, inner))}]")
-    at = 1
-    for size, stride in zip(reversed(inner), reversed(t.stride()[1:])):
-        if stride != at and size != 1:
-            raise ValueError(f"{name}: the elements of a row must be contiguous")
-        at *= size
-    if t.shape[0] > 1 and t.stride(0) < at:
+    if shape[1:] != inner:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [T, {', '.join(map(str, inner))}]")
+    stride, last = t.stride(), inner[-1]
+    row = last if len(inner) == 1 else inner[0] * last
+    if (stride[-1] != 1 and last != 1) or (len(inner) == 2 and stride[1] != last and inner[0] != 1):
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if shape[0] <= 1:
+        return row
+    if stride[0] < row:
         raise ValueError(f"{name}: the rows must not overlap")
-    return t.stride(0) if t.shape[0] > 1 else at
+    return stride[0]
 
 
 def _scratch(n, dev, stream):
@@ -802,6 +804,7 @@ class PagedKVCache:
             raise ValueError("PagedKVCache: the elements of a head must be contiguous")
         f8 = self.k.dtype == torch.float8_e4m3fn
         object.__setattr__(self, "device_index", dev)
+        object.__setattr__(self, "heads", tuple(self.k.shape[2:]))   # (Hkv, D)
         object.__setattr__(self, "_cs", _PagedKV(
             _ptr(self.k), _ptr(self.v), *self.k.shape, *self.k.stride()[:3], *self.v.stride()[:3],
             int(f8), float(self.k_scale), float(self.v_scale)))
@@ -813,11 +816,11 @@ class PagedKVCache:
 
     @property
     def Hkv(self):
-        return self._cs.Hkv
+        return self.heads[0]
 
     @property
     def D(self):
-        return self._cs.D
+        return self.heads[1]
 
 
 def kv_append(k, v, cache: PagedKVCache, block_table, positions, seq_ids=None, q=None, rope=None,
@@ -826,47 +829,49 @@ def kv_append(k, v, cache: PagedKVCache, block_table, positions, seq_ids=None, q
     sequences seq_ids int32 [T], or 0..T-1) through block_table int32 [B,width], k rotated by rope
     f32 [rows, R] (cos | sin; None: not at all). Returns the rotated q bf16 [T,Hq,D], or None
     without q. Rows of k, v and q may be slices of one projection's output."""
-    dev = cache.device_index
-    cs = cache._cs
+    dev, inner = cache.device_index, cache.heads
     if k.dim() != 3 or block_table.dim() != 2:
         raise ValueError("k [T, Hkv, D] and block_table [B, width] expected")
-    T, inner = k.shape[0], (cs.Hkv, cs.D)
+    T, D = k.shape[0], inner[1]
     ks, vs = _need_rows(k, "k", dev, inner), _need_rows(v, "v", dev, inner)
     if v.shape[0] != T:
         raise ValueError("v: as many tokens as k expected")
     _need(block_table, "block_table", dev, _I32, None)
     _need(positions, "positions", dev, _I32, (T,))
-    B = block_table.shape[0]
+    B, width = block_table.shape
     if seq_ids is not None:
         _need(seq_ids, "seq_ids", dev, _I32, (T,))
     elif T > B:
         raise ValueError("seq_ids: required for more tokens than block_table has rows")
-    Hq, qs = 0, 0
+    Hq = qs = qp = qo = 0
     if q is not None:
         if q.dim() != 3 or q.shape[0] != T:
             raise ValueError("q: [T, Hq, D] expected")
         Hq = q.shape[1]
-        qs = _need_rows(q, "q", dev, (Hq, cs.D))
+        qs = _need_rows(q, "q", dev, (Hq, D))
         if q_out is None:
-            q_out = torch.empty((T, Hq, cs.D), dtype=torch.bfloat16, device=q.device)
+            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
         else:
-            _need(q_out, "q_out", dev, BF16_BITS, (T, Hq, cs.D))
-    rows, dim = 0, 0
+            _need(q_out, "q_out", dev, BF16_BITS, (T, Hq, D))
+        qp, qo = q.data_ptr(), q_out.data_ptr()
+    rows = dim = rp = 0
     if rope is not None:
         if rope.dim() != 2:
             raise ValueError("rope: [rows, R] expected")
         _need(rope, "rope", dev, _F32, None)
         rows, dim = rope.shape
+        rp = rope.data_ptr()
     if workspace is not None:
         _need(workspace, "workspace", dev, None, None)
         if workspace.numel() < WORKSPACE_HEAD_BYTES:
             raise ValueError("workspace: at least WORKSPACE_HEAD_BYTES expected")
-    st = _LIB.ft_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q), qs,
-                           _ptr(q_out) if q is not None else 0, T, Hq, cache._ref,
-                           block_table.data_ptr(), B, block_table.shape[1], _ptr(seq_ids),
-                           positions.data_ptr(), _ptr(rope), rows, dim, _ptr(workspace),
+    st = _LIB.ft_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, qo, T, Hq, cache._ref,
+                           block_table.data_ptr(), B, width,
+                           0 if seq_ids is None else seq_ids.data_ptr(), positions.data_ptr(), rp,
+                           rows, dim, 0 if workspace is None else workspace.data_ptr(),
                            _stream(stream, dev))
-    _check(st, "ft_kv_append")
+    if st != FT_OK:
+        _check(st, "ft_kv_append")
     return q_out if q is not None else None
 
 
@@ -879,15 +884,15 @@ def paged_decode_attention(q, cache: PagedKVCache, block_table, seq_lens, scale=
     """ft_paged_decode_attention: q bf16 [B,Hq,D], one new token per sequence, over the first
     seq_lens int32 [B] slots of each (the last `window` of them if window > 0) through block_table
     int32 [B,width]. scale: 1/sqrt(D) by default. Returns (out bf16 [B,Hq,D], lse f32 [B,Hq])."""
-    dev = cache.device_index
-    D = cache._cs.D
+    dev, D = cache.device_index, cache.heads[1]
     if q.dim() != 3 or block_table.dim() != 2:
         raise ValueError("q [B, Hq, D] and block_table [B, width] expected")
-    B, Hq = q.shape[0], q.shape[1]
+    B, Hq, _ = q.shape
     qs = _need_rows(q, "q", dev, (Hq, D))
     _need(block_table, "block_table", dev, _I32, None)
-    if block_table.shape[0] != B:
-        raise ValueError(f"block_table: {block_table.shape[0]} rows for {B} sequences")
+    rows, width = block_table.shape
+    if rows != B:
+        raise ValueError(f"block_table: {rows} rows for {B} sequences")
     _need(seq_lens, "seq_lens", dev, _I32, (B,))
     if out is None:
         out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=q.device)
@@ -905,11 +910,12 @@ def paged_decode_attention(q, cache: PagedKVCache, block_table, seq_lens, scale=
             raise FtError(2, "ft_paged_attention_workspace_bytes")
         workspace = _scratch(n, dev, stream)
     st = _LIB.ft_paged_decode_attention(
-        q.data_ptr(), qs, B, Hq, cache._ref, block_table.data_ptr(), block_table.shape[1],
-        seq_lens.data_ptr(), D ** -0.5 if scale is None else scale, window, out.data_ptr(),
-        lse.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel(),
-        _stream(stream, dev))
-    _check(st, "ft_paged_decode_attention")
+        q.data_ptr(), qs, B, Hq, cache._ref, block_table.data_ptr(), width, seq_lens.data_ptr(),
+        D ** -0.5 if scale is None else scale, window, out.data_ptr(), lse.data_ptr(),
+        0 if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel(), _stream(stream, dev))
+    if st != FT_OK:
+        _check(st, "ft_paged_decode_attention")
     return out, lse
 
 
@@ -918,11 +924,11 @@ def _norm_inputs(y, residual, w_post, w_pre, gate):
     dev = _device_of(y, "ft_residual_norm")
     if y.dim() != 2:
         raise ValueError("y: [T, H] expected")
-    T, H = y.shape
-    _need(y, "y", dev, BF16_BITS, (T, H))
+    T, H = both = y.shape
+    _need(y, "y", dev, BF16_BITS, None)
     res = torch.bfloat16
     if residual is not None:
-        _need(residual, "residual", dev, _RES, (T, H))
+        _need(residual, "residual", dev, _RES, both)
         res = residual.dtype
     if w_post is not None:
         _need(w_post, "w_post", dev, BF16_BITS, (H,))
@@ -930,15 +936,15 @@ def _norm_inputs(y, residual, w_post, w_pre, gate):
         _need(w_pre, "w_pre", dev, BF16_BITS, (H,))
     kind = GATE_NONE
     if gate is not None:
-        shape = tuple(gate.shape)
-        if shape == (H,):
-            kind = GATE_CHANNEL
+        shape = gate.shape
+        if shape == both:
+            kind = GATE_ELEMENT
         elif shape == (T, 1):
             kind = GATE_TOKEN
-        elif shape == (T, H):
-            kind = GATE_ELEMENT
+        elif shape == (H,):
+            kind = GATE_CHANNEL
         else:
-            raise ValueError(f"gate: shape {shape}, expected ({H},), ({T}, 1) or ({T}, {H})")
+            raise ValueError(f"gate: shape {tuple(shape)}, expected ({H},), ({T}, 1) or ({T}, {H})")
         _need(gate, "gate", dev, BF16_BITS, None)
     return dev, T, H, kind, res
 
@@ -950,20 +956,26 @@ def residual_norm(y, residual=None, w_post=None, w_pre=None, gate=None, scale=1.
     Returns (r' in the residual's type, x' bf16 or None without w_pre)."""
     dev, T, H, kind, res = _norm_inputs(y, residual, w_post, w_pre, gate)
     if res_out is None:
-        res_out = torch.empty((T, H), dtype=res, device=y.device)
+        res_out = torch.empty_like(y if residual is None else residual, dtype=res)
     else:
         _need(res_out, "res_out", dev, _RES if residual is None else (res,), (T, H))
         res = res_out.dtype
+    x = 0
     if w_pre is None:
         x_out = None
-    elif x_out is None:
-        x_out = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
     else:
-        _need(x_out, "x_out", dev, BF16_BITS, (T, H))
-    st = _LIB.ft_residual_norm(y.data_ptr(), _ptr(residual), _ptr(w_post), _ptr(w_pre), _ptr(gate),
-                               kind, T, H, res is torch.float32, scale, eps, res_out.data_ptr(),
-                               _ptr(x_out), _stream(stream, dev))
-    _check(st, "ft_residual_norm")
+        if x_out is None:
+            x_out = torch.empty_like(y, dtype=torch.bfloat16)
+        else:
+            _need(x_out, "x_out", dev, BF16_BITS, (T, H))
+        x = x_out.data_ptr()
+    st = _LIB.ft_residual_norm(
+        y.data_ptr(), 0 if residual is None else residual.data_ptr(),
+        0 if w_post is None else w_post.data_ptr(), 0 if w_pre is None else w_pre.data_ptr(),
+        0 if gate is None else gate.data_ptr(), kind, T, H, res is torch.float32, scale, eps,
+        res_out.data_ptr(), x, _stream(stream, dev))
+    if st != FT_OK:
+        _check(st, "ft_residual_norm")
     return res_out, x_out
 
 
@@ -990,15 +1002,20 @@ def residual_norm_backward(y, residual, d_r, d_x=None, w_post=None, w_pre=None, 
         if d_x is None:
             raise ValueError("d_x: required with w_pre")
         _need(d_x, "d_x", dev, BF16_BITS, (T, H))
-    cuda, f32 = y.device, torch.float32
-    dy = torch.empty((T, H), dtype=torch.bfloat16, device=cuda)
-    dres = torch.empty((T, H), dtype=res, device=cuda)
-    dw_post = torch.empty(H, dtype=f32, device=cuda) if w_post is not None else None
-    dw_pre = torch.empty(H, dtype=f32, device=cuda) if w_pre is not None else None
-    dgate = None
+    f32 = torch.float32
+    dy = torch.empty_like(y, dtype=torch.bfloat16)
+    dres = torch.empty_like(y, dtype=res)
+    dw_post = dw_pre = dgate = None
+    post = pre = dx = gp = dg = 0
+    if w_post is not None:
+        dw_post = torch.empty_like(w_post, dtype=f32)
+        post = dw_post.data_ptr()
+    if w_pre is not None:
+        dw_pre = torch.empty_like(w_pre, dtype=f32)
+        pre, dx = dw_pre.data_ptr(), d_x.data_ptr()
     if gate is not None:
-        dgate = torch.empty(gate.shape, dtype=torch.bfloat16 if kind == GATE_ELEMENT else f32,
-                            device=cuda)
+        dgate = torch.empty_like(gate, dtype=torch.bfloat16 if kind == GATE_ELEMENT else f32)
+        gp, dg = gate.data_ptr(), dgate.data_ptr()
     if workspace is not None:
         _need(workspace, "workspace", dev, None, None)
     elif T > 0:
@@ -1007,11 +1024,14 @@ def residual_norm_backward(y, residual, d_r, d_x=None, w_post=None, w_pre=None, 
             raise FtError(2, "ft_residual_norm_backward_workspace_bytes")
         workspace = _scratch(n, dev, stream)
     st = _LIB.ft_residual_norm_backward(
-        y.data_ptr(), _ptr(residual), _ptr(w_post), _ptr(w_pre), _ptr(gate), kind, _ptr(d_r),
-        _ptr(d_x) if w_pre is not None else 0, T, H, res is torch.float32, scale, eps,
-        dy.data_ptr(), dres.data_ptr(), _ptr(dw_post), _ptr(dw_pre), _ptr(dgate), _ptr(workspace),
+        y.data_ptr(), 0 if residual is None else residual.data_ptr(),
+        0 if w_post is None else w_post.data_ptr(), 0 if w_pre is None else w_pre.data_ptr(), gp,
+        kind, 0 if d_r is None else d_r.data_ptr(), dx, T, H, res is f32, scale, eps,
+        dy.data_ptr(), dres.data_ptr(), post, pre, dg,
+        0 if workspace is None else workspace.data_ptr(),
         0 if workspace is None else workspace.numel(), _stream(stream, dev))
-    _check(st, "ft_residual_norm_backward")
+    if st != FT_OK:
+        _check(st, "ft_residual_norm_backward")
     return NormGradients(dy, dres, dw_post, dw_pre, dgate)
 
 
