@@ -192,7 +192,9 @@ ft_status ft_residual_norm(const uint16_t* y, const void* residual, const uint16
   a.y = y; a.r = residual; a.w_post = w_post; a.w_pre = w_pre; a.gate = gate;
   a.gate_kind = gate_kind; a.T = T; a.H = H; a.res_f32 = res_f32 ? 1 : 0;
   a.scale = scale; a.eps = eps; a.r_out = r_out; a.x_out = x_out;
-  return cuda_status(launch_norm(a, static_cast<cudaStream_t>(stream)));
+  const int sms = device_sms();
+  if (sms <= 0) return FT_ERR_CUDA;
+  return cuda_status(launch_norm(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t ft_residual_norm_backward_workspace_bytes(int32_t T, int32_t H) {

@@ -194,7 +194,7 @@ struct NormArgs {
 };
 // Blocks (rows of the workspace's partial sums) of the backward pass.
 int norm_bwd_groups(int T, int num_sms);
-cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream);
+cudaError_t launch_norm(const NormArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_norm_bwd(const NormArgs& a, int num_sms, cudaStream_t stream);
 
 // SM count of the current device (0: no device).

@@ -10,9 +10,17 @@
 //   dw_pre = sum_t dx r' s2 dz  = scale gate dr'                       dgate = scale z dr'
 //   h = dz w_post           dy  = s1 (h - y s1^2 mean(h y))            dw_post = sum_t dz y s1
 //
-// A row stays in the registers of one block (or of one warp, for short rows): each input is read
-// once and each output written once. Sums run in float32 in a fixed order; x' is taken from r'
-// before r' is rounded to its stored type.
+// Every input is read once and every output written once; the work is bound by memory, with float32
+// sums in a fixed order, and x' taken from r' before r' is rounded to its stored type. k_norm: a row per
+// block (or per warp, up to 512 elements) in registers. k_norm_rows (wide rows, many of them) and
+// k_norm_bwd: persistent blocks whose row groups get their rows by bulk copies into rings, so that the
+// next rows travel while one is worked on. The gradient's column sums stay in registers over all of a
+// block's rows; k_norm_cols adds the blocks' sums.
+//
+// Measured (of the copy rate of 6786 GB/s): forward 8191 x 4096 with a float32 stream 71 us (84 %), 8192 x
+// 8192 95 us (83 %); gradient 8192 x 8192 170 us (70 %), where about half of a row's 3 us is arithmetic
+// (9 unpackings and 9 packed operations an element) and two barriers; 2048 x 16384 168 us (35 %: 32 columns
+// a thread spill). One token: 2.9 us, a launch and three dependent latencies.
 #include <cuda_runtime.h>
 
 #include "ftmoe_internal.h"
@@ -151,23 +159,26 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 1024) k_norm(const Nor
 // travel while one is worked on. A row's values are read from shared memory where they are used; r', h
 // and the column sums stay in registers. Two barriers a row: the sum that y needs is taken for the next
 // row together with the last sums of this one.
-constexpr int kBwdThreads = 512;
-constexpr size_t kBwdRing = 224 * 1024;   // one stage of the widest rows: 16384, float32, every input
+constexpr int kRingThreads = 512;
+constexpr size_t kRingBytes = 224 * 1024;   // one stage of the widest rows: 16384, float32, every input
 
-struct BwdRing {   // a stage: y | r | dr | dx | gate rows
+struct RowRing {   // a stage: y | r | dr | dx | gate rows (dr, dx: the gradient's)
   int stage = 0, off_r = 0, off_dr = 0, off_dx = 0, off_gate = 0, stages = 0;
-  BwdRing() = default;
-  BwdRing(const NormArgs& a, int groups) {
+  RowRing(const NormArgs& a, int groups, size_t bytes) {
     const int res = a.H * (a.res_f32 ? 4 : 2);
     off_r = 2 * a.H;
     off_dr = off_r + (a.r ? res : 0);
     off_dx = off_dr + (a.dr ? res : 0);
-    off_gate = off_dx + (a.w_pre ? 2 * a.H : 0);
+    off_gate = off_dx + (a.dx ? 2 * a.H : 0);
     stage = off_gate + (a.gate_kind == FT_GATE_ELEMENT ? 2 * a.H : 0);
-    stages = (int)(kBwdRing / ((size_t)groups * stage));
+    stages = (int)(bytes / ((size_t)groups * stage));
     if (stages > 8) stages = 8;
   }
 };
+
+// Where a wait of k_norm_rows that runs out is recorded (the call has no workspace): only a copy that
+// never lands would let it.
+__device__ int g_norm_err;
 
 // Two float32 in one 64-bit register pair: half the arithmetic instructions (packed operations round
 // each half as the scalar ones do).
@@ -226,14 +237,151 @@ __device__ __forceinline__ void put8(float* p, const f2 (&f)[4]) {
   reinterpret_cast<ulonglong2*>(p)[1] = make_ulonglong2(f[2], f[3]);
 }
 
+// Many rows: the row groups and rings of the gradient. One barrier a row: the sum over r' for x' and the
+// one over the next row's y are taken together, and the row's stage is free once it is passed.
+template <int GT, int NV, typename RT>
+__global__ void __launch_bounds__(kRingThreads, NV == 2 ? 2 : 1) k_norm_rows(const NormArgs a, const RowRing ring) {
+  constexpr int RG = kRingThreads / GT, W = GT / 32;
+  extern __shared__ __align__(128) unsigned char ring_smem[];
+  __shared__ __align__(8) uint64_t full[RG][8];
+  __shared__ __align__(16) float2 red[RG][2][W];
+  const int g = threadIdx.x / GT, tid = threadIdx.x % GT, warp = tid >> 5, lane = tid & 31;
+  const int chunks = a.H >> 3, ST = ring.stages;
+  const float inv_h = 1.0f / (float)a.H;
+  const bool channel = a.gate_kind == FT_GATE_CHANNEL, element = a.gate_kind == FT_GATE_ELEMENT;
+  const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr;
+  const RT* const kind = nullptr;
+  if (tid < ST) mbar_init(&full[g][tid], 1);
+  if (tid == 0) asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  __syncthreads();
+  griddep_launch_dependents();
+  griddep_wait();
+  unsigned char* const mine = ring_smem + (size_t)g * ST * ring.stage;
+  const int t0 = blockIdx.x + g * gridDim.x, dt = RG * gridDim.x;   // rows of this group: t0, t0 + dt, ...
+  const int n_rows = t0 < a.T ? (a.T - t0 + dt - 1) / dt : 0;
+  auto send = [&](int i) {   // one thread: the copies of row i into stage i % ST
+    uint64_t* bar = &full[g][i % ST];
+    unsigned char* st = mine + (size_t)(i % ST) * ring.stage;
+    const size_t row = (size_t)(t0 + i * dt) * a.H;
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::
+                     "r"(smem_addr(bar)), "r"(ring.stage) : "memory");
+    auto copy = [&](int off, const void* src, size_t bytes_per) {
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
+                   "[%0], [%1], %2, [%3];" ::"r"(smem_addr(st + off)),
+                   "l"(static_cast<const char*>(src) + row * bytes_per),
+                   "r"((uint32_t)(a.H * bytes_per)), "r"(smem_addr(bar)) : "memory");
+    };
+    copy(0, a.y, 2);
+    if (a.r) copy(ring.off_r, a.r, sizeof(RT));
+    if (element) copy(ring.off_gate, a.gate, 2);
+  };
+  auto sum2 = [&](int which, float x, float y) -> float2 {   // two sums over the group's threads
+    x = warp_sum(x);
+    y = warp_sum(y);
+    if (lane == 0) red[g][which][warp] = make_float2(x, y);
+    asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "n"(GT) : "memory");
+    float2 v = red[g][which][lane % W];
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) {
+      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    }
+    return v;
+  };
+  // this thread's columns of w_post and w_pre
+  const uint4 one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+  uint4 wpost[NV], wpre[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = tid + v * GT;
+    wpost[v] = post && c < chunks ? *reinterpret_cast<const uint4*>(a.w_post + 8 * c) : one;
+    wpre[v] = pre && c < chunks ? *reinterpret_cast<const uint4*>(a.w_pre + 8 * c) : one;
+  }
+  auto square_sum = [&](const unsigned char* st) -> float {   // of this thread's part of y
+    f2 ss = 0ull;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = tid + v * GT;
+      if (c >= chunks) continue;
+      f2 y[4];
+      get8(st, c, a.y, y);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ss = fma2(y[j], y[j], ss);
+    }
+    return sum_of(ss);
+  };
+  auto arrived = [&](int i) {
+    mbar_wait(&full[g][i % ST], (uint32_t)(i / ST) & 1u, &g_norm_err, kErrTimeout);
+  };
+
+  if (tid == 0)
+    for (int i = 0; i < ST && i < n_rows; ++i) send(i);
+  if (n_rows == 0) return;   // a whole group: its barriers are its own
+  arrived(0);
+  float ss = sum2(1, post ? square_sum(mine) : 0.f, 0.f).x;
+  for (int i = 0; i < n_rows; ++i) {
+    const int t = t0 + i * dt;
+    const size_t row = (size_t)t * a.H;
+    const unsigned char* st = mine + (size_t)(i % ST) * ring.stage;
+    const float s1 = post ? rsqrtf(ss * inv_h + a.eps) : 1.f;
+    const f2 ts = both(a.scale * (a.gate_kind == FT_GATE_TOKEN ? one_bf16(a.gate + t) : 1.f) * s1);
+    f2 r[NV][4], rr = 0ull;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = tid + v * GT;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r[v][j] = 0ull;
+      if (c >= chunks) continue;
+      f2 y[4], w[4];
+      get8(st, c, a.y, y);
+      if (a.r) get8(st + ring.off_r, c, kind, r[v]);
+      open8(wpost[v], w);   // y times the weight and the gate, all bf16, is exact in float32
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = mul2(y[j], w[j]);
+      if (element || channel) {
+        if (element) get8(st + ring.off_gate, c, a.gate, w);
+        else open8(*reinterpret_cast<const uint4*>(a.gate + 8 * c), w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = mul2(y[j], w[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        r[v][j] = fma2(y[j], ts, r[v][j]);
+        rr = fma2(r[v][j], r[v][j], rr);
+      }
+      if (a.r_out) put8(static_cast<RT*>(a.r_out) + row + 8 * c, r[v]);
+    }
+    float next = 0.f;
+    if (i + 1 < n_rows) {
+      arrived(i + 1);
+      if (post) next = square_sum(mine + (size_t)((i + 1) % ST) * ring.stage);
+    }
+    const float2 sums = sum2(i & 1, sum_of(rr), next);
+    ss = sums.y;
+    if (tid == 0 && i + ST < n_rows) send(i + ST);   // every thread has read the row
+    if (!pre) continue;
+    const f2 s2 = both(rsqrtf(sums.x * inv_h + a.eps));
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = tid + v * GT;
+      if (c >= chunks) continue;
+      f2 w[4];
+      open8(wpre[v], w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r[v][j] = mul2(r[v][j], mul2(w[j], s2));
+      put8(a.x_out + row + 8 * c, r[v]);
+    }
+  }
+}
+
 // With u = w_post * (channel gate), tg = scale * (token gate) and e the elementwise gate:
 //   r' = r + (tg s1) y u e     h = tg dr' u e     dy = s1 h - y s1^3 mean(h y)
 //   A = sum_t tg s1 y dr' e    dw_post = A * (channel gate), dgate = A * w_post (channel: tg = scale)
 //   dgate = scale s1 sum_h y u dr' (token),  scale s1 y u dr' (element)
 // so one column sum serves both the weight and the channel's gate.
 template <int GT, int NV, typename RT>
-__global__ void __launch_bounds__(kBwdThreads, 1) k_norm_bwd(const NormArgs a, const BwdRing ring) {
-  constexpr int RG = kBwdThreads / GT, W = GT / 32;
+__global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd(const NormArgs a, const RowRing ring) {
+  constexpr int RG = kRingThreads / GT, W = GT / 32;
   extern __shared__ __align__(128) unsigned char bwd_smem[];
   __shared__ __align__(8) uint64_t full[RG][8];
   __shared__ float4 red[RG][2][W];
@@ -484,7 +632,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_norm_bwd(const NormArgs a, c
     }
     if constexpr (RG > 1) {
       __syncthreads();
-      for (int x = threadIdx.x; x < a.H; x += kBwdThreads) {
+      for (int x = threadIdx.x; x < a.H; x += kRingThreads) {
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < RG; ++w) v += cols[(size_t)w * a.H + x];
@@ -548,12 +696,44 @@ cudaError_t launch(K kernel, int grid, int threads, cudaStream_t stream, const N
 // Threads of a block that holds rows of `chunks` 8-element pieces, nv per thread.
 int row_threads(int chunks, int nv) { return ((chunks + nv - 1) / nv + 31) / 32 * 32; }
 
+// Many rows by rings, two blocks an SM (one for the widest rows). ok: false when a ring of two stages
+// does not fit.
+template <int GT, int NV, typename RT>
+cudaError_t launch_rows_t(const NormArgs& a, int num_sms, cudaStream_t stream, bool& ok) {
+  constexpr int blocks = NV == 2 ? 2 : 1;
+  const RowRing ring(a, kRingThreads / GT, kRingBytes / blocks);
+  ok = ring.stages >= 2;
+  if (!ok) return cudaSuccess;
+  const size_t smem = (size_t)kRingThreads / GT * ring.stages * ring.stage;
+  cudaError_t e;
+  // per device and host-side only: set on every call
+  if ((e = cudaFuncSetAttribute(k_norm_rows<GT, NV, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)smem)) != cudaSuccess)
+    return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(blocks * num_sms));
+  cfg.blockDim = dim3(kRingThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_norm_rows<GT, NV, RT>, a, ring);
+}
+template <int GT, int NV>
+cudaError_t launch_rows(const NormArgs& a, int num_sms, cudaStream_t stream, bool& ok) {
+  return a.res_f32 ? launch_rows_t<GT, NV, float>(a, num_sms, stream, ok)
+                   : launch_rows_t<GT, NV, uint16_t>(a, num_sms, stream, ok);
+}
+
 template <int GT, int NV, typename RT>
 cudaError_t launch_bwd_t(const NormArgs& a, int grid, cudaStream_t stream) {
-  const BwdRing ring(a, kBwdThreads / GT);
-  const size_t sums = (size_t)kBwdThreads / GT * a.H * 4;
-  size_t smem = (size_t)kBwdThreads / GT * ring.stages * ring.stage;
-  if (GT < kBwdThreads && smem < sums) smem = sums;
+  const RowRing ring(a, kRingThreads / GT, kRingBytes);
+  const size_t sums = (size_t)kRingThreads / GT * a.H * 4;
+  size_t smem = (size_t)kRingThreads / GT * ring.stages * ring.stage;
+  if (GT < kRingThreads && smem < sums) smem = sums;
   cudaError_t e;
   // per device and host-side only: set on every call
   if ((e = cudaFuncSetAttribute(k_norm_bwd<GT, NV, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -561,7 +741,7 @@ cudaError_t launch_bwd_t(const NormArgs& a, int grid, cudaStream_t stream) {
     return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kBwdThreads);
+  cfg.blockDim = dim3(kRingThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -582,8 +762,17 @@ cudaError_t launch_bwd(const NormArgs& a, int grid, cudaStream_t stream) {
 
 int norm_bwd_groups(int T, int num_sms) { return T < num_sms ? T : num_sms; }
 
-cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream) {
+cudaError_t launch_norm(const NormArgs& a, int num_sms, cudaStream_t stream) {
   const int chunks = a.H / 8;
+  // Rings for wide rows, from four rows a group on (us, one row a block or rings: 8192 x 8192 119 or 95,
+  // 2048 x 16384 67 or 48; 8192 x 2048 27 either way, and narrower rows alike)
+  if (chunks > 256 && (int64_t)a.T >= (int64_t)(chunks <= 512 ? 16 : chunks <= 1024 ? 8 : 4) * num_sms) {
+    bool ok = false;
+    const cudaError_t e = chunks <= 512    ? launch_rows<256, 2>(a, num_sms, stream, ok)
+                          : chunks <= 1024 ? launch_rows<512, 2>(a, num_sms, stream, ok)
+                                           : launch_rows<512, 4>(a, num_sms, stream, ok);
+    if (ok || e != cudaSuccess) return e;
+  }
   if (a.H <= kWarpRowMax) {
     const int grid = (a.T + kRowWarps - 1) / kRowWarps;
     return a.res_f32 ? launch(k_norm<2, float, true>, grid, kRowWarps * 32, stream, a)

@@ -100,6 +100,23 @@ def test_several_rows_per_block(T, H, res, gate, post, pre):
     check(T, H, res, post, pre, gate, T)
 
 
+@pytest.mark.parametrize("T,H,res,gate", [(19500, 72, torch.bfloat16, "channel"), (10001, 776, torch.float32, "element"),
+                                          (5003, 2048, torch.bfloat16, "token"), (2600, 4096, torch.float32, "element"),
+                                          (1300, 8192, torch.bfloat16, "channel"), (1250, 8200, torch.float32, "none"),
+                                          (700, 16384, torch.float32, "element"), (650, 16384, torch.bfloat16, "none")])
+@pytest.mark.parametrize("post,pre", [(True, True), (True, False), (False, True)])
+def test_many_rows(T, H, res, gate, post, pre):
+    """Several rows per block in the forward pass, in place as well."""
+    m = ftmoe()
+    a = inputs(np.random.default_rng(T), T, H, res, post, pre, gate)
+    d = {n: cuda(t) for n, t in a.items()}
+    kw = dict(w_post=d["w_post"], w_pre=d["w_pre"], gate=d["gate"], scale=0.7, eps=EPS)
+    r, x = m.residual_norm(d["y"], d["r"], **kw)
+    forward_close(r, x, a, 0.7)
+    again, _ = m.residual_norm(d["y"], d["r"], res_out=d["r"], x_out=d["y"] if pre else None, **kw)
+    assert torch.equal(again, r) and (x is None or torch.equal(d["y"], x))
+
+
 def test_no_residual_in_place_and_no_gradient_of_r():
     m = ftmoe()
     rng = np.random.default_rng(1)
