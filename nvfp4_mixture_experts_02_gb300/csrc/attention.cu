@@ -35,14 +35,15 @@ namespace ftmoe {
 
 namespace {
 
-template <int D, bool F8>
+template <int D, bool F8, int NG>
 struct AttnShape {
   static constexpr int kRow = D * (F8 ? 1 : 2);       // bytes of a key or value
   static constexpr int kCpr = kRow / 16;              // 16-byte pieces of it
   static constexpr int kKeys = kRow <= 128 ? 32 : 16; // keys of a warp's step
   static constexpr int kStageBytes = 2 * kKeys * kRow;   // those keys and values
-  // two blocks an SM where their rings fit: one streams while the other joins a piece's warps
-  static constexpr int kBlocks = kRow >= 512 ? 1 : 2;
+  // blocks an SM: the others stream while one joins a piece's warps. Three of two stages each, not two of
+  // three, where the registers allow it: 256 sequences up to 1024 with 8-bit keys of 128: 68 us for 79
+  static constexpr int kBlocks = kRow >= 512 ? 1 : kRow == 128 && NG == 1 ? kAttendBlocks : 2;
   static constexpr int kWarps = kRow >= 128 ? 4 : 8;
   static constexpr int kStages = 192 * 1024 / (kBlocks * kWarps * kStageBytes);
   static constexpr int kUnit = kKeys * kWarps;        // keys of a unit
@@ -96,8 +97,8 @@ __device__ __forceinline__ void span(int len, int window, int unit, int& first, 
 }
 
 template <int D, bool F8, int NG>
-__global__ void __launch_bounds__(AttnShape<D, F8>::kWarps * 32, AttnShape<D, F8>::kBlocks) k_attend(const AttendArgs a) {
-  using S = AttnShape<D, F8>;
+__global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D, F8, NG>::kBlocks) k_attend(const AttendArgs a) {
+  using S = AttnShape<D, F8, NG>;
   constexpr int W = S::kWarps, ST = S::kStages, CPR = S::kCpr, KS = D / 16, MT = D / 16;
   constexpr int KT = S::kKeys, NH = KT / 16;   // keys of a step, in 16-row tiles
   constexpr int LD = D + 4;   // floats between heads where the warps' sums are joined
@@ -597,13 +598,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_join(const AttendArgs a) {
 
 template <int D, bool F8, int NG>
 cudaError_t launch_d(const AttendArgs& a, int num_sms, cudaStream_t stream) {
-  using S = AttnShape<D, F8>;
+  using S = AttnShape<D, F8, NG>;
   const size_t smem = S::kRing + (a.B > 32 ? (size_t)(a.B + 1) * 4 : 0);
   cudaError_t e;
-  // set on every call: the attribute is per device and the call is host-side only
-  if ((e = cudaFuncSetAttribute(k_attend<D, F8, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)smem)) != cudaSuccess)
-    return e;
+  static SmemGrant grant;   // for the most sequences that a call may have
+  if ((e = grant_smem(grant, k_attend<D, F8, NG>, S::kRing + 4 * (kMaxSeqs + 1))) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   const int grid = S::kBlocks * num_sms;
   cfg.gridDim = dim3((unsigned)grid);

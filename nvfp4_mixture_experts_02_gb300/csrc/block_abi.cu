@@ -14,7 +14,6 @@ namespace {
 
 constexpr int kMaxLinearK = 32768;
 constexpr int kMaxLinearN = 1 << 30;
-constexpr int kMaxSeqs = 4096;
 constexpr int kMaxHeads = 1024;
 constexpr int kMaxAppend = 1 << 20;
 constexpr int kMaxNormH = 16384;

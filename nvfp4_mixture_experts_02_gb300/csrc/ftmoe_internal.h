@@ -1,6 +1,7 @@
 // Internal declarations shared by the library's translation units (not part of the ABI).
 #pragma once
 
+#include <atomic>
 #include <cuda_runtime.h>
 #include <cstdint>
 
@@ -161,14 +162,17 @@ struct AttendArgs {
   int same_strides;        // keys and values lie alike (set by the launch)
   int div_mul, div_shift;  // division by the page size (set by the launch)
 };
-// Workspace regions (byte offsets, 256-byte aligned).
+// Workspace regions (byte offsets, 256-byte aligned), for kAttendBlocks blocks an SM at most, two pieces
+// each.
+constexpr int kAttendBlocks = 3;
 struct AttendLayout {
   size_t segs = 0, ml = 0, o = 0, total = 0;
   AttendLayout(int D, int num_sms) {
     segs = 1024;
-    ml = align_up(segs + (size_t)num_sms * 2 * 16, 256);
-    o = align_up(ml + (size_t)num_sms * 4 * 16 * 2 * 4, 256);   // two blocks an SM, two pieces each
-    total = align_up(o + (size_t)num_sms * 4 * 16 * D * 4, 256);
+    const size_t runs = (size_t)num_sms * kAttendBlocks;
+    ml = align_up(segs + runs * 16, 256);
+    o = align_up(ml + runs * 2 * 16 * 2 * 4, 256);
+    total = align_up(o + runs * 2 * 16 * D * 4, 256);
   }
 };
 cudaError_t launch_attend(const AttendArgs& a, int num_sms, cudaStream_t stream);
@@ -199,5 +203,22 @@ cudaError_t launch_norm_bwd(const NormArgs& a, int num_sms, cudaStream_t stream)
 
 // SM count of the current device (0: no device).
 int device_sms();
+
+// Lets a kernel take up to `bytes` of dynamic shared memory, once per device (`done`: one flag per device
+// and kernel; setting it twice is harmless).
+struct SmemGrant {
+  std::atomic<bool> done[64];
+};
+template <typename K>
+cudaError_t grant_smem(SmemGrant& grant, K kernel, int bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (grant.done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) grant.done[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
 
 }  // namespace ftmoe

@@ -9,6 +9,7 @@ namespace ftmoe {
 constexpr int kMaxTopK = 32;
 constexpr int kMaxExperts = 4096;
 constexpr int kMaxDecodeT = 64;
+constexpr int kMaxSeqs = 4096;         // sequences of an attention call
 constexpr int kMaxGrid = 512;          // upper bound on the split-K grid (CTAs)
 constexpr size_t kDecodeXOnChip = 64 * 1024;   // f16 activations kept in each CTA's smem up to this
 constexpr size_t kDecodeSmem = 224 * 1024;     // decode shared memory (one CTA per SM)

@@ -619,11 +619,6 @@ __global__ void __launch_bounds__(kMoreRows) k_linear_join(const LinearArgs a, i
 template <typename K, typename... Args>
 cudaError_t start(K kernel, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,
                   Args... args) {
-  cudaError_t e;
-  if (smem > 32 * 1024 &&   // with the static part past 48 KB; per device and host-side only: set on every call that needs it
-      (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
-          cudaSuccess)
-    return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
@@ -655,6 +650,9 @@ cudaError_t launch_few(LinearArgs a, int num_sms, cudaStream_t stream) {
   // resident blocks: two an SM, one when x takes more than half of the shared memory
   const int most = (x_bytes(split) > kLinXMax / 2 ? 1 : 2) * num_sms / split;
   const int blocks = tiles < most ? tiles : most;
+  static SmemGrant grant;
+  const cudaError_t e = grant_smem(grant, k_linear_few<MT, AHEAD>, (int)kLinXMax);
+  if (e != cudaSuccess) return e;
   return start(k_linear_few<MT, AHEAD>, dim3((unsigned)(blocks * split)), kLinWarps * 32, x_bytes(split),
                split, stream, a);
 }
@@ -673,6 +671,9 @@ cudaError_t launch_mid(LinearArgs a, int num_sms, cudaStream_t stream) {
   a.split = split;
   const size_t sums = (size_t)TOK * (kMidRows + 4) * 4;
   const size_t smem = x_bytes(split) > sums ? x_bytes(split) : sums;
+  static SmemGrant grant;
+  const cudaError_t e = grant_smem(grant, k_linear_mid<NT>, (int)kLinXMax);
+  if (e != cudaSuccess) return e;
   return start(k_linear_mid<NT>, dim3((unsigned)(tiles * split), (unsigned)((a.T + TOK - 1) / TOK)),
                kLinWarps * 32, smem, split, stream, a);
 }
@@ -685,10 +686,13 @@ cudaError_t launch_more(const LinearArgs& a, int num_sms, cudaStream_t stream) {
   const int most = (NT <= 4 ? 2 : 1) * num_sms;   // resident blocks
   const int quota = (total + most - 1) / most;
   const int blocks = (total + quota - 1) / quota;
-  cudaError_t e = start(k_linear_x, dim3((unsigned)a.T), kPrepThreads, 0, 1, stream, a, TOK);
+  static SmemGrant grant;
+  constexpr size_t smem = (size_t)kMoreStages * TOK * kLinUnit * 2;
+  cudaError_t e = grant_smem(grant, k_linear_more<NT>, (int)smem);
   if (e != cudaSuccess) return e;
+  if ((e = start(k_linear_x, dim3((unsigned)a.T), kPrepThreads, 0, 1, stream, a, TOK)) != cudaSuccess) return e;
   e = start(k_linear_more<NT>, dim3((unsigned)blocks), kLinWarps * 32,
-            (size_t)kMoreStages * TOK * kLinUnit * 2, 1, stream, a, uk, quota);
+            smem, 1, stream, a, uk, quota);
   if (e != cudaSuccess || quota % uk == 0) return e;   // every run ends with a tile
   return start(k_linear_join, dim3((unsigned)tiles, (unsigned)((a.T + 3) / 4)), kMoreRows, 0, 1, stream,
                a, TOK, uk, quota);

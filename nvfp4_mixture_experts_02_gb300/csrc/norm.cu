@@ -706,10 +706,8 @@ cudaError_t launch_rows_t(const NormArgs& a, int num_sms, cudaStream_t stream, b
   if (!ok) return cudaSuccess;
   const size_t smem = (size_t)kRingThreads / GT * ring.stages * ring.stage;
   cudaError_t e;
-  // per device and host-side only: set on every call
-  if ((e = cudaFuncSetAttribute(k_norm_rows<GT, NV, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)smem)) != cudaSuccess)
-    return e;
+  static SmemGrant grant;
+  if ((e = grant_smem(grant, k_norm_rows<GT, NV, RT>, (int)kRingBytes)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(blocks * num_sms));
   cfg.blockDim = dim3(kRingThreads);
@@ -735,10 +733,8 @@ cudaError_t launch_bwd_t(const NormArgs& a, int grid, cudaStream_t stream) {
   size_t smem = (size_t)kRingThreads / GT * ring.stages * ring.stage;
   if (GT < kRingThreads && smem < sums) smem = sums;
   cudaError_t e;
-  // per device and host-side only: set on every call
-  if ((e = cudaFuncSetAttribute(k_norm_bwd<GT, NV, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)smem)) != cudaSuccess)
-    return e;
+  static SmemGrant grant;
+  if ((e = grant_smem(grant, k_norm_bwd<GT, NV, RT>, (int)kRingBytes)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kRingThreads);
