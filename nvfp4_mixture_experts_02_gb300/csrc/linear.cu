@@ -163,11 +163,29 @@ __device__ __forceinline__ void products(float (&acc)[MT][NT][4], const Piece<MT
   }
 }
 
-__device__ __forceinline__ uint4 to_f16(uint4 v, float up) {   // 8 bf16 times a power of two
-  return make_uint4(pack_f16(bf16_lo(v.x) * up, bf16_hi(v.x) * up),
-                    pack_f16(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
-                    pack_f16(bf16_lo(v.z) * up, bf16_hi(v.z) * up),
-                    pack_f16(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
+// Eight bf16 times a power of two `up` (splat, exact in bf16) as f16.
+__device__ __forceinline__ uint4 to_f16(uint4 v, uint32_t up) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(w[j]) : "r"(up));
+    w[j] = pack_f16(bf16_lo(w[j]), bf16_hi(w[j]));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Running largest magnitudes of bf16 pairs (NaN does not count).
+__device__ __forceinline__ void pair_top(uint32_t& top, uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(w[j] & 0x7FFF7FFFu));
+}
+__device__ __forceinline__ float top_of(uint32_t pair) { return fmaxf(bf16_lo(pair), bf16_hi(pair)); }
+__device__ __forceinline__ float finite_top8(uint4 v) {
+  return fmaxf(finite_top(v.x, v.y), finite_top(v.z, v.w));
+}
+__device__ __forceinline__ uint32_t splat_bf16(float v) {   // of a power of two
+  return __byte_perm(__float_as_uint(v), 0, 0x3232);
 }
 
 // 16-byte unit of elements k .. k + 7 of token n in the B operand's order, `tok` tokens wide: unit
@@ -186,7 +204,7 @@ __device__ __forceinline__ void stage_x(const LinearArgs& a, int t0, int n0, int
   const uint16_t* x = a.x + (size_t)(t0 + n0) * a.x_stride;
   const int cnt = min(T - n0, 4);
   uint4 v[4][2];
-  float top[4] = {};
+  uint32_t top[4] = {0, 0, 0, 0};
   auto get = [&](int j, int k) {
     return j < cnt && k < kb && k < a.K
                ? *reinterpret_cast<const uint4*>(x + (size_t)j * a.x_stride + k)
@@ -199,19 +217,22 @@ __device__ __forceinline__ void stage_x(const LinearArgs& a, int t0, int n0, int
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      top[j] = fmaxf(top[j], fmaxf(finite_top(v[j][i].x, v[j][i].y), finite_top(v[j][i].z, v[j][i].w)));
+    for (int i = 0; i < 2; ++i) pair_top(top[j], v[j][i]);
   for (int k = ka + lane * 8 + 512; k < kb; k += 256)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint4 w = get(j, k);
-      top[j] = fmaxf(top[j], fmaxf(finite_top(w.x, w.y), finite_top(w.z, w.w)));
-    }
-  float up[4];
+    for (int j = 0; j < 4; ++j) pair_top(top[j], get(j, k));
+  uint32_t up[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    float dn;
-    f16_scale(warp_max(top[j]), up[j], dn);
+    float most = warp_max(top_of(top[j]));
+    if (most == INFINITY) {   // an infinity among them: the largest finite one (uniform, rare)
+      most = 0.f;
+      for (int k = ka + lane * 8; k < kb; k += 256) most = fmaxf(most, finite_top8(get(j, k)));
+      most = warp_max(most);
+    }
+    float f, dn;
+    f16_scale(most, f, dn);
+    up[j] = splat_bf16(f);
     if (lane == 0 && j < cnt) down[n0 + j] = dn;
   }
 #pragma unroll
@@ -457,22 +478,20 @@ __global__ void __launch_bounds__(kPrepThreads) k_linear_x(const LinearArgs a, i
     return k < a.K ? *reinterpret_cast<const uint4*>(x + k) : make_uint4(0, 0, 0, 0);
   };
   uint4 v[kPrepKeep];
-  float top = 0.f;
 #pragma unroll
   for (int i = 0; i < kPrepKeep; ++i) v[i] = get((i * kPrepThreads + (int)threadIdx.x) * 8);
+  float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < kPrepKeep; ++i)
-    top = fmaxf(top, fmaxf(finite_top(v[i].x, v[i].y), finite_top(v[i].z, v[i].w)));
-  for (int k = (kPrepKeep * kPrepThreads + (int)threadIdx.x) * 8; k < a.K; k += kPrepThreads * 8) {
-    const uint4 w = get(k);
-    top = fmaxf(top, fmaxf(finite_top(w.x, w.y), finite_top(w.z, w.w)));
-  }
+  for (int i = 0; i < kPrepKeep; ++i) top = fmaxf(top, finite_top8(v[i]));
+  for (int k = (kPrepKeep * kPrepThreads + (int)threadIdx.x) * 8; k < a.K; k += kPrepThreads * 8)
+    top = fmaxf(top, finite_top8(get(k)));
   top = warp_max(top);
   if (lane == 0) red[threadIdx.x >> 5] = top;
   __syncthreads();
   top = warp_max(lane < kPrepThreads / 32 ? red[lane] : 0.f);
-  float up, down;
-  f16_scale(top, up, down);
+  float factor, down;
+  f16_scale(top, factor, down);
+  const uint32_t up = splat_bf16(factor);
   if (threadIdx.x == 0) a.xdown[t] = down;
   uint4* xh = reinterpret_cast<uint4*>(a.xh);
 #pragma unroll
@@ -662,11 +681,11 @@ cudaError_t launch_mid(LinearArgs a, int num_sms, cudaStream_t stream) {
   constexpr int TOK = NT * 8;
   const int tiles = (a.N + kMidRows - 1) / kMidRows, pieces = (a.K + 127) / 128;
   auto x_bytes = [&](int split) { return (size_t)((pieces + split - 1) / split) * 256 * TOK; };
-  // K over a cluster while there are fewer than two blocks an SM and every warp keeps two pieces, and
+  // K over a cluster while twice the blocks are at most two an SM and every warp keeps a piece, and
   // while x does not fit
   int split = 1;
   while (split < 8 && (x_bytes(split) > kLinXMax / 2 ||
-                       (tiles * split < 2 * num_sms && pieces >= 8 * split)))
+                       (tiles * split <= num_sms && pieces >= 4 * split)))
     split *= 2;
   a.split = split;
   const size_t sums = (size_t)TOK * (kMidRows + 4) * 4;
