@@ -637,11 +637,7 @@ cudaError_t launch_attend(const AttendArgs& args, int num_sms, cudaStream_t stre
   a.gt = (a.group + 15) / 16;
   a.same_strides = a.kv.k_page_stride == a.kv.v_page_stride && a.kv.k_slot_stride == a.kv.v_slot_stride &&
                    a.kv.k_head_stride == a.kv.v_head_stride;
-  // j / page_size for 0 <= j < 2^31 as (umulhi(mul, j) + j) >> shift
-  int shift = 0;
-  while ((1ll << shift) < a.kv.page_size) ++shift;
-  a.div_shift = shift;
-  a.div_mul = (int)(uint32_t)(((1ull << 32) * ((1ull << shift) - a.kv.page_size)) / a.kv.page_size + 1);
+  page_division(a.kv.page_size, a.div_mul, a.div_shift);
   switch (a.kv.D) {
     case 64: return launch_g<64>(a, num_sms, stream);
     case 128: return launch_g<128>(a, num_sms, stream);

@@ -127,6 +127,13 @@ struct LinearLayout {
 };
 cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream);
 
+// j / d for 0 <= j < 2^31 as (umulhi(mul, j) + j) >> shift.
+inline void page_division(int d, int& mul, int& shift) {
+  shift = 0;
+  while ((1ll << shift) < d) ++shift;
+  mul = (int)(uint32_t)(((1ull << 32) * ((1ull << shift) - (uint64_t)d)) / (uint64_t)d + 1);
+}
+
 // Rotary embedding and cache append (kv.cu). err: error word or null.
 struct AppendArgs {
   const uint16_t *k, *v, *q;
@@ -140,6 +147,7 @@ struct AppendArgs {
   const float* rope;
   int rope_rows, rope_dim;
   int* err;
+  int div_mul, div_shift;   // division by the page size (set by the launch)
 };
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
 

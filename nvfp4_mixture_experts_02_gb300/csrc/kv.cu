@@ -9,7 +9,12 @@
 // other, or two neighbours past R. A block takes one token, or a few of few heads; the values are on
 // their way before the token's page is known. Products and sums are rounded one by one (no fused
 // multiply-add), so that a value on the edge between two E4M3 codes falls as plain float32 arithmetic
-// lets it fall. Bound by memory: every value is read once and written once.
+// lets it fall.
+// Bound by memory: every value is read once and written once. 16000 tokens of 48 heads of 128 without
+// rotation 70 us (82 % of the measured copy rate); 4093 tokens, rotated, into E4M3 22 us (62 %), where the
+// conversions and the tables' reads (as many bytes as the values, from L1) come on top; three blocks an
+// SM of 512 threads at 40 registers beat two at 64 (25 us), also with two tokens a thread in flight, and a
+// persistent grid with the next token's values ahead (26 us).
 #include <cuda_runtime.h>
 
 #include "ftmoe_internal.h"
@@ -80,7 +85,8 @@ __global__ void __launch_bounds__(512, 3) k_kv_append(const AppendArgs a, int it
     int64_t at = -1;
     if (placed && kind != 0) {
       const int seq = a.seq_ids ? a.seq_ids[t] : t;
-      const int col = pos / a.kv.page_size, slot = pos - col * a.kv.page_size;
+      const int col = (int)((__umulhi((uint32_t)a.div_mul, (uint32_t)pos) + (uint32_t)pos) >> a.div_shift);
+      const int slot = pos - col * a.kv.page_size;
       if (seq >= 0 && seq < a.B && col < a.table_width) {
         const int64_t page = a.block_table[(int64_t)seq * a.table_width + col];
         if (page >= 0 && page < a.kv.num_pages)
@@ -146,7 +152,9 @@ cudaError_t launch_d(const AppendArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
+cudaError_t launch_kv_append(const AppendArgs& args, cudaStream_t stream) {
+  AppendArgs a = args;
+  page_division(a.kv.page_size, a.div_mul, a.div_shift);
   switch (a.kv.D) {
     case 64: return launch_d<64>(a, stream);
     case 128: return launch_d<128>(a, stream);
