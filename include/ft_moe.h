@@ -402,8 +402,9 @@ size_t ft_paged_attention_workspace_bytes(int32_t B, int32_t D);
  *   seq_lens     int32 [B] on the device (not read by the host); a length of zero or less gives
  *                out = 0 and lse = -inf, as does a row whose scores are all -inf
  *   block_table  int32 [B, table_width] as for ft_kv_append; entries past a sequence's last page
- *                are not read. A page outside [0, num_pages), or a length past the table, flags
- *                FT_ERR_DEVICE_FLAG in the workspace, and its keys and values read as zeros.
+ *                are not read. A page outside [0, num_pages) flags FT_ERR_DEVICE_FLAG in the
+ *                workspace, and its keys and values read as zeros; a length past the table (or 2^30)
+ *                flags it too and is cut to it.
  *   out          bf16 [B, Hq, D], lse float [B, Hq] or NULL, fully overwritten
  *   workspace    ft_paged_attention_workspace_bytes(B, D) bytes, 256-byte aligned, its first
  *                FT_MOE_WORKSPACE_HEAD_BYTES zeroed once (ft_moe_workspace_init); calls that

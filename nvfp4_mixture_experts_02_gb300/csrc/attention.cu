@@ -90,6 +90,9 @@ __device__ __forceinline__ void store_row(const AttendArgs& a, int64_t at, float
   *reinterpret_cast<uint2*>(a.out + at) = y;
 }
 
+// A sequence's length, cut to what its row of the block table can hold.
+__device__ __forceinline__ int length_of(const AttendArgs& a, int b) { return min(a.seq_lens[b], a.max_len); }
+
 // First key and number of units of a sequence.
 __device__ __forceinline__ void span(int len, int window, int unit, int& first, int& units) {
   first = window > 0 && len > window ? len - window : 0;
@@ -118,7 +121,11 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
   int all;
   if (a.B <= 32) {
     int first, n = 0;
-    if (lane < a.B) span(a.seq_lens[lane], a.window, S::kUnit, first, n);
+    if (lane < a.B) {
+      const int len = length_of(a, lane);
+      span(len, a.window, S::kUnit, first, n);
+      if (blockIdx.x == 0 && warp == 0 && a.seq_lens[lane] > len) atomicOr(a.err, kErrBadPage);
+    }
     inc = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -132,8 +139,10 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
     int mine = 0;
     for (int b = b0; b < min(b0 + per, a.B); ++b) {
       int first, n;
-      span(a.seq_lens[b], a.window, S::kUnit, first, n);
+      const int len = length_of(a, b);
+      span(len, a.window, S::kUnit, first, n);
       mine += n;
+      if (blockIdx.x == 0 && a.seq_lens[b] > len) atomicOr(a.err, kErrBadPage);
     }
     int upto = mine;
 #pragma unroll
@@ -147,7 +156,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
     for (int w = 0; w < warp; ++w) at += scan[w];
     for (int b = b0; b < min(b0 + per, a.B); ++b) {
       int first, n;
-      span(a.seq_lens[b], a.window, S::kUnit, first, n);
+      span(length_of(a, b), a.window, S::kUnit, first, n);
       cum[b] = at;
       at += n;
     }
@@ -179,7 +188,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
       b = lo;
       before = cum[b];
     }
-    const int len = a.seq_lens[b];
+    const int len = length_of(a, b);
     int first, units;
     span(len, a.window, S::kUnit, first, units);
     const int64_t local = u - (int64_t)before * HS;
@@ -209,7 +218,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
       if (i < n_sub && j >= first && j < key1) {
         const int col = (int)((__umulhi((uint32_t)a.div_mul, (uint32_t)j) + (uint32_t)j) >> a.div_shift);
         slot = j - col * a.kv.page_size;
-        page = col < a.table_width ? table[col] : a.kv.num_pages;
+        page = table[col];   // col < table_width: the length is cut to the table
       }
     };
     auto fetch = [&](int i) {     // the copies of step i, whose pages look_up has found
@@ -539,7 +548,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_join(const AttendArgs a) {
   const int4 seg = a.shared_segs[blockIdx.x];
   if (g == 0) {
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-      if (a.seq_lens[b] > 0) continue;
+      if (length_of(a, b) > 0) continue;
       for (int x = threadIdx.x; x < a.Hq * D / 8; x += kJoinWarps * 32)
         reinterpret_cast<uint4*>(a.out + (int64_t)b * a.Hq * D)[x] = make_uint4(0, 0, 0, 0);
       if (a.lse)
@@ -638,6 +647,8 @@ cudaError_t launch_attend(const AttendArgs& args, int num_sms, cudaStream_t stre
   a.same_strides = a.kv.k_page_stride == a.kv.v_page_stride && a.kv.k_slot_stride == a.kv.v_slot_stride &&
                    a.kv.k_head_stride == a.kv.v_head_stride;
   page_division(a.kv.page_size, a.div_mul, a.div_shift);
+  const int64_t slots = (int64_t)a.table_width * a.kv.page_size;
+  a.max_len = (int)(slots < (1 << 30) ? slots : 1 << 30);
   switch (a.kv.D) {
     case 64: return launch_g<64>(a, num_sms, stream);
     case 128: return launch_g<128>(a, num_sms, stream);

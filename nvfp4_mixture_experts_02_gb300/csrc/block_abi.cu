@@ -120,7 +120,7 @@ ft_status ft_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, i
   if (T > kMaxAppend || Hq > kMaxHeads || rope_dim % 16 != 0 || rope_dim > cache->D)
     return FT_ERR_UNSUPPORTED_SHAPE;
   if (T == 0) return FT_OK;
-  if (!k || !v || !block_table || !positions || (Hq > 0 && (!q || !q_out)) ||
+  if (!k || !v || (B > 0 && table_width > 0 && !block_table) || !positions || (Hq > 0 && (!q || !q_out)) ||
       (rope_dim > 0 && !rope) || (!seq_ids && T > B))
     return FT_ERR_INVALID_ARG;
   if (!aligned(k, 16) || !aligned(v, 16) || (Hq > 0 && (!aligned(q, 16) || !aligned(q_out, 16))) ||
@@ -158,7 +158,7 @@ ft_status ft_paged_decode_attention(const uint16_t* q, int64_t q_stride, int32_t
     return FT_ERR_INVALID_ARG;
   if (B > kMaxSeqs || Hq > kMaxHeads) return FT_ERR_UNSUPPORTED_SHAPE;
   if (B == 0) return FT_OK;
-  if (!q || !block_table || !seq_lens || !out || !workspace) return FT_ERR_INVALID_ARG;
+  if (!q || (table_width > 0 && !block_table) || !seq_lens || !out || !workspace) return FT_ERR_INVALID_ARG;
   if (!aligned(q, 16) || q_stride % 8 != 0 || !aligned(out, 16) || !aligned(lse, 4) ||
       !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(workspace, 256))
     return FT_ERR_MISALIGNED;

@@ -169,6 +169,7 @@ struct AttendArgs {
   int group, gt;           // query heads per key head, 16-head parts of them (set by the launch)
   int same_strides;        // keys and values lie alike (set by the launch)
   int div_mul, div_shift;  // division by the page size (set by the launch)
+  int max_len;             // slots of a row of the block table (set by the launch)
 };
 // Workspace regions (byte offsets, 256-byte aligned), for kAttendBlocks blocks an SM at most, two pieces
 // each.

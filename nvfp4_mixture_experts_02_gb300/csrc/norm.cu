@@ -51,7 +51,7 @@ __device__ __forceinline__ Factor row_factor(float sum, float inv_n, float inv_n
   float left = fmaf(-t, s, 1.f);   // 1 - (v + v_lo) s^2
   left = fmaf(-fmaf(v, s, -t), s, left);
   left = fmaf(-v_lo * s, s, left);
-  const float s_lo = 0.5f * s * left, hi = tg * s;
+  const float s_lo = s > 0.f ? 0.5f * s * left : 0.f, hi = tg * s;   // 0: the sum has overflowed
   return {hi, fmaf(tg, s, -hi) + fmaf(tg, s_lo, tg_lo * s), s + s_lo};
 }
 

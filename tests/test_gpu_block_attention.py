@@ -176,10 +176,18 @@ def test_bad_pages_are_flagged_and_not_followed():
     assert m.get_error(ws) == 6 and m.get_error(ws) == 0
     ref, _, mag = ob.attention(f64(q[1]), ks[1], vs[1], 40, 0.125)
     close(out[1], ref, mag, 2.0 ** -14)                    # the other sequence is as ever
-    n[1] = 49                                              # past the table's three pages
     table[0, 1] = 0
-    m.paged_decode_attention(q, m.PagedKVCache(kc, vc), table, n, workspace=ws)
-    assert m.get_error(ws) == 6
+    n[1] = 48                                              # the table's three pages, then lengths past them
+    kc.nan_to_num_()
+    vc.nan_to_num_()
+    want, _ = m.paged_decode_attention(q, m.PagedKVCache(kc, vc), table, n, workspace=ws)
+    assert m.get_error(ws) == 0
+    for past in (49, 1 << 20, (1 << 31) - 1):
+        n[1] = past
+        out, _ = m.paged_decode_attention(q, m.PagedKVCache(kc, vc), table, n, workspace=ws)
+        assert m.get_error(ws) == 6 and torch.equal(out, want)
+    out, lse = m.paged_decode_attention(q, m.PagedKVCache(kc, vc), table[:, :0].contiguous(), n, workspace=ws)
+    assert m.get_error(ws) == 6 and not out.any() and torch.isneginf(lse).all()
 
 
 def test_offsets_past_32_bits():
