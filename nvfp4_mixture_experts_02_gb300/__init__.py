@@ -6,5 +6,8 @@
     y = ftmoe.decode(x, idx, w, experts, shared)      # T <= 64
     y = ftmoe.prefill(x, idx, w, experts, shared)     # any T
 
+and the operators between two such layers: nvfp4_linear, kv_append, paged_decode_attention,
+residual_norm and residual_norm_backward.
+
 Importing ``ftmoe`` needs the built library; build it with ``build.build()``.
 """

@@ -25,12 +25,12 @@
 // them in order.
 //
 // What bounds it: a weight costs half a conversion, half a multiply and 1/256 of a product per eight
-// tokens on the warp schedulers. At 100003 x 4096 (34 us of memory time): 1 token 42 us, 81 % of the
-// measured copy rate; 5 tokens 44; 16 tokens 56; 32 and 64 tokens 92 and 144 us, where the m16n8k16 rate
+// tokens on the warp schedulers. At 100003 x 4096 (34 us of memory time): 1 token 41 us, 83 % of the
+// measured copy rate; 5 tokens 43; 16 tokens 57; 32 and 64 tokens 87 and 138 us, where the m16n8k16 rate
 // (1024 products per clock and SM: 44 and 88 us) is the larger bound. The same tiles through tcgen05 with
 // the converted weights in tensor memory took 103 us at 16 tokens and 118 at 64: its rate per 128 x 16
 // block does not depend on the tokens, but the hand-over through tensor memory and barriers costs 1.2 us
-// per 128 x 256 weights. Small matrices are bound by latency: 1 x 4096 x 4096 takes 6.3 us for 1.4 us of
+// per 128 x 256 weights. Small matrices are bound by latency: 1 x 4096 x 4096 takes 5.9 us for 1.4 us of
 // memory time, a chain of launch, load, conversion, sum and store.
 #include <cmath>
 #include <cuda_runtime.h>
