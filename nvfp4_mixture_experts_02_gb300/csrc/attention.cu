@@ -7,15 +7,15 @@
 // Every key and value is read once, by one block, for all the query heads that share it: the call
 // is bound by the cache's bytes (4 G operations per key element of 1 or 2 bytes).
 //
-// k_attend: the work is the list of (sequence, key head, unit of keys), in that order; every block
+// k_attend: the work is the list of (sequence, key heads, unit of keys), in that order; every block
 // takes an equal run of it, whatever the lengths, found from the lengths on the device (no host
-// synchronisation). A run covers pieces of one or more (sequence, head) segments. Inside a piece
-// the warps take 16 keys in turn, each with its own ring of asynchronous 16-byte copies (rows of
-// the pages to swizzled shared memory), its own running maximum and sum and its own 16 x D sums in
-// registers; they are joined at the piece's end. A piece that is its whole segment is finished
-// there; the others leave (maximum, sum, sums) in the workspace for k_join, which adds a segment's
-// pieces in order. Masked and missing keys are not read: their rows are zeros in shared memory, so
-// that whatever the pages hold there (NaN, stale values) cannot reach a sum.
+// synchronisation). A run covers pieces of one or more (sequence, key heads) segments. Inside a piece
+// each warp has a key head, or shares it with others and takes 16 or 32 keys in turn, with its own ring of
+// asynchronous 16-byte copies (rows of the pages to swizzled shared memory), its own running maximum and
+// sum and its own 16 x D sums in registers; a head's warps are joined at the piece's end. A piece that
+// is its whole segment is finished there; the others leave (maximum, sum, sums) in the workspace for
+// k_join, which adds a segment's pieces in order. Masked and missing keys are not read: their rows are
+// zeros in shared memory, so that whatever the pages hold there (NaN, stale values) cannot reach a sum.
 //
 // Products, m16n8k16 with float32 sums, the query heads as the eight columns (two groups of columns for
 // nine to sixteen heads): s^T = k q^T and o^T = v^T p^T, so that all 16 rows are keys, then dims, and
@@ -25,10 +25,10 @@
 // exactly, q is f16 after a scaling of its row by a power of two (exact but for elements under 2^-29
 // of the row's largest), p rounds to f16 (11 bits). Statistics and sums are float32.
 //
-// Measured (of the copy rate of 6786 GB/s): three sequences up to 131072, bf16, 962 MB: 151 us (94 %).
-// 48 ragged ones up to 8192, E4M3, 423 MB: 88 us (70 %): the conversions, with few warps to cover their
-// latency, and 128-byte rows 1 KB apart. One sequence of 777: 7.7 us, two launches and the chain length,
-// page, keys, scores, sums, join.
+// Measured (of the copy rate of 6786 GB/s): three sequences up to 131072, bf16, 962 MB: 153 us (93 %).
+// 48 ragged ones up to 8192, E4M3, 423 MB: 83 to 85 us (74 %), of which some 10 us are launches, fill and
+// join, and the runs' pieces differ in cost. One sequence of 777: 7.7 us, two launches and the chain
+// length, page, keys, scores, sums, join.
 #include <cmath>
 #include <cuda_runtime.h>
 
@@ -53,8 +53,16 @@ struct AttnShape {
   static constexpr int kStages = 192 * 1024 / (kBlocks * kWarps * kStageBytes);
   static constexpr int kUnit = kKeys * kWarps;        // keys of a unit
   static constexpr int kRing = kWarps * kStages * kStageBytes;
+  static constexpr int kSumsLd = D + 4;               // floats between heads of a warp's sums, in its ring
+  static_assert(8 * NG * kSumsLd * 4 <= kStages * kStageBytes && kBlocks * kWarps <= attend_warps(D));
 };
 
+// From this many units in a run, the warps of a block take several key heads at once instead of stripes of
+// one head's keys: rows of the same slot are then read together (256 sequences up to 1024, bf16, 8 heads of
+// 128: 97 us for 118; 8 of 32768, E4M3, 8 heads of 64: 54 for 80), and no join in the block holds the
+// copies up. Shorter runs would leave k_join as many times more pieces: 8 sequences up to 2048 14.0 us for 15.5
+// (from 8 units), 48 of 256 12.8 for 17.0 (from 2).
+constexpr int kLongRun = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -109,10 +117,11 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
   using S = AttnShape<D, F8, NG>;
   constexpr int W = S::kWarps, ST = S::kStages, CPR = S::kCpr, KS = D / 16, MT = D / 16;
   constexpr int KT = S::kKeys, NH = KT / 16;   // keys of a step, in 16-row tiles
-  constexpr int LD = D + 4;   // floats between heads where the warps' sums are joined
+  constexpr int LD = S::kSumsLd;
+  constexpr int kUnitLog2 = S::kUnit == 64 ? 6 : S::kUnit == 128 ? 7 : 8;
+  static_assert(S::kUnit == 1 << kUnitLog2);
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ float wm[W][16], wl[W][16];
-  __shared__ float2 joined[16];
+  __shared__ float wm[W][16], wl[W][16], share[W][16];
   __shared__ int scan[W];
   int* cum = reinterpret_cast<int*>(smem + S::kRing);   // [B + 1] units before each sequence (B > 32)
   griddep_launch_dependents();
@@ -174,6 +183,14 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
   int64_t u = quota * blockIdx.x;
   const int64_t u_end = min(u + quota, total);
   const uint32_t ring = smem_addr(smem) + (uint32_t)(warp * ST * S::kStageBytes);
+  // HW heads a block, W / HW stripes of keys each
+  const int hl = quota >= kLongRun ? a.heads_log2 : 0, HW = 1 << hl, stripes = W >> hl;
+  const int hw = warp & (HW - 1), stripe = warp >> hl;
+  const int unit = S::kUnit >> hl;
+  auto sync = [&]() {   // the warps that share a head
+    if (stripes == 1) __syncwarp();
+    else __syncthreads();
+  };
   if (u >= u_end && threadIdx.x == 0) a.shared_segs[blockIdx.x] = make_int4(-1, 0, 0, 0);
 
   while (u < u_end) {
@@ -197,28 +214,27 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
     int first, units;
     span(len, a.window, S::kUnit, first, units);
     const int64_t local = u - (int64_t)before * HS;
-    const int hs = (int)(local / units);
-    const int u0 = (int)(local - (int64_t)hs * units);
-    const int n_units = (int)min((int64_t)(units - u0), u_end - u);
+    const int cost = units << hl;   // of HW heads
+    const int hg = (int)(local / cost);
+    const int u0 = (int)(local - (int64_t)hg * cost);
+    const int n_units = (int)min((int64_t)(cost - u0), u_end - u);
+    const int hs = hg * HW + hw;
     const int kvh = hs / a.gt, g0 = (hs - kvh * a.gt) * 16;
     const int G = min(a.group - g0, 16);
     if (u == quota * blockIdx.x && threadIdx.x == 0) {
-      // for k_join: a segment that runs share belongs to the first run that begins inside it
-      const int64_t s0 = u - u0, s1 = s0 + units;
-      const bool mine = u0 > 0 && u - quota <= s0;
+      // for k_join: the segment that this run goes on with, if it does not begin here
+      const int64_t s0 = u - u0, s1 = s0 + cost;
       a.shared_segs[blockIdx.x] =
-          make_int4(mine ? b : -1, hs, (int)(s0 / quota) * 2 + (s0 % quota != 0), (int)((s1 - 1) / quota));
+          make_int4(u0 > 0 ? b : -1, hg * 16 + hl, (int)(s0 / quota) * 2 + (s0 % quota != 0), (int)((s1 - 1) / quota));
     }
-    const int key0 = (first / S::kUnit + u0) * S::kUnit;
-    const int key1 = min(len, key0 + n_units * S::kUnit);   // keys of the piece: [key0, key1)
-
-    // ---- the ring: step i of this warp = keys key0 + (i * W + warp) * KT ..
-    const int left = key1 - key0 - warp * KT;
-    const int n_sub = left > 0 ? (left + W * KT - 1) / (W * KT) : 0;
+    // this warp's keys of the piece: key0 + i * unit .. + KT - 1 in step i, up to key1
+    const int piece0 = first / S::kUnit * S::kUnit + u0 * unit;
+    const int key1 = min(len, piece0 + n_units * unit), key0 = piece0 + stripe * KT;
+    const int n_sub = key1 > key0 ? (key1 - key0 + unit - 1) >> (kUnitLog2 - hl) : 0;
     const int32_t* table = a.block_table + (int64_t)b * a.table_width;
     int page = -1, slot = 0;
     auto look_up = [&](int i) {   // lane l < KT: the page and slot of key l of step i
-      const int j = key0 + (i * W + warp) * KT + lane % KT;
+      const int j = key0 + i * unit + lane % KT;
       page = -1;
       if (i < n_sub && j >= first && j < key1) {
         const int col = (int)((__umulhi((uint32_t)a.div_mul, (uint32_t)j) + (uint32_t)j) >> a.div_shift);
@@ -236,7 +252,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
             vo = ((int64_t)page * a.kv.v_page_stride + (int64_t)slot * a.kv.v_slot_stride +
                   (int64_t)kvh * a.kv.v_head_stride) * (F8 ? 1 : 2);
         } else if (lane < KT) {
-          const int j = key0 + (i * W + warp) * KT + lane;
+          const int j = key0 + i * unit + lane;
           if (j >= first && j < key1) atomicOr(a.err, kErrBadPage);   // no such page: read as zeros
         }
         const uint32_t st = ring + (uint32_t)((i % ST) * S::kStageBytes);
@@ -316,6 +332,9 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
     for (int i = 0; i < n_sub; ++i) {
       cp_async_wait<ST - 2>();
       __syncwarp();
+      // the next copies go into the stage that the previous step has left
+      fetch(i + ST - 1);
+      look_up(i + ST);
       const uint32_t st = ring + (uint32_t)((i % ST) * S::kStageBytes);
       // s^T = k q^T: 16 keys a tile
       float s[NG][NH][4];
@@ -352,12 +371,9 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
             }
           }
       }
-      // the next copies go into the stage that the previous step has left
-      fetch(i + ST - 1);
-      look_up(i + ST);
       // scores in log2 units: key j0 + 16 h + r (elements 0, 1) and + 8; keys outside [first, key1)
       // do not count
-      const int j0 = key0 + (i * W + warp) * KT;
+      const int j0 = key0 + i * unit;
       bool up = false;
       float top[NG][2];
 #pragma unroll
@@ -469,9 +485,9 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
     }
     cp_async_wait<0>();
 
-    // ---- join the warps: sums [warp][head][LD] in the ring's memory
-    __syncthreads();
-    float* sums = reinterpret_cast<float*>(smem) + (size_t)warp * (8 * NG) * LD;
+    // ---- join the warps of a head: sums [head][LD] in each one's ring
+    sync();
+    float* sums = reinterpret_cast<float*>(smem + (size_t)warp * ST * S::kStageBytes);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
 #pragma unroll
@@ -493,126 +509,167 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
         }
       }
     }
-    __syncthreads();
-    // the warps' factors and the joined maximum and sum of each head
-    if (threadIdx.x < 16) {
-      const int g = threadIdx.x;
-      float top = -INFINITY, sum = 0.f;
+    sync();
+    // each warp's share in its heads' sums, and the joined maximum and sum
+    float2 ms = make_float2(-INFINITY, 0.f);
+    if (lane < G) {
 #pragma unroll
-      for (int w = 0; w < W; ++w) top = fmaxf(top, g < G ? wm[w][g] : -INFINITY);
-      const float base = top == -INFINITY ? 0.f : top;
+      for (int s = 0; s < W; ++s)
+        if (s < stripes) ms.x = fmaxf(ms.x, wm[hw + (s << hl)][lane]);
+      const float base = ms.x == -INFINITY ? 0.f : ms.x;
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const float f = g < G ? exp2_fast(wm[w][g] - base) : 0.f;
-        wm[w][g] = f;
-        sum = fmaf(f, g < G ? wl[w][g] : 0.f, sum);
-      }
-      joined[g] = make_float2(top, sum);
+      for (int s = 0; s < W; ++s)
+        if (s < stripes)
+          ms.y = fmaf(exp2_fast(wm[hw + (s << hl)][lane] - base), wl[hw + (s << hl)][lane], ms.y);
+      share[warp][lane] = exp2_fast(wm[warp][lane] - base);
     }
-    __syncthreads();
-    const bool whole = n_units == units;
-    const int64_t part = 2 * (int64_t)blockIdx.x + (u == quota * blockIdx.x ? 0 : 1);
-    for (int x = threadIdx.x; x < G * (D / 4); x += W * 32) {   // four dims of a head
-      const int g = x / (D / 4), d = (x - g * (D / 4)) * 4;
+    sync();
+    const bool whole = n_units == cost;
+    const int64_t part = ((2 * (int64_t)blockIdx.x + (u == quota * blockIdx.x ? 0 : 1)) * W + hw) * 16;
+    const int64_t row = (int64_t)b * a.Hq + kvh * a.group + g0;
+    if (lane < G && stripe == 0) {
+      if (!whole) *reinterpret_cast<float2*>(a.part_ml + (part + lane) * 2) = ms;
+      else if (a.lse) a.lse[row + lane] = (ms.x + log2f(ms.y)) * kLn2;
+    }
+    for (int x = stripe * 32; x < G * (D / 4); x += stripes * 32) {   // four dims of a head a lane
+      const int g = (x + lane) / (D / 4), d = (x + lane) % (D / 4) * 4;
+      const float sum = __shfl_sync(0xffffffffu, ms.y, g);
+      if (g >= G) continue;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const float f = wm[w][g];
-        const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem) +
-                                                          (size_t)(w * (8 * NG) + g) * LD + d);
+      for (int s = 0; s < W; ++s) {
+        if (s >= stripes) break;
+        const int w = hw + (s << hl);
+        const float f = share[w][g];
+        const float4 y = *reinterpret_cast<const float4*>(
+            reinterpret_cast<const float*>(smem + (size_t)w * ST * S::kStageBytes) + g * LD + d);
         v.x = fmaf(f, y.x, v.x); v.y = fmaf(f, y.y, v.y);
         v.z = fmaf(f, y.z, v.z); v.w = fmaf(f, y.w, v.w);
       }
-      const float2 ms = joined[g];
-      const int64_t row = (int64_t)b * a.Hq + kvh * a.group + g0 + g;
-      if (whole) {
-        store_row(a, row * D + d, v, ms.y);
-        if (d == 0 && a.lse) a.lse[row] = (ms.x + log2f(ms.y)) * kLn2;
-      } else {
-        *reinterpret_cast<float4*>(a.part_o + (part * 16 + g) * D + d) = v;
-        if (d == 0) *reinterpret_cast<float2*>(a.part_ml + (part * 16 + g) * 2) = ms;
-      }
+      if (whole) store_row(a, (row + g) * D + d, v, sum);
+      else *reinterpret_cast<float4*>(a.part_o + (part + g) * D + d) = v;
     }
-    __syncthreads();   // before the ring is filled again
+    sync();   // before the ring is filled again
     u += n_units;
   }
 }
 
-// Segments that several runs share, and empty sequences. Block (i, g): head g of the segment that run i
-// has left for it, if any; its pieces in order, eight warps a share of them each, joined in order. The
-// blocks also zero the heads of empty sequences.
-constexpr int kJoinWarps = 8;
-template <int D>
+// Segments that several runs share, and empty sequences. Block i belongs to run i: with the blocks of the
+// other runs that go on with the same segment it shares that segment's query heads. A head is a job of one
+// to kTeam warps, more where the pieces are many and the jobs few: each adds a share of the pieces in
+// order, the first of them adds the shares in order. The blocks also zero the heads of empty sequences. W:
+// warps of k_attend's blocks.
+constexpr int kJoinWarps = 16, kTeam = 8;   // warps of a block, of a job at most
+constexpr int kFlight = 4;                  // pieces of a warp in flight
+template <int D, int W>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_join(const AttendArgs a) {
-  __shared__ __align__(16) float sums[kJoinWarps][D];
-  __shared__ float wm[kJoinWarps], wl[kJoinWarps];
+  constexpr int E = D / 32;
+  __shared__ float sums[kJoinWarps][D], wm[kJoinWarps], wl[kJoinWarps];
   griddep_launch_dependents();
   griddep_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = blockIdx.y;
-  // sequence or -1, part of its heads, first run (* 2, + 1 where it begins inside that run), last run
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // sequence or -1; its part, * 16 + log2 of the key heads in it; first run (* 2, + 1 where the segment
+  // begins inside that run); last run
   const int4 seg = a.shared_segs[blockIdx.x];
-  if (g == 0) {
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-      if (length_of(a, b) > 0) continue;
-      for (int x = threadIdx.x; x < a.Hq * D / 8; x += kJoinWarps * 32)
-        reinterpret_cast<uint4*>(a.out + (int64_t)b * a.Hq * D)[x] = make_uint4(0, 0, 0, 0);
-      if (a.lse)
-        for (int x = threadIdx.x; x < a.Hq; x += kJoinWarps * 32)
-          a.lse[(int64_t)b * a.Hq + x] = -INFINITY;
-    }
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    if (length_of(a, b) > 0) continue;
+    for (int x = threadIdx.x; x < a.Hq * D / 8; x += kJoinWarps * 32)
+      reinterpret_cast<uint4*>(a.out + (int64_t)b * a.Hq * D)[x] = make_uint4(0, 0, 0, 0);
+    if (a.lse)
+      for (int x = threadIdx.x; x < a.Hq; x += kJoinWarps * 32)
+        a.lse[(int64_t)b * a.Hq + x] = -INFINITY;
   }
   if (seg.x < 0) return;
-  const int kvh = seg.y / a.gt, g0 = (seg.y - kvh * a.gt) * 16;
-  if (g0 + g >= a.group) return;
-  constexpr int E = D / 32;
-  float m = -INFINITY, l = 0.f, v[E];
+  const int heads = min(a.group, 16), hl = seg.y & 15, jobs = heads << hl;
+  const int run0 = seg.z >> 1, blocks = seg.w - run0, me = (int)blockIdx.x - run0 - 1;
+  const int mine = (jobs - me + blocks - 1) / blocks;   // jobs me, me + blocks, ..
+  int tl = 0;   // log2 of the warps of a job
+  while (2 << tl <= kTeam && kFlight << tl <= blocks && mine << (tl + 1) <= kJoinWarps) ++tl;
+  const int team = warp >> tl, part = warp & ((1 << tl) - 1), teams = kJoinWarps >> tl;
+  for (int i0 = 0; i0 < mine; i0 += teams) {
+    const int job = me + (i0 + team) * blocks;
+    const int hw = job / heads, g = job - hw * heads;
+    const int hs = ((seg.y >> 4) << hl) + hw, kvh = a.gt == 1 ? hs : hs / a.gt, g0 = (hs - kvh * a.gt) * 16;
+    const bool on = job < jobs && g0 + g < a.group;
+    float m = -INFINITY, l = 0.f, v[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) v[e] = 0.f;
-#pragma unroll 2
-  for (int p = (seg.z >> 1) + warp; p <= seg.w; p += kJoinWarps) {
-    // a run's first piece, but for a segment that begins inside its first run
-    const int64_t at = (2 * (int64_t)p + (p == seg.z >> 1 ? seg.z & 1 : 0)) * 16 + g;
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
-    float y[E];
+    for (int e = 0; e < E; ++e) v[e] = 0.f;
+    if (on) {
+      for (int p0 = run0 + part; p0 <= seg.w; p0 += kFlight << tl) {
+        float2 ml[kFlight];
+        float y[kFlight][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) y[e] = a.part_o[at * D + lane + 32 * e];
-    const float n = fmaxf(m, ml.x), base = n == -INFINITY ? 0.f : n;
-    const float f0 = exp2_fast(m - base), f1 = exp2_fast(ml.x - base);
-    m = n;
-    l = fmaf(l, f0, ml.y * f1);
+        for (int j = 0; j < kFlight; ++j) {
+          const int p = p0 + (j << tl);
+          // a run's first piece, but for a segment that begins inside its first run
+          const int64_t at = ((2 * (int64_t)p + (p == run0 ? seg.z & 1 : 0)) * W + hw) * 16 + g;
+          ml[j] = make_float2(-INFINITY, 0.f);
+          if (p <= seg.w) ml[j] = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = fmaf(v[e], f0, y[e] * f1);
+          for (int e = 0; e < E; ++e) y[j][e] = p <= seg.w ? a.part_o[at * D + lane + 32 * e] : 0.f;
+        }
+        float top = m;
+#pragma unroll
+        for (int j = 0; j < kFlight; ++j) top = fmaxf(top, ml[j].x);
+        const float base = top == -INFINITY ? 0.f : top, f = exp2_fast(m - base);
+        m = top;
+        l *= f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] *= f;
+#pragma unroll
+        for (int j = 0; j < kFlight; ++j) {
+          const float fj = exp2_fast(ml[j].x - base);
+          l = fmaf(fj, ml[j].y, l);
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[e] = fmaf(fj, y[j][e], v[e]);
+        }
+      }
+    }
+    if (tl > 0) {   // uniform over the block, as are i0 and mine
+#pragma unroll
+      for (int e = 0; e < E; ++e) sums[warp][lane + 32 * e] = v[e];
+      if (lane == 0) {
+        wm[warp] = m;
+        wl[warp] = l;
+      }
+      __syncthreads();
+      if (part == 0) {
+        float top = m;
+#pragma unroll
+        for (int w = 1; w < kTeam; ++w)
+          if (w < 1 << tl) top = fmaxf(top, wm[warp + w]);
+        const float base = top == -INFINITY ? 0.f : top, f0 = exp2_fast(m - base);
+        m = top;
+        l *= f0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] *= f0;
+#pragma unroll
+        for (int w = 1; w < kTeam; ++w) {
+          if (w >= 1 << tl) break;
+          const float f = exp2_fast(wm[warp + w] - base);
+          l = fmaf(f, wl[warp + w], l);
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[e] = fmaf(f, sums[warp + w][lane + 32 * e], v[e]);
+        }
+      }
+      __syncthreads();
+    }
+    if (on && part == 0) {
+      const int64_t row = (int64_t)seg.x * a.Hq + kvh * a.group + g0 + g;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        a.out[row * D + lane + 32 * e] =
+            (uint16_t)(pack_bf16(l == 0.f ? 0.f : v[e] / l * a.kv.v_scale, 0.f) & 0xFFFFu);
+      if (lane == 0 && a.lse) a.lse[row] = (m + log2f(l)) * kLn2;
+    }
   }
-#pragma unroll
-  for (int e = 0; e < E; ++e) sums[warp][lane + 32 * e] = v[e];
-  if (lane == 0) {
-    wm[warp] = m;
-    wl[warp] = l;
-  }
-  __syncthreads();
-  if (threadIdx.x >= D / 4) return;
-  const int d = threadIdx.x * 4;
-  float top = -INFINITY, sum = 0.f;
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, wm[w]);
-  const float from = top == -INFINITY ? 0.f : top;
-  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
-    const float f = exp2_fast(wm[w] - from);
-    sum = fmaf(f, wl[w], sum);
-    const float4 x = *reinterpret_cast<const float4*>(&sums[w][d]);
-    y.x = fmaf(f, x.x, y.x); y.y = fmaf(f, x.y, y.y);
-    y.z = fmaf(f, x.z, y.z); y.w = fmaf(f, x.w, y.w);
-  }
-  const int64_t row = (int64_t)seg.x * a.Hq + kvh * a.group + g0 + g;
-  store_row(a, row * D + d, y, sum);
-  if (d == 0 && a.lse) a.lse[row] = (top + log2f(sum)) * kLn2;
 }
 
 template <int D, bool F8, int NG>
-cudaError_t launch_d(const AttendArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_d(AttendArgs a, int num_sms, cudaStream_t stream) {
   using S = AttnShape<D, F8, NG>;
+  a.heads_log2 = 0;
+  while (2 << a.heads_log2 <= S::kWarps && a.kv.Hkv * a.gt % (2 << a.heads_log2) == 0) ++a.heads_log2;
   const size_t smem = S::kRing + (a.B > 32 ? (size_t)(a.B + 1) * 4 : 0);
   cudaError_t e;
   static SmemGrant grant;   // for the most sequences that a call may have
@@ -629,10 +686,9 @@ cudaError_t launch_d(const AttendArgs& a, int num_sms, cudaStream_t stream) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, k_attend<D, F8, NG>, a)) != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)grid, (unsigned)(a.group < 16 ? a.group : 16));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, k_join<D>, a);
+  return cudaLaunchKernelEx(&cfg, k_join<D, S::kWarps>, a);
 }
 
 template <int D>

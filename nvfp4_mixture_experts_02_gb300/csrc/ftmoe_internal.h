@@ -170,18 +170,20 @@ struct AttendArgs {
   int same_strides;        // keys and values lie alike (set by the launch)
   int div_mul, div_shift;  // division by the page size (set by the launch)
   int max_len;             // slots of a row of the block table (set by the launch)
+  int heads_log2;          // log2 of the key heads that a block may take at once (set by the launch)
 };
-// Workspace regions (byte offsets, 256-byte aligned), for kAttendBlocks blocks an SM at most, two pieces
-// each.
+// Workspace regions (byte offsets, 256-byte aligned), for kAttendBlocks blocks and attend_warps warps an SM
+// at most, two pieces each, 16 query heads a piece.
 constexpr int kAttendBlocks = 3;
+constexpr int attend_warps(int D) { return D == 64 ? 16 : D == 128 ? 12 : 8; }
 struct AttendLayout {
   size_t segs = 0, ml = 0, o = 0, total = 0;
   AttendLayout(int D, int num_sms) {
     segs = 1024;
-    const size_t runs = (size_t)num_sms * kAttendBlocks;
-    ml = align_up(segs + runs * 16, 256);
-    o = align_up(ml + runs * 2 * 16 * 2 * 4, 256);
-    total = align_up(o + runs * 2 * 16 * D * 4, 256);
+    const size_t rows = (size_t)num_sms * attend_warps(D) * 2 * 16;
+    ml = align_up(segs + (size_t)num_sms * kAttendBlocks * 16, 256);
+    o = align_up(ml + rows * 2 * 4, 256);
+    total = align_up(o + rows * D * 4, 256);
   }
 };
 cudaError_t launch_attend(const AttendArgs& a, int num_sms, cudaStream_t stream);

@@ -114,6 +114,21 @@ def test_many_short_sequences():
     check([int(n) for n in rng.integers(0, 40, 700)], 16, 2, 2, 64, torch.bfloat16, 4)
 
 
+@pytest.mark.parametrize("D,dtype,Hq,Hkv,window", [
+    (128, torch.bfloat16, 32, 8, 0), (128, F8, 64, 8, 0), (128, F8, 4, 2, 0), (128, torch.bfloat16, 6, 6, 777),
+    (128, F8, 9, 3, 0), (64, torch.bfloat16, 16, 4, 0), (64, F8, 16, 8, 0), (64, F8, 44, 4, 1501),
+    (256, torch.bfloat16, 8, 4, 0), (256, F8, 34, 2, 0), (128, torch.bfloat16, 80, 4, 0)])
+def test_several_key_heads_of_a_block(D, dtype, Hq, Hkv, window):
+    # work enough for long runs on every block; sequences that end and begin inside them
+    unit = 256 if D == 64 and dtype == F8 else 128
+    segments = Hkv * -(-Hq // Hkv // 16)
+    keys = 1900 * unit // segments
+    lens = [int(keys * x) + 1 for x in (0.4, 0.13, 0.2, 0.17, 0.1)] + [0, 1, 130]
+    if window:
+        lens = [n + 3 * window // 2 for n in lens] + [window + 5] * (keys // window)
+    check(lens, 48, Hq, Hkv, D, dtype, D + Hq, window=window)
+
+
 def test_large_scores_do_not_overflow():
     check([40, 300], 16, 4, 2, 64, torch.bfloat16, 5, scale=0.0)
     m = ftmoe()
