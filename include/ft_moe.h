@@ -326,7 +326,7 @@ size_t ft_nvfp4_linear_workspace_bytes(int32_t T, int32_t K);
 
 /*
  * ft_nvfp4_linear — y_t = W x_t for 0 <= T <= 64 tokens (T = 0 is a no-op): one launch for up to 8
- * tokens, or 32 of a matrix with few rows; two or three (x's layout, the products, the join) otherwise.
+ * tokens, or more of a matrix with few rows; two or three (x's layout, products, join) otherwise.
  *   x        bf16, token t at x + t * x_stride (16-byte aligned; x_stride a multiple of 8, >= K)
  *   out      [T, N], bf16 (out_f32 = 0, 2-byte aligned) or float (out_f32 = 1, 4-byte aligned),
  *            fully overwritten; float32 sums, the matrix's scale last, rounded once

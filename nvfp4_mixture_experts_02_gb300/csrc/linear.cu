@@ -15,8 +15,8 @@
 // fewer row tiles than SMs or x does not fit one block. Partial sums are added in a fixed order (warps
 // in shared memory, blocks through the cluster's).
 //
-// k_linear_mid (9 to 32 tokens, few rows): the same in one launch with tiles of 128 rows and K over a
-// cluster, each of whose blocks lays its own slice of x out.
+// k_linear_mid (from 9 tokens, few rows): the same in one launch with tiles of 128 rows by 16 or 32
+// tokens and K over a cluster, each of whose blocks lays its own slice of x out.
 //
 // k_linear_more (9 to 64 tokens, many rows): a launch of its own lays x out (k_linear_x). The work is
 // the list of (256-row tile, 256 elements of K); each block takes an equal run of it. Every warp has 32
@@ -680,12 +680,13 @@ template <int NT>
 cudaError_t launch_mid(LinearArgs a, int num_sms, cudaStream_t stream) {
   constexpr int TOK = NT * 8;
   const int tiles = (a.N + kMidRows - 1) / kMidRows, pieces = (a.K + 127) / 128;
+  const int groups = (a.T + TOK - 1) / TOK;
   auto x_bytes = [&](int split) { return (size_t)((pieces + split - 1) / split) * 256 * TOK; };
   // K over a cluster while twice the blocks are at most two an SM and every warp keeps a piece, and
   // while x does not fit
   int split = 1;
   while (split < 8 && (x_bytes(split) > kLinXMax / 2 ||
-                       (tiles * split <= num_sms && pieces >= 4 * split)))
+                       (tiles * groups * split <= num_sms && pieces >= 4 * split)))
     split *= 2;
   a.split = split;
   const size_t sums = (size_t)TOK * (kMidRows + 4) * 4;
@@ -693,7 +694,7 @@ cudaError_t launch_mid(LinearArgs a, int num_sms, cudaStream_t stream) {
   static SmemGrant grant;
   const cudaError_t e = grant_smem(grant, k_linear_mid<NT>, (int)kLinXMax);
   if (e != cudaSuccess) return e;
-  return start(k_linear_mid<NT>, dim3((unsigned)(tiles * split), (unsigned)((a.T + TOK - 1) / TOK)),
+  return start(k_linear_mid<NT>, dim3((unsigned)(tiles * split), (unsigned)groups),
                kLinWarps * 32, smem, split, stream, a);
 }
 
@@ -722,13 +723,18 @@ cudaError_t launch_more(const LinearArgs& a, int num_sms, cudaStream_t stream) {
 cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream) {
   // From 64 rows per SM on the wider forms win (us, K = 4096): one token, 16- or 32-row tiles: 6.3 or
   // 6.8 at 4096 rows, 48 or 42 at 100003; 32 tokens, one launch or three: 12.3 or 14.5 at 4096 rows, 37
-  // or 29 at 20000. Past 32 tokens one launch would read the matrix twice: 23 or 16 us at 64 tokens.
+  // or 29 at 20000.
   const bool wide = a.N >= 64 * num_sms;
   if (a.T <= kLinearFew)
     return wide ? launch_few<2, 2>(a, num_sms, stream) : launch_few<1, 4>(a, num_sms, stream);
   const int nt = (a.T + 7) / 8;
-  if (!wide && nt <= 4)
-    return nt <= 2 || a.K > 16384 ? launch_mid<2>(a, num_sms, stream) : launch_mid<4>(a, num_sms, stream);
+  // Groups of 16 tokens on blocks of their own read the matrix again, from L2, but where SMs are idle
+  // otherwise that pays (us, one group or groups of 16): 32 tokens 8.7 or 6.4 at 2048 x 2048, 11.6 or 10.9 at
+  // 4096 x 4096, 30 or 33 at 8000 x 8192; 64 tokens, three launches or groups of 16: 10.8 or 7.6 at 2048 x 2048, 15.6 or 10.7 at 2048 x 4096.
+  const int tiles = (a.N + kMidRows - 1) / kMidRows;
+  if (!wide && (nt <= 2 || tiles * ((nt + 1) / 2) * 2 <= num_sms || (nt <= 4 && a.K > 16384)))
+    return launch_mid<2>(a, num_sms, stream);
+  if (!wide && nt <= 4) return launch_mid<4>(a, num_sms, stream);
   if (nt <= 2) return launch_more<2>(a, num_sms, stream);
   if (nt <= 4) return launch_more<4>(a, num_sms, stream);
   if (nt <= 6) return launch_more<6>(a, num_sms, stream);

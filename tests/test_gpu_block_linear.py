@@ -48,6 +48,12 @@ def test_odd_sizes(T, N, K):
     check(T, N, K, torch.float32, N + K)
 
 
+@pytest.mark.parametrize("T", [17, 32, 33, 40, 49, 64])
+@pytest.mark.parametrize("N", [2333, 4777, 5003])
+def test_token_groups(T, N):
+    check(T, N, 608, torch.bfloat16, T + N)
+
+
 @pytest.mark.parametrize("T", [1, 8, 32])
 def test_many_rows(T):
     check(T, 20011, 512, torch.bfloat16, 3)
