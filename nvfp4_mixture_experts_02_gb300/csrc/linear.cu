@@ -30,8 +30,9 @@
 // (1024 products per clock and SM: 44 and 88 us) is the larger bound. The same tiles through tcgen05 with
 // the converted weights in tensor memory took 103 us at 16 tokens and 118 at 64: its rate per 128 x 16
 // block does not depend on the tokens, but the hand-over through tensor memory and barriers costs 1.2 us
-// per 128 x 256 weights. Small matrices are bound by latency: 1 x 4096 x 4096 takes 5.9 us for 1.4 us of
-// memory time, a chain of launch, load, conversion, sum and store.
+// per 128 x 256 weights. Small matrices are bound by latency: 1 x 4096 x 4096 takes 4.6 us for 1.4 us of
+// memory time, a chain of launch, x's layout, load, conversion, sum and store; two pieces ahead beat four
+// there (5.2 or 5.9 us before x's layout was one token's own code).
 #include <cmath>
 #include <cuda_runtime.h>
 
@@ -195,16 +196,17 @@ __device__ __forceinline__ int x_unit(int k, int n, int tok) {
   return (((k >> 7) * 4 + (k8 & 3)) * tok + n) * 4 + (k8 >> 2);
 }
 
-// x of tokens n0 .. n0 + 3 (of T), elements [ka, kb), to f16 at dst (units of the block's slice, which
+// x of tokens n0 .. n0 + TN - 1 (of T), elements [ka, kb), to f16 at dst (units of the block's slice, which
 // begins at element k0), with a power of two per token in down[]. One warp; up to 512 elements stay in
-// registers between the search for the largest and the conversion, four tokens' loads at a time.
+// registers between the search for the largest and the conversion, TN tokens' loads at a time.
+template <int TN>
 __device__ __forceinline__ void stage_x(const LinearArgs& a, int t0, int n0, int T, int ka, int kb, int k0,
                                         int tok, uint4* dst, float* down) {
   const int lane = threadIdx.x & 31;
   const uint16_t* x = a.x + (size_t)(t0 + n0) * a.x_stride;
-  const int cnt = min(T - n0, 4);
-  uint4 v[4][2];
-  uint32_t top[4] = {0, 0, 0, 0};
+  const int cnt = min(T - n0, TN);
+  uint4 v[TN][2];
+  uint32_t top[TN] = {};
   auto get = [&](int j, int k) {
     return j < cnt && k < kb && k < a.K
                ? *reinterpret_cast<const uint4*>(x + (size_t)j * a.x_stride + k)
@@ -213,17 +215,17 @@ __device__ __forceinline__ void stage_x(const LinearArgs& a, int t0, int n0, int
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j][i] = get(j, ka + lane * 8 + i * 256);
+    for (int j = 0; j < TN; ++j) v[j][i] = get(j, ka + lane * 8 + i * 256);
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < TN; ++j)
 #pragma unroll
     for (int i = 0; i < 2; ++i) pair_top(top[j], v[j][i]);
   for (int k = ka + lane * 8 + 512; k < kb; k += 256)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) pair_top(top[j], get(j, k));
-  uint32_t up[4];
+    for (int j = 0; j < TN; ++j) pair_top(top[j], get(j, k));
+  uint32_t up[TN];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < TN; ++j) {
     float most = warp_max(top_of(top[j]));
     if (most == INFINITY) {   // an infinity among them: the largest finite one (uniform, rare)
       most = 0.f;
@@ -238,13 +240,13 @@ __device__ __forceinline__ void stage_x(const LinearArgs& a, int t0, int n0, int
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < TN; ++j) {
       const int k = ka + lane * 8 + i * 256;
       if (j < cnt && k < kb) dst[x_unit(k - k0, n0 + j, tok)] = to_f16(v[j][i], up[j]);
     }
   for (int k = ka + lane * 8 + 512; k < kb; k += 256)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < TN; ++j)
       if (j < cnt) dst[x_unit(k - k0, n0 + j, tok)] = to_f16(get(j, k), up[j]);
 }
 
@@ -301,8 +303,12 @@ __global__ void __launch_bounds__(kLinWarps * 32, 2) k_linear_few(const LinearAr
 
   // this warp's slice of x
   uint4* xs = reinterpret_cast<uint4*>(few_smem);
-  for (int n = 0; n < T; n += 4)
-    stage_x(a, 0, n, T, p0 * 128, p1 * 128, b0 * 128, T, xs, down[warp]);
+  if (T == 1) {
+    stage_x<1>(a, 0, 0, T, p0 * 128, p1 * 128, b0 * 128, T, xs, down[warp]);
+  } else {
+    for (int n = 0; n < T; n += 2)
+      stage_x<2>(a, 0, n, T, p0 * 128, p1 * 128, b0 * 128, T, xs, down[warp]);
+  }
   __syncwarp();
   const float d0 = 2 * q < T ? down[warp][2 * q] : 0.f;
   const float d1 = 2 * q + 1 < T ? down[warp][2 * q + 1] : 0.f;
@@ -396,7 +402,7 @@ __global__ void __launch_bounds__(kLinWarps * 32, NT <= 4 ? 2 : 1) k_linear_mid(
   for (int job = warp; job < (T + 3) / 4 * WK; job += kLinWarps) {
     const int s = job & 1, n = (job >> 1) * 4;
     const int c0 = min(b0 + s * np, b1), c1 = min(c0 + np, b1);
-    stage_x(a, t0, n, T, c0 * 128, c1 * 128, b0 * 128, TOK, xs, down[s]);
+    stage_x<4>(a, t0, n, T, c0 * 128, c1 * 128, b0 * 128, TOK, xs, down[s]);
   }
   __syncthreads();
   float acc[2][NT][4];
@@ -721,12 +727,12 @@ cudaError_t launch_more(const LinearArgs& a, int num_sms, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream) {
-  // From 64 rows per SM on the wider forms win (us, K = 4096): one token, 16- or 32-row tiles: 6.3 or
-  // 6.8 at 4096 rows, 48 or 42 at 100003; 32 tokens, one launch or three: 12.3 or 14.5 at 4096 rows, 37
-  // or 29 at 20000.
+  // Up to 8 tokens: 32-row tiles once 16-row ones take more than one round of the resident blocks (us, one
+  // token, K = 4096, 16- or 32-row tiles: 4.6 or 5.6 at 4096 rows, 6.2 or 6.3 at 5120, 6.8 or 6.4 at 6144,
+  // 46 or 41 at 100003). 32 tokens, one launch or three: 12.3 or 14.5 at 4096 rows, 37 or 29 at 20000.
   const bool wide = a.N >= 64 * num_sms;
   if (a.T <= kLinearFew)
-    return wide ? launch_few<2, 2>(a, num_sms, stream) : launch_few<1, 4>(a, num_sms, stream);
+    return a.N > 32 * num_sms ? launch_few<2, 2>(a, num_sms, stream) : launch_few<1, 2>(a, num_sms, stream);
   const int nt = (a.T + 7) / 8;
   // Groups of 16 tokens on blocks of their own read the matrix again, from L2, but where SMs are idle
   // otherwise that pays (us, one group or groups of 16): 32 tokens 8.7 or 6.4 at 2048 x 2048, 11.6 or 10.9 at
