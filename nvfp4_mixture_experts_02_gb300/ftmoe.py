@@ -9,6 +9,7 @@ on every call.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import NamedTuple
@@ -879,6 +880,14 @@ def paged_attention_workspace_bytes(B, D) -> int:
     return _LIB.ft_paged_attention_workspace_bytes(B, D)
 
 
+@functools.lru_cache(maxsize=1024)
+def _attention_bytes(B, D, dev) -> int:   # a size of the device's, asked for once
+    n = _LIB.ft_paged_attention_workspace_bytes(B, D)
+    if n == 0:
+        raise FtError(2, "ft_paged_attention_workspace_bytes")
+    return n
+
+
 def paged_decode_attention(q, cache: PagedKVCache, block_table, seq_lens, scale=None, window=0,
                            out=None, lse=None, workspace=None, stream=None):
     """ft_paged_decode_attention: q bf16 [B,Hq,D], one new token per sequence, over the first
@@ -905,10 +914,7 @@ def paged_decode_attention(q, cache: PagedKVCache, block_table, seq_lens, scale=
     if workspace is not None:
         _need(workspace, "workspace", dev, None, None)
     elif B > 0:
-        n = _LIB.ft_paged_attention_workspace_bytes(B, D)
-        if n == 0:
-            raise FtError(2, "ft_paged_attention_workspace_bytes")
-        workspace = _scratch(n, dev, stream)
+        workspace = _scratch(_attention_bytes(B, D, dev), dev, stream)
     st = _LIB.ft_paged_decode_attention(
         q.data_ptr(), qs, B, Hq, cache._ref, block_table.data_ptr(), width, seq_lens.data_ptr(),
         D ** -0.5 if scale is None else scale, window, out.data_ptr(), lse.data_ptr(),
@@ -988,6 +994,14 @@ class NormGradients(NamedTuple):
     dgate: torch.Tensor | None
 
 
+@functools.lru_cache(maxsize=1024)
+def _norm_backward_bytes(T, H, dev) -> int:
+    n = _LIB.ft_residual_norm_backward_workspace_bytes(T, H)
+    if n == 0:
+        raise FtError(2, "ft_residual_norm_backward_workspace_bytes")
+    return n
+
+
 def residual_norm_backward(y, residual, d_r, d_x=None, w_post=None, w_pre=None, gate=None,
                            scale=1.0, eps=1e-6, workspace=None, stream=None) -> NormGradients:
     """ft_residual_norm_backward: the gradient of residual_norm for d_r (of r', its type; None: zero)
@@ -1019,10 +1033,7 @@ def residual_norm_backward(y, residual, d_r, d_x=None, w_post=None, w_pre=None, 
     if workspace is not None:
         _need(workspace, "workspace", dev, None, None)
     elif T > 0:
-        n = _LIB.ft_residual_norm_backward_workspace_bytes(T, H)
-        if n == 0:
-            raise FtError(2, "ft_residual_norm_backward_workspace_bytes")
-        workspace = _scratch(n, dev, stream)
+        workspace = _scratch(_norm_backward_bytes(T, H, dev), dev, stream)
     st = _LIB.ft_residual_norm_backward(
         y.data_ptr(), 0 if residual is None else residual.data_ptr(),
         0 if w_post is None else w_post.data_ptr(), 0 if w_pre is None else w_pre.data_ptr(), gp,
