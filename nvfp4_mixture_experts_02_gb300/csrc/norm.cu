@@ -18,7 +18,7 @@
 // block's rows; k_norm_cols adds the blocks' sums.
 //
 // Measured (of the copy rate of 6786 GB/s): forward 8191 x 4096 with a float32 stream 71 us (84 %), 8192 x
-// 8192 95 us (83 %); gradient 8192 x 8192 170 us (70 %), where about half of a row's 3 us is arithmetic
+// 8192 95 us (83 %); gradient 8192 x 8192 171 us (70 %), where about half of a row's 3 us is arithmetic
 // (9 unpackings and 9 packed operations an element) and two barriers; 2048 x 16384 168 us (35 %: 32 columns
 // a thread spill). One token: 2.9 us, a launch and three dependent latencies.
 #include <cuda_runtime.h>
@@ -155,10 +155,11 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 1024) k_norm(const Nor
   }
 }
 
-// The gradient. A block of 512 threads is RG row groups of GT threads, 8 NV columns per thread; a group's rows come whole by bulk copies into its ring of stages, so that the next rows
-// travel while one is worked on. A row's values are read from shared memory where they are used; r', h
-// and the column sums stay in registers. Two barriers a row: the sum that y needs is taken for the next
-// row together with the last sums of this one.
+// The gradient. A block of 512 threads is RG row groups of GT threads, 8 NV columns per thread; a group's
+// rows come whole by bulk copies into its ring of stages, so that the next rows travel while one is worked
+// on. A row's values are read from shared memory where they are used; r', h and the column sums stay in
+// registers. Two barriers a row: the sum that y needs is taken for the next row together with the last
+// sums of this one.
 constexpr int kRingThreads = 512;
 constexpr size_t kRingBytes = 224 * 1024;   // one stage of the widest rows: 16384, float32, every input
 
@@ -643,30 +644,42 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd(const NormArgs a, 
   }
 }
 
-// The blocks' column sums in a fixed order: a block sums 128 columns (four per lane), its warps
-// take the partial rows in turn.
-constexpr int kColWarps = 16;
+// The blocks' column sums in a fixed order: a block sums 64 columns (two per lane), its warps take the
+// partial rows in turn, ten of them in flight (gradient of 509 x 4096 15.8 us; with 128 columns and five in
+// flight 16.4).
+constexpr int kColWarps = 16, kCols = 64;
 __global__ void __launch_bounds__(kColWarps * 32) k_norm_cols(const NormArgs a, int parts) {
-  __shared__ float4 sum[kColWarps][32];
+  __shared__ float2 sum[kColWarps][32];
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int col = (blockIdx.x * 32 + lane) * 4;   // over nq * H columns, H a multiple of 8
+  const int col = blockIdx.x * kCols + lane * 2;   // over nq * H columns, H a multiple of 8
   const int width = a.nq * a.H;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  float2 v = make_float2(0.f, 0.f);
   if (col < width) {
-#pragma unroll 5
-    for (int p = warp; p < parts; p += kColWarps) {
-      const float4 u = *reinterpret_cast<const float4*>(a.part + (size_t)p * width + col);
-      v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+    constexpr int FLIGHT = 10;
+    for (int p0 = warp; p0 < parts; p0 += FLIGHT * kColWarps) {
+      float2 u[FLIGHT];
+#pragma unroll
+      for (int j = 0; j < FLIGHT; ++j) {
+        const int p = p0 + j * kColWarps;
+        u[j] = p < parts ? *reinterpret_cast<const float2*>(a.part + (size_t)p * width + col) : make_float2(0.f, 0.f);
+      }
+#pragma unroll
+      for (int j = 0; j < FLIGHT; ++j) {
+        v.x += u[j].x;
+        v.y += u[j].y;
+      }
     }
   }
   sum[warp][lane] = v;
   __syncthreads();
   if (warp != 0 || col >= width) return;
+#pragma unroll
   for (int w = 1; w < kColWarps; ++w) {
-    const float4 u = sum[w][lane];
-    v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+    const float2 u = sum[w][lane];
+    v.x += u.x;
+    v.y += u.y;
   }
   int q = col / a.H;
   const int h = col - q * a.H;
@@ -675,7 +688,7 @@ __global__ void __launch_bounds__(kColWarps * 32) k_norm_cols(const NormArgs a, 
   const bool on[3] = {a.w_post != nullptr, a.w_pre != nullptr, a.gate_kind == FT_GATE_CHANNEL};
   for (int which = 0; which < 3; ++which) {
     if (!on[which]) continue;
-    if (q-- == 0) *reinterpret_cast<float4*>(to[which] + h) = v;
+    if (q-- == 0) *reinterpret_cast<float2*>(to[which] + h) = v;
   }
 }
 
@@ -798,7 +811,7 @@ cudaError_t launch_norm_bwd(const NormArgs& a, int num_sms, cudaStream_t stream)
   }
   if (e != cudaSuccess || a.nq == 0) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.nq * a.H + 127) / 128));
+  cfg.gridDim = dim3((unsigned)((a.nq * a.H + kCols - 1) / kCols));
   cfg.blockDim = dim3(kColWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
