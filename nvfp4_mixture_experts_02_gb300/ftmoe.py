@@ -705,21 +705,21 @@ def _need_rows(t, name, dev, inner):
     return stride[0]
 
 
-def _scratch(n, dev, stream):
+def _scratch(n, dev):
     """n bytes of the workspace that calls without one share per (device, stream)."""
-    key = (dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    key = (dev, torch._C._cuda_getCurrentRawStream(dev))
     ws = _DEFAULT_WS.get(key)
     if ws is None or ws.numel() < n:
-        ws = _new_scratch(n, dev, stream)
+        ws = _new_scratch(n, dev)
         _DEFAULT_WS[key] = ws
     return ws
 
 
-def _new_scratch(n, dev, stream):
+def _new_scratch(n, dev):
     ws = torch.empty(n + 256, dtype=torch.uint8, device=torch.device("cuda", dev))
     off = (-ws.data_ptr()) % 256
     ws = ws[off:off + n]
-    _check(_LIB.ft_moe_workspace_init(_ptr(ws), n, _stream(stream, dev)), "ft_moe_workspace_init")
+    _check(_LIB.ft_moe_workspace_init(_ptr(ws), n, _stream(None, dev)), "ft_moe_workspace_init")
     return ws
 
 
@@ -757,6 +757,9 @@ def nvfp4_linear(x, weight: NvFP4Linear, out=None, out_dtype=torch.bfloat16, wor
                  stream=None):
     """ft_nvfp4_linear: x bf16 [T,K] (T <= 64; rows may be slices of a wider tensor) -> W x_t,
     [T,N] in bf16, or in float32 (out_dtype, or the type of `out`)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):   # what the call makes belongs to the stream that it runs on
+            return nvfp4_linear(x, weight, out, out_dtype, workspace)
     dev = weight.device_index
     if x.dim() != 2:
         raise ValueError("x: [T, K] expected")
@@ -775,10 +778,10 @@ def nvfp4_linear(x, weight: NvFP4Linear, out=None, out_dtype=torch.bfloat16, wor
     elif T > 8:   # fewer tokens need none
         n = _LIB.ft_nvfp4_linear_workspace_bytes(T, weight.K)
         if n > 0:
-            workspace = _scratch(n, dev, stream)
+            workspace = _scratch(n, dev)
             ws, ws_bytes = workspace.data_ptr(), workspace.numel()
     st = _LIB.ft_nvfp4_linear(x.data_ptr(), T, stride, weight._ref, out.data_ptr(),
-                              out.dtype is torch.float32, ws, ws_bytes, _stream(stream, dev))
+                              out.dtype is torch.float32, ws, ws_bytes, _stream(None, dev))
     _check(st, "ft_nvfp4_linear")
     return out
 
@@ -830,6 +833,9 @@ def kv_append(k, v, cache: PagedKVCache, block_table, positions, seq_ids=None, q
     sequences seq_ids int32 [T], or 0..T-1) through block_table int32 [B,width], k rotated by rope
     f32 [rows, R] (cos | sin; None: not at all). Returns the rotated q bf16 [T,Hq,D], or None
     without q. Rows of k, v and q may be slices of one projection's output."""
+    if stream is not None:
+        with torch.cuda.stream(stream):   # what the call makes belongs to the stream that it runs on
+            return kv_append(k, v, cache, block_table, positions, seq_ids, q, rope, q_out, workspace)
     dev, inner = cache.device_index, cache.heads
     if k.dim() != 3 or block_table.dim() != 2:
         raise ValueError("k [T, Hkv, D] and block_table [B, width] expected")
@@ -870,7 +876,7 @@ def kv_append(k, v, cache: PagedKVCache, block_table, positions, seq_ids=None, q
                            block_table.data_ptr(), B, width,
                            0 if seq_ids is None else seq_ids.data_ptr(), positions.data_ptr(), rp,
                            rows, dim, 0 if workspace is None else workspace.data_ptr(),
-                           _stream(stream, dev))
+                           _stream(None, dev))
     if st != FT_OK:
         _check(st, "ft_kv_append")
     return q_out if q is not None else None
@@ -893,6 +899,10 @@ def paged_decode_attention(q, cache: PagedKVCache, block_table, seq_lens, scale=
     """ft_paged_decode_attention: q bf16 [B,Hq,D], one new token per sequence, over the first
     seq_lens int32 [B] slots of each (the last `window` of them if window > 0) through block_table
     int32 [B,width]. scale: 1/sqrt(D) by default. Returns (out bf16 [B,Hq,D], lse f32 [B,Hq])."""
+    if stream is not None:
+        with torch.cuda.stream(stream):   # what the call makes belongs to the stream that it runs on
+            return paged_decode_attention(q, cache, block_table, seq_lens, scale, window, out, lse,
+                                          workspace)
     dev, D = cache.device_index, cache.heads[1]
     if q.dim() != 3 or block_table.dim() != 2:
         raise ValueError("q [B, Hq, D] and block_table [B, width] expected")
@@ -914,12 +924,12 @@ def paged_decode_attention(q, cache: PagedKVCache, block_table, seq_lens, scale=
     if workspace is not None:
         _need(workspace, "workspace", dev, None, None)
     elif B > 0:
-        workspace = _scratch(_attention_bytes(B, D, dev), dev, stream)
+        workspace = _scratch(_attention_bytes(B, D, dev), dev)
     st = _LIB.ft_paged_decode_attention(
         q.data_ptr(), qs, B, Hq, cache._ref, block_table.data_ptr(), width, seq_lens.data_ptr(),
         D ** -0.5 if scale is None else scale, window, out.data_ptr(), lse.data_ptr(),
         0 if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel(), _stream(stream, dev))
+        0 if workspace is None else workspace.numel(), _stream(None, dev))
     if st != FT_OK:
         _check(st, "ft_paged_decode_attention")
     return out, lse
@@ -960,6 +970,9 @@ def residual_norm(y, residual=None, w_post=None, w_pre=None, gate=None, scale=1.
     """ft_residual_norm: r' = residual + scale * gate * norm(y, w_post) and x' = norm(r', w_pre) for
     y bf16 [T,H]; a weight that is None leaves its norm out. gate bf16 [H], [T,1] or [T,H].
     Returns (r' in the residual's type, x' bf16 or None without w_pre)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):   # what the call makes belongs to the stream that it runs on
+            return residual_norm(y, residual, w_post, w_pre, gate, scale, eps, res_out, x_out)
     dev, T, H, kind, res = _norm_inputs(y, residual, w_post, w_pre, gate)
     if res_out is None:
         res_out = torch.empty_like(y if residual is None else residual, dtype=res)
@@ -979,7 +992,7 @@ def residual_norm(y, residual=None, w_post=None, w_pre=None, gate=None, scale=1.
         y.data_ptr(), 0 if residual is None else residual.data_ptr(),
         0 if w_post is None else w_post.data_ptr(), 0 if w_pre is None else w_pre.data_ptr(),
         0 if gate is None else gate.data_ptr(), kind, T, H, res is torch.float32, scale, eps,
-        res_out.data_ptr(), x, _stream(stream, dev))
+        res_out.data_ptr(), x, _stream(None, dev))
     if st != FT_OK:
         _check(st, "ft_residual_norm")
     return res_out, x_out
@@ -1008,6 +1021,10 @@ def residual_norm_backward(y, residual, d_r, d_x=None, w_post=None, w_pre=None, 
     and d_x (of x', bf16; required with w_pre): dy bf16, dresidual in the stream's type (the
     residual's, or d_r's without one), dw_post and dw_pre f32 [H], dgate f32 [H] or [T,1], or bf16
     [T,H]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):   # what the call makes belongs to the stream that it runs on
+            return residual_norm_backward(y, residual, d_r, d_x, w_post, w_pre, gate, scale, eps,
+                                          workspace)
     dev, T, H, kind, res = _norm_inputs(y, residual, w_post, w_pre, gate)
     if d_r is not None:
         _need(d_r, "d_r", dev, _RES if residual is None else (res,), (T, H))
@@ -1033,14 +1050,14 @@ def residual_norm_backward(y, residual, d_r, d_x=None, w_post=None, w_pre=None, 
     if workspace is not None:
         _need(workspace, "workspace", dev, None, None)
     elif T > 0:
-        workspace = _scratch(_norm_backward_bytes(T, H, dev), dev, stream)
+        workspace = _scratch(_norm_backward_bytes(T, H, dev), dev)
     st = _LIB.ft_residual_norm_backward(
         y.data_ptr(), 0 if residual is None else residual.data_ptr(),
         0 if w_post is None else w_post.data_ptr(), 0 if w_pre is None else w_pre.data_ptr(), gp,
         kind, 0 if d_r is None else d_r.data_ptr(), dx, T, H, res is f32, scale, eps,
         dy.data_ptr(), dres.data_ptr(), post, pre, dg,
         0 if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel(), _stream(stream, dev))
+        0 if workspace is None else workspace.numel(), _stream(None, dev))
     if st != FT_OK:
         _check(st, "ft_residual_norm_backward")
     return NormGradients(dy, dres, dw_post, dw_pre, dgate)

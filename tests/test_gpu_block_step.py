@@ -101,3 +101,33 @@ def test_steps_against_the_oracles_and_a_graph():
         off = np.linalg.norm(f64(got) - ref) / np.linalg.norm(ref)
         assert off <= 2e-2, (t, off)
     assert step.positions.tolist() == [20] * B
+
+
+def test_what_a_call_makes_belongs_to_the_stream_it_is_given():
+    m = ftmoe()
+    rng = np.random.default_rng(40)
+    on = lambda *shape: bf16(rng.standard_normal(shape)).cuda()  # noqa: E731
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    lin, x = on_gpu(m, *matrix(rng, 300, 512)), on(20, 512)
+    cache = m.PagedKVCache(on(8, 16, 2, 64), on(8, 16, 2, 64))
+    table, q, k = i32([[0, 1, 2], [3, 4, 5]]), on(2, 4, 64), on(2, 2, 64)
+    y, w = on(20, 512), on(512)
+
+    def calls(stream):
+        made = [m.nvfp4_linear(x, lin, stream=stream),
+                m.kv_append(k, k, cache, table, i32([3, 40]), q=q, stream=stream),
+                *m.paged_decode_attention(q, cache, table, i32([20, 41]), stream=stream),
+                *m.residual_norm(y, x, w_post=w, w_pre=w, gate=w, stream=stream)]
+        grads = m.residual_norm_backward(y, x, y, x, w_post=w, w_pre=w, gate=w, stream=stream)
+        return made + list(grads)
+
+    want = calls(None)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = calls(s)
+    s.synchronize()
+    home = {a: seg["stream"] for seg in torch.cuda.memory_snapshot()
+            for a in range(seg["address"], seg["address"] + seg["total_size"], 512)}
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+        assert home[b.data_ptr()] == s.cuda_stream != home[a.data_ptr()]
