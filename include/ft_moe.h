@@ -389,7 +389,8 @@ ft_status ft_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, i
                        void* stream);
 
 /* Workspace bytes of ft_paged_decode_attention for B sequences and heads of D elements on the
- * current device (0 for invalid sizes or without a device). */
+ * current device (0 for invalid sizes or without a device): two partial results for every warp that
+ * the device holds, 20 to 40 MB, of which a call touches what it splits. */
 size_t ft_paged_attention_workspace_bytes(int32_t B, int32_t D);
 
 /*

@@ -60,8 +60,8 @@ struct AttnShape {
 // From this many units in a run, the warps of a block take several key heads at once instead of stripes of
 // one head's keys: rows of the same slot are then read together (256 sequences up to 1024, bf16, 8 heads of
 // 128: 97 us for 118; 8 of 32768, E4M3, 8 heads of 64: 54 for 80), and no join in the block holds the
-// copies up. Shorter runs would leave k_join as many times more pieces: 8 sequences up to 2048 14.0 us for 15.5
-// (from 8 units), 48 of 256 12.8 for 17.0 (from 2).
+// copies up. Shorter runs would leave k_join as many times more pieces: 48 sequences of 256 take 12.8 us, and
+// 17.0 when runs of two units are long; 8 up to 2048 take 14.0 us, and 15.5 when only runs of eight are.
 constexpr int kLongRun = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -113,7 +113,8 @@ __device__ __forceinline__ void span(int len, int window, int unit, int& first, 
 }
 
 template <int D, bool F8, int NG>
-__global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D, F8, NG>::kBlocks) k_attend(const AttendArgs a) {
+__global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D, F8, NG>::kBlocks)
+    k_attend(const AttendArgs a) {
   using S = AttnShape<D, F8, NG>;
   constexpr int W = S::kWarps, ST = S::kStages, CPR = S::kCpr, KS = D / 16, MT = D / 16;
   constexpr int KT = S::kKeys, NH = KT / 16;   // keys of a step, in 16-row tiles
@@ -225,7 +226,8 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
       // for k_join: the segment that this run goes on with, if it does not begin here
       const int64_t s0 = u - u0, s1 = s0 + cost;
       a.shared_segs[blockIdx.x] =
-          make_int4(u0 > 0 ? b : -1, hg * 16 + hl, (int)(s0 / quota) * 2 + (s0 % quota != 0), (int)((s1 - 1) / quota));
+          make_int4(u0 > 0 ? b : -1, hg * 16 + hl, (int)(s0 / quota) * 2 + (s0 % quota != 0),
+                    (int)((s1 - 1) / quota));
     }
     // this warp's keys of the piece: key0 + i * unit .. + KT - 1 in step i, up to key1
     const int piece0 = first / S::kUnit * S::kUnit + u0 * unit;

@@ -1,10 +1,10 @@
 // Warp-level helpers of the decode-block kernels: m16n8k16 products, matrix loads from shared
 // memory, asynchronous 16-byte copies and warp sums.
 //
-// The products here have at most 16 rows of one operand (the tokens of a decode step, the query
-// heads that share a key head) against a stream of weights or keys that is read once, so they are
-// bound by memory; the warp-level product takes its operands from registers, where the conversions
-// leave them, with no trip through tensor memory.
+// The products here have few columns (up to 64 tokens of a decode step, up to 16 query heads that share
+// a key head) against a stream of weights or keys that is read once, so memory or the conversions bound
+// them up to some 16 columns; the warp-level product takes its operands from registers, where the
+// conversions leave them, with no trip through tensor memory.
 #pragma once
 
 #include <cstdint>

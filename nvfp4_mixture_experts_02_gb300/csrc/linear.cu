@@ -716,7 +716,8 @@ cudaError_t launch_more(const LinearArgs& a, int num_sms, cudaStream_t stream) {
   constexpr size_t smem = (size_t)kMoreStages * TOK * kLinUnit * 2;
   cudaError_t e = grant_smem(grant, k_linear_more<NT>, (int)smem);
   if (e != cudaSuccess) return e;
-  if ((e = start(k_linear_x, dim3((unsigned)a.T), kPrepThreads, 0, 1, stream, a, TOK)) != cudaSuccess) return e;
+  e = start(k_linear_x, dim3((unsigned)a.T), kPrepThreads, 0, 1, stream, a, TOK);
+  if (e != cudaSuccess) return e;
   e = start(k_linear_more<NT>, dim3((unsigned)blocks), kLinWarps * 32,
             smem, 1, stream, a, uk, quota);
   if (e != cudaSuccess || quota % uk == 0) return e;   // every run ends with a tile
@@ -736,7 +737,8 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
   const int nt = (a.T + 7) / 8;
   // Groups of 16 tokens on blocks of their own read the matrix again, from L2, but where SMs are idle
   // otherwise that pays (us, one group or groups of 16): 32 tokens 8.7 or 6.4 at 2048 x 2048, 11.6 or 10.9 at
-  // 4096 x 4096, 30 or 33 at 8000 x 8192; 64 tokens, three launches or groups of 16: 10.8 or 7.6 at 2048 x 2048, 15.6 or 10.7 at 2048 x 4096.
+  // 4096 x 4096, 30 or 33 at 8000 x 8192; 64 tokens, three launches or groups of 16: 10.8 or 7.6 at
+  // 2048 x 2048, 15.6 or 10.7 at 2048 x 4096.
   const int tiles = (a.N + kMidRows - 1) / kMidRows;
   if (!wide && (nt <= 2 || tiles * ((nt + 1) / 2) * 2 <= num_sms || (nt <= 4 && a.K > 16384)))
     return launch_mid<2>(a, num_sms, stream);

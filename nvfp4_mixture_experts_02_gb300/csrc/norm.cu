@@ -241,7 +241,8 @@ __device__ __forceinline__ void put8(float* p, const f2 (&f)[4]) {
 // Many rows: the row groups and rings of the gradient. One barrier a row: the sum over r' for x' and the
 // one over the next row's y are taken together, and the row's stage is free once it is passed.
 template <int GT, int NV, typename RT>
-__global__ void __launch_bounds__(kRingThreads, NV == 2 ? 2 : 1) k_norm_rows(const NormArgs a, const RowRing ring) {
+__global__ void __launch_bounds__(kRingThreads, NV == 2 ? 2 : 1)
+    k_norm_rows(const NormArgs a, const RowRing ring) {
   constexpr int RG = kRingThreads / GT, W = GT / 32;
   extern __shared__ __align__(128) unsigned char ring_smem[];
   __shared__ __align__(8) uint64_t full[RG][8];
@@ -663,7 +664,8 @@ __global__ void __launch_bounds__(kColWarps * 32) k_norm_cols(const NormArgs a, 
 #pragma unroll
       for (int j = 0; j < FLIGHT; ++j) {
         const int p = p0 + j * kColWarps;
-        u[j] = p < parts ? *reinterpret_cast<const float2*>(a.part + (size_t)p * width + col) : make_float2(0.f, 0.f);
+        u[j] = p < parts ? *reinterpret_cast<const float2*>(a.part + (size_t)p * width + col)
+                         : make_float2(0.f, 0.f);
       }
 #pragma unroll
       for (int j = 0; j < FLIGHT; ++j) {
