@@ -12,15 +12,18 @@
 //
 // Every input is read once and every output written once; the work is bound by memory, with float32
 // sums in a fixed order, and x' taken from r' before r' is rounded to its stored type. k_norm: a row per
-// block (or per warp, up to 512 elements) in registers. k_norm_rows (wide rows, many of them) and
-// k_norm_bwd: persistent blocks whose row groups get their rows by bulk copies into rings, so that the
-// next rows travel while one is worked on. The gradient's column sums stay in registers over all of a
-// block's rows; k_norm_cols adds the blocks' sums.
+// block, per warp (up to 512 elements) or per 8 or 16 lanes (up to 64 or 128, the heads of q and k) in
+// registers. k_norm_rows (wide rows, many of them) and k_norm_bwd: persistent blocks whose row groups get
+// their rows by bulk copies into rings, so that the next rows travel while one is worked on;
+// k_norm_bwd_narrow: rows of up to 256 elements by 8 to 32 lanes each. The gradient's column sums stay in
+// registers over all of a block's rows; k_norm_cols adds the blocks' sums.
 //
-// Measured (of the copy rate of 6786 GB/s): forward 8191 x 4096 with a float32 stream 71 us (84 %), 8192 x
-// 8192 95 us (83 %); gradient 8192 x 8192 171 us (70 %), where about half of a row's 3 us is arithmetic
-// (9 unpackings and 9 packed operations an element) and two barriers; 2048 x 16384 168 us (35 %: 32 columns
-// a thread spill). One token: 2.9 us, a launch and three dependent latencies.
+// Measured (of the copy rate of 6786 GB/s): forward 8191 x 4096 with a float32 stream 71 us (83 %), 8192 x
+// 8192 95 us (83 %), 131072 x 128 22 us (89 %; a warp per row 50); gradient 8192 x 8192 171 us (70 %), where
+// about half of a row's 3 us is arithmetic (9 unpackings and 9 packed operations an element) and two
+// barriers; 131072 x 128 43 us (70 %; rows of a warp through rings 121), 262144 x 64 42 us (234), 65536 x 256
+// 43 us (64); 2048 x 16384 168 us (35 %: 32 columns a thread spill). One token: 2.9 us, a launch and three
+// dependent latencies.
 #include <cuda_runtime.h>
 
 #include "ftmoe_internal.h"
@@ -32,7 +35,8 @@ namespace ftmoe {
 namespace {
 
 constexpr int kWarpRowMax = 512;    // elements of a row that one warp holds
-constexpr int kRowWarps = 8;        // rows (warps) per block in that form
+constexpr int kNarrowRowMax = 256;  // ... with one 8-element piece a lane, or several rows a warp
+constexpr int kRowThreads = 256;    // of a block in those forms
 
 // 1 / sqrt(sum / n + eps) and scale * gate times it, as a float and what it lacks: where r and the
 // block's output nearly cancel, r' keeps the error of this factor many times over. inv_n + inv_n_lo is
@@ -55,12 +59,20 @@ __device__ __forceinline__ Factor row_factor(float sum, float inv_n, float inv_n
   return {hi, fmaf(tg, s, -hi) + fmaf(tg, s_lo, tg_lo * s), s + s_lo};
 }
 
-// Sum over the row's threads: the warp, or the whole block through red[] (one array per call
-// site, so that one barrier per sum is enough).
-template <bool WARP>
+// Sum over groups of GS lanes.
+template <int GS>
+__device__ __forceinline__ float lane_sum(float v) {
+#pragma unroll
+  for (int o = GS / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Sum over the row's threads: GS lanes of a warp, or (GS = 0) the whole block through red[] (one array per
+// call site, so that one barrier per sum is enough).
+template <int GS>
 __device__ __forceinline__ float row_sum(float v, float* red) {
+  if constexpr (GS > 0) return lane_sum<GS>(v);
   v = warp_sum(v);
-  if constexpr (WARP) return v;
   const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
   if (lane == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
@@ -81,17 +93,19 @@ __device__ __forceinline__ float one_bf16(const uint16_t* p) {
   return __uint_as_float((uint32_t)*p << 16);
 }
 
-template <int NV, typename RT, bool WARP>
-__global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 1024) k_norm(const NormArgs a) {
+// A row per GS lanes, or (GS = 0) per block.
+template <int NV, typename RT, int GS>
+__global__ void __launch_bounds__(GS > 0 ? kRowThreads : 1024) k_norm(const NormArgs a) {
   __shared__ float red[2][32];
   griddep_launch_dependents();
   griddep_wait();
-  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const int nth = WARP ? 32 : blockDim.x;
-  const int t = WARP ? blockIdx.x * kRowWarps + (threadIdx.x >> 5) : blockIdx.x;
-  if (t >= a.T) return;   // a whole warp or block
+  constexpr int G = GS > 0 ? GS : 32;
+  const int tid = GS > 0 ? threadIdx.x % G : threadIdx.x;
+  const int nth = GS > 0 ? GS : blockDim.x;
+  const int64_t t = GS > 0 ? (int64_t)blockIdx.x * (kRowThreads / G) + threadIdx.x / G : blockIdx.x;
+  if (GS > 0 && GS < 32 ? t - (int)(threadIdx.x % 32) / G >= a.T : t >= a.T) return;   // a whole warp or block
+  const int chunks = t < a.T ? a.H >> 3 : 0;   // none in a warp's rows past the last
   const size_t row = (size_t)t * a.H;
-  const int chunks = a.H >> 3;
   const float inv_h = 1.0f / (float)a.H;
 
   float y[NV][8], r[NV][8];
@@ -115,8 +129,8 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 1024) k_norm(const Nor
     for (int j = 0; j < 8; ++j) ss = fmaf(y[i][j], y[i][j], ss);
   }
   float s1 = 1.f;
-  if (a.w_post) s1 = rsqrtf(row_sum<WARP>(ss, red[0]) * inv_h + a.eps);
-  const float ts = a.scale * (a.gate_kind == FT_GATE_TOKEN ? one_bf16(a.gate + t) : 1.f) * s1;
+  if (a.w_post) s1 = rsqrtf(row_sum<GS>(ss, red[0]) * inv_h + a.eps);
+  const float ts = a.scale * (a.gate_kind == FT_GATE_TOKEN && chunks > 0 ? one_bf16(a.gate + t) : 1.f) * s1;
   ss = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -142,7 +156,7 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 1024) k_norm(const Nor
     if (a.r_out) store8(static_cast<RT*>(a.r_out) + row + 8 * c, r[i]);
   }
   if (!a.w_pre) return;
-  const float s2 = rsqrtf(row_sum<WARP>(ss, red[1]) * inv_h + a.eps);
+  const float s2 = rsqrtf(row_sum<GS>(ss, red[1]) * inv_h + a.eps);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = tid + i * nth;
@@ -645,6 +659,169 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd(const NormArgs a, 
   }
 }
 
+// Narrow rows (heads): a row per GS lanes, one 8-element piece a lane, the next row's inputs in registers
+// while one is worked on; the sums are shuffles.
+constexpr int kNarrowThreads = 512;
+template <typename RT>
+struct RowPiece {   // eight elements as they are stored
+  static constexpr int Q = sizeof(RT) / 2;
+  uint4 q[Q];
+  __device__ __forceinline__ void load(const void* base, size_t at, bool on) {
+#pragma unroll
+    for (int i = 0; i < Q; ++i)
+      q[i] = on && base ? ld16(static_cast<const char*>(base) + at * sizeof(RT) + 16 * i) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void open(f2 (&f)[4]) const {
+    if constexpr (Q == 1) {
+      open8(q[0], f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < Q; ++i) {
+        f[2 * i] = make2(__uint_as_float(q[i].x), __uint_as_float(q[i].y));
+        f[2 * i + 1] = make2(__uint_as_float(q[i].z), __uint_as_float(q[i].w));
+      }
+    }
+  }
+};
+template <int GS, typename RT>
+__global__ void __launch_bounds__(kNarrowThreads, 1) k_norm_bwd_narrow(const NormArgs a) {
+  constexpr int RG = kNarrowThreads / GS;
+  __shared__ __align__(16) float cols[RG * GS * 8];   // [group][H]
+  griddep_launch_dependents();
+  griddep_wait();
+  const int g = threadIdx.x / GS, c = threadIdx.x % GS, chunks = a.H >> 3;
+  const float inv_h = 1.0f / (float)a.H, inv_h_lo = fmaf(-inv_h, (float)a.H, 1.f) * inv_h;
+  const bool channel = a.gate_kind == FT_GATE_CHANNEL, element = a.gate_kind == FT_GATE_ELEMENT;
+  const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr;
+  const uint4 one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+  const bool col = c < chunks;
+  f2 u[4], wpre[4], acc_post[4], acc_pre[4], chan[4];
+  open8(post && col ? *reinterpret_cast<const uint4*>(a.w_post + 8 * c) : one, u);
+  open8(channel && col ? *reinterpret_cast<const uint4*>(a.gate + 8 * c) : one, chan);
+  open8(pre && col ? *reinterpret_cast<const uint4*>(a.w_pre + 8 * c) : one, wpre);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    u[j] = mul2(u[j], chan[j]);
+    acc_post[j] = acc_pre[j] = 0ull;
+  }
+  struct Row {
+    RowPiece<uint16_t> y, dx, gate;
+    RowPiece<RT> r, dr;
+    float tgate;
+  };
+  auto load = [&](Row& w, int64_t t) {
+    const bool on = col && t < a.T;
+    const size_t at = (size_t)t * a.H + 8 * c;
+    w.y.load(a.y, at, on);
+    w.r.load(a.r, at, on);
+    w.dr.load(a.dr, at, on);
+    w.dx.load(pre ? a.dx : nullptr, at, on);
+    w.gate.load(element ? a.gate : nullptr, at, on);
+    w.tgate = a.gate_kind == FT_GATE_TOKEN && t < a.T ? one_bf16(a.gate + t) : 1.f;
+  };
+  const int step = (int)gridDim.x * RG;
+  Row now;
+  load(now, (int)blockIdx.x * RG + g);
+  for (int64_t t0 = (int)blockIdx.x * RG; t0 < a.T; t0 += step) {   // uniform over the block
+    const int64_t t = t0 + g;
+    const bool on = col && t < a.T;
+    const size_t at = (size_t)t * a.H + 8 * c;
+    const Row w = now;
+    load(now, t + step);
+    f2 y[4], r[4], d[4], gate[4], ss = 0ull;
+    w.y.open(y);
+    w.r.open(r);
+    if (post) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ss = fma2(y[j], y[j], ss);
+    }
+    const Factor factor = row_factor(post ? lane_sum<GS>(sum_of(ss)) : 0.f, inv_h, inv_h_lo, a.eps, a.scale,
+                                     w.tgate, post);
+    const float s1 = factor.root, tg = a.scale * w.tgate;
+    const f2 ts = both(factor.hi), ts_lo = both(factor.lo);
+    w.gate.open(gate);
+    w.dx.open(d);
+    f2 rr = 0ull, dot = 0ull;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {   // y u is exact
+      const f2 yu = mul2(element ? mul2(y[j], gate[j]) : y[j], u[j]);
+      r[j] = fma2(yu, ts_lo, fma2(yu, ts, r[j]));
+      rr = fma2(r[j], r[j], rr);
+      dot = fma2(mul2(d[j], wpre[j]), r[j], dot);
+    }
+    f2 s2 = 0ull, cr = 0ull;
+    if (pre) {
+      const float sum = lane_sum<GS>(sum_of(rr)), with = lane_sum<GS>(sum_of(dot));
+      const float s = rsqrtf(sum * inv_h + a.eps);
+      s2 = both(s);
+      cr = both(-(s * (s * s * (with * inv_h))));
+    }
+    f2 dr[4], h[4], hy = 0ull;
+    w.dr.open(dr);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = 0ull;
+    if (on) {
+      if (pre) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f2 ds = mul2(d[j], s2);
+          acc_pre[j] = fma2(ds, r[j], acc_pre[j]);
+          dr[j] = fma2(ds, wpre[j], fma2(r[j], cr, dr[j]));
+        }
+      }
+      put8(static_cast<RT*>(a.dres) + at, dr);
+      if (element) {
+        const f2 gs = both(a.scale * s1);
+        f2 dg[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          dg[j] = mul2(mul2(mul2(y[j], dr[j]), u[j]), gs);
+          dr[j] = mul2(dr[j], gate[j]);
+        }
+        put8(static_cast<uint16_t*>(a.dgate) + at, dg);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f2 yd = mul2(y[j], dr[j]);
+        acc_post[j] = fma2(yd, ts, acc_post[j]);
+        hy = fma2(yd, u[j], hy);
+        h[j] = mul2(dr[j], u[j]);
+      }
+    }
+    const float sum = lane_sum<GS>(sum_of(hy));
+    if (!on) continue;
+    if (a.gate_kind == FT_GATE_TOKEN && c == 0) static_cast<float*>(a.dgate)[t] = a.scale * s1 * sum;
+    const f2 k1 = both(post ? tg * s1 : tg), k2 = both(post ? -(tg * s1 * s1 * s1 * (sum * inv_h)) : 0.f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = post ? fma2(y[j], k2, mul2(h[j], k1)) : mul2(h[j], k1);
+    put8(a.dy + at, h);
+  }
+  // the block's column sums, its groups added in order: [block][quantity][H]
+  float* part = a.part + (size_t)blockIdx.x * a.nq * a.H;
+  int q = 0;
+#pragma unroll
+  for (int which = 0; which < 3; ++which) {
+    if (which == 0 ? !post : which == 1 ? !pre : !channel) continue;
+    __syncthreads();
+    if (col) {
+      f2 sum[4], w[4];
+      open8(which == 0 && channel ? *reinterpret_cast<const uint4*>(a.gate + 8 * c)
+            : which == 2 && post  ? *reinterpret_cast<const uint4*>(a.w_post + 8 * c) : one, w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[j] = which == 1 ? acc_pre[j] : mul2(acc_post[j], w[j]);
+      put8(cols + (size_t)g * a.H + 8 * c, sum);
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < a.H; x += kNarrowThreads) {
+      float v = 0.f;
+#pragma unroll 8
+      for (int w = 0; w < RG; ++w) v += cols[(size_t)w * a.H + x];
+      part[(size_t)q * a.H + x] = v;
+    }
+    ++q;
+  }
+}
+
 // The blocks' column sums in a fixed order: a block sums 64 columns (two per lane), its warps take the
 // partial rows in turn, ten of them in flight (gradient of 509 x 4096 15.8 us; with 128 columns and five in
 // flight 16.4).
@@ -785,20 +962,36 @@ cudaError_t launch_norm(const NormArgs& a, int num_sms, cudaStream_t stream) {
     if (ok || e != cudaSuccess) return e;
   }
   if (a.H <= kWarpRowMax) {
-    const int grid = (a.T + kRowWarps - 1) / kRowWarps;
-    return a.res_f32 ? launch(k_norm<2, float, true>, grid, kRowWarps * 32, stream, a)
-                     : launch(k_norm<2, uint16_t, true>, grid, kRowWarps * 32, stream, a);
+    const int gs = chunks <= 8 ? 8 : chunks <= 16 ? 16 : 32, rows = kRowThreads / gs;
+    const int grid = (a.T - 1) / rows + 1;
+    auto go = [&](auto kernel_f32, auto kernel_bf16) {
+      return a.res_f32 ? launch(kernel_f32, grid, kRowThreads, stream, a)
+                       : launch(kernel_bf16, grid, kRowThreads, stream, a);
+    };
+    if (a.H > kNarrowRowMax) return go(k_norm<2, float, 32>, k_norm<2, uint16_t, 32>);
+    if (gs == 32) return go(k_norm<1, float, 32>, k_norm<1, uint16_t, 32>);
+    if (gs == 16) return go(k_norm<1, float, 16>, k_norm<1, uint16_t, 16>);
+    return go(k_norm<1, float, 8>, k_norm<1, uint16_t, 8>);
   }
   const int th = row_threads(chunks, 2);
-  return a.res_f32 ? launch(k_norm<2, float, false>, a.T, th, stream, a)
-                   : launch(k_norm<2, uint16_t, false>, a.T, th, stream, a);
+  return a.res_f32 ? launch(k_norm<2, float, 0>, a.T, th, stream, a)
+                   : launch(k_norm<2, uint16_t, 0>, a.T, th, stream, a);
 }
 
 cudaError_t launch_norm_bwd(const NormArgs& a, int num_sms, cudaStream_t stream) {
   const int chunks = a.H / 8;
   const int grid = norm_bwd_groups(a.T, num_sms);
   cudaError_t e;
-  if (chunks <= 64) {
+  if (chunks <= 8) {
+    e = a.res_f32 ? launch(k_norm_bwd_narrow<8, float>, grid, kNarrowThreads, stream, a)
+                  : launch(k_norm_bwd_narrow<8, uint16_t>, grid, kNarrowThreads, stream, a);
+  } else if (chunks <= 16) {
+    e = a.res_f32 ? launch(k_norm_bwd_narrow<16, float>, grid, kNarrowThreads, stream, a)
+                  : launch(k_norm_bwd_narrow<16, uint16_t>, grid, kNarrowThreads, stream, a);
+  } else if (chunks <= 32) {
+    e = a.res_f32 ? launch(k_norm_bwd_narrow<32, float>, grid, kNarrowThreads, stream, a)
+                  : launch(k_norm_bwd_narrow<32, uint16_t>, grid, kNarrowThreads, stream, a);
+  } else if (chunks <= 64) {
     e = launch_bwd<32, 2>(a, grid, stream);
   } else if (chunks <= 128) {
     e = launch_bwd<64, 2>(a, grid, stream);

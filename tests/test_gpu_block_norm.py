@@ -84,6 +84,16 @@ def test_widths(H, res):
     check(5, H, res, True, True, "element", H)
 
 
+@pytest.mark.parametrize("H,gate", [(8, "token"), (40, "channel"), (64, "element"), (72, "none"), (128, "token"),
+                                    (128, "channel"), (200, "element"), (256, "channel")])
+@pytest.mark.parametrize("res", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T", [33, 10037])
+def test_narrow_rows(T, H, res, gate):
+    """Several rows a warp, and several rounds of them a block."""
+    check(T, H, res, True, True, gate, T + H)
+    check(T, H, res, H % 16 == 0, H % 16 != 0, gate, T + H + 1)
+
+
 @pytest.mark.parametrize("T", [1, 2, 7, 8, 9, 303, 305, 1000, 5003])
 @pytest.mark.parametrize("H", [64, 768])
 def test_row_counts(T, H):
