@@ -23,7 +23,8 @@
 // the other operand's by movmatrix. bf16 caches: bf16 operands; p, in (0, 1], is split into two bf16
 // (16 significant bits, so that p is not rounded to 8). E4M3 caches: keys and values become f16
 // exactly, q is f16 after a scaling of its row by a power of two (exact but for elements under 2^-29
-// of the row's largest), p rounds to f16 (11 bits). Statistics and sums are float32.
+// of the row's largest), p, in (0, 2^15], rounds to f16: 11 bits down to 2^-29 of the largest key's weight
+// (see kLift). Statistics and sums are float32.
 //
 // Measured (of the copy rate of 6786 GB/s): three sequences up to 131072, bf16, 962 MB: 153 us (93 %).
 // 48 ragged ones up to 8192, E4M3, 423 MB: 83 to 85 us (74 %), of which some 10 us are launches, fill and
@@ -65,6 +66,14 @@ struct AttnShape {
 constexpr int kLongRun = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// log2 of the largest weight. f16 holds 11 bits of weights down to 2^-14 and nothing under 2^-25: with
+// weights of up to 2^15 a key's weight keeps 11 bits down to 2^-29 of the largest key's, and is off by at
+// most 2^-40 of it below. The sums carry the same factor, which their quotient does not see.
+constexpr float kLift = 15.f;
+template <bool F8>
+__device__ __forceinline__ float lse_of(float m, float l) {   // ln of l 2^m
+  return F8 ? (m + kLift + log2f(l * (1.f / 32768.f))) * kLn2 : (m + log2f(l)) * kLn2;
+}
 
 // Offset of 16-byte piece c of row r in a tile of rows of kCpr pieces: pieces are exchanged within
 // groups of eight (four) so that eight rows' same piece lie in different banks.
@@ -400,6 +409,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
           for (int h = 1; h < NH; ++h) t = fmaxf(t, fmaxf(s[g][h][e], s[g][h][2 + e]));
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
+          if constexpr (F8) t = __fsub_ru(t, kLift);   // upwards: no weight above 2^15 at any size of t
           top[g][e] = t;
           up |= t > m[g][e];
         }
@@ -531,7 +541,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
     const int64_t row = (int64_t)b * a.Hq + kvh * a.group + g0;
     if (lane < G && stripe == 0) {
       if (!whole) *reinterpret_cast<float2*>(a.part_ml + (part + lane) * 2) = ms;
-      else if (a.lse) a.lse[row + lane] = (ms.x + log2f(ms.y)) * kLn2;
+      else if (a.lse) a.lse[row + lane] = lse_of<F8>(ms.x, ms.y);
     }
     for (int x = stripe * 32; x < G * (D / 4); x += stripes * 32) {   // four dims of a head a lane
       const int g = (x + lane) / (D / 4), d = (x + lane) % (D / 4) * 4;
@@ -662,7 +672,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_join(const AttendArgs a) {
       for (int e = 0; e < E; ++e)
         a.out[row * D + lane + 32 * e] =
             (uint16_t)(pack_bf16(l == 0.f ? 0.f : v[e] / l * a.kv.v_scale, 0.f) & 0xFFFFu);
-      if (lane == 0 && a.lse) a.lse[row] = (m + log2f(l)) * kLn2;
+      if (lane == 0 && a.lse)
+        a.lse[row] = a.kv.dtype == FT_KV_E4M3 ? lse_of<true>(m, l) : lse_of<false>(m, l);
     }
   }
 }
