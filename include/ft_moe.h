@@ -412,8 +412,7 @@ size_t ft_paged_attention_workspace_bytes(int32_t B, int32_t D);
  *                share it must be ordered on one stream. It may be shared with the layer calls.
  *   0 <= B <= 4096. Whatever masked slots hold does not reach the output. Float32 scores,
  *   statistics and sums. Before a weight meets its value it is rounded: to 16 bits with a bf16
- *   cache; to 11 with an E4M3 cache, down to 2^-29 of the largest key's weight (a smaller one is
- *   within 2^-40 of the largest). The work is split over the cache's length and joined in a fixed
+ *   cache; with an E4M3 cache to 22, or to within 2^-40 of the largest key's weight. The work is split over the cache's length and joined in a fixed
  *   order (two launches), deterministic.
  */
 ft_status ft_paged_decode_attention(const uint16_t* q, int64_t q_stride, int32_t B, int32_t Hq,

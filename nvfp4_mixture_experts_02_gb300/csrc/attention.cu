@@ -23,8 +23,11 @@
 // the other operand's by movmatrix. bf16 caches: bf16 operands; p, in (0, 1], is split into two bf16
 // (16 significant bits, so that p is not rounded to 8). E4M3 caches: keys and values become f16
 // exactly, q is f16 after a scaling of its row by a power of two (exact but for elements under 2^-29
-// of the row's largest), p, in (0, 2^15], rounds to f16: 11 bits down to 2^-29 of the largest key's weight
-// (see kLift). Statistics and sums are float32.
+// of the row's largest), p, in (0, 2^15], is split into two f16 (22 bits down to 2^-18 of the largest key's
+// weight, see kLift). One f16 for p moves outputs over their bf16 rounding: 48 ragged sequences are 8.1e-4 off the
+// rounded exact result with one, 0.8e-4 with two (bf16 caches 0.6e-4), at 0 to 1 % of the time, 5 % with 16 heads
+// a key head (16 x 8192, 41.1 and 43.2 us).
+// Statistics and sums are float32.
 //
 // Measured (of the copy rate of 6786 GB/s): three sequences up to 131072, bf16, 962 MB: 153 us (93 %).
 // 48 ragged ones up to 8192, E4M3, 423 MB: 83 to 85 us (74 %), of which some 10 us are launches, fill and
@@ -67,8 +70,8 @@ constexpr int kLongRun = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // log2 of the largest weight. f16 holds 11 bits of weights down to 2^-14 and nothing under 2^-25: with
-// weights of up to 2^15 a key's weight keeps 11 bits down to 2^-29 of the largest key's, and is off by at
-// most 2^-40 of it below. The sums carry the same factor, which their quotient does not see.
+// weights of up to 2^15 the two parts of a key's weight hold 22 bits of it, or all but 2^-40 of the largest
+// key's weight. The sums carry the same factor, which their quotient does not see.
 constexpr float kLift = 15.f;
 template <bool F8>
 __device__ __forceinline__ float lse_of(float m, float l) {   // ln of l 2^m
@@ -451,7 +454,9 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
           for (int x = 0; x < 2; ++x) {
             const float p0 = s[g][h][2 * x], p1 = s[g][h][2 * x + 1];
             if constexpr (F8) {
-              p[g][h][x] = transpose8(pack_f16(p0, p1));
+              const uint32_t v = pack_f16(p0, p1);
+              p[g][h][x] = transpose8(v);
+              rest[g][h][x] = transpose8(pack_f16(p0 - f16_lo(v), p1 - f16_hi(v)));
             } else {
               const uint32_t v = pack_bf16(p0, p1);
               p[g][h][x] = transpose8(v);
@@ -489,7 +494,10 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
               e4m3x4_to_f16(__byte_perm(v[2 * e], 0, 0x3120), a0, a1);
               e4m3x4_to_f16(__byte_perm(v[2 * e + 1], 0, 0x3120), a2, a3);
 #pragma unroll
-              for (int g = 0; g < NG; ++g) mma_f16(o[g][t + e], a0, a1, a2, a3, p[g][h][0], p[g][h][1]);
+              for (int g = 0; g < NG; ++g) {
+                mma_f16(o[g][t + e], a0, a1, a2, a3, p[g][h][0], p[g][h][1]);
+                mma_f16(o[g][t + e], a0, a1, a2, a3, rest[g][h][0], rest[g][h][1]);
+              }
             }
           }
       }

@@ -85,6 +85,9 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return d;
 }
 
+__device__ __forceinline__ float f16_lo(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)w)); }
+__device__ __forceinline__ float f16_hi(uint32_t w) { return f16_lo(w >> 16); }
+
 __device__ __forceinline__ uint4 ld16(const void* p) {   // 16 bytes, read once
   uint4 v;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"

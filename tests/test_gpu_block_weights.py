@@ -75,3 +75,23 @@ def test_scores_of_any_size_stay_finite(dtype, power):
     close(out[0], ref, mag, 2.0 ** -14 if dtype == torch.bfloat16 else 2.0 ** -10)
     # log2 units and back: two constants, three products and two sums, each within 2^-24 of the score
     assert np.all(np.abs(f64(lse[0]) - rlse) <= 2.0 ** -21 * np.abs(rlse) + 4e-5)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, F8])
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 4, 128), (32, 2, 64), (4, 4, 256)])
+def test_weights_keep_their_bits_where_the_values_cancel(dtype, Hq, Hkv, D):
+    """Two to five keys a sequence: in a few of a hundred dims the weighted values nearly cancel, so that the
+    output's own rounding is small and that of the weights shows. 2^-14 of sum p|v| with either cache."""
+    m = ftmoe()
+    rng = np.random.default_rng(Hq)
+    B, page = 48, 8
+    lens = rng.integers(2, 6, B)
+    draw = lambda: torch.from_numpy(rng.standard_normal((B, page, Hkv, D)).astype(np.float32)).to(dtype)  # noqa: E731
+    k, v = draw(), draw()
+    q = bf16(rng.standard_normal((B, Hq, D)))
+    out, _ = m.paged_decode_attention(q.cuda(), m.PagedKVCache(k.cuda(), v.cuda()),
+                                      torch.arange(B, dtype=torch.int32, device="cuda")[:, None],
+                                      torch.from_numpy(lens.astype(np.int32)).cuda())
+    for b, n in enumerate(lens):
+        ref, _, mag = ob.attention(f64(q[b]), f64(k[b].float()), f64(v[b].float()), int(n), D ** -0.5)
+        close(out[b], ref, mag, 2.0 ** -14, f"b={b}")
