@@ -241,7 +241,7 @@ ft_status ft_residual_norm_backward(const uint16_t* y, const void* residual,
   a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + 1024);
   a.y = y; a.r = residual; a.w_post = w_post; a.w_pre = w_pre; a.gate = gate;
   a.gate_kind = gate_kind; a.T = T; a.H = H; a.res_f32 = res_f32 ? 1 : 0;
-  a.scale = scale; a.eps = eps; a.dr = d_r; a.dx = d_x; a.dy = dy; a.dres = dresidual;
+  a.scale = scale; a.eps = eps; a.dr = d_r; a.dx = w_pre ? d_x : nullptr; a.dy = dy; a.dres = dresidual;
   a.dw_post = dw_post; a.dw_pre = dw_pre; a.dgate = dgate;
   return cuda_status(launch_norm_bwd(a, sms, s));
 }

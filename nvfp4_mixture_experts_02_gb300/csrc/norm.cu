@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(GS > 0 ? kRowThreads : 1024) k_norm(const Norm
 constexpr int kRingThreads = 512;
 constexpr size_t kRingBytes = 224 * 1024;   // one stage of the widest rows: 16384, float32, every input
 
-struct RowRing {   // a stage: y | r | dr | dx | gate rows (dr, dx: the gradient's)
+struct RowRing {   // a stage: y | r | dr | dx | gate rows (dr, dx: the gradient's), those that there are
   int stage = 0, off_r = 0, off_dr = 0, off_dx = 0, off_gate = 0, stages = 0;
   RowRing(const NormArgs& a, int groups, size_t bytes) {
     const int res = a.H * (a.res_f32 ? 4 : 2);
@@ -190,6 +190,26 @@ struct RowRing {   // a stage: y | r | dr | dx | gate rows (dr, dx: the gradient
     if (stages > 8) stages = 8;
   }
 };
+
+// One thread: the copies of row t into a stage. The stage's parts say what is copied, so that its barrier
+// expects what comes.
+__device__ __forceinline__ void send_row(const NormArgs& a, const RowRing& ring, uint64_t* bar, unsigned char* st,
+                                         int t) {
+  asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::
+                   "r"(smem_addr(bar)), "r"(ring.stage) : "memory");
+  auto copy = [&](int off, int end, const void* src) {
+    if (off == end) return;
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
+                 "[%0], [%1], %2, [%3];" ::"r"(smem_addr(st + off)),
+                 "l"(static_cast<const char*>(src) + (size_t)t * (end - off)), "r"(end - off),
+                 "r"(smem_addr(bar)) : "memory");
+  };
+  copy(0, ring.off_r, a.y);
+  copy(ring.off_r, ring.off_dr, a.r);
+  copy(ring.off_dr, ring.off_dx, a.dr);
+  copy(ring.off_dx, ring.off_gate, a.dx);
+  copy(ring.off_gate, ring.stage, a.gate);
+}
 
 // Where a wait of k_norm_rows that runs out is recorded (the call has no workspace): only a copy that
 // never lands would let it.
@@ -276,20 +296,7 @@ __global__ void __launch_bounds__(kRingThreads, NV == 2 ? 2 : 1)
   const int t0 = blockIdx.x + g * gridDim.x, dt = RG * gridDim.x;   // rows of this group: t0, t0 + dt, ...
   const int n_rows = t0 < a.T ? (a.T - t0 + dt - 1) / dt : 0;
   auto send = [&](int i) {   // one thread: the copies of row i into stage i % ST
-    uint64_t* bar = &full[g][i % ST];
-    unsigned char* st = mine + (size_t)(i % ST) * ring.stage;
-    const size_t row = (size_t)(t0 + i * dt) * a.H;
-    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::
-                     "r"(smem_addr(bar)), "r"(ring.stage) : "memory");
-    auto copy = [&](int off, const void* src, size_t bytes_per) {
-      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
-                   "[%0], [%1], %2, [%3];" ::"r"(smem_addr(st + off)),
-                   "l"(static_cast<const char*>(src) + row * bytes_per),
-                   "r"((uint32_t)(a.H * bytes_per)), "r"(smem_addr(bar)) : "memory");
-    };
-    copy(0, a.y, 2);
-    if (a.r) copy(ring.off_r, a.r, sizeof(RT));
-    if (element) copy(ring.off_gate, a.gate, 2);
+    send_row(a, ring, &full[g][i % ST], mine + (size_t)(i % ST) * ring.stage, t0 + i * dt);
   };
   auto sum2 = [&](int which, float x, float y) -> float2 {   // two sums over the group's threads
     x = warp_sum(x);
@@ -418,22 +425,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd(const NormArgs a, 
   const int t0 = blockIdx.x + g * gridDim.x, dt = RG * gridDim.x;
   const int n_rows = t0 < a.T ? (a.T - t0 + dt - 1) / dt : 0;
   auto send = [&](int i) {   // one thread: the copies of row i into stage i % ST
-    uint64_t* bar = &full[g][i % ST];
-    unsigned char* st = mine + (size_t)(i % ST) * ring.stage;
-    const size_t row = (size_t)(t0 + i * dt) * a.H;
-    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::
-                     "r"(smem_addr(bar)), "r"(ring.stage) : "memory");
-    auto copy = [&](int off, const void* src, size_t bytes_per) {
-      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
-                   "[%0], [%1], %2, [%3];" ::"r"(smem_addr(st + off)),
-                   "l"(static_cast<const char*>(src) + row * bytes_per),
-                   "r"((uint32_t)(a.H * bytes_per)), "r"(smem_addr(bar)) : "memory");
-    };
-    copy(0, a.y, 2);
-    if (a.r) copy(ring.off_r, a.r, sizeof(RT));
-    if (a.dr) copy(ring.off_dr, a.dr, sizeof(RT));
-    if (pre) copy(ring.off_dx, a.dx, 2);
-    if (element) copy(ring.off_gate, a.gate, 2);
+    send_row(a, ring, &full[g][i % ST], mine + (size_t)(i % ST) * ring.stage, t0 + i * dt);
   };
   auto barrier = [&]() {
     if constexpr (GT == 32) __syncwarp();
