@@ -437,7 +437,9 @@ ft_status ft_paged_decode_attention(const uint16_t* q, int64_t q_stride, int32_t
  *   bf16; x_out bf16 [T, H]; all 16-byte aligned (a token gate 2-byte) and contiguous. r_out may
  *   be NULL when only x' is wanted, and may be the residual itself; x_out may be y itself.
  *   H a multiple of 8, 8 <= H <= 16384; T >= 0; eps >= 0, scale finite. float32 inside; x' is
- *   taken from r' before its rounding.
+ *   taken from r' before its rounding. The squares of a row and their sum are float32: a root mean
+ *   square above 1.8e19 / sqrt(H) overflows it (the norm of that row is 0), and with eps = 0 one
+ *   below about 1e-18 loses bits. The gradient holds over the same range.
  */
 ft_status ft_residual_norm(const uint16_t* y, const void* residual, const uint16_t* w_post,
                            const uint16_t* w_pre, const uint16_t* gate, int32_t gate_kind,

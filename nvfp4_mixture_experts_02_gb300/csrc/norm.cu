@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kRingThreads, NV == 2 ? 2 : 1)
 }
 
 // With u = w_post * (channel gate), tg = scale * (token gate) and e the elementwise gate:
-//   r' = r + (tg s1) y u e     h = tg dr' u e     dy = s1 h - y s1^3 mean(h y)
+//   r' = r + (tg s1) y u e     h = tg dr' u e     dy = s1 (h - y s1^2 mean(h y))
 //   A = sum_t tg s1 y dr' e    dw_post = A * (channel gate), dgate = A * w_post (channel: tg = scale)
 //   dgate = scale s1 sum_h y u dr' (token),  scale s1 y u dr' (element)
 // so one column sum serves both the weight and the channel's gate.
@@ -594,7 +594,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd(const NormArgs a, 
     if (ahead && !pre) refill();
     if (a.gate_kind == FT_GATE_TOKEN && tid == 0)
       static_cast<float*>(a.dgate)[t] = a.scale * s1 * sums.x;
-    const f2 k1 = both(post ? tg * s1 : tg), k2 = both(post ? -(tg * s1 * s1 * s1 * (sums.x * inv_h)) : 0.f);
+    // one factor s1 at a time: s1^3 leaves float32's range for rows of 1e13, or of 1e-13, already
+    const f2 k1 = both(post ? tg * s1 : tg), k2 = both(post ? -(s1 * (s1 * (sums.x * inv_h))) : 0.f);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = tid + v * GT;
@@ -603,7 +604,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd(const NormArgs a, 
         f2 y[4];
         get8(st, c, a.y, y);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[v][j] = fma2(y[j], k2, mul2(h[v][j], k1));
+        for (int j = 0; j < 4; ++j) h[v][j] = mul2(fma2(y[j], k2, h[v][j]), k1);
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) h[v][j] = mul2(h[v][j], k1);
@@ -783,9 +784,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) k_norm_bwd_narrow(const Nor
     const float sum = lane_sum<GS>(sum_of(hy));
     if (!on) continue;
     if (a.gate_kind == FT_GATE_TOKEN && c == 0) static_cast<float*>(a.dgate)[t] = a.scale * s1 * sum;
-    const f2 k1 = both(post ? tg * s1 : tg), k2 = both(post ? -(tg * s1 * s1 * s1 * (sum * inv_h)) : 0.f);
+    const f2 k1 = both(post ? tg * s1 : tg), k2 = both(post ? -(s1 * (s1 * (sum * inv_h))) : 0.f);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = post ? fma2(y[j], k2, mul2(h[j], k1)) : mul2(h[j], k1);
+    for (int j = 0; j < 4; ++j) h[j] = mul2(post ? fma2(y[j], k2, h[j]) : h[j], k1);
     put8(a.dy + at, h);
   }
   // the block's column sums, its groups added in order: [block][quantity][H]
