@@ -60,28 +60,38 @@ class DecodeStep:
         self.lse = torch.empty((batch, Hq), **f32)
         self.y = torch.empty((batch, H), **bf)
         self.logits = torch.empty((batch, w_logits.N), **f32)
+        # one workspace for all of the step's calls: its flags can be read after a replay of the captured step
+        sizes = [ftmoe.paged_attention_workspace_bytes(batch, D)]
+        for layer in layers:
+            e = layer.experts
+            sizes.append(ftmoe.workspace_bytes(batch, layer.k, e.E, e.H, e.I, layer.shared is not None))
+            sizes += [ftmoe.nvfp4_linear_workspace_bytes(batch, w.K) for w in (layer.w_qkv, layer.w_o, w_logits)]
+        self.workspace = torch.zeros(max(sizes), dtype=torch.uint8, device=dev)
 
     def step(self, x_in):
         """x_in bf16 [batch, H], the new tokens' embeddings -> logits f32 [batch, N]; positions and
         lengths advance."""
-        Hq, Hkv = self.Hq, self.Hkv
+        Hq, Hkv, ws = self.Hq, self.Hkv, self.workspace
         # the residual stream begins as the embedding, in float32
         ftmoe.residual_norm(x_in, None, w_pre=self.first_pre, eps=EPS, res_out=self.r, x_out=self.x)
         for layer, cache in zip(self.layers, self.caches):
             qkv = self.qkv
-            ftmoe.nvfp4_linear(self.x, layer.w_qkv, out=qkv.view(qkv.shape[0], -1))
+            ftmoe.nvfp4_linear(self.x, layer.w_qkv, out=qkv.view(qkv.shape[0], -1), workspace=ws)
             q, k, v = qkv.split([Hq, Hkv, Hkv], 1)
-            ftmoe.kv_append(k, v, cache, self.table, self.positions, q=q, rope=self.rope, q_out=self.q)
-            ftmoe.paged_decode_attention(self.q, cache, self.table, self.lengths, out=self.a, lse=self.lse)
-            ftmoe.nvfp4_linear(self.a.view(self.a.shape[0], -1), layer.w_o, out=self.y)
+            ftmoe.kv_append(k, v, cache, self.table, self.positions, q=q, rope=self.rope, q_out=self.q,
+                            workspace=ws)
+            ftmoe.paged_decode_attention(self.q, cache, self.table, self.lengths, out=self.a, lse=self.lse,
+                                         workspace=ws)
+            ftmoe.nvfp4_linear(self.a.view(self.a.shape[0], -1), layer.w_o, out=self.y, workspace=ws)
             ftmoe.residual_norm(self.y, self.r, w_post=layer.attn_post, w_pre=layer.moe_pre,
                                 scale=self.scale, eps=EPS, res_out=self.r, x_out=self.x)
             scores, _ = ftmoe.router_logits(self.x, layer.w_router)
-            ftmoe.decode_routed(self.x, scores, layer.k, layer.experts, layer.shared, out=self.y)
+            ftmoe.decode_routed(self.x, scores, layer.k, layer.experts, layer.shared, out=self.y,
+                                workspace=ws)
             ftmoe.residual_norm(self.y, self.r, w_post=layer.moe_post, w_pre=layer.next_pre,
                                 gate=layer.moe_gate, scale=self.scale, eps=EPS, res_out=self.r,
                                 x_out=self.x)
-        ftmoe.nvfp4_linear(self.x, self.w_logits, out=self.logits)
+        ftmoe.nvfp4_linear(self.x, self.w_logits, out=self.logits, workspace=ws)
         self.positions.add_(1)
         self.lengths.add_(1)
         return self.logits
@@ -145,6 +155,7 @@ def main():
         graph.replay()
     end.record()
     torch.cuda.synchronize()
+    assert ftmoe.get_error(model.workspace) == 0
     print(f"{args.steps} steps of {args.layers} layers for {args.batch} sequences: "
           f"{begin.elapsed_time(end) / args.steps * 1e3:.1f} us a step, last tokens {tokens.tolist()}")
 

@@ -332,6 +332,7 @@ size_t ft_nvfp4_linear_workspace_bytes(int32_t T, int32_t K);
  *            fully overwritten; float32 sums, the matrix's scale last, rounded once
  *   workspace ft_nvfp4_linear_workspace_bytes(T, K) bytes, 256-byte aligned (NULL when that is 0);
  *            any contents past the error word; calls that share it must be ordered on one stream
+ *            and made by one thread at a time (a call may be several launches)
  *   A NaN block scale gives NaN; x is used as it is (infinities and NaN propagate).
  */
 ft_status ft_nvfp4_linear(const uint16_t* x, int32_t T, int64_t x_stride,
@@ -409,7 +410,8 @@ size_t ft_paged_attention_workspace_bytes(int32_t B, int32_t D);
  *   out          bf16 [B, Hq, D], lse float [B, Hq] or NULL, fully overwritten
  *   workspace    ft_paged_attention_workspace_bytes(B, D) bytes, 256-byte aligned, its first
  *                FT_MOE_WORKSPACE_HEAD_BYTES zeroed once (ft_moe_workspace_init); calls that
- *                share it must be ordered on one stream. It may be shared with the layer calls.
+ *                share it must be ordered on one stream and made by one thread at a time (a call is
+ *                two launches). It may be shared with the layer calls.
  *   0 <= B <= 4096. Whatever masked slots hold does not reach the output. Float32 scores,
  *   statistics and sums. Before a weight meets its value it is rounded: to 16 bits with a bf16
  *   cache; with an E4M3 cache to 22, or to within 2^-40 of the largest key's weight. The work is split over the cache's length and joined in a fixed

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import threading
 from dataclasses import dataclass
 from typing import NamedTuple
 
@@ -458,26 +459,55 @@ def new_workspace(T, k, experts: NvFP4Experts, has_shared, prefill=False, device
     return ws
 
 
-# Calls made without a workspace share one per (device, stream): launches on one stream run
-# in order, so a call never finds its workspace in use by an earlier call that is still
-# running. It grows (a new, larger one) when a call needs more; nothing is allocated on
-# calls that fit.
-_DEFAULT_WS = {}
+# Calls made without a workspace share one per (host thread, device, stream). Launches on one
+# stream run in order, so a call never finds its workspace in use by an earlier call that is
+# still running; a call of several launches is not one step for another thread, whose launches
+# may come between them, so threads do not share. The workspace grows (a new, larger one) when a
+# call needs more; nothing is allocated on calls that fit. The old one goes back to its stream's
+# pool, and no graph holds its address: a call that is being captured takes a workspace from
+# the capture's own pool, which lives as long as the graph.
+class _Kept(threading.local):
+    def __init__(self):
+        self.by_stream = {}
+
+
+_KEPT = _Kept()
+
+
+def _new_scratch(n, dev, head=True):
+    ws = torch.empty(n + 256, dtype=torch.uint8, device=torch.device("cuda", dev))
+    off = (-ws.data_ptr()) % 256
+    ws = ws[off:off + n]
+    if head:
+        _check(_LIB.ft_moe_workspace_init(_ptr(ws), n, _stream(None, dev)), "ft_moe_workspace_init")
+    return ws
+
+
+def _scratch(n, dev, head=False):
+    """n bytes at least for a call on the current stream of cuda:dev. head: its counters are needed
+    (zeroed in a captured workspace too; kept ones always are)."""
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return _new_scratch(n, dev, head)
+    kept, key = _KEPT.by_stream, (dev, torch._C._cuda_getCurrentRawStream(dev))
+    ws = kept.get(key)
+    if ws is None or ws.numel() < n:
+        old, ws = ws, _new_scratch(n, dev)
+        if old is not None:
+            ws[:4].copy_(old[:4])   # the flags of earlier calls
+        kept[key] = ws
+    return ws
 
 
 def default_workspace(T, k, experts: NvFP4Experts, has_shared, prefill=False, stream=None):
-    """The workspace a call without one uses: kept per (device, stream) and reused."""
+    """The workspace a call without one uses: kept per (host thread, device, stream) and reused,
+    or, while the stream is captured, one of the capture's own."""
+    if stream is not None:
+        with torch.cuda.stream(stream):   # it belongs to the stream that uses it
+            return default_workspace(T, k, experts, has_shared, prefill)
     n = workspace_bytes(T, k, experts.E, experts.H, experts.I, has_shared, prefill)
     if n == 0:
-        return new_workspace(T, k, experts, has_shared, prefill, stream=stream)
-    if stream is None:
-        stream = torch.cuda.current_stream(experts.device_index)
-    key = (experts.device_index, stream.cuda_stream)
-    ws = _DEFAULT_WS.get(key)
-    if ws is None or ws.numel() < n:
-        ws = new_workspace(T, k, experts, has_shared, prefill, stream=stream)
-        _DEFAULT_WS[key] = ws
-    return ws
+        return new_workspace(T, k, experts, has_shared, prefill)
+    return _scratch(n, experts.device_index, True)
 
 
 def _call_tensors(experts, shared, x, out, workspace, T_name="x"):
@@ -703,24 +733,6 @@ def _need_rows(t, name, dev, inner):
     if stride[0] < row:
         raise ValueError(f"{name}: the rows must not overlap")
     return stride[0]
-
-
-def _scratch(n, dev):
-    """n bytes of the workspace that calls without one share per (device, stream)."""
-    key = (dev, torch._C._cuda_getCurrentRawStream(dev))
-    ws = _DEFAULT_WS.get(key)
-    if ws is None or ws.numel() < n:
-        ws = _new_scratch(n, dev)
-        _DEFAULT_WS[key] = ws
-    return ws
-
-
-def _new_scratch(n, dev):
-    ws = torch.empty(n + 256, dtype=torch.uint8, device=torch.device("cuda", dev))
-    off = (-ws.data_ptr()) % 256
-    ws = ws[off:off + n]
-    _check(_LIB.ft_moe_workspace_init(_ptr(ws), n, _stream(None, dev)), "ft_moe_workspace_init")
-    return ws
 
 
 @dataclass(frozen=True)
