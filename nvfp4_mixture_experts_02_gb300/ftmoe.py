@@ -844,7 +844,8 @@ def kv_append(k, v, cache: PagedKVCache, block_table, positions, seq_ids=None, q
     """ft_kv_append: k, v bf16 [T,Hkv,D] into the cache's slots of `positions` int32 [T] (of the
     sequences seq_ids int32 [T], or 0..T-1) through block_table int32 [B,width], k rotated by rope
     f32 [rows, R] (cos | sin; None: not at all). Returns the rotated q bf16 [T,Hq,D], or None
-    without q. Rows of k, v and q may be slices of one projection's output."""
+    without q. Rows of k, v and q may be slices of one projection's output. A token whose page,
+    sequence or position lies outside its table stores nothing and flags it (get_error)."""
     if stream is not None:
         with torch.cuda.stream(stream):   # what the call makes belongs to the stream that it runs on
             return kv_append(k, v, cache, block_table, positions, seq_ids, q, rope, q_out, workspace)
@@ -884,6 +885,8 @@ def kv_append(k, v, cache: PagedKVCache, block_table, positions, seq_ids=None, q
         _need(workspace, "workspace", dev, None, None)
         if workspace.numel() < WORKSPACE_HEAD_BYTES:
             raise ValueError("workspace: at least WORKSPACE_HEAD_BYTES expected")
+    elif T > 0:
+        workspace = _scratch(WORKSPACE_HEAD_BYTES, dev)   # for its flags
     st = _LIB.ft_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, qo, T, Hq, cache._ref,
                            block_table.data_ptr(), B, width,
                            0 if seq_ids is None else seq_ids.data_ptr(), positions.data_ptr(), rp,
@@ -1075,7 +1078,15 @@ def residual_norm_backward(y, residual, d_r, d_x=None, w_post=None, w_pre=None, 
     return NormGradients(dy, dres, dw_post, dw_pre, dgate)
 
 
-def get_error(workspace, stream=None) -> int:
+def get_error(workspace=None, stream=None) -> int:
+    """ft_moe_get_error: what the calls with this workspace have flagged since the last look, or,
+    without one, those that this thread made on the stream (the current one) without a workspace.
+    A captured call without a workspace has nowhere to flag: give it one."""
+    if workspace is None:
+        dev = torch.cuda.current_device() if stream is None else stream.device_index
+        workspace = _KEPT.by_stream.get((dev, _stream(stream, dev)))
+        if workspace is None:
+            return FT_OK
     dev = _device_of(workspace, "ft_moe_get_error")
     return _LIB.ft_moe_get_error(_ptr(workspace), _stream(stream, dev))
 

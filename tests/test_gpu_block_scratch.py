@@ -113,3 +113,37 @@ def test_the_workspace_belongs_to_the_stream_it_is_asked_for():
     home = [seg["stream"] for seg in torch.cuda.memory_snapshot()
             if seg["address"] <= ws.data_ptr() < seg["address"] + seg["total_size"]]
     assert home == [s.cuda_stream]
+
+
+def test_flags_of_calls_without_a_workspace_can_be_read():
+    m = ftmoe()
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache = m.PagedKVCache(*(torch.zeros((4, 16, 1, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2)))
+    one = torch.ones((1, 1, 64), dtype=torch.bfloat16, device="cuda")
+    table = i32([[0, 9]])
+
+    def append(pos):
+        m.kv_append(one, one, cache, table, i32([pos]))
+
+    def attend(n):
+        m.paged_decode_attention(one, cache, table, i32([n]))
+
+    m.get_error()                                     # what earlier tests of this thread left
+    for f, arg, bad in ((append, 3, 0), (append, 17, 6), (append, 40, 6), (append, -1, 0), (attend, 4, 0),
+                        (attend, 20, 6), (attend, 33, 6)):
+        f(arg)
+        assert m.get_error() == bad and m.get_error() == 0, (f, arg)
+    append(17)                                        # another thread or stream has its own
+    s, seen = torch.cuda.Stream(), []
+    t = threading.Thread(target=lambda: seen.extend([m.get_error(), m.get_error(stream=s)]))
+    t.start()
+    t.join()
+    assert seen == [0, 0] and m.get_error(stream=s) == 0
+    with torch.cuda.stream(s):
+        append(3)
+        append(17)
+        attend(4)                                     # a larger workspace takes the flags along
+        assert m.get_error() == 6
+    append(17)
+    s.synchronize()
+    assert m.get_error(stream=s) == 0 and m.get_error() == 6
