@@ -442,6 +442,8 @@ ft_status ft_paged_decode_attention(const uint16_t* q, int64_t q_stride, int32_t
  *   taken from r' before its rounding. The squares of a row and their sum are float32: a root mean
  *   square above 1.8e19 / sqrt(H) overflows it (the norm of that row is 0), and with eps = 0 one
  *   below about 1e-18 loses bits. The gradient holds over the same range.
+ *   There is no workspace and so no error word: should an asynchronous copy of a row not arrive
+ *   within about a second, that row's r' and x' are NaN.
  */
 ft_status ft_residual_norm(const uint16_t* y, const void* residual, const uint16_t* w_post,
                            const uint16_t* w_pre, const uint16_t* gate, int32_t gate_kind,
@@ -482,11 +484,13 @@ ft_status ft_moe_get_error(void* workspace, void* stream);
 
 /* Test hook for the failure path; the pages have no counterpart. Sets, for this process,
  * how many times a decode kernel polls for the other CTAs' results (the grid barrier of
- * the several-token kernel, the slot-completion counters of the one-token kernel) before
- * it gives up: it then sets FT_ERR_TIMEOUT in the workspace error word, goes on with what
+ * the several-token kernel, the slot-completion counters of the one-token kernel), or a
+ * dense product, norm or gradient for its asynchronous copies, before it gives up: it then sets FT_ERR_TIMEOUT in the workspace error word, goes on with what
  * it has (the output is then undefined) and returns normally, and the workspace is left
  * ready for the next call. iterations < 0 restores the default bound (about a second of
- * waiting); 0 makes a wait give up at its first poll that finds the results incomplete.
+ * waiting); 0 makes a wait give up at its first poll that finds the results incomplete (for
+ * copies: without a poll). ft_residual_norm has no workspace to flag: rows of more than 2048
+ * elements whose copies did not arrive in time are NaN.
  * Returns FT_OK. Not for production use: set it only while no decode call is being
  * enqueued by another thread. */
 ft_status ft_moe_debug_set_wait_limit(int64_t iterations);

@@ -111,6 +111,7 @@ struct LinearArgs {
   uint16_t* xh;
   float* part;
   int split;               // blocks of a cluster that share K (set by the launch)
+  unsigned wait_rounds;    // of a wait for x (set by the launch)
 };
 // Workspace regions (byte offsets, 256-byte aligned): none for the calls that lay x out themselves.
 constexpr int kLinearFew = 8;   // tokens up to which they do

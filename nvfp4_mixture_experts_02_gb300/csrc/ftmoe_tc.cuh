@@ -28,21 +28,25 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
                : "memory");
 }
 
+// One round of a wait: has the phase of the given parity completed, now or within kWaitSuspendNs?
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(kWaitSuspendNs)
+      : "memory");
+  return done != 0;
+}
+
 // Bounded wait for the given phase parity; returns false (and sets the timeout bit of the
-// error word) when the limit is reached, so a lost completion cannot hang the GPU.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* err, int bit) {
-  const uint32_t a = smem_addr(bar);
-  for (uint32_t it = 0; it < kWaitRounds; ++it) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(a), "r"(parity), "r"(kWaitSuspendNs)
-        : "memory");
-    if (done) return true;
-  }
-  atomicOr(err, bit);
+// error word, if there is one) when the limit is reached, so a lost completion cannot hang the GPU.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* err, int bit,
+                                          uint32_t rounds = kWaitRounds) {
+  for (uint32_t it = 0; it < rounds; ++it)
+    if (mbar_poll(bar, parity)) return true;
+  if (err) atomicOr(err, bit);
   return false;
 }
 

@@ -541,8 +541,9 @@ __global__ void __launch_bounds__(kLinWarps * 32, NT <= 4 ? 2 : 1)
                  "l"(reinterpret_cast<const char*>(a.xh) + (size_t)((u0 + i) % uk) * kX), "r"(kX),
                  "r"(smem_addr(&full[st])) : "memory");
   };
+  int sent = 0;   // units of x (one thread)
   if (threadIdx.x == 0)
-    for (int i = 0; i < ST && u0 + i < u1; ++i) send(i);
+    for (; sent < ST && u0 + sent < u1; ++sent) send(sent);
 
   // the cursor of the loads: units from u0 on, PU pieces each
   Piece<2> buf[AHEAD];
@@ -575,7 +576,13 @@ __global__ void __launch_bounds__(kLinWarps * 32, NT <= 4 ? 2 : 1)
     for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
   for (int u = u0; u < u1; ++u) {
     const int i = u - u0, st = i % ST;
-    if (!mbar_wait(&full[st], (uint32_t)(i / ST) & 1u, a.err, kErrTimeout)) break;
+    if (!mbar_wait(&full[st], (uint32_t)(i / ST) & 1u, a.err, kErrTimeout, a.wait_rounds)) {
+      // flagged, the results are undefined; the block leaves once its copies have landed
+      if (threadIdx.x == 0)
+        for (int j = sent > ST ? sent - ST : 0; j < sent; ++j)
+          mbar_wait(&full[j % ST], (uint32_t)(j / ST) & 1u, nullptr, 0);
+      break;
+    }
     __syncwarp();
     const uint4* xu = reinterpret_cast<const uint4*>(more_smem + st * kX) + lane;
 #pragma unroll
@@ -586,9 +593,9 @@ __global__ void __launch_bounds__(kLinWarps * 32, NT <= 4 ? 2 : 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[st]);
     // the stage before this one again, once every warp has read it
-    if (threadIdx.x == 0 && i > 0 && u - 1 + ST < u1 &&
-        mbar_wait(&empty[(i - 1) % ST], (uint32_t)((i - 1) / ST) & 1u, a.err, kErrTimeout))
-      send(i - 1 + ST);
+    if (threadIdx.x == 0 && i > 0 && sent == i - 1 + ST && u0 + sent < u1 &&
+        mbar_wait(&empty[(i - 1) % ST], (uint32_t)((i - 1) / ST) & 1u, a.err, kErrTimeout, a.wait_rounds))
+      send(sent++);
     const int tile = u / uk;
     if (u + 1 < u1 && (u + 1) % uk != 0) continue;
     // the end of the tile or of the run: lane has rows r + 8 i of tokens 8 n + 2 q, + 1
@@ -705,7 +712,8 @@ cudaError_t launch_mid(LinearArgs a, int num_sms, cudaStream_t stream) {
 }
 
 template <int NT>
-cudaError_t launch_more(const LinearArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_more(LinearArgs a, int num_sms, cudaStream_t stream) {
+  a.wait_rounds = wait_limit(kWaitRounds);
   constexpr int TOK = NT * 8;
   const int uk = (a.K + kLinUnit - 1) / kLinUnit;
   const int tiles = (a.N + kMoreRows - 1) / kMoreRows, total = tiles * uk;

@@ -179,6 +179,7 @@ constexpr size_t kRingBytes = 224 * 1024;   // one stage of the widest rows: 163
 
 struct RowRing {   // a stage: y | r | dr | dx | gate rows (dr, dx: the gradient's), those that there are
   int stage = 0, off_r = 0, off_dr = 0, off_dx = 0, off_gate = 0, stages = 0;
+  uint32_t rounds = wait_limit(kWaitRounds);   // of a wait for a row
   RowRing(const NormArgs& a, int groups, size_t bytes) {
     const int res = a.H * (a.res_f32 ? 4 : 2);
     off_r = 2 * a.H;
@@ -211,9 +212,37 @@ __device__ __forceinline__ void send_row(const NormArgs& a, const RowRing& ring,
   copy(ring.off_gate, ring.stage, a.gate);
 }
 
-// Where a wait of k_norm_rows that runs out is recorded (the call has no workspace): only a copy that
-// never lands would let it.
-__device__ int g_norm_err;
+// What a row group keeps in shared memory beside its ring.
+template <typename V, int W>
+struct RowGroup {
+  V red[2][W];        // the warps' sums, two arrays in turn
+  uint64_t full[8];   // a stage's row has arrived
+  int lost, sent;     // a wait has run out; rows sent
+};
+
+// A row's wait. One that runs out (only a copy that never lands would let it) sets lost: the group sends no
+// more, its later waits are one poll each, and before its block leaves, one thread waits for what the group's
+// last copies still bring, so that no copy comes to shared memory that is someone else's. The rare part is a
+// function of its own: inside the loops it costs registers that they spill (8192 x 2048 gradient, float32
+// stream, 56.4 us for 52.0).
+__device__ __noinline__ bool row_late(uint64_t* bar, uint32_t parity, uint32_t rounds, volatile int* lost, int* err) {
+  for (uint32_t it = 0; it < rounds && !*lost; ++it)
+    if (mbar_poll(bar, parity)) return true;
+  *lost = 1;
+  if (err) atomicOr(err, kErrTimeout);
+  return false;
+}
+template <typename G>
+__device__ __forceinline__ bool row_arrived(G& grp, int i, int stages, uint32_t rounds, int* err) {
+  uint64_t* bar = &grp.full[i % stages];
+  const uint32_t parity = (uint32_t)(i / stages) & 1u;
+  return (rounds > 0 && mbar_poll(bar, parity)) || row_late(bar, parity, rounds, &grp.lost, err);
+}
+template <typename G>
+__device__ __forceinline__ void drain_rows(G& grp, int stages) {
+  for (int i = grp.sent > stages ? grp.sent - stages : 0; i < grp.sent; ++i)
+    mbar_wait(&grp.full[i % stages], (uint32_t)(i / stages) & 1u, nullptr, 0);
+}
 
 // Two float32 in one 64-bit register pair: half the arithmetic instructions (packed operations round
 // each half as the scalar ones do).
@@ -279,16 +308,19 @@ __global__ void __launch_bounds__(kRingThreads, NV == 2 ? 2 : 1)
     k_norm_rows(const NormArgs a, const RowRing ring) {
   constexpr int RG = kRingThreads / GT, W = GT / 32;
   extern __shared__ __align__(128) unsigned char ring_smem[];
-  __shared__ __align__(8) uint64_t full[RG][8];
-  __shared__ __align__(16) float2 red[RG][2][W];
+  __shared__ __align__(16) RowGroup<float2, W> groups[RG];
+  RowGroup<float2, W>& grp = groups[threadIdx.x / GT];
   const int g = threadIdx.x / GT, tid = threadIdx.x % GT, warp = tid >> 5, lane = tid & 31;
   const int chunks = a.H >> 3, ST = ring.stages;
   const float inv_h = 1.0f / (float)a.H;
   const bool channel = a.gate_kind == FT_GATE_CHANNEL, element = a.gate_kind == FT_GATE_ELEMENT;
   const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr;
   const RT* const kind = nullptr;
-  if (tid < ST) mbar_init(&full[g][tid], 1);
-  if (tid == 0) asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  if (tid < ST) mbar_init(&grp.full[tid], 1);
+  if (tid == 0) {
+    grp.lost = grp.sent = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   __syncthreads();
   griddep_launch_dependents();
   griddep_wait();
@@ -296,14 +328,14 @@ __global__ void __launch_bounds__(kRingThreads, NV == 2 ? 2 : 1)
   const int t0 = blockIdx.x + g * gridDim.x, dt = RG * gridDim.x;   // rows of this group: t0, t0 + dt, ...
   const int n_rows = t0 < a.T ? (a.T - t0 + dt - 1) / dt : 0;
   auto send = [&](int i) {   // one thread: the copies of row i into stage i % ST
-    send_row(a, ring, &full[g][i % ST], mine + (size_t)(i % ST) * ring.stage, t0 + i * dt);
+    send_row(a, ring, &grp.full[i % ST], mine + (size_t)(i % ST) * ring.stage, t0 + i * dt);
   };
   auto sum2 = [&](int which, float x, float y) -> float2 {   // two sums over the group's threads
     x = warp_sum(x);
     y = warp_sum(y);
-    if (lane == 0) red[g][which][warp] = make_float2(x, y);
+    if (lane == 0) grp.red[which][warp] = make_float2(x, y);
     asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "n"(GT) : "memory");
-    float2 v = red[g][which][lane % W];
+    float2 v = grp.red[which][lane % W];
 #pragma unroll
     for (int o = W / 2; o > 0; o >>= 1) {
       v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
@@ -333,20 +365,22 @@ __global__ void __launch_bounds__(kRingThreads, NV == 2 ? 2 : 1)
     }
     return sum_of(ss);
   };
-  auto arrived = [&](int i) {
-    mbar_wait(&full[g][i % ST], (uint32_t)(i / ST) & 1u, &g_norm_err, kErrTimeout);
+  auto y_sum = [&](int i) -> float {   // waits for row i; NaN if it does not come
+    if (!row_arrived(grp, i, ST, ring.rounds, nullptr)) return __int_as_float(0x7FC00000);
+    return post ? square_sum(mine + (size_t)(i % ST) * ring.stage) : 0.f;
   };
 
-  if (tid == 0)
-    for (int i = 0; i < ST && i < n_rows; ++i) send(i);
   if (n_rows == 0) return;   // a whole group: its barriers are its own
-  arrived(0);
-  float ss = sum2(1, post ? square_sum(mine) : 0.f, 0.f).x;
+  if (tid == 0) {
+    grp.sent = min(ST, n_rows);
+    for (int i = 0; i < ST && i < n_rows; ++i) send(i);
+  }
+  float ss = sum2(1, y_sum(0), 0.f).x;
   for (int i = 0; i < n_rows; ++i) {
     const int t = t0 + i * dt;
     const size_t row = (size_t)t * a.H;
     const unsigned char* st = mine + (size_t)(i % ST) * ring.stage;
-    const float s1 = post ? rsqrtf(ss * inv_h + a.eps) : 1.f;
+    const float s1 = post ? rsqrtf(ss * inv_h + a.eps) : 1.f + ss;
     const f2 ts = both(a.scale * (a.gate_kind == FT_GATE_TOKEN ? one_bf16(a.gate + t) : 1.f) * s1);
     f2 r[NV][4], rr = 0ull;
 #pragma unroll
@@ -374,14 +408,13 @@ __global__ void __launch_bounds__(kRingThreads, NV == 2 ? 2 : 1)
       }
       if (a.r_out) put8(static_cast<RT*>(a.r_out) + row + 8 * c, r[v]);
     }
-    float next = 0.f;
-    if (i + 1 < n_rows) {
-      arrived(i + 1);
-      if (post) next = square_sum(mine + (size_t)((i + 1) % ST) * ring.stage);
-    }
+    const float next = i + 1 < n_rows ? y_sum(i + 1) : 0.f;
     const float2 sums = sum2(i & 1, sum_of(rr), next);
     ss = sums.y;
-    if (tid == 0 && i + ST < n_rows) send(i + ST);   // every thread has read the row
+    if (tid == 0 && i + ST < n_rows && !grp.lost) {   // every thread has read the row
+      send(i + ST);
+      grp.sent = i + ST + 1;
+    }
     if (!pre) continue;
     const f2 s2 = both(rsqrtf(sums.x * inv_h + a.eps));
 #pragma unroll
@@ -395,6 +428,7 @@ __global__ void __launch_bounds__(kRingThreads, NV == 2 ? 2 : 1)
       put8(a.x_out + row + 8 * c, r[v]);
     }
   }
+  if (tid == 0 && grp.lost) drain_rows(grp, ST);
 }
 
 // With u = w_post * (channel gate), tg = scale * (token gate) and e the elementwise gate:
@@ -406,8 +440,8 @@ template <int GT, int NV, typename RT>
 __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd(const NormArgs a, const RowRing ring) {
   constexpr int RG = kRingThreads / GT, W = GT / 32;
   extern __shared__ __align__(128) unsigned char bwd_smem[];
-  __shared__ __align__(8) uint64_t full[RG][8];
-  __shared__ float4 red[RG][2][W];
+  __shared__ __align__(16) RowGroup<float4, W> groups[RG];
+  RowGroup<float4, W>& grp = groups[threadIdx.x / GT];
   const int g = threadIdx.x / GT, tid = threadIdx.x % GT, warp = tid >> 5, lane = tid & 31;
   const int chunks = a.H >> 3, ST = ring.stages;
   const bool ahead = ST >= 3;   // stages enough to look at the next row's y within this one
@@ -415,8 +449,11 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd(const NormArgs a, 
   const bool channel = a.gate_kind == FT_GATE_CHANNEL, element = a.gate_kind == FT_GATE_ELEMENT;
   const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr;
   const RT* const kind = nullptr;
-  if (tid < ST) mbar_init(&full[g][tid], 1);
-  if (tid == 0) asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  if (tid < ST) mbar_init(&grp.full[tid], 1);
+  if (tid == 0) {
+    grp.lost = grp.sent = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   __syncthreads();
   griddep_launch_dependents();
   griddep_wait();
@@ -425,7 +462,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd(const NormArgs a, 
   const int t0 = blockIdx.x + g * gridDim.x, dt = RG * gridDim.x;
   const int n_rows = t0 < a.T ? (a.T - t0 + dt - 1) / dt : 0;
   auto send = [&](int i) {   // one thread: the copies of row i into stage i % ST
-    send_row(a, ring, &full[g][i % ST], mine + (size_t)(i % ST) * ring.stage, t0 + i * dt);
+    send_row(a, ring, &grp.full[i % ST], mine + (size_t)(i % ST) * ring.stage, t0 + i * dt);
   };
   auto barrier = [&]() {
     if constexpr (GT == 32) __syncwarp();
@@ -435,9 +472,9 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd(const NormArgs a, 
   auto sum2 = [&](int which, float x, float y) -> float2 {
     x = warp_sum(x);
     y = warp_sum(y);
-    if (lane == 0) red[g][which][warp] = make_float4(x, y, 0.f, 0.f);
+    if (lane == 0) grp.red[which][warp] = make_float4(x, y, 0.f, 0.f);
     barrier();
-    float4 v = red[g][which][lane % W];
+    float4 v = grp.red[which][lane % W];
 #pragma unroll
     for (int o = W / 2; o > 0; o >>= 1) {
       v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
@@ -476,11 +513,13 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd(const NormArgs a, 
     return sum_of(ss);
   };
   auto arrived = [&](int i) {
-    mbar_wait(&full[g][i % ST], (uint32_t)(i / ST) & 1u, a.err, kErrTimeout);
+    row_arrived(grp, i, ST, ring.rounds, a.err);   // one that does not come is flagged
   };
 
-  if (tid == 0)
+  if (tid == 0) {
+    grp.sent = min(ST, n_rows);
     for (int i = 0; i < ST && i < n_rows; ++i) send(i);
+  }
   float ss = 0.f;   // of the coming row's y, already summed
   if (n_rows > 0 && ahead) {
     arrived(0);
@@ -493,7 +532,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd(const NormArgs a, 
     const unsigned char* st = mine + (size_t)(i % ST) * ring.stage;
     // once every thread is past the row before this one its stage takes a new row
     auto refill = [&]() {
-      if (ST > 1 && tid == 0 && i > 0 && i - 1 + ST < n_rows) send(i - 1 + ST);
+      if (ST > 1 && tid == 0 && i > 0 && i - 1 + ST < n_rows && !grp.lost) {
+        send(i - 1 + ST);
+        grp.sent = i + ST;
+      }
     };
     if (!ahead) {
       arrived(i);
@@ -613,12 +655,16 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_norm_bwd(const NormArgs a, 
     }
     if (ST == 1) {
       barrier();
-      if (tid == 0 && i + 1 < n_rows) send(i + 1);
+      if (tid == 0 && i + 1 < n_rows && !grp.lost) {
+        send(i + 1);
+        grp.sent = i + 2;
+      }
     } else if (!pre || !ahead) {
       barrier();   // red[0] is written again before another barrier of the next row
     }
   }
 
+  if (tid == 0 && grp.lost) drain_rows(grp, ST);
   // the block's column sums, its groups added in order: [block][quantity][H]
   float* part = a.part + (size_t)blockIdx.x * a.nq * a.H;
   float* cols = reinterpret_cast<float*>(bwd_smem);   // [group][H], over the rings
