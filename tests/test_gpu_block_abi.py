@@ -43,3 +43,23 @@ def test_a_gradient_of_x_without_its_weight_is_ignored(H, gate, res):
     backward(m, d, gate, *got, None, dgate, torch.full_like(d["y"], float("nan")))
     for a, b in zip([*got, dgate], (want.dy, want.dresidual, want.dw_post, want.dgate)):
         assert (a is None and b is None) or torch.equal(a, b)
+
+
+@pytest.mark.parametrize("H,gate,res,T", [(64, "token", torch.bfloat16, 10037), (128, "element", torch.float32, 9001),
+                                          (256, "none", torch.bfloat16, 5003), (504, "channel", torch.float32, 9001),
+                                          (520, "element", torch.bfloat16, 4001), (1032, "token", torch.float32, 4001),
+                                          (4096, "channel", torch.bfloat16, 1500), (4096, "element", torch.float32, 1500),
+                                          (8192, "none", torch.bfloat16, 700), (8192, "element", torch.float32, 700),
+                                          (16384, "none", torch.bfloat16, 500), (16384, "element", torch.float32, 500)])
+@pytest.mark.parametrize("onto", ["y", "dx"])
+def test_gradients_in_place(H, gate, res, T, onto):
+    """dresidual over d_r, dy over y or d_x, with several rows a group and one to eight stages of them."""
+    m = ftmoe()
+    d = {n: cuda(t) for n, t in inputs(np.random.default_rng(H + T), T, H, res, True, True, gate).items()}
+    want = m.residual_norm_backward(d["y"], d["r"], d["dr"], d["dx"], w_post=d["w_post"], w_pre=d["w_pre"],
+                                    gate=d["gate"], scale=0.7, eps=1e-5)
+    sums = [torch.empty_like(t) for t in (want.dw_post, want.dw_pre)]
+    dgate = None if want.dgate is None else torch.empty_like(want.dgate)
+    backward(m, d, gate, d[onto], d["dr"], *sums, dgate, d["dx"])
+    for a, b in zip([d[onto], d["dr"], *sums, dgate], want):
+        assert (a is None and b is None) or torch.equal(a, b)
