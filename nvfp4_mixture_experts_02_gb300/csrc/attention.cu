@@ -4,8 +4,9 @@
 //   out = sum_j exp(s_j - m) v_scale v_j / sum_j exp(s_j - m),  m = max_j s_j
 //   lse = m + ln(sum_j exp(s_j - m));   an empty sequence: out = 0, lse = -inf
 //
-// Every key and value is read once, by one block, for all the query heads that share it: the call
-// is bound by the cache's bytes (4 G operations per key element of 1 or 2 bytes).
+// Every key and value is read once, by one block, for up to 16 query heads that share it, and once more
+// for every 16 beyond: the call is bound by the cache's bytes (4 G operations per key element of 1 or 2
+// bytes).
 //
 // k_attend: the work is the list of (sequence, key heads, unit of keys), in that order; every block
 // takes an equal run of it, whatever the lengths, found from the lengths on the device (no host
@@ -29,9 +30,9 @@
 // a key head (16 x 8192, 41.1 and 43.2 us).
 // Statistics and sums are float32.
 //
-// Measured (of the copy rate of 6786 GB/s): three sequences up to 131072, bf16, 962 MB: 153 us (93 %).
-// 48 ragged ones up to 8192, E4M3, 423 MB: 83 to 85 us (74 %), of which some 10 us are launches, fill and
-// join, and the runs' pieces differ in cost. One sequence of 777: 7.7 us, two launches and the chain
+// Measured (of the copy rate of 6786 GB/s): three sequences up to 131072, bf16, 962 MB: 155 us (91 %).
+// 48 ragged ones up to 8192, E4M3, 423 MB: 85 us (73 %), of which some 10 us are launches, fill and
+// join, and the runs' pieces differ in cost. One sequence of 777: 7.8 us, two launches and the chain
 // length, page, keys, scores, sums, join.
 #include <cmath>
 #include <cuda_runtime.h>
@@ -51,7 +52,8 @@ struct AttnShape {
   static constexpr int kKeys = kRow <= 128 ? 32 : 16; // keys of a warp's step
   static constexpr int kStageBytes = 2 * kKeys * kRow;   // those keys and values
   // blocks an SM: the others stream while one joins a piece's warps. Three of two stages each, not two of
-  // three, where the registers allow it: 256 sequences up to 1024 with 8-bit keys of 128: 68 us for 79
+  // three, where the registers allow it: 256 sequences up to 1024 with 8-bit keys of 128: 68 us for 79.
+  // (Past some 2600 sequences their running sums in shared memory leave room for two.)
   static constexpr int kBlocks = kRow >= 512 ? 1 : kRow == 128 && NG == 1 ? kAttendBlocks : 2;
   static constexpr int kWarps = kRow >= 128 ? 4 : 8;
   static constexpr int kStages = 192 * 1024 / (kBlocks * kWarps * kStageBytes);

@@ -28,9 +28,9 @@
 // tokens on the warp schedulers. At 100003 x 4096 (34 us of memory time): 1 token 41 us, 83 % of the
 // measured copy rate; 5 tokens 43; 16 tokens 57; 32 and 64 tokens 87 and 138 us, where the m16n8k16 rate
 // (1024 products per clock and SM: 44 and 88 us) is the larger bound. The same tiles through tcgen05 with
-// the converted weights in tensor memory took 103 us at 16 tokens and 118 at 64: its rate per 128 x 16
-// block does not depend on the tokens, but the hand-over through tensor memory and barriers costs 1.2 us
-// per 128 x 256 weights. Small matrices are bound by latency: 1 x 4096 x 4096 takes 4.6 us for 1.4 us of
+// the converted weights in tensor memory took 103 us at 16 tokens and 118 at 64, where it was the faster; it
+// is not in this file. Its rate per 128 x 16 block does not depend on the tokens, but the hand-over through
+// tensor memory and barriers costs 1.2 us per 128 x 256 weights. Small matrices are bound by latency: 1 x 4096 x 4096 takes 4.6 us for 1.4 us of
 // memory time, a chain of launch, x's layout, load, conversion, sum and store; two pieces ahead beat four
 // there (5.2 or 5.9 us before x's layout was one token's own code).
 #include <cmath>
@@ -696,7 +696,9 @@ cudaError_t launch_mid(LinearArgs a, int num_sms, cudaStream_t stream) {
   const int groups = (a.T + TOK - 1) / TOK;
   auto x_bytes = [&](int split) { return (size_t)((pieces + split - 1) / split) * 256 * TOK; };
   // K over a cluster while twice the blocks are at most two an SM and every warp keeps a piece, and
-  // while x does not fit
+  // while x does not fit. This counts blocks, not rounds: 256 blocks (32 tokens of 4096 x 4096) leave 104 SMs
+  // with two of them and 48 with one, and clusters of eight take two rounds from 34 row tiles on (11 x 4718 x
+  // 4096 12.5 us, 9.3 with clusters of four).
   int split = 1;
   while (split < 8 && (x_bytes(split) > kLinXMax / 2 ||
                        (tiles * groups * split <= num_sms && pieces >= 4 * split)))

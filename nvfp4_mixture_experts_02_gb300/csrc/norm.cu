@@ -18,8 +18,8 @@
 // k_norm_bwd_narrow: rows of up to 256 elements by 8 to 32 lanes each. The gradient's column sums stay in
 // registers over all of a block's rows; k_norm_cols adds the blocks' sums.
 //
-// Measured (of the copy rate of 6786 GB/s): forward 8191 x 4096 with a float32 stream 71 us (83 %), 8192 x
-// 8192 95 us (83 %), 131072 x 128 22 us (89 %; a warp per row 50); gradient 8192 x 8192 171 us (70 %), where
+// Measured (of the copy rate of 6786 GB/s): forward 8191 x 4096 with a float32 stream 72 us (82 %), 8192 x
+// 8192 93 us (85 %), 131072 x 128 22 us (89 %; a warp per row 50); gradient 8192 x 8192 170 us (70 %), where
 // about half of a row's 3 us is arithmetic (9 unpackings and 9 packed operations an element) and two
 // barriers; 131072 x 128 43 us (70 %; rows of a warp through rings 121), 262144 x 64 42 us (234), 65536 x 256
 // 43 us (64); 2048 x 16384 168 us (35 %: 32 columns a thread spill). One token: 2.9 us, a launch and three
@@ -991,7 +991,7 @@ int norm_bwd_groups(int T, int num_sms) { return T < num_sms ? T : num_sms; }
 
 cudaError_t launch_norm(const NormArgs& a, int num_sms, cudaStream_t stream) {
   const int chunks = a.H / 8;
-  // Rings for wide rows, from four rows a group on (us, one row a block or rings: 8192 x 8192 119 or 95,
+  // Rings for wide rows, from four rows a group on (us, one row a block or rings: 8192 x 8192 119 or 93,
   // 2048 x 16384 67 or 48; 8192 x 2048 27 either way, and narrower rows alike)
   if (chunks > 256 && (int64_t)a.T >= (int64_t)(chunks <= 512 ? 16 : chunks <= 1024 ? 8 : 4) * num_sms) {
     bool ok = false;
