@@ -143,9 +143,10 @@ size_t ft_moe_decode_smem_bytes(int32_t T, int32_t k, int32_t E, int32_t H, int3
 
 /* Zero a workspace once after allocating it. Enqueued on `stream`.
  * Only the first FT_MOE_WORKSPACE_HEAD_BYTES bytes (the error word and the barrier and
- * completion counters) must be zero before a call, and every call leaves them at zero
- * again; the rest is scratch that a call writes before it reads it, so its contents
- * (stale results, NaN bit patterns) never reach an output. */
+ * completion counters) must be zero before the first call, and belong to the calls from then
+ * on: none writes over another kind's counters, so calls of every kind may share a workspace of
+ * one device. The rest is scratch that a call writes before it reads it, so its
+ * contents (stale results, NaN bit patterns) never reach an output. */
 #define FT_MOE_WORKSPACE_HEAD_BYTES 1024
 ft_status ft_moe_workspace_init(void* workspace, size_t workspace_bytes, void* stream);
 

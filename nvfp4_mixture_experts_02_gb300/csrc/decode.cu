@@ -1284,8 +1284,8 @@ DecodeLayout::DecodeLayout(int T, int k, int E, int H, int I, bool shared, int g
   max_pairs = T * k + (shared ? T : 0);
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, 256); return at; };
-  // the head (error word, barrier counter, completion counters) must be zero before a call;
-  // every call leaves it at zero again
+  // the head (error word, barrier counter, completion counters) is zeroed once: a call leaves the
+  // completion counters at zero and the barrier counter at a multiple of its grid, which is the device's
   err = take(16);
   bar = take(16);
   ready = take(4 * (kMaxTopK + 2));

@@ -269,6 +269,7 @@ F8Layout::F8Layout(int T, int k, int H, int I, bool shared) {
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, 256); return at; };
   err = take(16);
+  o = FT_MOE_WORKSPACE_HEAD_BYTES;   // the rest of the head is the decode calls' counters
   xf = take(2 * (size_t)T * H);
   xscale = take(4 * (size_t)T);
   gdot = take(4 * (size_t)T);

@@ -712,6 +712,7 @@ PrefillLayout::PrefillLayout(int T, int k, int E, int H, int I, bool shared) {
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, 256); return at; };
   err = take(16);
+  o = FT_MOE_WORKSPACE_HEAD_BYTES;   // the rest of the head is the decode calls' counters
   hdr = take(64);
   act_expert = take(4 * (size_t)(E + 2));
   act_pair0 = take(4 * (size_t)(E + 3));
