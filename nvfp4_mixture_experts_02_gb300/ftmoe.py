@@ -479,7 +479,8 @@ def _new_scratch(n, dev, head=True):
     off = (-ws.data_ptr()) % 256
     ws = ws[off:off + n]
     if head:
-        _check(_LIB.ft_moe_workspace_init(_ptr(ws), n, _stream(None, dev)), "ft_moe_workspace_init")
+        _check(_LIB.ft_moe_workspace_init(_ptr(ws), min(n, WORKSPACE_HEAD_BYTES), _stream(None, dev)),
+               "ft_moe_workspace_init")
     return ws
 
 
