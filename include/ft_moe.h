@@ -350,8 +350,8 @@ ft_status ft_nvfp4_linear(const uint16_t* x, int32_t T, int64_t x_stride,
  * p * page_stride + s * slot_stride + h * head_stride + d (strides in elements), so both
  * [page, slot, head, d] and [page, head, slot, d] orders are accepted. Base pointers 16-byte
  * aligned and strides multiples of 16 bytes. D is 64, 128 or 256; page_size >= 1.
- * E4M3 caches stand for code * k_scale and code * v_scale (positive, finite; bf16 caches too are
- * multiplied by their scales, 1 as a rule).
+ * An element stands for its stored value times k_scale or v_scale (positive, finite; 1 as a rule for
+ * bf16 caches).
  */
 typedef struct {
   void* k;
@@ -377,7 +377,7 @@ typedef struct {
  *   rope       float [rope_rows, rope_dim] (16-byte aligned): cos in the first half of a row, sin
  *              in the second; element i and i + rope_dim/2 of a head turn together, elements past
  *              rope_dim are left alone. rope_dim a multiple of 16, <= D; 0 (rope NULL): none
- *   E4M3 caches store e4m3(value * (1 / scale)) rounded to nearest, saturated at +-448.
+ *   What is stored is value * (1 / scale), rounded to nearest (E4M3: saturated at +-448).
  *   workspace  at least FT_MOE_WORKSPACE_HEAD_BYTES, its error word collects
  *              FT_ERR_DEVICE_FLAG, or NULL. A page, sequence or position outside its table stores
  *              nothing and flags. No two tokens of a call may share a slot.

@@ -3,7 +3,7 @@
 //   rotary   for i < R/2: (u_i, u_{i+R/2}) -> (u_i c_i - u_{i+R/2} s_i, u_{i+R/2} c_i + u_i s_i)
 //            with c, s = rope[position][i], rope[position][R/2 + i]; elements past R unchanged
 //   cache    page = block_table[seq][position / page_size], slot = position % page_size;
-//            bf16, or E4M3 of the value times 1 / scale, saturated at +-448
+//            bf16 or E4M3 of the value times 1 / scale (E4M3: saturated at +-448)
 //
 // A thread takes two 8-element pieces of one head: a pair of pieces R/2 apart, which rotate into each
 // other, or two neighbours past R. A block takes one token, or a few of few heads; the values are on
@@ -35,14 +35,14 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 
 template <bool F8>
 __device__ __forceinline__ void store_cache(void* base, int64_t at, float inv, const float (&f)[8]) {
-  if constexpr (F8) {
-    float g[8];
+  float g[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) g[j] = __fmul_rn(f[j], inv);
+  for (int j = 0; j < 8; ++j) g[j] = __fmul_rn(f[j], inv);
+  if constexpr (F8) {
     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + at) =
         make_uint2(e4m3x4(g[0], g[1], g[2], g[3]), e4m3x4(g[4], g[5], g[6], g[7]));
   } else {
-    store8(static_cast<uint16_t*>(base) + at, f);
+    store8(static_cast<uint16_t*>(base) + at, g);
   }
 }
 

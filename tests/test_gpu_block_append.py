@@ -48,3 +48,25 @@ def test_every_token_has_a_place(dtype, D, R, Hq, Hkv, page, order):
     ref = torch.from_numpy(rotate32(q, rope, np.maximum(pos, 0))).bfloat16()
     ref[torch.from_numpy(pos < 0)] = 0
     assert np.array_equal(bits(got), bits(ref))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, F8])
+def test_scales_of_the_cache_cancel(dtype):
+    """What is appended under a scale is read back under it: powers of two change nothing."""
+    m = ftmoe()
+    rng = np.random.default_rng(7)
+    n, D = 70, 64
+    k, v = (bf16(rng.standard_normal((n, 2, D))).cuda() for _ in range(2))
+    q = bf16(rng.standard_normal((1, 4, D))).cuda()
+    table = torch.randperm(8).to(torch.int32)[None].cuda()
+    pos, seq = torch.arange(n, dtype=torch.int32, device="cuda"), torch.zeros(n, dtype=torch.int32, device="cuda")
+    outs = []
+    for scales in ((1.0, 1.0), (0.25, 4.0)):
+        cache = m.PagedKVCache(*(torch.zeros((8, 16, 2, D), dtype=torch.uint8).to(dtype).cuda() for _ in range(2)), *scales)
+        m.kv_append(k, v, cache, table, pos, seq_ids=seq)
+        outs.append(m.paged_decode_attention(q, cache, table, torch.tensor([n], dtype=torch.int32, device="cuda")))
+    if dtype == torch.bfloat16:
+        assert torch.equal(outs[0][0], outs[1][0])
+        assert (outs[0][1] - outs[1][1]).abs().max() <= 1e-5
+    else:   # E4M3 rounds subnormals otherwise
+        assert (outs[0][0].float() - outs[1][0].float()).abs().max() <= 0.02
