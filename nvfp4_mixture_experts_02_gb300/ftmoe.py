@@ -712,6 +712,7 @@ def fp8block_decode(x, topk_idx, topk_w, experts: Fp8BlockExperts, shared=None, 
 # what the kernels require beyond them (multiples, ranges) is refused by the library with its
 # status, what they would read out of bounds is refused here.
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_ELEMENT = range(4)
+_MAX_I32 = 2 ** 31 - 1   # sizes are 32-bit in the C ABI, and ctypes drops the bits above
 _RES = (torch.bfloat16, torch.float32)
 
 
@@ -751,6 +752,8 @@ class NvFP4Linear:
         N, K = self.codes.shape[0], self.codes.shape[1] * 2
         if K % 32 != 0 or K == 0 or N == 0:
             raise ValueError("NvFP4Linear: K is a multiple of 32, and N is not 0")
+        if N > _MAX_I32 or K > _MAX_I32:
+            raise ValueError(f"NvFP4Linear: [{N}, {K}] is too large")
         _need(self.codes, "codes", dev, None, (N, K // 2))
         _need(self.scales, "scales", dev, None, (N, K // 16))
         _need_scalar(self.gscale, "gscale", dev)
@@ -819,6 +822,8 @@ class PagedKVCache:
             raise TypeError("PagedKVCache: k and v are both bfloat16 or both float8_e4m3fn")
         if self.k.stride(3) != 1 or self.v.stride(3) != 1:
             raise ValueError("PagedKVCache: the elements of a head must be contiguous")
+        if max(self.k.shape) > _MAX_I32:
+            raise ValueError(f"PagedKVCache: {tuple(self.k.shape)} is too large")
         f8 = self.k.dtype == torch.float8_e4m3fn
         object.__setattr__(self, "device_index", dev)
         object.__setattr__(self, "heads", tuple(self.k.shape[2:]))   # (Hkv, D)
@@ -860,6 +865,8 @@ def kv_append(k, v, cache: PagedKVCache, block_table, positions, seq_ids=None, q
     _need(block_table, "block_table", dev, _I32, None)
     _need(positions, "positions", dev, _I32, (T,))
     B, width = block_table.shape
+    if T > _MAX_I32 or B > _MAX_I32 or width > _MAX_I32:
+        raise ValueError(f"{T} tokens, block_table [{B}, {width}]: too large")
     if seq_ids is not None:
         _need(seq_ids, "seq_ids", dev, _I32, (T,))
     elif T > B:
@@ -881,6 +888,8 @@ def kv_append(k, v, cache: PagedKVCache, block_table, positions, seq_ids=None, q
             raise ValueError("rope: [rows, R] expected")
         _need(rope, "rope", dev, _F32, None)
         rows, dim = rope.shape
+        if rows > _MAX_I32:
+            raise ValueError(f"rope: {rows} rows are too many")
         rp = rope.data_ptr()
     if workspace is not None:
         _need(workspace, "workspace", dev, None, None)
@@ -928,6 +937,8 @@ def paged_decode_attention(q, cache: PagedKVCache, block_table, seq_lens, scale=
     rows, width = block_table.shape
     if rows != B:
         raise ValueError(f"block_table: {rows} rows for {B} sequences")
+    if B > _MAX_I32 or width > _MAX_I32 or window > _MAX_I32:
+        raise ValueError(f"{B} sequences, {width} pages each, window {window}: out of range")
     _need(seq_lens, "seq_lens", dev, _I32, (B,))
     if out is None:
         out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=q.device)
@@ -957,6 +968,8 @@ def _norm_inputs(y, residual, w_post, w_pre, gate):
     if y.dim() != 2:
         raise ValueError("y: [T, H] expected")
     T, H = both = y.shape
+    if T > _MAX_I32:
+        raise ValueError(f"y: {T} rows are too many")
     _need(y, "y", dev, BF16_BITS, None)
     res = torch.bfloat16
     if residual is not None:
