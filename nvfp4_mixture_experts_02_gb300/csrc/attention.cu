@@ -26,8 +26,8 @@
 // exactly, q is f16 after a scaling of its row by a power of two (exact but for elements under 2^-29
 // of the row's largest), p, in (0, 2^15], is split into two f16 (22 bits down to 2^-18 of the largest key's
 // weight, see kLift). One f16 for p moves outputs over their bf16 rounding: 48 ragged sequences are 8.1e-4 off the
-// rounded exact result with one, 0.8e-4 with two (bf16 caches 0.6e-4), at 0 to 1 % of the time, 5 % with 16 heads
-// a key head (16 x 8192, 41.1 and 43.2 us).
+// rounded exact result with one, 0.8e-4 with two (bf16 caches 0.6e-4), at 0 to 1 % of the time, 4 to 5 % with heads
+// of 64 (200 ragged sequences up to 700, 26.3 and 27.5 us) or 16 heads a key head (16 x 8192, 40.9 and 43.2 us).
 // Statistics and sums are float32.
 //
 // Measured (of the copy rate of 6786 GB/s): three sequences up to 131072, bf16, 962 MB: 155 us (91 %).
