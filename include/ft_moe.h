@@ -390,6 +390,84 @@ ft_status ft_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, i
                        const float* rope, int32_t rope_rows, int32_t rope_dim, void* workspace,
                        void* stream);
 
+/*
+ * Rotary positions with several axes (time, height and width of images and video; 1 to 4 of them):
+ * pair i of a head, elements i and i + rope_dim / 2, turns by row positions[axis[i]][token] of the
+ * table. A host struct that a call copies; only `positions` is device memory.
+ *   positions  int32 [axes, T], axis a at positions + a * stride (4-byte aligned). A position outside
+ *              the table flags, and its token is treated like one whose place is outside; those of
+ *              padding tokens are not looked at
+ *   axis       the axis of each of the rope_dim / 2 pairs, below `axes`
+ */
+typedef struct {
+  const int32_t* positions;
+  int64_t stride;
+  int32_t axes;
+  uint8_t axis[128];
+} ft_rope_axes;
+
+/* ft_kv_append_axes — ft_kv_append with several rotary axes (axes NULL: one, the token's place; `positions`
+ * stays the place in the cache, and is not held against rope_rows when axes are given). */
+ft_status ft_kv_append_axes(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                            const uint16_t* q, int64_t q_stride, uint16_t* q_out, int32_t T,
+                            int32_t Hq, const ft_paged_kv* cache, const int32_t* block_table,
+                            int32_t B, int32_t table_width, const int32_t* seq_ids,
+                            const int32_t* positions, const float* rope, int32_t rope_rows,
+                            int32_t rope_dim, const ft_rope_axes* axes, void* workspace, void* stream);
+
+/*
+ * A paged key-value cache in NVFP4, the layout of the weights along each head: two E2M1 codes a byte, the
+ * even element in the low nibble, an E4M3 scale per 16 elements, and a float scale for all keys and one
+ * for all values. Element d of a head stands for e2m1(code d) * e4m3(scale d / 16) * gscale. Strides are
+ * in bytes, of the codes [.., D/2] and of the scales [.., D/16]; both orders of slots and heads are
+ * accepted. Codes and their strides are multiples of 16 bytes, scales and theirs of D / 16 bytes. D is 64,
+ * 128 or 256; 2^-100 <= gscale <= 2^100.
+ */
+typedef struct {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+  int32_t num_pages, page_size, Hkv, D;
+  int64_t k_page_stride, k_slot_stride, k_head_stride;
+  int64_t v_page_stride, v_slot_stride, v_head_stride;
+  int64_t ks_page_stride, ks_slot_stride, ks_head_stride;
+  int64_t vs_page_stride, vs_slot_stride, vs_head_stride;
+  float k_gscale, v_gscale;
+} ft_nvfp4_kv;
+
+/*
+ * ft_nvfp4_kv_append — ft_kv_append into an NVFP4 cache (axes as for ft_kv_append_axes, or NULL): one
+ * launch. A block of 16 elements x is stored as
+ *   s = e4m3(max|x| * (1 / (6 gscale))),  code = e2m1(x * (1 / (s * gscale)))   (zeros where s is 0)
+ * in float32, each step rounded to nearest (ties to even), both saturated: +-infinity is stored as the
+ * largest magnitude. A NaN in a block makes its scale NaN, so that all of the block reads as NaN.
+ *   rope_dim a multiple of 32 here; other arguments, limits, flags and errors as for ft_kv_append.
+ */
+ft_status ft_nvfp4_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                             const uint16_t* q, int64_t q_stride, uint16_t* q_out, int32_t T,
+                             int32_t Hq, const ft_nvfp4_kv* cache, const int32_t* block_table,
+                             int32_t B, int32_t table_width, const int32_t* seq_ids,
+                             const int32_t* positions, const float* rope, int32_t rope_rows,
+                             int32_t rope_dim, const ft_rope_axes* axes, void* workspace, void* stream);
+
+/*
+ * ft_kv_gather, ft_nvfp4_kv_gather — cached tokens read back as dense bf16 (for the attention of a prompt
+ * over what is cached, or to move a prefix): one launch.
+ *   positions, seq_ids, block_table, workspace  as for ft_kv_append: token t of the result is place
+ *              positions[t] of sequence seq_ids[t] (NULL: t). Tokens may repeat, in any order.
+ *   k_out, v_out  bf16 [T, Hkv, D] contiguous, 32-byte aligned, fully overwritten: the value that an
+ *              element stands for, rounded to nearest. A negative position (padding) gives zeros; so does
+ *              a page, sequence or position outside its table, which flags.
+ *   T <= 2^26.
+ */
+ft_status ft_kv_gather(const ft_paged_kv* cache, const int32_t* block_table, int32_t B,
+                       int32_t table_width, const int32_t* seq_ids, const int32_t* positions, int32_t T,
+                       uint16_t* k_out, uint16_t* v_out, void* workspace, void* stream);
+ft_status ft_nvfp4_kv_gather(const ft_nvfp4_kv* cache, const int32_t* block_table, int32_t B,
+                             int32_t table_width, const int32_t* seq_ids, const int32_t* positions,
+                             int32_t T, uint16_t* k_out, uint16_t* v_out, void* workspace, void* stream);
+
 /* Workspace bytes of ft_paged_decode_attention for B sequences and heads of D elements on the
  * current device (0 for invalid sizes or without a device): two partial results for every warp that
  * the device holds, 20 to 40 MB, of which a call touches what it splits. */
@@ -423,6 +501,17 @@ ft_status ft_paged_decode_attention(const uint16_t* q, int64_t q_stride, int32_t
                                     int32_t table_width, const int32_t* seq_lens, float scale,
                                     int32_t window, uint16_t* out, float* lse, void* workspace,
                                     size_t workspace_bytes, void* stream);
+
+/*
+ * ft_nvfp4_paged_decode_attention — ft_paged_decode_attention over an NVFP4 cache: the same arguments,
+ * workspace, flags and errors. Keys and values enter their products exactly (e2m1 * e4m3 is an f16); a
+ * weight is rounded as with an E4M3 cache. A NaN block scale gives NaN.
+ */
+ft_status ft_nvfp4_paged_decode_attention(const uint16_t* q, int64_t q_stride, int32_t B, int32_t Hq,
+                                          const ft_nvfp4_kv* cache, const int32_t* block_table,
+                                          int32_t table_width, const int32_t* seq_lens, float scale,
+                                          int32_t window, uint16_t* out, float* lse, void* workspace,
+                                          size_t workspace_bytes, void* stream);
 
 /* What a gate of ft_residual_norm multiplies: nothing (no gate), bf16 [H], [T] or [T, H]. */
 #define FT_GATE_NONE 0

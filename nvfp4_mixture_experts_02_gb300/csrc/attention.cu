@@ -45,17 +45,19 @@ namespace ftmoe {
 
 namespace {
 
-template <int D, bool F8, int NG>
+// DT: the cache's type (FT_KV_BF16, FT_KV_E4M3, kKvNvfp4).
+template <int D, int DT, int NG>
 struct AttnShape {
-  static constexpr int kRow = D * (F8 ? 1 : 2);       // bytes of a key or value
+  static constexpr int kRow = DT == kKvNvfp4 ? D / 2 : DT == FT_KV_E4M3 ? D : 2 * D;   // bytes of a key or value
   static constexpr int kCpr = kRow / 16;              // 16-byte pieces of it
+  static constexpr int kScaleRow = DT == kKvNvfp4 ? D / 16 : 0;   // bytes of its block scales
   static constexpr int kKeys = kRow <= 128 ? 32 : 16; // keys of a warp's step
-  static constexpr int kStageBytes = 2 * kKeys * kRow;   // those keys and values
+  static constexpr int kStageBytes = 2 * kKeys * (kRow + kScaleRow);   // those keys and values
   // blocks an SM: the others stream while one joins a piece's warps. Three of two stages each, not two of
   // three, where the registers allow it: 256 sequences up to 1024 with 8-bit keys of 128: 68 us for 79.
   // (Past some 2600 sequences their running sums in shared memory leave room for two.)
-  static constexpr int kBlocks = kRow >= 512 ? 1 : kRow == 128 && NG == 1 ? kAttendBlocks : 2;
-  static constexpr int kWarps = kRow >= 128 ? 4 : 8;
+  static constexpr int kBlocks = kRow >= 512 ? 1 : (DT == kKvNvfp4 ? D == 128 : kRow == 128) && NG == 1 ? kAttendBlocks : 2;
+  static constexpr int kWarps = (DT == kKvNvfp4 ? D >= 128 : kRow >= 128) ? 4 : 8;
   static constexpr int kStages = 192 * 1024 / (kBlocks * kWarps * kStageBytes);
   static constexpr int kUnit = kKeys * kWarps;        // keys of a unit
   static constexpr int kRing = kWarps * kStages * kStageBytes;
@@ -75,9 +77,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // weights of up to 2^15 the two parts of a key's weight hold 22 bits of it, or all but 2^-40 of the largest
 // key's weight. The sums carry the same factor, which their quotient does not see.
 constexpr float kLift = 15.f;
-template <bool F8>
+template <bool F16>
 __device__ __forceinline__ float lse_of(float m, float l) {   // ln of l 2^m
-  return F8 ? (m + kLift + log2f(l * (1.f / 32768.f))) * kLn2 : (m + log2f(l)) * kLn2;
+  return F16 ? (m + kLift + log2f(l * (1.f / 32768.f))) * kLn2 : (m + log2f(l)) * kLn2;
 }
 
 // Offset of 16-byte piece c of row r in a tile of rows of kCpr pieces: pieces are exchanged within
@@ -99,6 +101,83 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t v, uint32_t& lo, uint32_t
   asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
       "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
       : "=r"(lo), "=r"(hi) : "r"(v));
+}
+
+// NVFP4 rows. Lane (r, c) = (lane / 4, lane % 4) of a 16-key tile takes D/4 consecutive elements of keys r and
+// r + 8 as the row operand of k q^T, and D/8 consecutive elements, from r D/8 on, of keys 2c, 2c + 1, 2c + 8 and
+// 2c + 9 as that of v^T p^T: whole words of codes under one scale or two. Which key is row i of a tile, and where
+// its 16-byte pieces lie, is chosen so that both reads find 32 banks.
+template <int D>
+__device__ __forceinline__ int key_of_row(int i) {   // 0 <= i < 8; 8 + i follows
+  return D == 64 ? i ^ (i >> 2) : D == 128 ? i ^ ((i >> 1) & 1) : i;
+}
+template <int D>
+__device__ __forceinline__ uint32_t piece4(int row, int ch) {   // offset of 16-byte piece ch of a row
+  return (uint32_t)(row * (D / 2) + (D == 64 ? ch : D == 128 ? ch ^ (2 * ((row >> 2) & 1)) : ch ^ (row & 7)) * 16);
+}
+
+// N bytes (4, 8 or 16) from global to shared memory; zeros (and no access) when !valid.
+template <int N>
+__device__ __forceinline__ void cp_async_scales(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(valid ? N : 0)
+               : "memory");
+}
+// W words from shared memory.
+template <int W>
+__device__ __forceinline__ void lds(uint32_t (&v)[W], uint32_t addr) {
+  static_assert(W == 1 || W == 2 || W % 4 == 0);
+  if constexpr (W == 1) {
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[0]) : "r"(addr) : "memory");
+  } else if constexpr (W == 2) {
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(addr) : "memory");
+  } else {
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(addr)
+                 : "memory");
+  }
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .u16 t;\n\tld.shared.u16 t, [%1];\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+// The scales of lane c's elements of a key, each in both halves of a word.
+template <int D>
+__device__ __forceinline__ void key_scales(uint32_t (&s)[D / 64], uint32_t row, int c) {
+  if constexpr (D == 64) {
+    s[0] = splat_lo(e4m3x2_to_f16x2(lds_u8(row + c)));
+  } else if constexpr (D == 128) {
+    const uint32_t v = e4m3x2_to_f16x2(lds_u16(row + 2 * c));
+    s[0] = splat_lo(v);
+    s[1] = splat_hi(v);
+  } else {
+    uint32_t w[1], lo, hi;
+    lds(w, row + 4 * c);
+    e4m3x4_to_f16(w[0], lo, hi);
+    s[0] = splat_lo(lo);
+    s[1] = splat_hi(lo);
+    s[2] = splat_lo(hi);
+    s[3] = splat_hi(hi);
+  }
+}
+// The scales of lane r's elements of two values, the first one's in the lower half of a word.
+template <int D>
+__device__ __forceinline__ void value_scales(uint32_t (&s)[D == 256 ? 2 : 1], uint32_t row0, uint32_t row1, int r) {
+  if constexpr (D == 256) {
+    const uint32_t a = lds_u16(row0 + 2 * r), b = lds_u16(row1 + 2 * r);
+    s[0] = e4m3x2_to_f16x2(__byte_perm(a, b, 0x0040));
+    s[1] = e4m3x2_to_f16x2(__byte_perm(a, b, 0x0051));
+  } else {
+    const int at = D == 64 ? r >> 1 : r;
+    const uint32_t a = lds_u8(row0 + at), b = lds_u8(row1 + at);
+    s[0] = e4m3x2_to_f16x2(a | b << 8);
+  }
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -126,10 +205,11 @@ __device__ __forceinline__ void span(int len, int window, int unit, int& first, 
   units = len > 0 ? (len + unit - 1) / unit - first / unit : 0;
 }
 
-template <int D, bool F8, int NG>
-__global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D, F8, NG>::kBlocks)
+template <int D, int DT, int NG>
+__global__ void __launch_bounds__(AttnShape<D, DT, NG>::kWarps * 32, AttnShape<D, DT, NG>::kBlocks)
     k_attend(const AttendArgs a) {
-  using S = AttnShape<D, F8, NG>;
+  using S = AttnShape<D, DT, NG>;
+  constexpr bool F4 = DT == kKvNvfp4, F16 = DT != FT_KV_BF16;   // f16 products
   constexpr int W = S::kWarps, ST = S::kStages, CPR = S::kCpr, KS = D / 16, MT = D / 16;
   constexpr int KT = S::kKeys, NH = KT / 16;   // keys of a step, in 16-row tiles
   constexpr int LD = S::kSumsLd;
@@ -263,15 +343,23 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
         int64_t ko = -1, vo = -1;
         if (page >= 0 && page < a.kv.num_pages) {
           ko = ((int64_t)page * a.kv.k_page_stride + (int64_t)slot * a.kv.k_slot_stride +
-                (int64_t)kvh * a.kv.k_head_stride) * (F8 ? 1 : 2);
+                (int64_t)kvh * a.kv.k_head_stride) * (F16 ? 1 : 2);
           if (!a.same_strides)
             vo = ((int64_t)page * a.kv.v_page_stride + (int64_t)slot * a.kv.v_slot_stride +
-                  (int64_t)kvh * a.kv.v_head_stride) * (F8 ? 1 : 2);
+                  (int64_t)kvh * a.kv.v_head_stride) * (F16 ? 1 : 2);
         } else if (lane < KT) {
           const int j = key0 + i * unit + lane;
           if (j >= first && j < key1) atomicOr(a.err, kErrBadPage);   // no such page: read as zeros
         }
         const uint32_t st = ring + (uint32_t)((i % ST) * S::kStageBytes);
+        if constexpr (F4) {   // each lane's key brings its scales
+          const bool on = ko >= 0;
+          const int64_t p = on ? page : 0, sl = on ? slot : 0;
+          cp_async_scales<S::kScaleRow>(st + 2 * KT * S::kRow + lane * S::kScaleRow,
+                                        a.sc.k + p * a.sc.k_page + sl * a.sc.k_slot + kvh * a.sc.k_head, on);
+          cp_async_scales<S::kScaleRow>(st + KT * (2 * S::kRow + S::kScaleRow) + lane * S::kScaleRow,
+                                        a.sc.v + p * a.sc.v_page + sl * a.sc.v_slot + kvh * a.sc.v_head, on);
+        }
         constexpr int RPI = 32 / CPR;   // rows of one warp-wide copy
 #pragma unroll
         for (int p = 0; p < KT / RPI; ++p) {
@@ -279,10 +367,9 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
           const int64_t k_at = __shfl_sync(0xffffffffu, ko, row);
           const int64_t v_at = a.same_strides ? k_at : __shfl_sync(0xffffffffu, vo, row);
           const bool on = k_at >= 0;
-          cp_async16(st + swz<CPR>(row, ch),
-                     static_cast<const char*>(a.kv.k) + (on ? k_at + ch * 16 : 0), on);
-          cp_async16(st + KT * S::kRow + swz<CPR>(row, ch),
-                     static_cast<const char*>(a.kv.v) + (on ? v_at + ch * 16 : 0), on);
+          const uint32_t to = st + (F4 ? piece4<D>(row, ch) : swz<CPR>(row, ch));
+          cp_async16(to, static_cast<const char*>(a.kv.k) + (on ? k_at + ch * 16 : 0), on);
+          cp_async16(to + KT * S::kRow, static_cast<const char*>(a.kv.v) + (on ? v_at + ch * 16 : 0), on);
         }
       }
       cp_async_commit();
@@ -304,7 +391,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
         const bool on = 8 * g + r < G;
         const uint16_t* qh = qb + (8 * g + r) * D;
         sl[g][0] = sl[g][1] = a.scale * a.kv.k_scale * kLog2e;
-        if constexpr (!F8) {
+        if constexpr (!F16) {
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
             q[g][ks][0] = on ? *reinterpret_cast<const uint32_t*>(qh + 16 * ks + 2 * c) : 0u;
@@ -313,9 +400,9 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
         } else {
           float top = 0.f;
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {   // E4M3 keys come four elements to a lane
+          for (int ks = 0; ks < KS; ++ks) {   // E4M3 keys come four elements to a lane, NVFP4 ones D/4
             uint2 v = make_uint2(0, 0);
-            if (on) v = *reinterpret_cast<const uint2*>(qh + 16 * ks + 4 * c);
+            if (on) v = *reinterpret_cast<const uint2*>(qh + (F4 ? D / 4 * c + 4 * ks : 16 * ks + 4 * c));
             q[g][ks][0] = v.x;
             q[g][ks][1] = v.y;
             top = fmaxf(top, finite_top(v.x, v.y));
@@ -358,7 +445,50 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
       for (int g = 0; g < NG; ++g)
 #pragma unroll
         for (int h = 0; h < NH; ++h) s[g][h][0] = s[g][h][1] = s[g][h][2] = s[g][h][3] = 0.f;
-      if constexpr (!F8) {
+      if constexpr (F4) {
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          constexpr int NW = D / 32;   // words of a lane's elements of a key
+          const int row = 16 * h + key_of_row<D>(r);
+          uint32_t k0[NW], k1[NW], s0[D / 64], s1[D / 64];
+          const uint32_t sc = st + 2 * KT * S::kRow + row * S::kScaleRow;
+          if constexpr (D == 64) {
+            lds(k0, st + piece4<D>(row, c >> 1) + (c & 1) * 8);
+            lds(k1, st + piece4<D>(row + 8, c >> 1) + (c & 1) * 8);
+          } else {
+#pragma unroll
+            for (int x = 0; x < NW / 4; ++x) {
+              uint32_t t0[4], t1[4];
+              lds(t0, st + piece4<D>(row, NW / 4 * c + x));
+              lds(t1, st + piece4<D>(row + 8, NW / 4 * c + x));
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                k0[4 * x + y] = t0[y];
+                k1[4 * x + y] = t1[y];
+              }
+            }
+          }
+          key_scales<D>(s0, sc, c);
+          key_scales<D>(s1, sc + 8 * S::kScaleRow, c);
+#pragma unroll
+          for (int j = 0; j < NW; ++j) {
+            uint32_t x[4], y[4];
+            e2m1x8_to_f16x2x4(k0[j], x[0], x[1], x[2], x[3]);
+            e2m1x8_to_f16x2x4(k1[j], y[0], y[1], y[2], y[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {   // exact: six significant bits
+              x[e] = hmul2(x[e], s0[j / 2]);
+              y[e] = hmul2(y[e], s1[j / 2]);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int g = 0; g < NG; ++g)
+                mma_f16(s[g][h], x[2 * e], y[2 * e], x[2 * e + 1], y[2 * e + 1], q[g][2 * j + e][0],
+                        q[g][2 * j + e][1]);
+          }
+        }
+      } else if constexpr (!F16) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
@@ -403,7 +533,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
           for (int h = 0; h < NH; ++h)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int j = j0 + 16 * h + r + (e >> 1) * 8;
+              const int j = j0 + 16 * h + (F4 ? key_of_row<D>(r) : r) + (e >> 1) * 8;
               if (j < first || j >= key1) s[g][h][e] = -INFINITY;
             }
         }
@@ -414,7 +544,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
           for (int h = 1; h < NH; ++h) t = fmaxf(t, fmaxf(s[g][h][e], s[g][h][2 + e]));
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
-          if constexpr (F8) t = __fsub_ru(t, kLift);   // upwards: no weight above 2^15 at any size of t
+          if constexpr (F16) t = __fsub_ru(t, kLift);   // upwards: no weight above 2^15 at any size of t
           top[g][e] = t;
           up |= t > m[g][e];
         }
@@ -455,7 +585,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const float p0 = s[g][h][2 * x], p1 = s[g][h][2 * x + 1];
-            if constexpr (F8) {
+            if constexpr (F16) {
               const uint32_t v = pack_f16(p0, p1);
               p[g][h][x] = transpose8(v);
               rest[g][h][x] = transpose8(pack_f16(p0 - f16_lo(v), p1 - f16_hi(v)));
@@ -468,7 +598,42 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
       }
       // o^T += v^T p^T: 16 dims at a time
       const uint32_t vs = st + KT * S::kRow;
-      if constexpr (!F8) {
+      if constexpr (F4) {
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          constexpr int NW = D / 64;   // words of a lane's elements of a value
+          constexpr int NS = D == 256 ? 2 : 1;
+          uint32_t v[4][NW], s01[NS], s89[NS];   // keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9
+          const uint32_t sc = st + KT * (2 * S::kRow + S::kScaleRow);
+          const int row0 = 16 * h + key_of_row<D>(2 * c), row1 = 16 * h + key_of_row<D>(2 * c + 1);
+          const int rows[4] = {row0, row1, row0 + 8, row1 + 8};
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            lds(v[x], vs + piece4<D>(rows[x], D * r / 256) + (D * r / 16 & 15));
+          value_scales<D>(s01, sc + row0 * S::kScaleRow, sc + row1 * S::kScaleRow, r);
+          value_scales<D>(s89, sc + (row0 + 8) * S::kScaleRow, sc + (row1 + 8) * S::kScaleRow, r);
+#pragma unroll
+          for (int j = 0; j < NW; ++j) {
+            // elements 2 i (a0, a2) and 2 i + 1 (a1, a3) of two keys in byte i of a word
+            uint32_t a0[4], a1[4], a2[4], a3[4];
+            const uint32_t lo = 0x0F0F0F0Fu;
+            e2m1x8_to_f16x2x4((v[0][j] & lo) | (v[1][j] << 4 & ~lo), a0[0], a0[1], a0[2], a0[3]);
+            e2m1x8_to_f16x2x4((v[0][j] >> 4 & lo) | (v[1][j] & ~lo), a1[0], a1[1], a1[2], a1[3]);
+            e2m1x8_to_f16x2x4((v[2][j] & lo) | (v[3][j] << 4 & ~lo), a2[0], a2[1], a2[2], a2[3]);
+            e2m1x8_to_f16x2x4((v[2][j] >> 4 & lo) | (v[3][j] & ~lo), a3[0], a3[1], a3[2], a3[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t b0 = hmul2(a0[e], s01[j / 2]), b1 = hmul2(a1[e], s01[j / 2]);
+              const uint32_t b2 = hmul2(a2[e], s89[j / 2]), b3 = hmul2(a3[e], s89[j / 2]);
+#pragma unroll
+              for (int g = 0; g < NG; ++g) {
+                mma_f16(o[g][4 * j + e], b0, b1, b2, b3, p[g][h][0], p[g][h][1]);
+                mma_f16(o[g][4 * j + e], b0, b1, b2, b3, rest[g][h][0], rest[g][h][1]);
+              }
+            }
+          }
+        }
+      } else if constexpr (!F16) {
         const int vrow = half * 8 + (lane & 7), vch = (lane >> 3) & 1;
 #pragma unroll
         for (int t = 0; t < MT; ++t)
@@ -524,7 +689,8 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
         if (h < G) {
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
-            const int d0 = F8 ? 16 * t + 2 * r : 16 * t + r, d1 = F8 ? d0 + 1 : d0 + 8;
+            const int d0 = F4 ? D / 8 * r + 2 * t : F16 ? 16 * t + 2 * r : 16 * t + r;
+            const int d1 = F16 ? d0 + 1 : d0 + 8;
             sums[h * LD + d0] = o[g][t][e];
             sums[h * LD + d1] = o[g][t][2 + e];
           }
@@ -551,7 +717,7 @@ __global__ void __launch_bounds__(AttnShape<D, F8, NG>::kWarps * 32, AttnShape<D
     const int64_t row = (int64_t)b * a.Hq + kvh * a.group + g0;
     if (lane < G && stripe == 0) {
       if (!whole) *reinterpret_cast<float2*>(a.part_ml + (part + lane) * 2) = ms;
-      else if (a.lse) a.lse[row + lane] = lse_of<F8>(ms.x, ms.y);
+      else if (a.lse) a.lse[row + lane] = lse_of<F16>(ms.x, ms.y);
     }
     for (int x = stripe * 32; x < G * (D / 4); x += stripes * 32) {   // four dims of a head a lane
       const int g = (x + lane) / (D / 4), d = (x + lane) % (D / 4) * 4;
@@ -683,20 +849,20 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_join(const AttendArgs a) {
         a.out[row * D + lane + 32 * e] =
             (uint16_t)(pack_bf16(l == 0.f ? 0.f : v[e] / l * a.kv.v_scale, 0.f) & 0xFFFFu);
       if (lane == 0 && a.lse)
-        a.lse[row] = a.kv.dtype == FT_KV_E4M3 ? lse_of<true>(m, l) : lse_of<false>(m, l);
+        a.lse[row] = a.kv.dtype != FT_KV_BF16 ? lse_of<true>(m, l) : lse_of<false>(m, l);
     }
   }
 }
 
-template <int D, bool F8, int NG>
+template <int D, int DT, int NG>
 cudaError_t launch_d(AttendArgs a, int num_sms, cudaStream_t stream) {
-  using S = AttnShape<D, F8, NG>;
+  using S = AttnShape<D, DT, NG>;
   a.heads_log2 = 0;
   while (2 << a.heads_log2 <= S::kWarps && a.kv.Hkv * a.gt % (2 << a.heads_log2) == 0) ++a.heads_log2;
   const size_t smem = S::kRing + (a.B > 32 ? (size_t)(a.B + 1) * 4 : 0);
   cudaError_t e;
   static SmemGrant grant;   // for the most sequences that a call may have
-  if ((e = grant_smem(grant, k_attend<D, F8, NG>, S::kRing + 4 * (kMaxSeqs + 1))) != cudaSuccess) return e;
+  if ((e = grant_smem(grant, k_attend<D, DT, NG>, S::kRing + 4 * (kMaxSeqs + 1))) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   const int grid = S::kBlocks * num_sms;
   cfg.gridDim = dim3((unsigned)grid);
@@ -708,18 +874,25 @@ cudaError_t launch_d(AttendArgs a, int num_sms, cudaStream_t stream) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, k_attend<D, F8, NG>, a)) != cudaSuccess) return e;
+  if ((e = cudaLaunchKernelEx(&cfg, k_attend<D, DT, NG>, a)) != cudaSuccess) return e;
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, k_join<D, S::kWarps>, a);
 }
 
-template <int D>
+template <int D, int DT>
 cudaError_t launch_g(const AttendArgs& a, int num_sms, cudaStream_t stream) {
-  const bool f8 = a.kv.dtype == FT_KV_E4M3;
-  if (a.group <= 8)
-    return f8 ? launch_d<D, true, 1>(a, num_sms, stream) : launch_d<D, false, 1>(a, num_sms, stream);
-  return f8 ? launch_d<D, true, 2>(a, num_sms, stream) : launch_d<D, false, 2>(a, num_sms, stream);
+  return a.group <= 8 ? launch_d<D, DT, 1>(a, num_sms, stream) : launch_d<D, DT, 2>(a, num_sms, stream);
+}
+
+template <int DT>
+cudaError_t launch_t(const AttendArgs& a, int num_sms, cudaStream_t stream) {
+  switch (a.kv.D) {
+    case 64: return launch_g<64, DT>(a, num_sms, stream);
+    case 128: return launch_g<128, DT>(a, num_sms, stream);
+    case 256: return launch_g<256, DT>(a, num_sms, stream);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -733,12 +906,11 @@ cudaError_t launch_attend(const AttendArgs& args, int num_sms, cudaStream_t stre
   page_division(a.kv.page_size, a.div_mul, a.div_shift);
   const int64_t slots = (int64_t)a.table_width * a.kv.page_size;
   a.max_len = (int)(slots < (1 << 30) ? slots : 1 << 30);
-  switch (a.kv.D) {
-    case 64: return launch_g<64>(a, num_sms, stream);
-    case 128: return launch_g<128>(a, num_sms, stream);
-    case 256: return launch_g<256>(a, num_sms, stream);
+  switch (a.kv.dtype) {
+    case FT_KV_BF16: return launch_t<FT_KV_BF16>(a, num_sms, stream);
+    case FT_KV_E4M3: return launch_t<FT_KV_E4M3>(a, num_sms, stream);
   }
-  return cudaErrorInvalidValue;
+  return launch_t<kKvNvfp4>(a, num_sms, stream);
 }
 
 }  // namespace ftmoe

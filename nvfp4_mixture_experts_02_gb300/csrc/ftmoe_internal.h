@@ -135,6 +135,14 @@ inline void page_division(int d, int& mul, int& shift) {
   mul = (int)(uint32_t)(((1ull << 32) * ((1ull << shift) - (uint64_t)d)) / (uint64_t)d + 1);
 }
 
+// An NVFP4 cache inside the library: ft_paged_kv with strides and offsets of the codes in bytes, gscale for
+// scale and this dtype, and its block scales.
+constexpr int kKvNvfp4 = 2;
+struct KvScales {
+  uint8_t *k, *v;
+  int64_t k_page, k_slot, k_head, v_page, v_slot, v_head;   // strides in bytes
+};
+
 // Rotary embedding and cache append (kv.cu). err: error word or null.
 struct AppendArgs {
   const uint16_t *k, *v, *q;
@@ -149,8 +157,25 @@ struct AppendArgs {
   int rope_rows, rope_dim;
   int* err;
   int div_mul, div_shift;   // division by the page size (set by the launch)
+  KvScales sc;              // NVFP4: inv_k, inv_v are 1 / (6 gscale)
+  const int* axis_pos;      // several rotary axes: positions [axes], axis_stride apart, or null
+  int64_t axis_stride;
+  int axes;
+  uint32_t axis_of[8];      // the axis of each pair, two bits each
 };
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
+
+// Cached tokens as dense bf16 (kv.cu).
+struct GatherArgs {
+  ft_paged_kv kv;
+  KvScales sc;
+  const int *block_table, *seq_ids, *positions;
+  int B, table_width, T;
+  uint16_t *k_out, *v_out;
+  int* err;
+  int div_mul, div_shift;   // division by the page size (set by the launch)
+};
+cudaError_t launch_kv_gather(const GatherArgs& a, cudaStream_t stream);
 
 // Paged attention of one new token per sequence (attention.cu).
 struct AttendArgs {
@@ -172,6 +197,7 @@ struct AttendArgs {
   int div_mul, div_shift;  // division by the page size (set by the launch)
   int max_len;             // slots of a row of the block table (set by the launch)
   int heads_log2;          // log2 of the key heads that a block may take at once (set by the launch)
+  KvScales sc;             // NVFP4
 };
 // Workspace regions (byte offsets, 256-byte aligned), for kAttendBlocks blocks and attend_warps warps an SM
 // at most, two pieces each, 16 query heads a piece.

@@ -33,7 +33,8 @@ EXPORTED = ["ft_moe_abi_version", "ft_status_string", "ft_moe_route", "ft_moe_wo
             "ft_moe_fp8block_workspace_bytes", "ft_moe_fp8block_decode",
             "ft_moe_router_logits", "ft_moe_router_route",
             "ft_nvfp4_linear_workspace_bytes", "ft_nvfp4_linear", "ft_kv_append", "ft_paged_attention_workspace_bytes",
-            "ft_paged_decode_attention", "ft_residual_norm",
+            "ft_paged_decode_attention", "ft_kv_append_axes", "ft_nvfp4_kv_append", "ft_kv_gather",
+            "ft_nvfp4_kv_gather", "ft_nvfp4_paged_decode_attention", "ft_residual_norm",
             "ft_residual_norm_backward_workspace_bytes", "ft_residual_norm_backward"]
 
 # Leading bytes of a workspace that must be zero before a call (FT_MOE_WORKSPACE_HEAD_BYTES);
@@ -89,6 +90,19 @@ class _PagedKV(ctypes.Structure):
                 ("v_scale", ctypes.c_float)]
 
 
+class _NvFP4KV(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scales", "v_scales")] +
+                [(n, ctypes.c_int32) for n in ("num_pages", "page_size", "Hkv", "D")] +
+                [(f"{n}_{of}_stride", ctypes.c_int64) for n in ("k", "v", "ks", "vs")
+                 for of in ("page", "slot", "head")] +
+                [("k_gscale", ctypes.c_float), ("v_gscale", ctypes.c_float)])
+
+
+class _RopeAxes(ctypes.Structure):
+    _fields_ = [("positions", ctypes.c_void_p), ("stride", ctypes.c_int64), ("axes", ctypes.c_int32),
+                ("axis", ctypes.c_uint8 * 128)]
+
+
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"{path} is missing: build it with __graft_entry__.build() "
@@ -141,11 +155,22 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ft_kv_append.restype = ctypes.c_int
     lib.ft_kv_append.argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, i32, ctypes.POINTER(_PagedKV),
                                  vp, i32, i32, vp, vp, vp, i32, i32, vp, vp]
+    axes, cache4 = ctypes.POINTER(_RopeAxes), ctypes.POINTER(_NvFP4KV)
+    for name, cache in (("ft_kv_append_axes", ctypes.POINTER(_PagedKV)), ("ft_nvfp4_kv_append", cache4)):
+        getattr(lib, name).restype = ctypes.c_int
+        getattr(lib, name).argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, i32, cache, vp, i32, i32, vp, vp,
+                                       vp, i32, i32, axes, vp, vp]
+    for name, cache in (("ft_kv_gather", ctypes.POINTER(_PagedKV)), ("ft_nvfp4_kv_gather", cache4)):
+        getattr(lib, name).restype = ctypes.c_int
+        getattr(lib, name).argtypes = [cache, vp, i32, i32, vp, vp, i32, vp, vp, vp, vp]
     lib.ft_paged_attention_workspace_bytes.restype = sz
     lib.ft_paged_attention_workspace_bytes.argtypes = [i32, i32]
     lib.ft_paged_decode_attention.restype = ctypes.c_int
     lib.ft_paged_decode_attention.argtypes = [vp, i64, i32, i32, ctypes.POINTER(_PagedKV), vp, i32,
                                               vp, f32, i32, vp, vp, vp, sz, vp]
+    lib.ft_nvfp4_paged_decode_attention.restype = ctypes.c_int
+    lib.ft_nvfp4_paged_decode_attention.argtypes = [vp, i64, i32, i32, cache4, vp, i32, vp, f32, i32, vp, vp,
+                                                    vp, sz, vp]
     lib.ft_residual_norm.restype = ctypes.c_int
     lib.ft_residual_norm.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, f32, f32, vp, vp, vp]
     lib.ft_residual_norm_backward_workspace_bytes.restype = sz
@@ -845,23 +870,83 @@ class PagedKVCache:
         return self.heads[1]
 
 
-def kv_append(k, v, cache: PagedKVCache, block_table, positions, seq_ids=None, q=None, rope=None,
-              q_out=None, workspace=None, stream=None):
-    """ft_kv_append: k, v bf16 [T,Hkv,D] into the cache's slots of `positions` int32 [T] (of the
-    sequences seq_ids int32 [T], or 0..T-1) through block_table int32 [B,width], k rotated by rope
-    f32 [rows, R] (cos | sin; None: not at all). Returns the rotated q bf16 [T,Hq,D], or None
-    without q. Rows of k, v and q may be slices of one projection's output. A token whose page,
-    sequence or position lies outside its table stores nothing and flags it (get_error)."""
-    if stream is not None:
-        with torch.cuda.stream(stream):   # what the call makes belongs to the stream that it runs on
-            return kv_append(k, v, cache, block_table, positions, seq_ids, q, rope, q_out, workspace)
-    dev, inner = cache.device_index, cache.heads
-    if k.dim() != 3 or block_table.dim() != 2:
-        raise ValueError("k [T, Hkv, D] and block_table [B, width] expected")
-    T, D = k.shape[0], inner[1]
-    ks, vs = _need_rows(k, "k", dev, inner), _need_rows(v, "v", dev, inner)
-    if v.shape[0] != T:
-        raise ValueError("v: as many tokens as k expected")
+@dataclass(frozen=True)
+class NvFP4KVCache:
+    """A paged key-value cache in NVFP4 on the device, the layout of the weights along each head: k and v u8
+    codes [num_pages, page_size, Hkv, D/2], k_scales and v_scales E4M3 [num_pages, page_size, Hkv, D/16] (any
+    1-byte type), a float scale for all keys and one for all values (about the largest magnitude / 2688).
+    Codes and scales of a head contiguous, the other strides free. Checked when built."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scales: torch.Tensor
+    v_scales: torch.Tensor
+    k_gscale: float = 1.0
+    v_gscale: float = 1.0
+
+    def __post_init__(self):
+        dev = _device_of(self.k, "NvFP4KVCache")
+        if self.k.dim() != 4 or self.k.shape != self.v.shape:
+            raise ValueError("NvFP4KVCache: k and v [num_pages, page_size, Hkv, D/2] of one shape")
+        P, page, Hkv, half = self.k.shape
+        for name in ("k", "v", "k_scales", "v_scales"):
+            t = getattr(self, name)
+            if t.get_device() != dev:
+                raise ValueError("NvFP4KVCache: codes and scales must be on one device")
+            if t.element_size() != 1:
+                raise TypeError(f"NvFP4KVCache: {name} has 1-byte elements, got {t.dtype}")
+            if name.endswith("scales") and (half % 8 != 0 or t.shape != (P, page, Hkv, half // 8)):
+                raise ValueError(f"NvFP4KVCache: {name} [num_pages, page_size, Hkv, D/16] expected")
+            if t.stride(3) != 1:
+                raise ValueError("NvFP4KVCache: the elements of a head must be contiguous")
+        if max(P, page, Hkv, 2 * half) > _MAX_I32:
+            raise ValueError(f"NvFP4KVCache: {tuple(self.k.shape)} is too large")
+        tensors = (self.k, self.v, self.k_scales, self.v_scales)
+        object.__setattr__(self, "device_index", dev)
+        object.__setattr__(self, "heads", (Hkv, 2 * half))   # (Hkv, D)
+        object.__setattr__(self, "_cs", _NvFP4KV(
+            *(_ptr(t) for t in tensors), P, page, Hkv, 2 * half,
+            *(n for t in tensors for n in t.stride()[:3]), float(self.k_gscale), float(self.v_gscale)))
+        object.__setattr__(self, "_ref", ctypes.byref(self._cs))
+
+    page_size, Hkv, D = PagedKVCache.page_size, PagedKVCache.Hkv, PagedKVCache.D
+
+
+@dataclass(frozen=True)
+class RopeAxes:
+    """Which of up to four axes (time, height, width, ..) turns each rotary pair: axes, R/2 numbers from 0 on."""
+    axes: tuple
+
+    def __post_init__(self):
+        axes = tuple(int(a) for a in self.axes)
+        if not 0 < len(axes) <= 128 or min(axes) < 0 or max(axes) > 3:
+            raise ValueError("RopeAxes: the axis, 0 to 3, of each of 1 to 128 pairs")
+        object.__setattr__(self, "axes", axes)
+        object.__setattr__(self, "count", max(axes) + 1)
+        object.__setattr__(self, "_axis", (ctypes.c_uint8 * 128)(*axes))
+
+    @staticmethod
+    def of_sections(sections, interleaved=False) -> RopeAxes:
+        """sections: the number of pairs of each axis. They follow one another, or, interleaved, pair i goes
+        to axis i mod len(sections) while that one has pairs left, then to the first that has."""
+        left, axes = [int(n) for n in sections], []
+        if not left or min(left) < 0:
+            raise ValueError("RopeAxes: the number of pairs of each axis")
+        if not interleaved:
+            return RopeAxes(tuple(a for a, n in enumerate(left) for _ in range(n)))
+        for i in range(sum(left)):
+            a = i % len(left)
+            if left[a] == 0:
+                a = next(j for j, n in enumerate(left) if n)
+            left[a] -= 1
+            axes.append(a)
+        return RopeAxes(tuple(axes))
+
+
+def _tokens(cache, block_table, positions, seq_ids, T, dev):
+    """The places of T tokens in a cache: block_table [B,width], positions [T], seq_ids [T] or None.
+    Returns (B, width)."""
+    if block_table.dim() != 2:
+        raise ValueError("block_table: [B, width] expected")
     _need(block_table, "block_table", dev, _I32, None)
     _need(positions, "positions", dev, _I32, (T,))
     B, width = block_table.shape
@@ -871,6 +956,40 @@ def kv_append(k, v, cache: PagedKVCache, block_table, positions, seq_ids=None, q
         _need(seq_ids, "seq_ids", dev, _I32, (T,))
     elif T > B:
         raise ValueError("seq_ids: required for more tokens than block_table has rows")
+    return B, width
+
+
+def _flags(workspace, T, dev):
+    """The workspace whose head collects the flags of a call on T tokens."""
+    if workspace is not None:
+        _need(workspace, "workspace", dev, None, None)
+        if workspace.numel() < WORKSPACE_HEAD_BYTES:
+            raise ValueError("workspace: at least WORKSPACE_HEAD_BYTES expected")
+    elif T > 0:
+        workspace = _scratch(WORKSPACE_HEAD_BYTES, dev)
+    return workspace
+
+
+def kv_append(k, v, cache, block_table, positions, seq_ids=None, q=None, rope=None,
+              q_out=None, workspace=None, stream=None, rope_positions=None, rope_axes=None):
+    """ft_kv_append: k, v bf16 [T,Hkv,D] into the cache's (PagedKVCache or NvFP4KVCache) slots of `positions`
+    int32 [T] (of the sequences seq_ids int32 [T], or 0..T-1) through block_table int32 [B,width], k rotated by
+    rope f32 [rows, R] (cos | sin; None: not at all). With rope_axes (a RopeAxes of R/2 pairs), each pair turns by
+    the row that rope_positions int32 [axes,T] gives its axis. Returns the rotated q bf16 [T,Hq,D], or None
+    without q. Rows of k, v and q may be slices of one projection's output. A token whose page,
+    sequence or position lies outside its table stores nothing and flags it (get_error)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):   # what the call makes belongs to the stream that it runs on
+            return kv_append(k, v, cache, block_table, positions, seq_ids, q, rope, q_out, workspace, None,
+                             rope_positions, rope_axes)
+    dev, inner = cache.device_index, cache.heads
+    if k.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("k [T, Hkv, D] and block_table [B, width] expected")
+    T, D = k.shape[0], inner[1]
+    ks, vs = _need_rows(k, "k", dev, inner), _need_rows(v, "v", dev, inner)
+    if v.shape[0] != T:
+        raise ValueError("v: as many tokens as k expected")
+    B, width = _tokens(cache, block_table, positions, seq_ids, T, dev)
     Hq = qs = qp = qo = 0
     if q is not None:
         if q.dim() != 3 or q.shape[0] != T:
@@ -891,20 +1010,71 @@ def kv_append(k, v, cache: PagedKVCache, block_table, positions, seq_ids=None, q
         if rows > _MAX_I32:
             raise ValueError(f"rope: {rows} rows are too many")
         rp = rope.data_ptr()
-    if workspace is not None:
-        _need(workspace, "workspace", dev, None, None)
-        if workspace.numel() < WORKSPACE_HEAD_BYTES:
-            raise ValueError("workspace: at least WORKSPACE_HEAD_BYTES expected")
-    elif T > 0:
-        workspace = _scratch(WORKSPACE_HEAD_BYTES, dev)   # for its flags
-    st = _LIB.ft_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, qo, T, Hq, cache._ref,
-                           block_table.data_ptr(), B, width,
-                           0 if seq_ids is None else seq_ids.data_ptr(), positions.data_ptr(), rp,
-                           rows, dim, 0 if workspace is None else workspace.data_ptr(),
-                           _stream(None, dev))
+    axes = None
+    if rope_axes is not None:
+        if rope is None or rope_positions is None:
+            raise ValueError("rope_axes: rope and rope_positions are required with it")
+        if dim != 2 * len(rope_axes.axes):
+            raise ValueError(f"rope_axes: {len(rope_axes.axes)} pairs for a rope of {dim} elements")
+        _need(rope_positions, "rope_positions", dev, _I32, None)
+        if rope_positions.dim() != 2 or rope_positions.shape[0] < rope_axes.count or rope_positions.shape[1] != T:
+            raise ValueError(f"rope_positions: [axes, T] with at least {rope_axes.count} axes expected")
+        axes = ctypes.byref(_RopeAxes(rope_positions.data_ptr(), T, rope_axes.count, rope_axes._axis))
+    elif rope_positions is not None:
+        raise ValueError("rope_positions: rope_axes is required with them")
+    workspace = _flags(workspace, T, dev)
+    where = (block_table.data_ptr(), B, width, 0 if seq_ids is None else seq_ids.data_ptr(),
+             positions.data_ptr(), rp, rows, dim)
+    ws = 0 if workspace is None else workspace.data_ptr()
+    if type(cache) is NvFP4KVCache:
+        name = "ft_nvfp4_kv_append"
+        st = _LIB.ft_nvfp4_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, qo, T, Hq, cache._ref, *where,
+                                     axes, ws, _stream(None, dev))
+    elif axes is not None:
+        name = "ft_kv_append_axes"
+        st = _LIB.ft_kv_append_axes(k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, qo, T, Hq, cache._ref, *where,
+                                    axes, ws, _stream(None, dev))
+    else:
+        name = "ft_kv_append"
+        st = _LIB.ft_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, qo, T, Hq, cache._ref, *where, ws,
+                               _stream(None, dev))
     if st != FT_OK:
-        _check(st, "ft_kv_append")
+        _check(st, name)
     return q_out if q is not None else None
+
+
+def kv_gather(cache, block_table, positions, seq_ids=None, k_out=None, v_out=None, workspace=None,
+              stream=None):
+    """ft_kv_gather: the keys and values of the cache's (PagedKVCache or NvFP4KVCache) slots of `positions`
+    int32 [T] (of the sequences seq_ids int32 [T], or 0..T-1) through block_table int32 [B,width], as dense
+    bf16 [T,Hkv,D]. Negative positions give zeros; so does what lies outside its table, which flags it
+    (get_error)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):   # what the call makes belongs to the stream that it runs on
+            return kv_gather(cache, block_table, positions, seq_ids, k_out, v_out, workspace)
+    dev, inner = cache.device_index, cache.heads
+    if positions.dim() != 1:
+        raise ValueError("positions: [T] expected")
+    T = positions.shape[0]
+    B, width = _tokens(cache, block_table, positions, seq_ids, T, dev)
+    shape = (T, *inner)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=positions.device)
+    else:
+        _need(k_out, "k_out", dev, BF16_BITS, shape)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=positions.device)
+    else:
+        _need(v_out, "v_out", dev, BF16_BITS, shape)
+    workspace = _flags(workspace, T, dev)
+    four = type(cache) is NvFP4KVCache
+    st = (_LIB.ft_nvfp4_kv_gather if four else _LIB.ft_kv_gather)(
+        cache._ref, block_table.data_ptr(), B, width, 0 if seq_ids is None else seq_ids.data_ptr(),
+        positions.data_ptr(), T, k_out.data_ptr(), v_out.data_ptr(),
+        0 if workspace is None else workspace.data_ptr(), _stream(None, dev))
+    if st != FT_OK:
+        _check(st, "ft_nvfp4_kv_gather" if four else "ft_kv_gather")
+    return k_out, v_out
 
 
 def paged_attention_workspace_bytes(B, D) -> int:
@@ -919,10 +1089,10 @@ def _attention_bytes(B, D, dev) -> int:   # a size of the device's, asked for on
     return n
 
 
-def paged_decode_attention(q, cache: PagedKVCache, block_table, seq_lens, scale=None, window=0,
+def paged_decode_attention(q, cache, block_table, seq_lens, scale=None, window=0,
                            out=None, lse=None, workspace=None, stream=None):
     """ft_paged_decode_attention: q bf16 [B,Hq,D], one new token per sequence, over the first
-    seq_lens int32 [B] slots of each (the last `window` of them if window > 0) through block_table
+    seq_lens int32 [B] slots of each in the cache (PagedKVCache or NvFP4KVCache) (the last `window` of them if window > 0) through block_table
     int32 [B,width]. scale: 1/sqrt(D) by default. Returns (out bf16 [B,Hq,D], lse f32 [B,Hq])."""
     if stream is not None:
         with torch.cuda.stream(stream):   # what the call makes belongs to the stream that it runs on
@@ -952,13 +1122,14 @@ def paged_decode_attention(q, cache: PagedKVCache, block_table, seq_lens, scale=
         _need(workspace, "workspace", dev, None, None)
     elif B > 0:
         workspace = _scratch(_attention_bytes(B, D, dev), dev)
-    st = _LIB.ft_paged_decode_attention(
+    four = type(cache) is NvFP4KVCache
+    st = (_LIB.ft_nvfp4_paged_decode_attention if four else _LIB.ft_paged_decode_attention)(
         q.data_ptr(), qs, B, Hq, cache._ref, block_table.data_ptr(), width, seq_lens.data_ptr(),
         D ** -0.5 if scale is None else scale, window, out.data_ptr(), lse.data_ptr(),
         0 if workspace is None else workspace.data_ptr(),
         0 if workspace is None else workspace.numel(), _stream(None, dev))
     if st != FT_OK:
-        _check(st, "ft_paged_decode_attention")
+        _check(st, "ft_nvfp4_paged_decode_attention" if four else "ft_paged_decode_attention")
     return out, lse
 
 

@@ -4,6 +4,9 @@ TEST INFRASTRUCTURE — see the package docstring for who may import this.
 
 * linear: y_t = W x_t with W dequantised (oracle.nvfp4).
 * rotary: element i and i + R/2 of a head turn by the position's angle i.
+* rotary with several axes: pair i turns by the position on its own axis.
+* NVFP4 rows: blocks of 16 elements, s = e4m3(max|x| / (6 g)), code = e2m1(x / (s g)), in the float32
+  steps that the cache append is defined by.
 * attention: softmax(scale q K^T) V over the last `window` of a sequence's first `len` slots.
 * norms: r' = r + scale gate norm(y), x' = norm(r'), norm(v) = v / sqrt(mean v^2 + eps) * w, and
   the gradient by the chain rule over each row.
@@ -15,7 +18,7 @@ from __future__ import annotations
 
 import numpy as np
 
-from .nvfp4 import dequantize
+from .nvfp4 import E2M1_VALUES, E4M3_VALUES, dequantize
 
 
 def linear(x, codes, scales, gscale):
@@ -37,6 +40,51 @@ def rotate(v, rope, positions):
         out[t, :, :h] = a * c - b * s
         out[t, :, h:2 * h] = b * c + a * s
     return out
+
+
+def rotate_axes(v, rope, positions, axis):
+    """v [T,heads,D]; positions [axes,T]; axis: one number for each of the R/2 pairs."""
+    v = np.array(v, np.float64)
+    h, axis = rope.shape[1] // 2, np.asarray(axis)
+    at = np.asarray(positions)[axis].T                  # [T, pairs]
+    c = rope[at, np.arange(h)].astype(np.float64)[:, None]
+    s = rope[at, h + np.arange(h)].astype(np.float64)[:, None]
+    out = v.copy()
+    out[..., :h] = v[..., :h] * c - v[..., h:2 * h] * s
+    out[..., h:2 * h] = v[..., h:2 * h] * c + v[..., :h] * s
+    return out
+
+
+def _nearest(v, values):
+    """Index of the value nearest to v >= 0 among `values` (ascending from 0), ties to the even index,
+    past the largest: the largest."""
+    v = np.asarray(v, np.float64)
+    middle = (values[:-1].astype(np.float64) + values[1:]) / 2
+    i = np.searchsorted(middle, v, side="left")         # a tie: the lower one
+    tie = (i < len(middle)) & (v == middle[np.minimum(i, len(middle) - 1)])
+    return (i + (tie & (i % 2 == 1))).astype(np.uint8)
+
+
+def nvfp4_rows(x, g):
+    """float32 [..., D] -> (codes u8 [..., D/2], scales u8 [..., D/16]) under the tensor scale g."""
+    g, x = np.float32(g), np.asarray(x, np.float32)
+    b = x.reshape(*x.shape[:-1], x.shape[-1] // 16, 16)
+    nan = np.isnan(b).any(-1)
+    top = np.where(np.isnan(b), 0, np.abs(b)).max(-1)
+    with np.errstate(all="ignore"):
+        s = _nearest(top * (np.float32(1) / (np.float32(6) * g)), E4M3_VALUES[:127])
+        d = E4M3_VALUES[s] * g
+        r = np.where(d > 0, np.float32(1) / np.where(d > 0, d, np.float32(1)), np.float32(0))
+        y = b * r[..., None]
+    code = _nearest(np.abs(np.where(np.isnan(y), 0, y)), E2M1_VALUES[:8]) | (np.signbit(y).astype(np.uint8) << 3)
+    s = np.where(nan, np.uint8(0x7F), s)
+    code = code.reshape(x.shape)
+    return code[..., 0::2] | (code[..., 1::2] << 4), s
+
+
+def nvfp4_values(codes, scales, g):
+    """What codes u8 [..., D/2] under scales u8 [..., D/16] stand for, float32."""
+    return dequantize(codes, scales, g)
 
 
 def attention(q, keys, values, length, scale, window=0):
