@@ -37,6 +37,7 @@
 #include <cmath>
 #include <cuda_runtime.h>
 
+#include "ftmoe_attend4.cuh"
 #include "ftmoe_internal.h"
 #include "ftmoe_mma.cuh"
 #include "ftmoe_tc.cuh"
@@ -88,102 +89,6 @@ template <int CPR>
 __device__ __forceinline__ uint32_t swz(int r, int c) {
   if constexpr (CPR >= 8) return (uint32_t)(r * CPR + (c ^ (r & 7))) * 16;
   else return (uint32_t)(r * CPR + (c ^ ((r >> 1) & 3))) * 16;
-}
-
-__device__ __forceinline__ uint32_t transpose8(uint32_t v) {   // an 8 x 8 matrix of 16-bit elements
-  uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
-  return d;
-}
-
-// Four E4M3 bytes -> f16x2 of the lower two and of the upper two, exact.
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t v, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-      : "=r"(lo), "=r"(hi) : "r"(v));
-}
-
-// NVFP4 rows. Lane (r, c) = (lane / 4, lane % 4) of a 16-key tile takes D/4 consecutive elements of keys r and
-// r + 8 as the row operand of k q^T, and D/8 consecutive elements, from r D/8 on, of keys 2c, 2c + 1, 2c + 8 and
-// 2c + 9 as that of v^T p^T: whole words of codes under one scale or two. Which key is row i of a tile, and where
-// its 16-byte pieces lie, is chosen so that both reads find 32 banks.
-template <int D>
-__device__ __forceinline__ int key_of_row(int i) {   // 0 <= i < 8; 8 + i follows
-  return D == 64 ? i ^ (i >> 2) : D == 128 ? i ^ ((i >> 1) & 1) : i;
-}
-template <int D>
-__device__ __forceinline__ uint32_t piece4(int row, int ch) {   // offset of 16-byte piece ch of a row
-  return (uint32_t)(row * (D / 2) + (D == 64 ? ch : D == 128 ? ch ^ (2 * ((row >> 2) & 1)) : ch ^ (row & 7)) * 16);
-}
-
-// N bytes (4, 8 or 16) from global to shared memory; zeros (and no access) when !valid.
-template <int N>
-__device__ __forceinline__ void cp_async_scales(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(valid ? N : 0)
-               : "memory");
-}
-// W words from shared memory.
-template <int W>
-__device__ __forceinline__ void lds(uint32_t (&v)[W], uint32_t addr) {
-  static_assert(W == 1 || W == 2 || W % 4 == 0);
-  if constexpr (W == 1) {
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[0]) : "r"(addr) : "memory");
-  } else if constexpr (W == 2) {
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(addr) : "memory");
-  } else {
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                 : "r"(addr)
-                 : "memory");
-  }
-}
-__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
-  uint32_t v;
-  asm volatile("{\n\t.reg .u16 t;\n\tld.shared.u16 t, [%1];\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-// The scales of lane c's elements of a key, each in both halves of a word.
-template <int D>
-__device__ __forceinline__ void key_scales(uint32_t (&s)[D / 64], uint32_t row, int c) {
-  if constexpr (D == 64) {
-    s[0] = splat_lo(e4m3x2_to_f16x2(lds_u8(row + c)));
-  } else if constexpr (D == 128) {
-    const uint32_t v = e4m3x2_to_f16x2(lds_u16(row + 2 * c));
-    s[0] = splat_lo(v);
-    s[1] = splat_hi(v);
-  } else {
-    uint32_t w[1], lo, hi;
-    lds(w, row + 4 * c);
-    e4m3x4_to_f16(w[0], lo, hi);
-    s[0] = splat_lo(lo);
-    s[1] = splat_hi(lo);
-    s[2] = splat_lo(hi);
-    s[3] = splat_hi(hi);
-  }
-}
-// The scales of lane r's elements of two values, the first one's in the lower half of a word.
-template <int D>
-__device__ __forceinline__ void value_scales(uint32_t (&s)[D == 256 ? 2 : 1], uint32_t row0, uint32_t row1, int r) {
-  if constexpr (D == 256) {
-    const uint32_t a = lds_u16(row0 + 2 * r), b = lds_u16(row1 + 2 * r);
-    s[0] = e4m3x2_to_f16x2(__byte_perm(a, b, 0x0040));
-    s[1] = e4m3x2_to_f16x2(__byte_perm(a, b, 0x0051));
-  } else {
-    const int at = D == 64 ? r >> 1 : r;
-    const uint32_t a = lds_u8(row0 + at), b = lds_u8(row1 + at);
-    s[0] = e4m3x2_to_f16x2(a | b << 8);
-  }
-}
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // Four values of an output row, divided by the weights' sum (no weight at all: zeros).
@@ -327,6 +232,18 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kWarps * 32, AttnShape<D
     const int piece0 = first / S::kUnit * S::kUnit + u0 * unit;
     const int key1 = min(len, piece0 + n_units * unit), key0 = piece0 + stripe * KT;
     const int n_sub = key1 > key0 ? (key1 - key0 + unit - 1) >> (kUnitLog2 - hl) : 0;
+    float o[NG][MT][4], m[NG][2], l[NG][2];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t) o[g][t][0] = o[g][t][1] = o[g][t][2] = o[g][t][3] = 0.f;
+      m[g][0] = m[g][1] = -INFINITY;
+      l[g][0] = l[g][1] = 0.f;
+    }
+    if constexpr (F4) {
+      attend_piece4<D, NG, S>(a, reinterpret_cast<char*>(smem) + warp * ST * S::kStageBytes, b, kvh, g0, G, first, key0, key1,
+                              unit, n_sub, o, m, l);
+    } else {
     const int32_t* table = a.block_table + (int64_t)b * a.table_width;
     int page = -1, slot = 0;
     auto look_up = [&](int i) {   // lane l < KT: the page and slot of key l of step i
@@ -352,14 +269,6 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kWarps * 32, AttnShape<D
           if (j >= first && j < key1) atomicOr(a.err, kErrBadPage);   // no such page: read as zeros
         }
         const uint32_t st = ring + (uint32_t)((i % ST) * S::kStageBytes);
-        if constexpr (F4) {   // each lane's key brings its scales
-          const bool on = ko >= 0;
-          const int64_t p = on ? page : 0, sl = on ? slot : 0;
-          cp_async_scales<S::kScaleRow>(st + 2 * KT * S::kRow + lane * S::kScaleRow,
-                                        a.sc.k + p * a.sc.k_page + sl * a.sc.k_slot + kvh * a.sc.k_head, on);
-          cp_async_scales<S::kScaleRow>(st + KT * (2 * S::kRow + S::kScaleRow) + lane * S::kScaleRow,
-                                        a.sc.v + p * a.sc.v_page + sl * a.sc.v_slot + kvh * a.sc.v_head, on);
-        }
         constexpr int RPI = 32 / CPR;   // rows of one warp-wide copy
 #pragma unroll
         for (int p = 0; p < KT / RPI; ++p) {
@@ -367,7 +276,7 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kWarps * 32, AttnShape<D
           const int64_t k_at = __shfl_sync(0xffffffffu, ko, row);
           const int64_t v_at = a.same_strides ? k_at : __shfl_sync(0xffffffffu, vo, row);
           const bool on = k_at >= 0;
-          const uint32_t to = st + (F4 ? piece4<D>(row, ch) : swz<CPR>(row, ch));
+          const uint32_t to = st + swz<CPR>(row, ch);
           cp_async16(to, static_cast<const char*>(a.kv.k) + (on ? k_at + ch * 16 : 0), on);
           cp_async16(to + KT * S::kRow, static_cast<const char*>(a.kv.v) + (on ? v_at + ch * 16 : 0), on);
         }
@@ -400,9 +309,9 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kWarps * 32, AttnShape<D
         } else {
           float top = 0.f;
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {   // E4M3 keys come four elements to a lane, NVFP4 ones D/4
+          for (int ks = 0; ks < KS; ++ks) {   // E4M3 keys come four elements to a lane
             uint2 v = make_uint2(0, 0);
-            if (on) v = *reinterpret_cast<const uint2*>(qh + (F4 ? D / 4 * c + 4 * ks : 16 * ks + 4 * c));
+            if (on) v = *reinterpret_cast<const uint2*>(qh + 16 * ks + 4 * c);
             q[g][ks][0] = v.x;
             q[g][ks][1] = v.y;
             top = fmaxf(top, finite_top(v.x, v.y));
@@ -422,14 +331,6 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kWarps * 32, AttnShape<D
       }
     }
 
-    float o[NG][MT][4], m[NG][2], l[NG][2];
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-#pragma unroll
-      for (int t = 0; t < MT; ++t) o[g][t][0] = o[g][t][1] = o[g][t][2] = o[g][t][3] = 0.f;
-      m[g][0] = m[g][1] = -INFINITY;
-      l[g][0] = l[g][1] = 0.f;
-    }
     const int krow = ((lane >> 3) & 1) * 8 + (lane & 7), half = lane >> 4;
 
     for (int i = 0; i < n_sub; ++i) {
@@ -445,50 +346,7 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kWarps * 32, AttnShape<D
       for (int g = 0; g < NG; ++g)
 #pragma unroll
         for (int h = 0; h < NH; ++h) s[g][h][0] = s[g][h][1] = s[g][h][2] = s[g][h][3] = 0.f;
-      if constexpr (F4) {
-#pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          constexpr int NW = D / 32;   // words of a lane's elements of a key
-          const int row = 16 * h + key_of_row<D>(r);
-          uint32_t k0[NW], k1[NW], s0[D / 64], s1[D / 64];
-          const uint32_t sc = st + 2 * KT * S::kRow + row * S::kScaleRow;
-          if constexpr (D == 64) {
-            lds(k0, st + piece4<D>(row, c >> 1) + (c & 1) * 8);
-            lds(k1, st + piece4<D>(row + 8, c >> 1) + (c & 1) * 8);
-          } else {
-#pragma unroll
-            for (int x = 0; x < NW / 4; ++x) {
-              uint32_t t0[4], t1[4];
-              lds(t0, st + piece4<D>(row, NW / 4 * c + x));
-              lds(t1, st + piece4<D>(row + 8, NW / 4 * c + x));
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                k0[4 * x + y] = t0[y];
-                k1[4 * x + y] = t1[y];
-              }
-            }
-          }
-          key_scales<D>(s0, sc, c);
-          key_scales<D>(s1, sc + 8 * S::kScaleRow, c);
-#pragma unroll
-          for (int j = 0; j < NW; ++j) {
-            uint32_t x[4], y[4];
-            e2m1x8_to_f16x2x4(k0[j], x[0], x[1], x[2], x[3]);
-            e2m1x8_to_f16x2x4(k1[j], y[0], y[1], y[2], y[3]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {   // exact: six significant bits
-              x[e] = hmul2(x[e], s0[j / 2]);
-              y[e] = hmul2(y[e], s1[j / 2]);
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int g = 0; g < NG; ++g)
-                mma_f16(s[g][h], x[2 * e], y[2 * e], x[2 * e + 1], y[2 * e + 1], q[g][2 * j + e][0],
-                        q[g][2 * j + e][1]);
-          }
-        }
-      } else if constexpr (!F16) {
+      if constexpr (!F16) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
@@ -533,7 +391,7 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kWarps * 32, AttnShape<D
           for (int h = 0; h < NH; ++h)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int j = j0 + 16 * h + (F4 ? key_of_row<D>(r) : r) + (e >> 1) * 8;
+              const int j = j0 + 16 * h + r + (e >> 1) * 8;
               if (j < first || j >= key1) s[g][h][e] = -INFINITY;
             }
         }
@@ -598,42 +456,7 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kWarps * 32, AttnShape<D
       }
       // o^T += v^T p^T: 16 dims at a time
       const uint32_t vs = st + KT * S::kRow;
-      if constexpr (F4) {
-#pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          constexpr int NW = D / 64;   // words of a lane's elements of a value
-          constexpr int NS = D == 256 ? 2 : 1;
-          uint32_t v[4][NW], s01[NS], s89[NS];   // keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9
-          const uint32_t sc = st + KT * (2 * S::kRow + S::kScaleRow);
-          const int row0 = 16 * h + key_of_row<D>(2 * c), row1 = 16 * h + key_of_row<D>(2 * c + 1);
-          const int rows[4] = {row0, row1, row0 + 8, row1 + 8};
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            lds(v[x], vs + piece4<D>(rows[x], D * r / 256) + (D * r / 16 & 15));
-          value_scales<D>(s01, sc + row0 * S::kScaleRow, sc + row1 * S::kScaleRow, r);
-          value_scales<D>(s89, sc + (row0 + 8) * S::kScaleRow, sc + (row1 + 8) * S::kScaleRow, r);
-#pragma unroll
-          for (int j = 0; j < NW; ++j) {
-            // elements 2 i (a0, a2) and 2 i + 1 (a1, a3) of two keys in byte i of a word
-            uint32_t a0[4], a1[4], a2[4], a3[4];
-            const uint32_t lo = 0x0F0F0F0Fu;
-            e2m1x8_to_f16x2x4((v[0][j] & lo) | (v[1][j] << 4 & ~lo), a0[0], a0[1], a0[2], a0[3]);
-            e2m1x8_to_f16x2x4((v[0][j] >> 4 & lo) | (v[1][j] & ~lo), a1[0], a1[1], a1[2], a1[3]);
-            e2m1x8_to_f16x2x4((v[2][j] & lo) | (v[3][j] << 4 & ~lo), a2[0], a2[1], a2[2], a2[3]);
-            e2m1x8_to_f16x2x4((v[2][j] >> 4 & lo) | (v[3][j] & ~lo), a3[0], a3[1], a3[2], a3[3]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t b0 = hmul2(a0[e], s01[j / 2]), b1 = hmul2(a1[e], s01[j / 2]);
-              const uint32_t b2 = hmul2(a2[e], s89[j / 2]), b3 = hmul2(a3[e], s89[j / 2]);
-#pragma unroll
-              for (int g = 0; g < NG; ++g) {
-                mma_f16(o[g][4 * j + e], b0, b1, b2, b3, p[g][h][0], p[g][h][1]);
-                mma_f16(o[g][4 * j + e], b0, b1, b2, b3, rest[g][h][0], rest[g][h][1]);
-              }
-            }
-          }
-        }
-      } else if constexpr (!F16) {
+      if constexpr (!F16) {
         const int vrow = half * 8 + (lane & 7), vch = (lane >> 3) & 1;
 #pragma unroll
         for (int t = 0; t < MT; ++t)
@@ -671,6 +494,7 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kWarps * 32, AttnShape<D
       __syncwarp();   // every lane has read the stage before it is filled again
     }
     cp_async_wait<0>();
+    }
 
     // ---- join the warps of a head: sums [head][LD] in each one's ring
     sync();
@@ -902,7 +726,8 @@ cudaError_t launch_attend(const AttendArgs& args, int num_sms, cudaStream_t stre
   a.group = a.Hq / a.kv.Hkv;
   a.gt = (a.group + 15) / 16;
   a.same_strides = a.kv.k_page_stride == a.kv.v_page_stride && a.kv.k_slot_stride == a.kv.v_slot_stride &&
-                   a.kv.k_head_stride == a.kv.v_head_stride;
+                   a.kv.k_head_stride == a.kv.v_head_stride && a.sc.k_page == a.sc.v_page &&
+                   a.sc.k_slot == a.sc.v_slot && a.sc.k_head == a.sc.v_head;
   page_division(a.kv.page_size, a.div_mul, a.div_shift);
   const int64_t slots = (int64_t)a.table_width * a.kv.page_size;
   a.max_len = (int)(slots < (1 << 30) ? slots : 1 << 30);

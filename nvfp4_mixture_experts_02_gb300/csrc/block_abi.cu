@@ -307,6 +307,17 @@ ft_status ft_nvfp4_paged_decode_attention(const uint16_t* q, int64_t q_stride, i
   AttendArgs a = {};
   const ft_status st = nvfp4_cache(cache, a.kv, a.sc);
   if (st != FT_OK) return st;
+  // the kernel's offsets of rows are 32 bits of 16-byte pieces of codes, and of rows of scales
+  const auto spans = [&](int64_t page_stride, int64_t slot_stride, int64_t head_stride, int64_t unit) {
+    const auto far = [&](int64_t n, int64_t stride) { return (double)(n - 1) * (double)(stride / unit); };
+    return far(cache->num_pages, page_stride) + far(cache->page_size, slot_stride) + far(cache->Hkv, head_stride) <
+           4294967296.0;
+  };
+  if (!spans(cache->k_page_stride, cache->k_slot_stride, cache->k_head_stride, 16) ||
+      !spans(cache->v_page_stride, cache->v_slot_stride, cache->v_head_stride, 16) ||
+      !spans(cache->ks_page_stride, cache->ks_slot_stride, cache->ks_head_stride, cache->D / 16) ||
+      !spans(cache->vs_page_stride, cache->vs_slot_stride, cache->vs_head_stride, cache->D / 16))
+    return FT_ERR_UNSUPPORTED_SHAPE;
   return attend(a, q, q_stride, B, Hq, block_table, table_width, seq_lens, scale, window, out, lse, workspace,
                 workspace_bytes, stream);
 }

@@ -1,0 +1,432 @@
+// One warp's keys of a piece of paged attention (attention.cu) over an NVFP4 cache.
+//
+// Row operands from registers. Lane (r, c) = (lane / 4, lane % 4) of a 16-key tile takes D/4 consecutive elements of
+// keys r and r + 8 as the row operand of k q^T, and D/8 consecutive elements, from r D/8 on, of keys 2c, 2c + 1,
+// 2c + 8 and 2c + 9 as that of v^T p^T: whole words of codes under one scale or two. Products do not care which
+// element is which column (q is laid out to match), nor which key is which row.
+#pragma once
+
+#include <cmath>
+
+#include "ftmoe_internal.h"
+#include "ftmoe_mma.cuh"
+#include "ftmoe_tc.cuh"
+
+namespace ftmoe {
+
+// Which key of a tile is its row i (0 <= i < 8; 8 + i follows), and where the 16-byte pieces of a row lie: so that
+// the rows of k that eight lanes read at once, and the pieces of v, find 32 banks.
+template <int D>
+__device__ __forceinline__ int key_of_row(int i) {
+  return D == 64 ? i ^ (i >> 2) : D == 128 ? i ^ ((i >> 1) & 1) : i;
+}
+template <int D>
+__device__ __forceinline__ int piece4(int row, int ch) {   // offset of 16-byte piece ch of a row
+  return row * (D / 2) + (D == 64 ? ch : D == 128 ? ch ^ (2 * ((row >> 2) & 1)) : ch ^ (row & 7)) * 16;
+}
+
+// N bytes (4, 8 or 16) from global to shared memory; zeros (and no access) when !valid.
+template <int N>
+__device__ __forceinline__ void cp_async_scales(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(valid ? N : 0)
+               : "memory");
+}
+
+// Pairs of floats.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair_mul(uint64_t x, uint64_t y) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair_add(uint64_t x, uint64_t y) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {   // an 8 x 8 matrix of 16-bit elements
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Four E4M3 bytes -> f16x2 of the lower two and of the upper two, exact.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(v));
+}
+
+// W words from shared memory.
+template <int W>
+__device__ __forceinline__ void words(uint32_t (&v)[W], const char* p) {
+  if constexpr (W == 1) {
+    v[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (W == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    v[0] = x.x; v[1] = x.y;
+  } else {
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+  }
+}
+
+// The scales of lane c's elements of a key, each in both halves of a word.
+template <int D>
+__device__ __forceinline__ void key_scales(uint32_t (&s)[D / 64], const char* row, int c) {
+  if constexpr (D == 64) {
+    s[0] = splat_lo(e4m3x2_to_f16x2(*reinterpret_cast<const uint8_t*>(row + c)));
+  } else if constexpr (D == 128) {
+    const uint32_t v = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(row + 2 * c));
+    s[0] = splat_lo(v);
+    s[1] = splat_hi(v);
+  } else {
+    uint32_t lo, hi;
+    e4m3x4_to_f16(*reinterpret_cast<const uint32_t*>(row + 4 * c), lo, hi);
+    s[0] = splat_lo(lo);
+    s[1] = splat_hi(lo);
+    s[2] = splat_lo(hi);
+    s[3] = splat_hi(hi);
+  }
+}
+// The scales of lane r's elements of two values, the first one's in the lower half of a word.
+template <int D>
+__device__ __forceinline__ void value_scales(uint32_t (&s)[D == 256 ? 2 : 1], const char* row0, const char* row1, int r) {
+  if constexpr (D == 256) {
+    const uint32_t x = *reinterpret_cast<const uint16_t*>(row0 + 2 * r);
+    const uint32_t y = *reinterpret_cast<const uint16_t*>(row1 + 2 * r);
+    s[0] = e4m3x2_to_f16x2(__byte_perm(x, y, 0x0040));
+    s[1] = e4m3x2_to_f16x2(__byte_perm(x, y, 0x0051));
+  } else {
+    const int at = D == 64 ? r >> 1 : r;
+    const uint32_t x = *reinterpret_cast<const uint8_t*>(row0 + at), y = *reinterpret_cast<const uint8_t*>(row1 + at);
+    s[0] = e4m3x2_to_f16x2(x | y << 8);
+  }
+}
+
+// A weight is at most 2^kTop4, and the largest of a head's is set to 2^kSet4 where the running maximum is set anew,
+// which is when one would pass 2^kTop4: few steps after the first do, and the others need no maximum over the
+// lanes. One f16 holds 11 bits of weights down to 2^-14, 2^-24 of the largest, and nothing under 2^-25.
+constexpr float kTop4 = 15.f, kSet4 = 10.f;
+
+// Steps of S::kKeys keys, key0 + i * unit on, up to key1 (and from `first` on). Leaves the warp's o^T, running
+// maximum (log2, less kSet4 or so) and sums of weights of heads 2c and 2c + 1 over this lane's rows.
+template <int D, int NG, class S>
+__device__ __forceinline__ void attend_piece4(const AttendArgs& a, char* ring, int b, int kvh, int g0, int G, int first,
+                                              int key0, int key1, int unit, int n_sub, float (&o)[NG][D / 16][4],
+                                              float (&m)[NG][2], float (&l)[NG][2]) {
+  constexpr int KT = S::kKeys, NH = KT / 16, ST = S::kStages, KS = D / 16, ROW = D / 2, SROW = D / 16;
+  constexpr int V = KT * ROW, KSC = 2 * V, VSC = KSC + KT * SROW;   // values, scales of a stage
+  const int lane = threadIdx.x & 31, c = lane & 3, r = lane >> 2;
+  const int32_t* table = a.block_table + (int64_t)b * a.table_width;
+
+  // ---- copies: lane l looks after key l of a step
+  // offsets of rows in 16-byte pieces, of scales in rows of them: 32 bits (checked on the host)
+  const uint32_t head_k = (uint32_t)(kvh * (a.kv.k_head_stride >> 4)), head_v = (uint32_t)(kvh * (a.kv.v_head_stride >> 4));
+  const uint32_t head_ks = (uint32_t)(kvh * (a.sc.k_head / SROW)), head_vs = (uint32_t)(kvh * (a.sc.v_head / SROW));
+  int page = -1, slot = 0;
+  bool live = false;
+  auto look_up = [&](int i) {
+    const int j = key0 + i * unit + lane;
+    live = i < n_sub && j >= first && j < key1;
+    page = -1;
+    if (live) {
+      const int col = (int)((__umulhi((uint32_t)a.div_mul, (uint32_t)j) + (uint32_t)j) >> a.div_shift);
+      slot = j - col * a.kv.page_size;
+      page = table[col];   // col < table_width: the length is cut to the table
+    }
+  };
+  constexpr int CPR = ROW / 16, RPI = 32 / CPR;   // 16-byte pieces of a row, rows of one warp-wide copy
+  const int ch = lane % CPR;
+  const char* const kb = static_cast<const char*>(a.kv.k) + ch * 16;
+  const char* const vb = static_cast<const char*>(a.kv.v) + ch * 16;
+  const uint32_t to0 = smem_addr(ring);
+  auto fetch = [&](int i, uint32_t stage) {   // the copies of step i, whose pages look_up has found
+    if (i < n_sub) {
+      const bool in = (uint32_t)page < (uint32_t)a.kv.num_pages;
+      if (live && !in) atomicOr(a.err, kErrBadPage);   // no such page: read as zeros
+      const uint32_t p = in ? (uint32_t)page : 0u, s = in ? (uint32_t)slot : 0u;
+      const uint32_t st = to0 + stage;
+      const uint32_t ko = p * (uint32_t)(a.kv.k_page_stride >> 4) + s * (uint32_t)(a.kv.k_slot_stride >> 4) + head_k;
+      const uint32_t kso = p * (uint32_t)(a.sc.k_page / SROW) + s * (uint32_t)(a.sc.k_slot / SROW) + head_ks;
+      uint32_t vo = ko, vso = kso;
+      if (!a.same_strides) {
+        vo = p * (uint32_t)(a.kv.v_page_stride >> 4) + s * (uint32_t)(a.kv.v_slot_stride >> 4) + head_v;
+        vso = p * (uint32_t)(a.sc.v_page / SROW) + s * (uint32_t)(a.sc.v_slot / SROW) + head_vs;
+      }
+      cp_async_scales<SROW>(st + KSC + lane * SROW, a.sc.k + (uint64_t)kso * SROW, in);
+      cp_async_scales<SROW>(st + VSC + lane * SROW, a.sc.v + (uint64_t)vso * SROW, in);
+      const uint32_t rows_in = __ballot_sync(0xffffffffu, in);
+#pragma unroll
+      for (int x = 0; x < KT / RPI; ++x) {
+        const int row = x * RPI + lane / CPR;
+        const uint32_t k_at = __shfl_sync(0xffffffffu, ko, row);
+        const uint32_t v_at = a.same_strides ? k_at : __shfl_sync(0xffffffffu, vo, row);
+        const bool on = rows_in >> row & 1;
+        const uint32_t to = st + piece4<D>(row, ch);
+        cp_async16(to, kb + (uint64_t)k_at * 16, on);
+        cp_async16(to + V, vb + (uint64_t)v_at * 16, on);
+      }
+    }
+    cp_async_commit();
+  };
+  look_up(0);
+#pragma unroll
+  for (int i = 0; i < ST - 1; ++i) {
+    fetch(i, i * S::kStageBytes);
+    look_up(i + 1);
+  }
+
+  // ---- q as the column operand, f16 after a power of two: column l / 4 of group g is head 8 g + l / 4. The
+  // sign of the scale goes into q, so that a larger product is a larger score.
+  uint32_t q[NG][KS][2];
+  uint64_t sl[NG];   // log2 units per unit of the raw product, heads 8 g + 2 c, + 1
+  {
+    const uint16_t* qb = a.q + (int64_t)b * a.q_stride + (int64_t)(kvh * a.group + g0) * D;
+    const float unit_s = fabsf(a.scale) * a.kv.k_scale * 1.4426950408889634f;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const bool on = 8 * g + r < G;
+      const uint16_t* qh = qb + (8 * g + r) * D + D / 4 * c;
+      float top = 0.f, up, down;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint2 v = make_uint2(0, 0);
+        if (on) v = *reinterpret_cast<const uint2*>(qh + 4 * ks);
+        q[g][ks][0] = v.x;
+        q[g][ks][1] = v.y;
+        top = fmaxf(top, finite_top(v.x, v.y));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      f16_scale(top, up, down);
+      if (a.scale < 0.f) up = -up;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) q[g][ks][e] = pack_f16(bf16_lo(q[g][ks][e]) * up, bf16_hi(q[g][ks][e]) * up);
+      sl[g] = pair(unit_s * __shfl_sync(0xffffffffu, down, 8 * c),   // head 2 c: lanes 8 c ..
+                   unit_s * __shfl_sync(0xffffffffu, down, 8 * c + 4));
+    }
+  }
+
+  uint64_t less[NG], sum[NG];   // - the running maximum (0 without one), sums of weights
+  float bar[NG][2];             // scores past it set the maximum anew
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    less[g] = sum[g] = 0;
+    bar[g][0] = bar[g][1] = -INFINITY;
+  }
+  float s[NG][NH][4];
+  uint32_t p[NG][NH][2];   // p^T: columns heads, rows keys 0-7 and 8-15 of a tile
+
+  // s^T = k q^T of a stage
+  const int krow = key_of_row<D>(r);
+  auto products = [&](const char* st) {
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      constexpr int NW = D / 32;   // words of a lane's elements of a key
+      uint32_t k0[NW], k1[NW], s0[D / 64], s1[D / 64];
+      const int row = 16 * h + krow;
+      if constexpr (D == 64) {
+        words(k0, st + piece4<D>(row, c >> 1) + (c & 1) * 8);
+        words(k1, st + piece4<D>(row + 8, c >> 1) + (c & 1) * 8);
+      } else {
+#pragma unroll
+        for (int x = 0; x < NW / 4; ++x) {
+          uint32_t t0[4], t1[4];
+          words(t0, st + piece4<D>(row, NW / 4 * c + x));
+          words(t1, st + piece4<D>(row + 8, NW / 4 * c + x));
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            k0[4 * x + y] = t0[y];
+            k1[4 * x + y] = t1[y];
+          }
+        }
+      }
+      key_scales<D>(s0, st + KSC + row * SROW, c);
+      key_scales<D>(s1, st + KSC + (row + 8) * SROW, c);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) s[g][h][0] = s[g][h][1] = s[g][h][2] = s[g][h][3] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NW; ++j) {
+        uint32_t x[4], y[4];
+        e2m1x8_to_f16x2x4(k0[j], x[0], x[1], x[2], x[3]);
+        e2m1x8_to_f16x2x4(k1[j], y[0], y[1], y[2], y[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {   // exact: six significant bits
+          x[e] = hmul2(x[e], s0[j / 2]);
+          y[e] = hmul2(y[e], s1[j / 2]);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+            mma_f16(s[g][h], x[2 * e], y[2 * e], x[2 * e + 1], y[2 * e + 1], q[g][2 * j + e][0], q[g][2 * j + e][1]);
+      }
+    }
+  };
+
+  // weights of the scores of step i: key j0 + 16 h + row r (elements 0, 1) and + 8
+  auto weigh = [&](int i) {
+    const int j0 = key0 + i * unit;
+    uint64_t x[NG][NH][2];
+    bool past = false;
+    float top[NG][2];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        x[g][h][0] = pair_mul(pair(s[g][h][0], s[g][h][1]), sl[g]);
+        x[g][h][1] = pair_mul(pair(s[g][h][2], s[g][h][3]), sl[g]);
+      }
+    }
+    if (j0 < first || j0 + KT > key1) {   // keys outside do not count
+#pragma unroll
+      for (int h = 0; h < NH; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = j0 + 16 * h + krow + 8 * e;
+          if (j < first || j >= key1) {
+#pragma unroll
+            for (int g = 0; g < NG; ++g) x[g][h][e] = pair(-INFINITY, -INFINITY);
+          }
+        }
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      top[g][0] = top[g][1] = -INFINITY;
+#pragma unroll
+      for (int h = 0; h < NH; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 v = unpair(x[g][h][e]);
+          top[g][0] = fmaxf(top[g][0], v.x);
+          top[g][1] = fmaxf(top[g][1], v.y);
+        }
+      past |= top[g][0] > bar[g][0] || top[g][1] > bar[g][1];
+    }
+    if (__any_sync(0xffffffffu, past)) {   // a new maximum: what is summed shrinks
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        float f[2], n[2];
+        const float2 was = unpair(less[g]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float t = top[g][e];
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
+          const bool none = bar[g][e] == -INFINITY;
+          const float old = e ? -was.y : -was.x;
+          t = __fsub_ru(t, kSet4);   // upwards: no weight above 2^kSet4 at any size of t
+          n[e] = none ? t : fmaxf(old, t);
+          f[e] = none ? 0.f : exp2_fast(old - n[e]);
+          bar[g][e] = n[e] + kTop4;
+          if (n[e] == -INFINITY) n[e] = 0.f;   // no key yet: every weight is 0
+        }
+        less[g] = pair(-n[0], -n[1]);
+        sum[g] = pair_mul(sum[g], pair(f[0], f[1]));
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t) {
+          o[g][t][0] *= f[0]; o[g][t][1] *= f[1];
+          o[g][t][2] *= f[0]; o[g][t][3] *= f[1];
+        }
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int h = 0; h < NH; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 v = unpair(pair_add(x[g][h][e], less[g]));
+          const float w0 = exp2_fast(v.x), w1 = exp2_fast(v.y);
+          sum[g] = pair_add(sum[g], pair(w0, w1));
+          p[g][h][e] = transpose8(pack_f16(w0, w1));
+        }
+  };
+
+  // o^T += v^T p^T of a stage
+  const int vrow0 = key_of_row<D>(2 * c), vrow1 = key_of_row<D>(2 * c + 1);
+  auto add_values = [&](const char* st) {
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      constexpr int NW = D / 64;   // words of a lane's elements of a value
+      constexpr int NS = D == 256 ? 2 : 1;
+      uint32_t v[4][NW], s01[NS], s89[NS];   // keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9
+      const int rows[4] = {16 * h + vrow0, 16 * h + vrow1, 16 * h + vrow0 + 8, 16 * h + vrow1 + 8};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) words(v[x], st + V + piece4<D>(rows[x], D * r / 256) + (D * r / 16 & 15));
+      const char* sc = st + VSC;
+      value_scales<D>(s01, sc + rows[0] * SROW, sc + rows[1] * SROW, r);
+      value_scales<D>(s89, sc + rows[2] * SROW, sc + rows[3] * SROW, r);
+#pragma unroll
+      for (int j = 0; j < NW; ++j) {
+        // elements 2 i (a0, a2) and 2 i + 1 (a1, a3) of two keys in byte i of a word
+        uint32_t a0[4], a1[4], a2[4], a3[4];
+        const uint32_t lo = 0x0F0F0F0Fu;
+        e2m1x8_to_f16x2x4((v[0][j] & lo) | (v[1][j] << 4 & ~lo), a0[0], a0[1], a0[2], a0[3]);
+        e2m1x8_to_f16x2x4((v[0][j] >> 4 & lo) | (v[1][j] & ~lo), a1[0], a1[1], a1[2], a1[3]);
+        e2m1x8_to_f16x2x4((v[2][j] & lo) | (v[3][j] << 4 & ~lo), a2[0], a2[1], a2[2], a2[3]);
+        e2m1x8_to_f16x2x4((v[2][j] >> 4 & lo) | (v[3][j] & ~lo), a3[0], a3[1], a3[2], a3[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t b0 = hmul2(a0[e], s01[j / 2]), b1 = hmul2(a1[e], s01[j / 2]);
+          const uint32_t b2 = hmul2(a2[e], s89[j / 2]), b3 = hmul2(a3[e], s89[j / 2]);
+#pragma unroll
+          for (int g = 0; g < NG; ++g) mma_f16(o[g][4 * j + e], b0, b1, b2, b3, p[g][h][0], p[g][h][1]);
+        }
+      }
+    }
+  };
+
+  // the products of step i + 1 beside the values of step i
+  if (n_sub > 0) {
+    cp_async_wait<ST - 2>();
+    __syncwarp();
+    products(ring);
+    weigh(0);
+    uint32_t at = 0, to = (ST - 1) * S::kStageBytes;   // stage of step i; of step i + ST - 1
+    constexpr uint32_t END = ST * S::kStageBytes;
+    for (int i = 0; i + 1 < n_sub; ++i) {
+      // these copies go into the stage whose values the last turn added
+      __syncwarp();
+      fetch(i + ST - 1, to);
+      look_up(i + ST);
+      to = to + S::kStageBytes == END ? 0 : to + S::kStageBytes;
+      const uint32_t next = at + S::kStageBytes == END ? 0 : at + S::kStageBytes;
+      cp_async_wait<ST - 2>();
+      __syncwarp();
+      products(ring + next);
+      add_values(ring + at);
+      weigh(i + 1);
+      at = next;
+    }
+    add_values(ring + at);
+  }
+  cp_async_wait<0>();
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    const float2 n = unpair(less[g]), w = unpair(sum[g]);
+    m[g][0] = bar[g][0] == -INFINITY ? -INFINITY : -n.x;
+    m[g][1] = bar[g][1] == -INFINITY ? -INFINITY : -n.y;
+    l[g][0] = w.x;
+    l[g][1] = w.y;
+  }
+}
+
+}  // namespace ftmoe
