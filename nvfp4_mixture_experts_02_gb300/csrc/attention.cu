@@ -57,13 +57,16 @@ struct AttnShape {
   // blocks an SM: the others stream while one joins a piece's warps. Three of two stages each, not two of
   // three, where the registers allow it: 256 sequences up to 1024 with 8-bit keys of 128: 68 us for 79.
   // (Past some 2600 sequences their running sums in shared memory leave room for two.)
-  static constexpr int kBlocks = kRow >= 512 ? 1 : (DT == kKvNvfp4 ? D == 128 : kRow == 128) && NG == 1 ? kAttendBlocks : 2;
-  static constexpr int kWarps = (DT == kKvNvfp4 ? D >= 128 : kRow >= 128) ? 4 : 8;
-  static constexpr int kStages = 192 * 1024 / (kBlocks * kWarps * kStageBytes);
+  static constexpr int kBlocks =
+      kRow >= 512 || DT == kKvNvfp4 ? 1 : kRow == 128 && NG == 1 ? kAttendBlocks : 2;
+  // NVFP4: one block an SM, whose groups of warps each do what a block does otherwise
+  static constexpr int kGroups = DT != kKvNvfp4 ? 1 : D == 128 && NG == 1 ? kAttendBlocks : 2;
+  static constexpr int kWarps = (DT == kKvNvfp4 ? D >= 128 : kRow >= 128) ? 4 : 8;   // of a group
+  static constexpr int kStages = 192 * 1024 / (kBlocks * kGroups * kWarps * kStageBytes);
   static constexpr int kUnit = kKeys * kWarps;        // keys of a unit
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kSumsLd = D + 4;               // floats between heads of a warp's sums, in its ring
-  static_assert(8 * NG * kSumsLd * 4 <= kStages * kStageBytes && kBlocks * kWarps <= attend_warps(D));
+  static_assert(8 * NG * kSumsLd * 4 <= kStages * kStageBytes && kBlocks * kGroups * kWarps <= attend_warps(D));
 };
 
 // From this many units in a run, the warps of a block take several key heads at once instead of stripes of
@@ -111,7 +114,8 @@ __device__ __forceinline__ void span(int len, int window, int unit, int& first, 
 }
 
 template <int D, int DT, int NG>
-__global__ void __launch_bounds__(AttnShape<D, DT, NG>::kWarps * 32, AttnShape<D, DT, NG>::kBlocks)
+__global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, DT, NG>::kWarps * 32,
+                                  AttnShape<D, DT, NG>::kBlocks)
     k_attend(const AttendArgs a) {
   using S = AttnShape<D, DT, NG>;
   constexpr bool F4 = DT == kKvNvfp4, F16 = DT != FT_KV_BF16;   // f16 products
@@ -121,12 +125,20 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kWarps * 32, AttnShape<D
   constexpr int kUnitLog2 = S::kUnit == 64 ? 6 : S::kUnit == 128 ? 7 : 8;
   static_assert(S::kUnit == 1 << kUnitLog2);
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ float wm[W][16], wl[W][16], share[W][16];
-  __shared__ int scan[W];
-  int* cum = reinterpret_cast<int*>(smem + S::kRing);   // [B + 1] units before each sequence (B > 32)
+  constexpr int GR = S::kGroups;
+  __shared__ float all_wm[GR * W][16], all_wl[GR * W][16], all_share[GR * W][16];
+  __shared__ int scan[GR * W];
+  int* cum = reinterpret_cast<int*>(smem + GR * S::kRing);   // [B + 1] units before each sequence (B > 32)
   griddep_launch_dependents();
   griddep_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
+  const int group = GR > 1 ? (int)threadIdx.x / (W * 32) : 0;
+  const int warp = (int)(threadIdx.x >> 5) - group * W, tid = threadIdx.x - group * W * 32;   // in the group
+  const int block = (int)(blockIdx.x + group * gridDim.x), blocks = (int)gridDim.x * GR;   // groups stand for blocks
+  float (*const wm)[16] = all_wm + group * W;
+  float (*const wl)[16] = all_wl + group * W;
+  float (*const share)[16] = all_share + group * W;
+  unsigned char* const rings = smem + group * S::kRing;
   const int c = lane & 3, r = lane >> 2;
   const int HS = a.kv.Hkv * a.gt;   // segments of a sequence
 
@@ -138,7 +150,7 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kWarps * 32, AttnShape<D
     if (lane < a.B) {
       const int len = length_of(a, lane);
       span(len, a.window, S::kUnit, first, n);
-      if (blockIdx.x == 0 && warp == 0 && a.seq_lens[lane] > len) atomicOr(a.err, kErrBadPage);
+      if (block == 0 && warp == 0 && a.seq_lens[lane] > len) atomicOr(a.err, kErrBadPage);
     }
     inc = n;
 #pragma unroll
@@ -148,7 +160,7 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kWarps * 32, AttnShape<D
     }
     all = __shfl_sync(0xffffffffu, inc, 31);
   } else {
-    const int per = (a.B + W * 32 - 1) / (W * 32);
+    const int per = (a.B + GR * W * 32 - 1) / (GR * W * 32);
     const int b0 = threadIdx.x * per;
     int mine = 0;
     for (int b = b0; b < min(b0 + per, a.B); ++b) {
@@ -164,10 +176,10 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kWarps * 32, AttnShape<D
       const int v = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += v;
     }
-    if (lane == 31) scan[warp] = upto;
+    if (lane == 31) scan[threadIdx.x >> 5] = upto;
     __syncthreads();
     int at = upto - mine;
-    for (int w = 0; w < warp; ++w) at += scan[w];
+    for (int w = 0; w < (int)(threadIdx.x >> 5); ++w) at += scan[w];
     for (int b = b0; b < min(b0 + per, a.B); ++b) {
       int first, n;
       span(length_of(a, b), a.window, S::kUnit, first, n);
@@ -179,19 +191,20 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kWarps * 32, AttnShape<D
     all = cum[a.B];
   }
   const int64_t total = (int64_t)all * HS;
-  const int64_t quota = (total + gridDim.x - 1) / gridDim.x;
-  int64_t u = quota * blockIdx.x;
+  const int64_t quota = (total + blocks - 1) / blocks;
+  int64_t u = quota * block;
   const int64_t u_end = min(u + quota, total);
-  const uint32_t ring = smem_addr(smem) + (uint32_t)(warp * ST * S::kStageBytes);
+  const uint32_t ring = smem_addr(rings) + (uint32_t)(warp * ST * S::kStageBytes);
   // HW heads a block, W / HW stripes of keys each
   const int hl = quota >= kLongRun ? a.heads_log2 : 0, HW = 1 << hl, stripes = W >> hl;
   const int hw = warp & (HW - 1), stripe = warp >> hl;
   const int unit = S::kUnit >> hl;
   auto sync = [&]() {   // the warps that share a head
     if (stripes == 1) __syncwarp();
-    else __syncthreads();
+    else if constexpr (GR == 1) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(W * 32) : "memory");
   };
-  if (u >= u_end && threadIdx.x == 0) a.shared_segs[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (u >= u_end && tid == 0) a.shared_segs[block] = make_int4(-1, 0, 0, 0);
 
   while (u < u_end) {
     // the piece that begins at u: sequence b, with `before` units ahead of it
@@ -221,10 +234,10 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kWarps * 32, AttnShape<D
     const int hs = hg * HW + hw;
     const int kvh = hs / a.gt, g0 = (hs - kvh * a.gt) * 16;
     const int G = min(a.group - g0, 16);
-    if (u == quota * blockIdx.x && threadIdx.x == 0) {
+    if (u == quota * block && tid == 0) {
       // for k_join: the segment that this run goes on with, if it does not begin here
       const int64_t s0 = u - u0, s1 = s0 + cost;
-      a.shared_segs[blockIdx.x] =
+      a.shared_segs[block] =
           make_int4(u0 > 0 ? b : -1, hg * 16 + hl, (int)(s0 / quota) * 2 + (s0 % quota != 0),
                     (int)((s1 - 1) / quota));
     }
@@ -241,7 +254,7 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kWarps * 32, AttnShape<D
       l[g][0] = l[g][1] = 0.f;
     }
     if constexpr (F4) {
-      attend_piece4<D, NG, S>(a, reinterpret_cast<char*>(smem) + warp * ST * S::kStageBytes, b, kvh, g0, G, first, key0, key1,
+      attend_piece4<D, NG, S>(a, reinterpret_cast<char*>(rings) + warp * ST * S::kStageBytes, b, kvh, g0, G, first, key0, key1,
                               unit, n_sub, o, m, l);
     } else {
     const int32_t* table = a.block_table + (int64_t)b * a.table_width;
@@ -498,7 +511,7 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kWarps * 32, AttnShape<D
 
     // ---- join the warps of a head: sums [head][LD] in each one's ring
     sync();
-    float* sums = reinterpret_cast<float*>(smem + (size_t)warp * ST * S::kStageBytes);
+    float* sums = reinterpret_cast<float*>(rings + (size_t)warp * ST * S::kStageBytes);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
 #pragma unroll
@@ -537,7 +550,7 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kWarps * 32, AttnShape<D
     }
     sync();
     const bool whole = n_units == cost;
-    const int64_t part = ((2 * (int64_t)blockIdx.x + (u == quota * blockIdx.x ? 0 : 1)) * W + hw) * 16;
+    const int64_t part = ((2 * (int64_t)block + (u == quota * block ? 0 : 1)) * W + hw) * 16;
     const int64_t row = (int64_t)b * a.Hq + kvh * a.group + g0;
     if (lane < G && stripe == 0) {
       if (!whole) *reinterpret_cast<float2*>(a.part_ml + (part + lane) * 2) = ms;
@@ -554,7 +567,7 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kWarps * 32, AttnShape<D
         const int w = hw + (s << hl);
         const float f = share[w][g];
         const float4 y = *reinterpret_cast<const float4*>(
-            reinterpret_cast<const float*>(smem + (size_t)w * ST * S::kStageBytes) + g * LD + d);
+            reinterpret_cast<const float*>(rings + (size_t)w * ST * S::kStageBytes) + g * LD + d);
         v.x = fmaf(f, y.x, v.x); v.y = fmaf(f, y.y, v.y);
         v.z = fmaf(f, y.z, v.z); v.w = fmaf(f, y.w, v.w);
       }
@@ -571,9 +584,9 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kWarps * 32, AttnShape<D
 // to kTeam warps, more where the pieces are many and the jobs few: each adds a share of the pieces in
 // order, the first of them adds the shares in order. The blocks also zero the heads of empty sequences. W:
 // warps of k_attend's blocks.
-constexpr int kJoinWarps = 16, kTeam = 8;   // warps of a block, of a job at most
+constexpr int kTeam = 8;                    // warps of a job at most
 constexpr int kFlight = 4;                  // pieces of a warp in flight
-template <int D, int W>
+template <int D, int W, int kJoinWarps>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_join(const AttendArgs a) {
   constexpr int E = D / 32;
   __shared__ float sums[kJoinWarps][D], wm[kJoinWarps], wl[kJoinWarps];
@@ -683,14 +696,13 @@ cudaError_t launch_d(AttendArgs a, int num_sms, cudaStream_t stream) {
   using S = AttnShape<D, DT, NG>;
   a.heads_log2 = 0;
   while (2 << a.heads_log2 <= S::kWarps && a.kv.Hkv * a.gt % (2 << a.heads_log2) == 0) ++a.heads_log2;
-  const size_t smem = S::kRing + (a.B > 32 ? (size_t)(a.B + 1) * 4 : 0);
+  const size_t smem = S::kGroups * S::kRing + (a.B > 32 ? (size_t)(a.B + 1) * 4 : 0);
   cudaError_t e;
   static SmemGrant grant;   // for the most sequences that a call may have
-  if ((e = grant_smem(grant, k_attend<D, DT, NG>, S::kRing + 4 * (kMaxSeqs + 1))) != cudaSuccess) return e;
+  if ((e = grant_smem(grant, k_attend<D, DT, NG>, S::kGroups * S::kRing + 4 * (kMaxSeqs + 1))) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  const int grid = S::kBlocks * num_sms;
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(S::kWarps * 32);
+  cfg.gridDim = dim3((unsigned)(S::kBlocks * num_sms));
+  cfg.blockDim = dim3(S::kGroups * S::kWarps * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -699,9 +711,13 @@ cudaError_t launch_d(AttendArgs a, int num_sms, cudaStream_t stream) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, k_attend<D, DT, NG>, a)) != cudaSuccess) return e;
+  // Warps of a block of k_join. NVFP4: eight, so that all blocks run at once (48 ragged sequences 58.2 us, 60.5 with
+  // sixteen; one of 777 keys 6.8 us with either).
+  constexpr int kJoinWarps = DT == kKvNvfp4 ? 8 : 16;
+  cfg.gridDim = dim3((unsigned)(S::kBlocks * S::kGroups * num_sms));   // a block for every run
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, k_join<D, S::kWarps>, a);
+  return cudaLaunchKernelEx(&cfg, k_join<D, S::kWarps, kJoinWarps>, a);
 }
 
 template <int D, int DT>

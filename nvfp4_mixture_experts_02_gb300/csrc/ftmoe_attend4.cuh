@@ -32,6 +32,11 @@ __device__ __forceinline__ void cp_async_scales(uint32_t dst, const void* src, b
                : "memory");
 }
 
+// 16 bytes from global to shared memory, past L1.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // Pairs of floats.
 __device__ __forceinline__ uint64_t pair(float x, float y) {
   uint64_t d;
@@ -71,6 +76,16 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t v, uint32_t& lo, uint32_t
       : "=r"(lo), "=r"(hi) : "r"(v));
 }
 
+// x times the lower (upper) half of s.
+__device__ __forceinline__ uint32_t hmul2_lo(uint32_t x, uint32_t s) {
+  const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&x), __low2half2(*reinterpret_cast<__half2*>(&s)));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+__device__ __forceinline__ uint32_t hmul2_hi(uint32_t x, uint32_t s) {
+  const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&x), __high2half2(*reinterpret_cast<__half2*>(&s)));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+
 // W words from shared memory.
 template <int W>
 __device__ __forceinline__ void words(uint32_t (&v)[W], const char* p) {
@@ -85,23 +100,12 @@ __device__ __forceinline__ void words(uint32_t (&v)[W], const char* p) {
   }
 }
 
-// The scales of lane c's elements of a key, each in both halves of a word.
+// The scales of lane c's elements of a key, two in a word (with heads of 64: one).
 template <int D>
-__device__ __forceinline__ void key_scales(uint32_t (&s)[D / 64], const char* row, int c) {
-  if constexpr (D == 64) {
-    s[0] = splat_lo(e4m3x2_to_f16x2(*reinterpret_cast<const uint8_t*>(row + c)));
-  } else if constexpr (D == 128) {
-    const uint32_t v = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(row + 2 * c));
-    s[0] = splat_lo(v);
-    s[1] = splat_hi(v);
-  } else {
-    uint32_t lo, hi;
-    e4m3x4_to_f16(*reinterpret_cast<const uint32_t*>(row + 4 * c), lo, hi);
-    s[0] = splat_lo(lo);
-    s[1] = splat_hi(lo);
-    s[2] = splat_lo(hi);
-    s[3] = splat_hi(hi);
-  }
+__device__ __forceinline__ void key_scales(uint32_t (&s)[D == 256 ? 2 : 1], const char* row, int c) {
+  if constexpr (D == 64) s[0] = e4m3x2_to_f16x2(*reinterpret_cast<const uint8_t*>(row + c));
+  else if constexpr (D == 128) s[0] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(row + 2 * c));
+  else e4m3x4_to_f16(*reinterpret_cast<const uint32_t*>(row + 4 * c), s[0], s[1]);
 }
 // The scales of lane r's elements of two values, the first one's in the lower half of a word.
 template <int D>
@@ -136,8 +140,6 @@ __device__ __forceinline__ void attend_piece4(const AttendArgs& a, char* ring, i
 
   // ---- copies: lane l looks after key l of a step
   // offsets of rows in 16-byte pieces, of scales in rows of them: 32 bits (checked on the host)
-  const uint32_t head_k = (uint32_t)(kvh * (a.kv.k_head_stride >> 4)), head_v = (uint32_t)(kvh * (a.kv.v_head_stride >> 4));
-  const uint32_t head_ks = (uint32_t)(kvh * (a.sc.k_head / SROW)), head_vs = (uint32_t)(kvh * (a.sc.v_head / SROW));
   int page = -1, slot = 0;
   bool live = false;
   auto look_up = [&](int i) {
@@ -152,34 +154,44 @@ __device__ __forceinline__ void attend_piece4(const AttendArgs& a, char* ring, i
   };
   constexpr int CPR = ROW / 16, RPI = 32 / CPR;   // 16-byte pieces of a row, rows of one warp-wide copy
   const int ch = lane % CPR;
-  const char* const kb = static_cast<const char*>(a.kv.k) + ch * 16;
-  const char* const vb = static_cast<const char*>(a.kv.v) + ch * 16;
+  const char* const kb = static_cast<const char*>(a.kv.k) + kvh * a.kv.k_head_stride + ch * 16;
+  const char* const vb = static_cast<const char*>(a.kv.v) + kvh * a.kv.v_head_stride + ch * 16;
+  const uint8_t *const ksb = a.sc.k + kvh * a.sc.k_head, *const vsb = a.sc.v + kvh * a.sc.v_head;
   const uint32_t to0 = smem_addr(ring);
   auto fetch = [&](int i, uint32_t stage) {   // the copies of step i, whose pages look_up has found
     if (i < n_sub) {
       const bool in = (uint32_t)page < (uint32_t)a.kv.num_pages;
       if (live && !in) atomicOr(a.err, kErrBadPage);   // no such page: read as zeros
+      // A key that is not there has codes and scales of zero.
       const uint32_t p = in ? (uint32_t)page : 0u, s = in ? (uint32_t)slot : 0u;
       const uint32_t st = to0 + stage;
-      const uint32_t ko = p * (uint32_t)(a.kv.k_page_stride >> 4) + s * (uint32_t)(a.kv.k_slot_stride >> 4) + head_k;
-      const uint32_t kso = p * (uint32_t)(a.sc.k_page / SROW) + s * (uint32_t)(a.sc.k_slot / SROW) + head_ks;
+      const uint32_t ko = p * (uint32_t)(a.kv.k_page_stride >> 4) + s * (uint32_t)(a.kv.k_slot_stride >> 4);
+      const uint32_t kso = p * (uint32_t)(a.sc.k_page / SROW) + s * (uint32_t)(a.sc.k_slot / SROW);
       uint32_t vo = ko, vso = kso;
       if (!a.same_strides) {
-        vo = p * (uint32_t)(a.kv.v_page_stride >> 4) + s * (uint32_t)(a.kv.v_slot_stride >> 4) + head_v;
-        vso = p * (uint32_t)(a.sc.v_page / SROW) + s * (uint32_t)(a.sc.v_slot / SROW) + head_vs;
+        vo = p * (uint32_t)(a.kv.v_page_stride >> 4) + s * (uint32_t)(a.kv.v_slot_stride >> 4);
+        vso = p * (uint32_t)(a.sc.v_page / SROW) + s * (uint32_t)(a.sc.v_slot / SROW);
       }
-      cp_async_scales<SROW>(st + KSC + lane * SROW, a.sc.k + (uint64_t)kso * SROW, in);
-      cp_async_scales<SROW>(st + VSC + lane * SROW, a.sc.v + (uint64_t)vso * SROW, in);
-      const uint32_t rows_in = __ballot_sync(0xffffffffu, in);
+      cp_async_scales<SROW>(st + KSC + lane * SROW, ksb + (uint64_t)kso * SROW, in);
+      cp_async_scales<SROW>(st + VSC + lane * SROW, vsb + (uint64_t)vso * SROW, in);
+      const uint32_t rows = __ballot_sync(0xffffffffu, in);
+      if (rows == 0xffffffffu && a.same_strides) {   // as a rule
 #pragma unroll
-      for (int x = 0; x < KT / RPI; ++x) {
-        const int row = x * RPI + lane / CPR;
-        const uint32_t k_at = __shfl_sync(0xffffffffu, ko, row);
-        const uint32_t v_at = a.same_strides ? k_at : __shfl_sync(0xffffffffu, vo, row);
-        const bool on = rows_in >> row & 1;
-        const uint32_t to = st + piece4<D>(row, ch);
-        cp_async16(to, kb + (uint64_t)k_at * 16, on);
-        cp_async16(to + V, vb + (uint64_t)v_at * 16, on);
+        for (int x = 0; x < KT / RPI; ++x) {
+          const uint32_t at = __shfl_sync(0xffffffffu, ko, x * RPI + lane / CPR);
+          const uint32_t to = st + piece4<D>(x * RPI + lane / CPR, ch);
+          copy16(to, kb + (uint64_t)at * 16);
+          copy16(to + V, vb + (uint64_t)at * 16);
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < KT / RPI; ++x) {
+          const int row = x * RPI + lane / CPR;
+          const bool on = rows >> row & 1;
+          const uint32_t to = st + piece4<D>(row, ch);
+          cp_async16(to, kb + (uint64_t)__shfl_sync(0xffffffffu, ko, row) * 16, on);
+          cp_async16(to + V, vb + (uint64_t)__shfl_sync(0xffffffffu, vo, row) * 16, on);
+        }
       }
     }
     cp_async_commit();
@@ -240,7 +252,7 @@ __device__ __forceinline__ void attend_piece4(const AttendArgs& a, char* ring, i
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
       constexpr int NW = D / 32;   // words of a lane's elements of a key
-      uint32_t k0[NW], k1[NW], s0[D / 64], s1[D / 64];
+      uint32_t k0[NW], k1[NW], s0[D == 256 ? 2 : 1], s1[D == 256 ? 2 : 1];
       const int row = 16 * h + krow;
       if constexpr (D == 64) {
         words(k0, st + piece4<D>(row, c >> 1) + (c & 1) * 8);
@@ -269,8 +281,8 @@ __device__ __forceinline__ void attend_piece4(const AttendArgs& a, char* ring, i
         e2m1x8_to_f16x2x4(k1[j], y[0], y[1], y[2], y[3]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {   // exact: six significant bits
-          x[e] = hmul2(x[e], s0[j / 2]);
-          y[e] = hmul2(y[e], s1[j / 2]);
+          x[e] = j / 2 % 2 ? hmul2_hi(x[e], s0[j / 4]) : hmul2_lo(x[e], s0[j / 4]);
+          y[e] = j / 2 % 2 ? hmul2_hi(y[e], s1[j / 4]) : hmul2_lo(y[e], s1[j / 4]);
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e)
