@@ -5,16 +5,25 @@
 //   cache    page = block_table[seq][position / page_size], slot = position % page_size;
 //            bf16 or E4M3 of the value times 1 / scale (E4M3: saturated at +-448)
 //
+//   NVFP4    block of 16: s = e4m3(max|x| / (6 g)), code = e2m1(x / (s g)); see the header
+//   axes     pair i turns by the position on its own axis
+//
 // A thread takes two 8-element pieces of one head: a pair of pieces R/2 apart, which rotate into each
-// other, or two neighbours past R. A block takes one token, or a few of few heads; the values are on
-// their way before the token's page is known. Products and sums are rounded one by one (no fused
-// multiply-add), so that a value on the edge between two E4M3 codes falls as plain float32 arithmetic
-// lets it fall.
-// Bound by memory: every value is read once and written once. 16000 tokens of 48 heads of 128 without
-// rotation 70 us (82 % of the measured copy rate); 4093 tokens, rotated, into E4M3 22 us (62 %), where the
-// conversions and the tables' reads (as many bytes as the values, from L1) come on top; three blocks an
-// SM of 512 threads at 40 registers beat two at 64 (25 us), also with two tokens a thread in flight, and
-// persistent blocks with the next token's values ahead (26 us) or tokens in a ring of bulk copies (28 us).
+// other, or two neighbours past R. Products and sums are rounded one by one (no fused multiply-add), so
+// that a value on the edge between two codes falls as plain float32 arithmetic lets it fall.
+//
+// k_kv_append: a block takes one token, or a few of few heads; the values are on their way before the token's page
+// is known. Three dependent loads (position, row of the table of angles or page, then the stores), no barrier: for
+// few tokens (four 2.2 us) and without rotation (16000 tokens of 48 heads of 128 71 us, 82 % of the measured copy
+// rate). Bound by load latency at the 48 warps an SM that 40 registers allow: 4093 rotated tokens into E4M3 23.3 us.
+// k_kv_append_many: the blocks that the device holds at once share the tokens. A block looks up the places of all of
+// its tokens and lays their cosines and sines out in shared memory, where all heads of a token read them and each
+// pair's axis has been chosen; then a thread keeps its piece of a head and goes through the tokens with the next one's
+// values on their way. 4093 tokens into NVFP4 20.7 us, 9001 with three axes 41 us (65 % and 70 % of the copy rate);
+// what is left are the loads' latency at 2 blocks of 64 registers and the conversions.
+// k_kv_gather: a thread takes 16 elements of a key and of its value. Bound by memory: 115 thousand tokens of 8 heads
+// of 128 from NVFP4 122 us (90 %), most of it for the results.
+#include <algorithm>
 #include <cuda_runtime.h>
 
 #include "ftmoe_internal.h"
@@ -25,6 +34,13 @@ namespace ftmoe {
 namespace {
 
 constexpr int kAppendThreads = 256;   // of a block, or as many as one token needs up to 512
+// From this many tokens a block (of those that the device holds at once) on, rotated ones go through
+// k_kv_append_many: 1200 tokens of 32 + 16 heads of 128 into NVFP4 8.5 us for 9.7, 4093 20.7 for 25.9 (into E4M3 20.4
+// for 23.3); 20000 of 2 + 2 heads of 64, three a block, would take 10.6 for 9.3. Without rotation k_kv_append is the
+// faster (16000 tokens 71 us for 77). Several axes always take k_kv_append_many: 37 tokens 2.7 us, 3.2 with the
+// choice of rows in each thread, 9001 41 us for 110.
+constexpr int kManyTokens = 4;
+constexpr int kAppendTokens = 32, kAppendBytes = 40 * 1024;   // most tokens of a group, most shared memory
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   uint16_t lo, hi;
@@ -112,32 +128,31 @@ __device__ __forceinline__ int64_t page_of(const A& a, int t, int col) {
   return page >= 0 && page < a.kv.num_pages ? page : -1;
 }
 
-// cos and sin of four pairs from pair c0 on, whose axes `which` names, two bits each.
-__device__ __forceinline__ void axis_rows(const AppendArgs& a, const int (&pos)[4], int c0, uint32_t which,
-                                          float (&c)[4], float (&s)[4]) {
-  const int half = a.rope_dim / 2;
-#pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    bool any = false;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) any |= ((which >> (2 * e)) & 3) == x;
-    if (!any) continue;
-    const float* rp = a.rope + (int64_t)pos[x] * a.rope_dim + c0;
-    const float4 vc = *reinterpret_cast<const float4*>(rp);
-    const float4 vs = *reinterpret_cast<const float4*>(rp + half);
-    const float cc[4] = {vc.x, vc.y, vc.z, vc.w}, ss[4] = {vs.x, vs.y, vs.z, vs.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (((which >> (2 * e)) & 3) == x) {
-        c[e] = cc[e];
-        s[e] = ss[e];
-      }
+// Two pieces of eight of a head as codes and scales. The halves of a block of 16 are this thread's own, or, where
+// they turn, this thread's and its neighbour's (item ^ 1: rope_dim is a multiple of 32, so they turn both, and items
+// a head are even, so they are lanes 2 i and 2 i + 1).
+__device__ __forceinline__ void store_codes(uint8_t* codes, uint8_t* scales, bool turn, int item, int c0, int c1,
+                                            float (&u)[8], float (&w)[8], float inv6, float g) {
+  float tu = top8(u), tw = top8(w), mu, mw;
+  if (turn) {
+    const uint32_t both = 3u << (threadIdx.x & 30);
+    tu = max_nan(tu, __shfl_xor_sync(both, tu, 1));
+    tw = max_nan(tw, __shfl_xor_sync(both, tw, 1));
+    const uint8_t su = block_scale(tu, inv6, g, mu), sw = block_scale(tw, inv6, g, mw);
+    if (!(item & 1)) {
+      scales[c0 / 16] = su;
+      scales[c1 / 16] = sw;
+    }
+  } else {
+    scales[c0 / 16] = block_scale(max_nan(tu, tw), inv6, g, mu);
+    mw = mu;
   }
+  *reinterpret_cast<uint32_t*>(codes + c0 / 2) = codes8(u, mu);
+  *reinterpret_cast<uint32_t*>(codes + c1 / 2) = codes8(w, mw);
 }
 
-template <int D, int DT, bool AXES>
-__global__ void __launch_bounds__(512, DT == kKvNvfp4 || AXES ? 2 : 3)
-    k_kv_append(const AppendArgs a, int items, int tokens) {
+template <int D, int DT>
+__global__ void __launch_bounds__(512, DT == kKvNvfp4 ? 2 : 3) k_kv_append(const AppendArgs a, int items, int tokens) {
   constexpr int PER_HEAD = D / 16;
   constexpr bool F8 = DT == FT_KV_E4M3, F4 = DT == kKvNvfp4;
   griddep_launch_dependents();
@@ -160,54 +175,36 @@ __global__ void __launch_bounds__(512, DT == kKvNvfp4 || AXES ? 2 : 3)
     // stored nor an error
     const int pos = a.positions[t];
     bool placed = pos >= 0;
-    int on_axis[4] = {pos, pos, pos, pos};
-    if constexpr (AXES) {
-      bool in = true;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < a.axes) {
-          on_axis[i] = a.axis_pos[i * a.axis_stride + t];
-          in &= on_axis[i] >= 0 && on_axis[i] < a.rope_rows;
-        }
-      if (placed && !in) {
-        placed = false;
-        if (a.err) atomicOr(a.err, kErrBadPage);
-      }
-    } else if (placed && a.rope_dim > 0 && pos >= a.rope_rows) {
+    if (placed && a.rope_dim > 0 && pos >= a.rope_rows) {
       placed = false;
       if (a.err) atomicOr(a.err, kErrBadPage);
     }
-    int64_t page = -1;
-    int slot = 0;
+    int64_t at = -1;
+    [[maybe_unused]] int64_t scales_at = 0;
     if (placed && kind != 0) {
       const Place p = place_of(a, pos);
-      slot = p.slot;
-      page = page_of(a, t, p.col);
-      if (page < 0 && a.err) atomicOr(a.err, kErrBadPage);
+      const int slot = p.slot;
+      const int64_t page = page_of(a, t, p.col);
+      if (page >= 0) {
+        at = kind == 1 ? page * a.kv.k_page_stride + slot * a.kv.k_slot_stride + head * a.kv.k_head_stride
+                       : page * a.kv.v_page_stride + slot * a.kv.v_slot_stride + head * a.kv.v_head_stride;
+        if constexpr (F4)
+          scales_at = kind == 1 ? page * a.sc.k_page + slot * a.sc.k_slot + head * a.sc.k_head
+                                : page * a.sc.v_page + slot * a.sc.v_slot + head * a.sc.v_head;
+      }
+      if (at < 0 && a.err) atomicOr(a.err, kErrBadPage);
     }
     float u[8], w[8];
     unpack8(x, u);
     unpack8(y, w);
     if (turn && placed) {
+      const float* rp = a.rope + (int64_t)pos * a.rope_dim + c0;
       const int half = a.rope_dim / 2;
-      uint32_t which = 0;   // the axes of the eight pairs, two bits each
-      bool one = true;      // they turn alike
-      if constexpr (AXES) {
-        which = a.axis_of[item >> 1] >> (16 * (item & 1)) & 0xFFFFu;
-        one = which == (which & 3) * 0x5555u;
-      }
-      const float* rp = a.rope + (int64_t)(AXES ? on_axis[which & 3] : pos) * a.rope_dim + c0;
 #pragma unroll
       for (int j = 0; j < 8; j += 4) {
-        float cc[4], sn[4];
-        if (!AXES || one) {
-          const float4 c = *reinterpret_cast<const float4*>(rp + j);
-          const float4 s = *reinterpret_cast<const float4*>(rp + half + j);
-          cc[0] = c.x; cc[1] = c.y; cc[2] = c.z; cc[3] = c.w;
-          sn[0] = s.x; sn[1] = s.y; sn[2] = s.z; sn[3] = s.w;
-        } else {
-          axis_rows(a, on_axis, c0 + j, which >> (2 * j), cc, sn);
-        }
+        const float4 c = *reinterpret_cast<const float4*>(rp + j);
+        const float4 s = *reinterpret_cast<const float4*>(rp + half + j);
+        const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float p = u[j + e], r = w[j + e];
@@ -224,40 +221,155 @@ __global__ void __launch_bounds__(512, DT == kKvNvfp4 || AXES ? 2 : 3)
       }
       store8(to + c0, u);
       store8(to + c1, w);
-    } else if (page >= 0) {
-      const int64_t at =
-          kind == 1 ? page * a.kv.k_page_stride + slot * a.kv.k_slot_stride + head * a.kv.k_head_stride
-                    : page * a.kv.v_page_stride + slot * a.kv.v_slot_stride + head * a.kv.v_head_stride;
+    } else if (at >= 0) {
       void* to = kind == 1 ? a.kv.k : a.kv.v;
       const float inv = kind == 1 ? a.inv_k : a.inv_v;
       if constexpr (F4) {
-        // The two pieces of a block of 16 are this thread's own, or, where they turn, this thread's and
-        // its neighbour's (item ^ 1: rope_dim is a multiple of 32, so they turn both, and items a head
-        // are even, so they are lanes 2 i and 2 i + 1).
-        const float g = kind == 1 ? a.kv.k_scale : a.kv.v_scale;
-        uint8_t* scales =
-            kind == 1 ? a.sc.k + page * a.sc.k_page + slot * a.sc.k_slot + head * a.sc.k_head
-                      : a.sc.v + page * a.sc.v_page + slot * a.sc.v_slot + head * a.sc.v_head;
-        float tu = top8(u), tw = top8(w), mu, mw;
-        if (turn) {
-          const uint32_t both = 3u << (threadIdx.x & 30);
-          tu = max_nan(tu, __shfl_xor_sync(both, tu, 1));
-          tw = max_nan(tw, __shfl_xor_sync(both, tw, 1));
-          const uint8_t su = block_scale(tu, inv, g, mu), sw = block_scale(tw, inv, g, mw);
-          if (!(item & 1)) {
-            scales[c0 / 16] = su;
-            scales[c1 / 16] = sw;
-          }
-        } else {
-          scales[c0 / 16] = block_scale(max_nan(tu, tw), inv, g, mu);
-          mw = mu;
-        }
-        uint8_t* codes = static_cast<uint8_t*>(to) + at;
-        *reinterpret_cast<uint32_t*>(codes + c0 / 2) = codes8(u, mu);
-        *reinterpret_cast<uint32_t*>(codes + c1 / 2) = codes8(w, mw);
+        store_codes(static_cast<uint8_t*>(to) + at, (kind == 1 ? a.sc.k : a.sc.v) + scales_at, turn, item, c0, c1, u, w,
+                    inv, kind == 1 ? a.kv.k_scale : a.kv.v_scale);
       } else {
         store_cache<F8>(to, at + c0, inv, u);
         store_cache<F8>(to, at + c1, inv, w);
+      }
+    }
+  }
+}
+
+// Where a token goes: offsets of its row without the head, in the unit of the strides.
+struct TokenPlace {
+  int64_t k_at, v_at, ks_at, vs_at;
+  int placed, stored;   // it has a position (else its query is zero); it has a page
+};
+
+// Two pieces of a head: u and w of a turning pair, or neighbours.
+struct Pieces {
+  uint4 x, y;
+};
+
+template <int D, int DT, bool AXES>
+__global__ void __launch_bounds__(512, 2)
+    k_kv_append_many(const AppendArgs a, int items, int groups, int per) {
+  constexpr int PER_HEAD = D / 16;
+  constexpr bool F8 = DT == FT_KV_E4M3, F4 = DT == kKvNvfp4;
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int R = a.rope_dim, half = R / 2;
+  float* const factors = reinterpret_cast<float*>(smem);                                   // [token][R]
+  TokenPlace* const places = reinterpret_cast<TokenPlace*>(factors + groups * per * R);    // [token]
+  griddep_launch_dependents();
+  griddep_wait();
+  const int group = groups > 1 ? (int)threadIdx.x / items : 0;
+  const int t0 = blockIdx.x * groups * per, n = min(groups * per, a.T - t0);   // the block's tokens
+  bool first = true;
+  for (int id = threadIdx.x - group * items;; id += blockDim.x) {
+    const bool mine = group < groups && id < items;
+    if (!first && !mine) break;
+    const int row = id / PER_HEAD, item = id % PER_HEAD;
+    const int kind = row < a.Hq ? 0 : row < a.Hq + a.kv.Hkv ? 1 : 2;   // q, k, v
+    const int head = kind == 0 ? row : kind == 1 ? row - a.Hq : row - a.Hq - a.kv.Hkv;
+    const int pairs = kind == 2 ? 0 : R / 16;
+    const bool turn = item < pairs;
+    const int c0 = turn ? 8 * item : kind == 2 ? 16 * item : R + 16 * (item - pairs);
+    const int c1 = turn ? c0 + half : c0 + 8;
+    const uint16_t* src = (kind == 0 ? a.q : kind == 1 ? a.k : a.v) + head * D;
+    const int64_t stride = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
+    auto load = [&](int j) {
+      const uint16_t* p = src + (t0 + j) * stride;
+      return Pieces{ld16(p + c0), ld16(p + c1)};
+    };
+    Pieces next = {};
+    if (mine && group < n) next = load(group);
+    if (first) {   // places and factors of the block's tokens, while the first values travel
+      first = false;
+      for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const int t = t0 + i, pos = a.positions[t];
+        TokenPlace p = {0, 0, 0, 0, pos >= 0, 0};   // a negative position: a padding token, not an error
+        if (pos >= 0) {
+          bool in = true;
+          if constexpr (AXES) {
+            for (int x = 0; x < a.axes; ++x) {
+              const int at = a.axis_pos[x * a.axis_stride + t];
+              in &= at >= 0 && at < a.rope_rows;
+            }
+          } else {
+            in = R == 0 || pos < a.rope_rows;
+          }
+          const Place where = place_of(a, pos);
+          const int64_t page = in ? page_of(a, t, where.col) : -1;
+          p.placed = in;
+          if (page >= 0) {
+            p.stored = 1;
+            p.k_at = page * a.kv.k_page_stride + where.slot * a.kv.k_slot_stride;
+            p.v_at = page * a.kv.v_page_stride + where.slot * a.kv.v_slot_stride;
+            if constexpr (F4) {
+              p.ks_at = page * a.sc.k_page + where.slot * a.sc.k_slot;
+              p.vs_at = page * a.sc.v_page + where.slot * a.sc.v_slot;
+            }
+          } else if (a.err) {
+            atomicOr(a.err, kErrBadPage);
+          }
+        }
+        places[i] = p;
+      }
+      // Factor f of pair 8 i + 4 j + e lies at 4 (R/16 j + i) + e of its half: the threads of a head read
+      // neighbouring 16 bytes.
+      for (int i = threadIdx.x; i < n * half; i += blockDim.x) {
+        const int j = i / half, pair = i - j * half, t = t0 + j;
+        int at;
+        if constexpr (AXES) at = a.axis_pos[(a.axis_of[pair >> 4] >> (2 * (pair & 15)) & 3) * a.axis_stride + t];
+        else at = a.positions[t];
+        float c = 1.f, s = 0.f;
+        if (at >= 0 && at < a.rope_rows) {
+          c = a.rope[(int64_t)at * R + pair];
+          s = a.rope[(int64_t)at * R + half + pair];
+        }
+        float* to = factors + j * R + 4 * ((R / 16) * (pair >> 2 & 1) + (pair >> 3)) + (pair & 3);
+        to[0] = c;
+        to[half] = s;
+      }
+      __syncthreads();
+    }
+    if (!mine) break;
+    for (int j = group; j < n; j += groups) {
+      const Pieces now = next;
+      if (j + groups < n) next = load(j + groups);
+      const TokenPlace& place = places[j];
+      float u[8], w[8];
+      unpack8(now.x, u);
+      unpack8(now.y, w);
+      if (turn) {   // without a place nothing comes of it
+        const float4* f = reinterpret_cast<const float4*>(factors + j * R) + item;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float4 c = f[x * (R / 16)], s = f[R / 8 + x * (R / 16)];
+          const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float p = u[4 * x + e], r = w[4 * x + e];
+            u[4 * x + e] = __fsub_rn(__fmul_rn(p, cc[e]), __fmul_rn(r, sn[e]));
+            w[4 * x + e] = __fadd_rn(__fmul_rn(r, cc[e]), __fmul_rn(p, sn[e]));
+          }
+        }
+      }
+      if (kind == 0) {
+        uint16_t* to = a.q_out + ((int64_t)(t0 + j) * a.Hq + head) * D;
+        if (!place.placed) {   // the query of a token without a position: zeros
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u[e] = w[e] = 0.f;
+        }
+        store8(to + c0, u);
+        store8(to + c1, w);
+      } else if (place.stored) {
+        const int64_t at = kind == 1 ? place.k_at + head * a.kv.k_head_stride : place.v_at + head * a.kv.v_head_stride;
+        void* to = kind == 1 ? a.kv.k : a.kv.v;
+        const float inv = kind == 1 ? a.inv_k : a.inv_v;
+        if constexpr (F4) {
+          store_codes(static_cast<uint8_t*>(to) + at,
+                      kind == 1 ? a.sc.k + place.ks_at + head * a.sc.k_head : a.sc.v + place.vs_at + head * a.sc.v_head,
+                      turn, item, c0, c1, u, w, inv, kind == 1 ? a.kv.k_scale : a.kv.v_scale);
+        } else {
+          store_cache<F8>(to, at + c0, inv, u);
+          store_cache<F8>(to, at + c1, inv, w);
+        }
       }
     }
   }
@@ -344,19 +456,31 @@ __global__ void __launch_bounds__(256) k_kv_gather(const GatherArgs a) {
 }
 
 template <int D, int DT>
-cudaError_t launch_axes(const cudaLaunchConfig_t& cfg, const AppendArgs& a, int items, int tokens) {
-  return a.axis_pos ? cudaLaunchKernelEx(&cfg, k_kv_append<D, DT, true>, a, items, tokens)
-                    : cudaLaunchKernelEx(&cfg, k_kv_append<D, DT, false>, a, items, tokens);
+cudaError_t launch_t(cudaLaunchConfig_t cfg, const AppendArgs& a, int num_sms) {
+  const int items = (a.Hq + 2 * a.kv.Hkv) * (D / 16);   // of a token
+  const int groups = items < kAppendThreads ? kAppendThreads / items : 1;
+  const int turns = (items + 511) / 512;
+  const int threads = ((turns > 1 ? (items + turns - 1) / turns : items * groups) + 31) / 32 * 32;
+  const int resident = num_sms * (1024 / threads);   // blocks of k_kv_append_many at once
+  int per = (int)(((int64_t)a.T + (int64_t)resident * groups - 1) / ((int64_t)resident * groups));
+  if (!a.axis_pos && (per < kManyTokens || a.rope_dim == 0)) {
+    const int need = (items * groups + 31) / 32 * 32;
+    cfg.gridDim = dim3((unsigned)((a.T + groups - 1) / groups));
+    cfg.blockDim = dim3((unsigned)(need < 512 ? need : 512));
+    return cudaLaunchKernelEx(&cfg, k_kv_append<D, DT>, a, items, groups);
+  }
+  const int bytes = groups * (a.rope_dim * (int)sizeof(float) + (int)sizeof(TokenPlace));   // for one token each
+  per = std::min(per, std::min(kAppendBytes / bytes, kAppendTokens));
+  cfg.gridDim = dim3((unsigned)((a.T + groups * per - 1) / (groups * per)));
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)(per * bytes);
+  return a.axis_pos ? cudaLaunchKernelEx(&cfg, k_kv_append_many<D, DT, true>, a, items, groups, per)
+                    : cudaLaunchKernelEx(&cfg, k_kv_append_many<D, DT, false>, a, items, groups, per);
 }
 
 template <int D>
-cudaError_t launch_d(const AppendArgs& a, cudaStream_t stream) {
-  const int items = (a.Hq + 2 * a.kv.Hkv) * (D / 16);
-  const int tokens = items < kAppendThreads ? kAppendThreads / items : 1;
-  const int need = (items * tokens + 31) / 32 * 32;
+cudaError_t launch_d(const AppendArgs& a, int num_sms, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.T + tokens - 1) / tokens));
-  cfg.blockDim = dim3((unsigned)(need < 512 ? need : 512));
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -364,10 +488,10 @@ cudaError_t launch_d(const AppendArgs& a, cudaStream_t stream) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   switch (a.kv.dtype) {
-    case FT_KV_BF16: return launch_axes<D, FT_KV_BF16>(cfg, a, items, tokens);
-    case FT_KV_E4M3: return launch_axes<D, FT_KV_E4M3>(cfg, a, items, tokens);
+    case FT_KV_BF16: return launch_t<D, FT_KV_BF16>(cfg, a, num_sms);
+    case FT_KV_E4M3: return launch_t<D, FT_KV_E4M3>(cfg, a, num_sms);
   }
-  return launch_axes<D, kKvNvfp4>(cfg, a, items, tokens);
+  return launch_t<D, kKvNvfp4>(cfg, a, num_sms);
 }
 
 template <int D>
@@ -393,11 +517,13 @@ cudaError_t launch_gather_d(const GatherArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_kv_append(const AppendArgs& args, cudaStream_t stream) {
   AppendArgs a = args;
+  const int sms = device_sms();
+  if (sms <= 0) return cudaErrorNoDevice;
   page_division(a.kv.page_size, a.div_mul, a.div_shift);
   switch (a.kv.D) {
-    case 64: return launch_d<64>(a, stream);
-    case 128: return launch_d<128>(a, stream);
-    case 256: return launch_d<256>(a, stream);
+    case 64: return launch_d<64>(a, sms, stream);
+    case 128: return launch_d<128>(a, sms, stream);
+    case 256: return launch_d<256>(a, sms, stream);
   }
   return cudaErrorInvalidValue;
 }
