@@ -52,7 +52,7 @@ struct AttnShape {
   static constexpr int kRow = DT == kKvNvfp4 ? D / 2 : DT == FT_KV_E4M3 ? D : 2 * D;   // bytes of a key or value
   static constexpr int kCpr = kRow / 16;              // 16-byte pieces of it
   static constexpr int kScaleRow = DT == kKvNvfp4 ? D / 16 : 0;   // bytes of its block scales
-  static constexpr int kKeys = kRow <= 128 ? 32 : 16; // keys of a warp's step
+  static constexpr int kKeys = DT == kKvNvfp4 ? (D == 256 ? 16 : 32) : kRow <= 128 ? 32 : 16;   // keys of a warp's step
   static constexpr int kStageBytes = 2 * kKeys * (kRow + kScaleRow);   // those keys and values
   // blocks an SM: the others stream while one joins a piece's warps. Three of two stages each, not two of
   // three, where the registers allow it: 256 sequences up to 1024 with 8-bit keys of 128: 68 us for 79.
@@ -62,11 +62,17 @@ struct AttnShape {
   // NVFP4: one block an SM, whose groups of warps each do what a block does otherwise
   static constexpr int kGroups = DT != kKvNvfp4 ? 1 : D == 128 && NG == 1 ? kAttendBlocks : 2;
   static constexpr int kWarps = (DT == kKvNvfp4 ? D >= 128 : kRow >= 128) ? 4 : 8;   // of a group
-  static constexpr int kStages = 192 * 1024 / (kBlocks * kGroups * kWarps * kStageBytes);
+  static constexpr int kQShared = DT != kKvNvfp4 || NG == 1 ? 0 : D == 256 ? 2 : D == 64 ? 1 : 0;   // groups of q in shared memory
+  static constexpr int kQBytes = kQShared * (D / 16) * 256;
+  static constexpr int kStages =
+      ((DT == kKvNvfp4 ? 208 : 192) * 1024 / (kBlocks * kGroups * kWarps) - kQBytes) / kStageBytes;
+  static constexpr int kWarpBytes = kStages * kStageBytes + kQBytes;
   static constexpr int kUnit = kKeys * kWarps;        // keys of a unit
-  static constexpr int kRing = kWarps * kStages * kStageBytes;
-  static constexpr int kSumsLd = D + 4;               // floats between heads of a warp's sums, in its ring
-  static_assert(8 * NG * kSumsLd * 4 <= kStages * kStageBytes && kBlocks * kGroups * kWarps <= attend_warps(D));
+  static constexpr int kRing = kWarps * kWarpBytes;
+  // floats between heads of a warp's sums, in its ring. NVFP4: lane r has elements D/8 r + 2 t, + 1 of a head, which
+  // lie at 20 t + 2 r, so that neither the lanes that write them nor those that read four of them share banks.
+  static constexpr int kSumsLd = (DT == kKvNvfp4 ? 20 * (D / 16) : D) + 4;
+  static_assert(8 * NG * kSumsLd * 4 <= kWarpBytes && kBlocks * kGroups * kWarps <= attend_warps(D));
 };
 
 // From this many units in a run, the warps of a block take several key heads at once instead of stripes of
@@ -194,7 +200,7 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
   const int64_t quota = (total + blocks - 1) / blocks;
   int64_t u = quota * block;
   const int64_t u_end = min(u + quota, total);
-  const uint32_t ring = smem_addr(rings) + (uint32_t)(warp * ST * S::kStageBytes);
+  const uint32_t ring = smem_addr(rings) + (uint32_t)(warp * S::kWarpBytes);
   // HW heads a block, W / HW stripes of keys each
   const int hl = quota >= kLongRun ? a.heads_log2 : 0, HW = 1 << hl, stripes = W >> hl;
   const int hw = warp & (HW - 1), stripe = warp >> hl;
@@ -254,7 +260,7 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
       l[g][0] = l[g][1] = 0.f;
     }
     if constexpr (F4) {
-      attend_piece4<D, NG, S>(a, reinterpret_cast<char*>(rings) + warp * ST * S::kStageBytes, b, kvh, g0, G, first, key0, key1,
+      attend_piece4<D, NG, S>(a, reinterpret_cast<char*>(rings) + warp * S::kWarpBytes, b, kvh, g0, G, first, key0, key1,
                               unit, n_sub, o, m, l);
     } else {
     const int32_t* table = a.block_table + (int64_t)b * a.table_width;
@@ -511,7 +517,7 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
 
     // ---- join the warps of a head: sums [head][LD] in each one's ring
     sync();
-    float* sums = reinterpret_cast<float*>(rings + (size_t)warp * ST * S::kStageBytes);
+    float* sums = reinterpret_cast<float*>(rings + (size_t)warp * S::kWarpBytes);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
 #pragma unroll
@@ -526,7 +532,11 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
         if (h < G) {
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
-            const int d0 = F4 ? D / 8 * r + 2 * t : F16 ? 16 * t + 2 * r : 16 * t + r;
+            if constexpr (F4) {
+              *reinterpret_cast<float2*>(sums + h * LD + 20 * t + 2 * r) = make_float2(o[g][t][e], o[g][t][2 + e]);
+              continue;
+            }
+            const int d0 = F16 ? 16 * t + 2 * r : 16 * t + r;
             const int d1 = F16 ? d0 + 1 : d0 + 8;
             sums[h * LD + d0] = o[g][t][e];
             sums[h * LD + d1] = o[g][t][2 + e];
@@ -566,8 +576,15 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
         if (s >= stripes) break;
         const int w = hw + (s << hl);
         const float f = share[w][g];
-        const float4 y = *reinterpret_cast<const float4*>(
-            reinterpret_cast<const float*>(rings + (size_t)w * ST * S::kStageBytes) + g * LD + d);
+        const float* from = reinterpret_cast<const float*>(rings + (size_t)w * S::kWarpBytes) + g * LD;
+        float4 y;
+        if constexpr (F4) {
+          const float* at = from + 10 * (d % (D / 8)) + 2 * (d / (D / 8));
+          const float2 y0 = *reinterpret_cast<const float2*>(at), y1 = *reinterpret_cast<const float2*>(at + 20);
+          y = make_float4(y0.x, y0.y, y1.x, y1.y);
+        } else {
+          y = *reinterpret_cast<const float4*>(from + d);
+        }
         v.x = fmaf(f, y.x, v.x); v.y = fmaf(f, y.y, v.y);
         v.z = fmaf(f, y.z, v.z); v.w = fmaf(f, y.w, v.w);
       }
@@ -586,8 +603,28 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
 // warps of k_attend's blocks.
 constexpr int kTeam = 8;                    // warps of a job at most
 constexpr int kFlight = 4;                  // pieces of a warp in flight
+// Adds N pieces to a running maximum, sum and row.
+template <int N, int E>
+__device__ __forceinline__ void add_pieces(const float2* ml, const float (*y)[E], float& m, float& l, float (&v)[E]) {
+  float top = m;
+#pragma unroll
+  for (int j = 0; j < N; ++j) top = fmaxf(top, ml[j].x);
+  const float base = top == -INFINITY ? 0.f : top, f = exp2_fast(m - base);
+  m = top;
+  l *= f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] *= f;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float fj = exp2_fast(ml[j].x - base);
+    l = fmaf(fj, ml[j].y, l);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = fmaf(fj, y[j][e], v[e]);
+  }
+}
+
 template <int D, int W, int kJoinWarps>
-__global__ void __launch_bounds__(kJoinWarps * 32) k_join(const AttendArgs a) {
+__global__ void __launch_bounds__(kJoinWarps * 32, kJoinWarps == 8 ? 3 : 1) k_join(const AttendArgs a) {
   constexpr int E = D / 32;
   __shared__ float sums[kJoinWarps][D], wm[kJoinWarps], wl[kJoinWarps];
   griddep_launch_dependents();
@@ -611,48 +648,90 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_join(const AttendArgs a) {
   int tl = 0;   // log2 of the warps of a job
   while (2 << tl <= kTeam && kFlight << tl <= blocks && mine << (tl + 1) <= kJoinWarps) ++tl;
   const int team = warp >> tl, part = warp & ((1 << tl) - 1), teams = kJoinWarps >> tl;
-  for (int i0 = 0; i0 < mine; i0 += teams) {
-    const int job = me + (i0 + team) * blocks;
+  // a job's output row, its head among the segment's key heads, or -1 where the group of heads is not full
+  auto row_of = [&](int job) -> int64_t {
     const int hw = job / heads, g = job - hw * heads;
     const int hs = ((seg.y >> 4) << hl) + hw, kvh = a.gt == 1 ? hs : hs / a.gt, g0 = (hs - kvh * a.gt) * 16;
-    const bool on = job < jobs && g0 + g < a.group;
+    if (job >= jobs || g0 + g >= a.group) return -1;
+    return (int64_t)seg.x * a.Hq + kvh * a.group + g0 + g;
+  };
+  auto piece_of = [&](int job, int p) -> int64_t {   // where piece p of a job lies
+    const int hw = job / heads, g = job - hw * heads;
+    // a run's first piece, but for a segment that begins inside its first run
+    return ((2 * (int64_t)p + (p == run0 ? seg.z & 1 : 0)) * W + hw) * 16 + g;
+  };
+  auto finish = [&](int64_t row, float m, float l, const float (&v)[E]) {
+    uint32_t y[E / 2];
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+      y[e / 2] = l == 0.f ? 0u : pack_bf16(v[e] / l * a.kv.v_scale, v[e + 1] / l * a.kv.v_scale);
+    uint16_t* to = a.out + row * D + lane * E;
+    if constexpr (E == 2) *reinterpret_cast<uint32_t*>(to) = y[0];
+    else if constexpr (E == 4) *reinterpret_cast<uint2*>(to) = make_uint2(y[0], y[1]);
+    else *reinterpret_cast<uint4*>(to) = make_uint4(y[0], y[1], y[2], y[3]);
+    if (lane == 0 && a.lse)
+      a.lse[row] = a.kv.dtype != FT_KV_BF16 ? lse_of<true>(m, l) : lse_of<false>(m, l);
+  };
+  auto load = [&](int64_t at, bool on, float2& ml, float (&y)[E]) {
+    ml = make_float2(-INFINITY, 0.f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[e] = 0.f;
+    if (!on) return;
+    ml = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+    const float* p = a.part_o + at * D + lane * E;
+    if constexpr (E == 2) {
+      const float2 x = *reinterpret_cast<const float2*>(p);
+      y[0] = x.x; y[1] = x.y;
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p + e);
+        y[e] = x.x; y[e + 1] = x.y; y[e + 2] = x.z; y[e + 3] = x.w;
+      }
+    }
+  };
+  float2 ml[kFlight];
+  float y[kFlight][E];
+  if (seg.w - run0 < 2) {   // two pieces: as many jobs of a warp at once as are in flight
+    constexpr int JF = kFlight / 2;
+    for (int i0 = warp; i0 < mine; i0 += JF * kJoinWarps) {
+#pragma unroll
+      for (int j = 0; j < kFlight; ++j) {
+        const int job = me + (i0 + (j >> 1) * kJoinWarps) * blocks;
+        load(piece_of(job, run0 + (j & 1)), row_of(job) >= 0, ml[j], y[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < JF; ++j) {
+        const int64_t row = row_of(me + (i0 + j * kJoinWarps) * blocks);
+        if (row < 0) continue;
+        float m = -INFINITY, l = 0.f, v[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = 0.f;
+        add_pieces<2, E>(ml + 2 * j, y + 2 * j, m, l, v);
+        finish(row, m, l, v);
+      }
+    }
+    return;
+  }
+  for (int i0 = 0; i0 < mine; i0 += teams) {
+    const int job = me + (i0 + team) * blocks;
+    const int64_t row = row_of(job);
     float m = -INFINITY, l = 0.f, v[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = 0.f;
-    if (on) {
+    if (row >= 0) {
       for (int p0 = run0 + part; p0 <= seg.w; p0 += kFlight << tl) {
-        float2 ml[kFlight];
-        float y[kFlight][E];
 #pragma unroll
         for (int j = 0; j < kFlight; ++j) {
           const int p = p0 + (j << tl);
-          // a run's first piece, but for a segment that begins inside its first run
-          const int64_t at = ((2 * (int64_t)p + (p == run0 ? seg.z & 1 : 0)) * W + hw) * 16 + g;
-          ml[j] = make_float2(-INFINITY, 0.f);
-          if (p <= seg.w) ml[j] = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
-#pragma unroll
-          for (int e = 0; e < E; ++e) y[j][e] = p <= seg.w ? a.part_o[at * D + lane + 32 * e] : 0.f;
+          load(piece_of(job, p), p <= seg.w, ml[j], y[j]);
         }
-        float top = m;
-#pragma unroll
-        for (int j = 0; j < kFlight; ++j) top = fmaxf(top, ml[j].x);
-        const float base = top == -INFINITY ? 0.f : top, f = exp2_fast(m - base);
-        m = top;
-        l *= f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] *= f;
-#pragma unroll
-        for (int j = 0; j < kFlight; ++j) {
-          const float fj = exp2_fast(ml[j].x - base);
-          l = fmaf(fj, ml[j].y, l);
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[e] = fmaf(fj, y[j][e], v[e]);
-        }
+        add_pieces<kFlight, E>(ml, y, m, l, v);
       }
     }
     if (tl > 0) {   // uniform over the block, as are i0 and mine
 #pragma unroll
-      for (int e = 0; e < E; ++e) sums[warp][lane + 32 * e] = v[e];
+      for (int e = 0; e < E; ++e) sums[warp][lane * E + e] = v[e];
       if (lane == 0) {
         wm[warp] = m;
         wl[warp] = l;
@@ -674,20 +753,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_join(const AttendArgs a) {
           const float f = exp2_fast(wm[warp + w] - base);
           l = fmaf(f, wl[warp + w], l);
 #pragma unroll
-          for (int e = 0; e < E; ++e) v[e] = fmaf(f, sums[warp + w][lane + 32 * e], v[e]);
+          for (int e = 0; e < E; ++e) v[e] = fmaf(f, sums[warp + w][lane * E + e], v[e]);
         }
       }
       __syncthreads();
     }
-    if (on && part == 0) {
-      const int64_t row = (int64_t)seg.x * a.Hq + kvh * a.group + g0 + g;
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        a.out[row * D + lane + 32 * e] =
-            (uint16_t)(pack_bf16(l == 0.f ? 0.f : v[e] / l * a.kv.v_scale, 0.f) & 0xFFFFu);
-      if (lane == 0 && a.lse)
-        a.lse[row] = a.kv.dtype != FT_KV_BF16 ? lse_of<true>(m, l) : lse_of<false>(m, l);
-    }
+    if (row >= 0 && part == 0) finish(row, m, l, v);
   }
 }
 

@@ -144,7 +144,7 @@ __device__ __forceinline__ void attend_piece4(const AttendArgs& a, char* ring, i
   bool live = false;
   auto look_up = [&](int i) {
     const int j = key0 + i * unit + lane;
-    live = i < n_sub && j >= first && j < key1;
+    live = i < n_sub && lane < KT && j >= first && j < key1;
     page = -1;
     if (live) {
       const int col = (int)((__umulhi((uint32_t)a.div_mul, (uint32_t)j) + (uint32_t)j) >> a.div_shift);
@@ -172,10 +172,12 @@ __device__ __forceinline__ void attend_piece4(const AttendArgs& a, char* ring, i
         vo = p * (uint32_t)(a.kv.v_page_stride >> 4) + s * (uint32_t)(a.kv.v_slot_stride >> 4);
         vso = p * (uint32_t)(a.sc.v_page / SROW) + s * (uint32_t)(a.sc.v_slot / SROW);
       }
-      cp_async_scales<SROW>(st + KSC + lane * SROW, ksb + (uint64_t)kso * SROW, in);
-      cp_async_scales<SROW>(st + VSC + lane * SROW, vsb + (uint64_t)vso * SROW, in);
+      if (KT == 32 || lane < KT) {
+        cp_async_scales<SROW>(st + KSC + lane * SROW, ksb + (uint64_t)kso * SROW, in);
+        cp_async_scales<SROW>(st + VSC + lane * SROW, vsb + (uint64_t)vso * SROW, in);
+      }
       const uint32_t rows = __ballot_sync(0xffffffffu, in);
-      if (rows == 0xffffffffu && a.same_strides) {   // as a rule
+      if (rows == 0xffffffffu >> (32 - KT) && a.same_strides) {   // as a rule
 #pragma unroll
         for (int x = 0; x < KT / RPI; ++x) {
           const uint32_t at = __shfl_sync(0xffffffffu, ko, x * RPI + lane / CPR);
@@ -206,6 +208,10 @@ __device__ __forceinline__ void attend_piece4(const AttendArgs& a, char* ring, i
   // ---- q as the column operand, f16 after a power of two: column l / 4 of group g is head 8 g + l / 4. The
   // sign of the scale goes into q, so that a larger product is a larger score.
   uint32_t q[NG][KS][2];
+  // Of two groups, one (two with heads of 256) stays in shared memory, where each lane keeps its own words: its
+  // registers would cost warps.
+  constexpr int QS = S::kQShared;
+  uint2* const qs = reinterpret_cast<uint2*>(ring + ST * S::kStageBytes) + lane;
   uint64_t sl[NG];   // log2 units per unit of the raw product, heads 8 g + 2 c, + 1
   {
     const uint16_t* qb = a.q + (int64_t)b * a.q_stride + (int64_t)(kvh * a.group + g0) * D;
@@ -234,6 +240,10 @@ __device__ __forceinline__ void attend_piece4(const AttendArgs& a, char* ring, i
       sl[g] = pair(unit_s * __shfl_sync(0xffffffffu, down, 8 * c),   // head 2 c: lanes 8 c ..
                    unit_s * __shfl_sync(0xffffffffu, down, 8 * c + 4));
     }
+#pragma unroll
+    for (int g = 0; g < QS; ++g)
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) qs[32 * (g * KS + ks)] = make_uint2(q[NG - 1 - g][ks][0], q[NG - 1 - g][ks][1]);
   }
 
   uint64_t less[NG], sum[NG];   // - the running maximum (0 without one), sums of weights
@@ -285,10 +295,14 @@ __device__ __forceinline__ void attend_piece4(const AttendArgs& a, char* ring, i
           y[e] = j / 2 % 2 ? hmul2_hi(y[e], s1[j / 4]) : hmul2_lo(y[e], s1[j / 4]);
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < 2; ++e) {
 #pragma unroll
-          for (int g = 0; g < NG; ++g)
-            mma_f16(s[g][h], x[2 * e], y[2 * e], x[2 * e + 1], y[2 * e + 1], q[g][2 * j + e][0], q[g][2 * j + e][1]);
+          for (int g = 0; g < NG; ++g) {
+            uint2 w = make_uint2(q[g][2 * j + e][0], q[g][2 * j + e][1]);
+            if (NG - 1 - g < QS) w = qs[32 * ((NG - 1 - g) * KS + 2 * j + e)];
+            mma_f16(s[g][h], x[2 * e], y[2 * e], x[2 * e + 1], y[2 * e + 1], w.x, w.y);
+          }
+        }
       }
     }
   };
