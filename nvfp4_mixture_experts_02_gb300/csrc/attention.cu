@@ -602,7 +602,6 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
 // order, the first of them adds the shares in order. The blocks also zero the heads of empty sequences. W:
 // warps of k_attend's blocks.
 constexpr int kTeam = 8;                    // warps of a job at most
-constexpr int kFlight = 4;                  // pieces of a warp in flight
 // Adds N pieces to a running maximum, sum and row.
 template <int N, int E>
 __device__ __forceinline__ void add_pieces(const float2* ml, const float (*y)[E], float& m, float& l, float (&v)[E]) {
@@ -623,7 +622,7 @@ __device__ __forceinline__ void add_pieces(const float2* ml, const float (*y)[E]
   }
 }
 
-template <int D, int W, int kJoinWarps>
+template <int D, int W, int kJoinWarps, int kFlight>   // kFlight: pieces of a warp in flight
 __global__ void __launch_bounds__(kJoinWarps * 32, kJoinWarps == 8 ? 3 : 1) k_join(const AttendArgs a) {
   constexpr int E = D / 32;
   __shared__ float sums[kJoinWarps][D], wm[kJoinWarps], wl[kJoinWarps];
@@ -788,7 +787,7 @@ cudaError_t launch_d(AttendArgs a, int num_sms, cudaStream_t stream) {
   cfg.gridDim = dim3((unsigned)(S::kBlocks * S::kGroups * num_sms));   // a block for every run
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, k_join<D, S::kWarps, kJoinWarps>, a);
+  return cudaLaunchKernelEx(&cfg, k_join<D, S::kWarps, kJoinWarps, DT == kKvNvfp4 && D <= 128 ? 8 : 4>, a);
 }
 
 template <int D, int DT>
