@@ -504,8 +504,10 @@ ft_status ft_paged_decode_attention(const uint16_t* q, int64_t q_stride, int32_t
 
 /*
  * ft_nvfp4_paged_decode_attention — ft_paged_decode_attention over an NVFP4 cache: the same arguments,
- * workspace, flags and errors. Keys and values enter their products exactly (e2m1 * e4m3 is an f16); a
- * weight is rounded as with an E4M3 cache. A NaN block scale gives NaN.
+ * workspace, flags and errors. Keys and values enter their products exactly (e2m1 * e4m3 is an f16);
+ * before a weight meets its value it is rounded to 11 bits, or to within 2^-35 of the largest key's
+ * weight. A NaN block scale gives NaN. From the first element of a cache's codes to its last there may be
+ * 64 GiB, from the first of its scales to the last 2^28 * D bytes (FT_ERR_UNSUPPORTED_SHAPE beyond).
  */
 ft_status ft_nvfp4_paged_decode_attention(const uint16_t* q, int64_t q_stride, int32_t B, int32_t Hq,
                                           const ft_nvfp4_kv* cache, const int32_t* block_table,

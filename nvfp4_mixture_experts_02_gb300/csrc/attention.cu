@@ -28,12 +28,18 @@
 // weight, see kLift). One f16 for p moves outputs over their bf16 rounding: 48 ragged sequences are 8.1e-4 off the
 // rounded exact result with one, 0.8e-4 with two (bf16 caches 0.6e-4), at 0 to 1 % of the time, 4 to 5 % with heads
 // of 64 (200 ragged sequences up to 700, 26.3 and 27.5 us) or 16 heads a key head (16 x 8192, 40.9 and 43.2 us).
-// Statistics and sums are float32.
+// NVFP4 caches (ftmoe_attend4.cuh): f16 products as for E4M3, a weight in one f16. Statistics and sums are float32.
 //
 // Measured (of the copy rate of 6786 GB/s): three sequences up to 131072, bf16, 962 MB: 155 us (91 %).
 // 48 ragged ones up to 8192, E4M3, 423 MB: 85 us (73 %), of which some 10 us are launches, fill and
 // join, and the runs' pieces differ in cost. One sequence of 777: 7.8 us, two launches and the chain
 // length, page, keys, scores, sums, join.
+// NVFP4: the three 56 us (270 MB, 71 %), the 48 56 us (239 MB, 63 %), 64 of 6500 91.5 us with pages head by head and 97
+// slot by slot (481 MB, 78 and 73 %): the products' own part runs at 93 % of the copy rate (870 of the 806 cycles that
+// a step's bytes take, of which 604 issue an instruction); the first data arrive after 4.5 us and the join takes 7.
+// Without any arithmetic those take 83 and 92 us. With heads of 64 (200 sequences, a window of 1023: 30 us for 7.4)
+// rows of 32 bytes copy at 77 % and a step has as many instructions for half the bytes; with 16 heads a key head the
+// warp products' rate bounds the steps (64 products of 16 cycles in 1225; heads of 256: 46 us for 14.6).
 #include <cmath>
 #include <cuda_runtime.h>
 
@@ -68,6 +74,8 @@ struct AttnShape {
       ((DT == kKvNvfp4 ? 208 : 192) * 1024 / (kBlocks * kGroups * kWarps) - kQBytes) / kStageBytes;
   static constexpr int kWarpBytes = kStages * kStageBytes + kQBytes;
   static constexpr int kUnit = kKeys * kWarps;        // keys of a unit
+  // Units that a segment is charged for (see kChargeFrom).
+  static constexpr int kCharge = DT != kKvNvfp4 ? 0 : D == 256 ? 4 : 1;
   static constexpr int kRing = kWarps * kWarpBytes;
   // floats between heads of a warp's sums, in its ring. NVFP4: lane r has elements D/8 r + 2 t, + 1 of a head, which
   // lie at 20 t + 2 r, so that neither the lanes that write them nor those that read four of them share banks.
@@ -81,6 +89,11 @@ struct AttnShape {
 // copies up. Shorter runs would leave k_join as many times more pieces: 48 sequences of 256 take 12.8 us, and
 // 17.0 when runs of two units are long; 8 up to 2048 take 14.0 us, and 15.5 when only runs of eight are.
 constexpr int kLongRun = 4;
+// NVFP4, runs of at least this many units: a segment begins with kCharge units without keys, for the copies that
+// begin anew and the results that are joined. With 0, 1, 2 and 4 of them 48 ragged sequences up to 8192 take 57.0, 56.1,
+// 57.2 and 58.6 us, 100 up to 4000 51.2, 48.0, 50.3 and 52.9, 19 of 22272 89.5, 92.5, 91.6 and 93.3; with heads of 256
+// (units half as long) 13 up to 24001 50.2, 47.8, 47.4 and 45.9, 16 of 8192 43.1, 40.7, 39.9 and 39.9.
+constexpr int kChargeFrom = 12;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // log2 of the largest weight. f16 holds 11 bits of weights down to 2^-14 and nothing under 2^-25: with
@@ -133,7 +146,7 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
   extern __shared__ __align__(1024) unsigned char smem[];
   constexpr int GR = S::kGroups;
   __shared__ float all_wm[GR * W][16], all_wl[GR * W][16], all_share[GR * W][16];
-  __shared__ int scan[GR * W];
+  __shared__ int scan[GR * W], scan_some[F4 ? GR * W : 1];
   int* cum = reinterpret_cast<int*>(smem + GR * S::kRing);   // [B + 1] units before each sequence (B > 32)
   griddep_launch_dependents();
   griddep_wait();
@@ -149,6 +162,10 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
   const int HS = a.kv.Hkv * a.gt;   // segments of a sequence
 
   // units before each sequence: in every warp's lanes, or in shared memory past 32 sequences
+  // NVFP4: a segment's first units may stand for the cost of a piece's copies beginning and its results being
+  // joined, `charge` of them
+  auto charge_of = [&](int units) { return (int64_t)units * HS >= (int64_t)kChargeFrom * blocks ? S::kCharge : 0; };
+  int charge = 0;
   int inc = 0;       // B <= 32: units up to and with sequence `lane`
   int all;
   if (a.B <= 32) {
@@ -165,15 +182,22 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
       if (lane >= o) inc += v;
     }
     all = __shfl_sync(0xffffffffu, inc, 31);
+    if constexpr (F4) {
+      const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
+      charge = charge_of(all);
+      inc += charge * __popc(some & (0xffffffffu >> (31 - lane)));
+      all += charge * __popc(some);
+    }
   } else {
     const int per = (a.B + GR * W * 32 - 1) / (GR * W * 32);
     const int b0 = threadIdx.x * per;
-    int mine = 0;
+    int mine = 0, some = 0;   // units, sequences with any
     for (int b = b0; b < min(b0 + per, a.B); ++b) {
       int first, n;
       const int len = length_of(a, b);
       span(len, a.window, S::kUnit, first, n);
       mine += n;
+      some += n > 0;
       if (blockIdx.x == 0 && a.seq_lens[b] > len) atomicOr(a.err, kErrBadPage);
     }
     int upto = mine;
@@ -183,14 +207,36 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
       if (lane >= o) upto += v;
     }
     if (lane == 31) scan[threadIdx.x >> 5] = upto;
+    int some_upto = some;
+    if constexpr (F4) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, some_upto, o);
+        if (lane >= o) some_upto += v;
+      }
+      if (lane == 31) scan_some[threadIdx.x >> 5] = some_upto;
+    }
     __syncthreads();
     int at = upto - mine;
-    for (int w = 0; w < (int)(threadIdx.x >> 5); ++w) at += scan[w];
+    if constexpr (F4) {
+      int units = 0, before = some_upto - some;
+#pragma unroll
+      for (int w = 0; w < GR * W; ++w) {
+        const bool ahead = w < (int)(threadIdx.x >> 5);
+        units += scan[w];
+        at += ahead ? scan[w] : 0;
+        before += ahead ? scan_some[w] : 0;
+      }
+      charge = charge_of(units);
+      at += charge * before;
+    } else {
+      for (int w = 0; w < (int)(threadIdx.x >> 5); ++w) at += scan[w];
+    }
     for (int b = b0; b < min(b0 + per, a.B); ++b) {
       int first, n;
       span(length_of(a, b), a.window, S::kUnit, first, n);
       cum[b] = at;
-      at += n;
+      at += n + (n > 0 ? charge : 0);
     }
     if (b0 < a.B && b0 + per >= a.B) cum[a.B] = at;
     __syncthreads();
@@ -233,7 +279,7 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
     int first, units;
     span(len, a.window, S::kUnit, first, units);
     const int64_t local = u - (int64_t)before * HS;
-    const int cost = units << hl;   // of HW heads
+    const int cost = (units + charge) << hl;   // of HW heads
     const int hg = (int)(local / cost);
     const int u0 = (int)(local - (int64_t)hg * cost);
     const int n_units = (int)min((int64_t)(cost - u0), u_end - u);
@@ -248,8 +294,9 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
                     (int)((s1 - 1) / quota));
     }
     // this warp's keys of the piece: key0 + i * unit .. + KT - 1 in step i, up to key1
-    const int piece0 = first / S::kUnit * S::kUnit + u0 * unit;
-    const int key1 = min(len, piece0 + n_units * unit), key0 = piece0 + stripe * KT;
+    const int at0 = max(u0 - (charge << hl), 0), at1 = max(u0 + n_units - (charge << hl), 0);
+    const int piece0 = first / S::kUnit * S::kUnit + at0 * unit;
+    const int key1 = min(len, first / S::kUnit * S::kUnit + at1 * unit), key0 = piece0 + stripe * KT;
     const int n_sub = key1 > key0 ? (key1 - key0 + unit - 1) >> (kUnitLog2 - hl) : 0;
     float o[NG][MT][4], m[NG][2], l[NG][2];
 #pragma unroll

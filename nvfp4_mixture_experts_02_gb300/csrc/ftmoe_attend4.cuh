@@ -4,6 +4,17 @@
 // keys r and r + 8 as the row operand of k q^T, and D/8 consecutive elements, from r D/8 on, of keys 2c, 2c + 1,
 // 2c + 8 and 2c + 9 as that of v^T p^T: whole words of codes under one scale or two. Products do not care which
 // element is which column (q is laid out to match), nor which key is which row.
+//
+// A code becomes f16 by one conversion for two and one multiplication by its scale (e2m1 * e4m3 has six significant
+// bits), so a step of 32 keys of 128 elements issues 604 instructions (256 of them these), which the 12 warps of an SM
+// overlap with the copies: products of the next step and values of this one are independent and stand side by side.
+// A weight is one f16: 11 bits, a relative error of 2^-12 where the outputs are rounded to 2^-9 and the values hold four
+// bits. The rest as a second f16, as for E4M3 caches, costs 8 % (48 ragged sequences 57.3 -> 62.2 us) to 13 % (three
+// long ones 57.1 -> 64.3): twice the products.
+// Measured and not kept: 16 warps of 128 registers (spills and two stages: 123 us for 103 at 64 x 6500, with three
+// stages 109), four stages for three (no change), groups held to the slowest one's pace (2 to 5 % slower), copies of
+// whole tiles by the tensor memory accelerator (rows of 64 bytes at 6.5 TB/s for 6.7, of 32 at 4.6 for 5.2 in a copy
+// of the same pattern), hints that fetch 128 or 256 bytes into L2 (no change).
 #pragma once
 
 #include <cmath>
