@@ -1,6 +1,6 @@
 """One decode step of a transformer block around the MoE layer, on one GPU.
 
-    python examples/decode_block.py [--batch 4] [--steps 16] [--layers 2]
+    python examples/decode_block.py [--batch 4] [--steps 16] [--layers 2] [--cache bf16|nvfp4]
 
 Every layer runs, for the next token of each sequence of a batch,
 
@@ -13,8 +13,9 @@ Every layer runs, for the next token of each sequence of a batch,
     r, x  = r + s * gate * norm(y), norm(r)           residual_norm
 
 and the last x gives the next-token logits (nvfp4_linear, float32). The step reads positions and
-lengths from device tensors, so one CUDA graph serves every step. The weights are random: the
-program shows the calls, their order and their buffers.
+lengths from device tensors, so one CUDA graph serves every step. With --cache nvfp4 the keys and
+values are kept in four bits. The weights are random: the program shows the calls, their order and
+their buffers.
 """
 from __future__ import annotations
 
@@ -29,6 +30,7 @@ import torch  # noqa: E402
 from nvfp4_mixture_experts_02_gb300 import ftmoe  # noqa: E402
 
 EPS = 1e-6
+KV_GSCALE = 0.005   # of a four-bit cache: block scales up to 448 reach magnitudes of 6 * 448 * 0.005 = 13
 
 
 class Layer:
@@ -111,7 +113,7 @@ def random_matrix(N, K, device):
 
 
 def random_model(batch, n_layers, device, H=1024, Hq=8, Hkv=2, D=128, E=16, k=4, I=512, vocabulary=1000,
-                 page=16, room=256):
+                 page=16, room=256, cache="bf16"):
     ones = lambda: torch.ones(H, dtype=torch.bfloat16, device=device)  # noqa: E731
     byte = lambda *s: torch.randint(0, 256, s, dtype=torch.uint8, device=device)  # noqa: E731
     block = lambda *s: torch.randint(0x28, 0x38, s, dtype=torch.uint8, device=device)  # noqa: E731
@@ -125,8 +127,12 @@ def random_model(batch, n_layers, device, H=1024, Hq=8, Hkv=2, D=128, E=16, k=4,
         layers.append(Layer(random_matrix((Hq + 2 * Hkv) * D, H, device), random_matrix(H, Hq * D, device),
                             (0.03 * torch.randn(E, H, device=device)).bfloat16(), experts, ones(), ones(),
                             ones(), ones(), ones(), k))
-        pool = lambda: torch.zeros((batch * width, page, Hkv, D), dtype=torch.bfloat16, device=device)  # noqa: E731
-        caches.append(ftmoe.PagedKVCache(pool(), pool()))
+        pool = lambda w, t: torch.zeros((batch * width, page, Hkv, w), dtype=t, device=device)  # noqa: E731
+        if cache == "nvfp4":
+            codes, scales = (lambda: pool(D // 2, torch.uint8)), (lambda: pool(D // 16, torch.uint8))
+            caches.append(ftmoe.NvFP4KVCache(codes(), codes(), scales(), scales(), KV_GSCALE, KV_GSCALE))
+        else:
+            caches.append(ftmoe.PagedKVCache(pool(D, torch.bfloat16), pool(D, torch.bfloat16)))
     return DecodeStep(layers, caches, table, rotary_table(room, D, device), Hq, ones(),
                       random_matrix(vocabulary, H, device), batch, scale=0.5)
 
@@ -136,10 +142,11 @@ def main():
     ap.add_argument("--batch", type=int, default=4)
     ap.add_argument("--steps", type=int, default=16)
     ap.add_argument("--layers", type=int, default=2)
+    ap.add_argument("--cache", choices=("bf16", "nvfp4"), default="bf16")
     args = ap.parse_args()
     device = torch.device("cuda")
     torch.manual_seed(0)
-    model = random_model(args.batch, args.layers, device)
+    model = random_model(args.batch, args.layers, device, cache=args.cache)
     embedding = torch.randn(1000, model.x.shape[1], device=device).bfloat16()
     x_in = embedding[:args.batch].clone()
     model.step(x_in)   # one eager step before the capture: per-device set-up

@@ -77,7 +77,8 @@ def test_gather(m, four, over, expect):  # noqa: F811
     (dict(B=-1), 1), (dict(B=4097), 2), (dict(Hq=0), 1), (dict(Hq=5), 1), (dict(Hq=2048), 2),
     (dict(window=-1), 1), (dict(scale=NAN), 1), (dict(width=-1), 1), (dict(B=0, q=0), 0), (dict(q=0), 1),
     (dict(table=0), 1), (dict(lens=0), 1), (dict(out=0), 1), (dict(ws=0), 1), (dict(q=0x30008), 3),
-    (dict(q_stride=260), 3), (dict(lse=0x60002), 3), (dict(ws=0x90010), 3), (dict(bytes=4096), 4)])
+    (dict(q_stride=260), 3), (dict(lse=0x60002), 3), (dict(ws=0x90010), 3), (dict(bytes=4096), 4),
+    (dict(kp=1 << 35), 2), (dict(vs=1 << 33), 2), (dict(ksp=1 << 33), 2), (dict(vsh=1 << 34), 2)])
 def test_attention(m, over, expect):  # noqa: F811
     over = dict(over)
     c = _cache4(m, over)
