@@ -672,6 +672,7 @@ __device__ __forceinline__ void add_pieces(const float2* ml, const float (*y)[E]
 template <int D, int W, int kJoinWarps, int kFlight>   // kFlight: pieces of a warp in flight
 __global__ void __launch_bounds__(kJoinWarps * 32, kJoinWarps == 8 ? 3 : 1) k_join(const AttendArgs a) {
   constexpr int E = D / 32;
+  static_assert(kJoinWarps % kTeam == 0);   // whole teams
   __shared__ float sums[kJoinWarps][D], wm[kJoinWarps], wl[kJoinWarps];
   griddep_launch_dependents();
   griddep_wait();
@@ -829,7 +830,7 @@ cudaError_t launch_d(AttendArgs a, int num_sms, cudaStream_t stream) {
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, k_attend<D, DT, NG>, a)) != cudaSuccess) return e;
   // Warps of a block of k_join. NVFP4: eight, so that all blocks run at once (48 ragged sequences 58.2 us, 60.5 with
-  // sixteen; one of 777 keys 6.8 us with either).
+  // sixteen of as many registers, 57.2 for 56.3 with sixteen of 40; one of 777 keys 6.7, 6.8 and 7.8).
   constexpr int kJoinWarps = DT == kKvNvfp4 ? 8 : 16;
   cfg.gridDim = dim3((unsigned)(S::kBlocks * S::kGroups * num_sms));   // a block for every run
   cfg.blockDim = dim3(kJoinWarps * 32);
