@@ -744,18 +744,24 @@ _RES = (torch.bfloat16, torch.float32)
 def _need_rows(t, name, dev, inner):
     """t on cuda:dev, bf16 bits [T, *inner] whose rows are contiguous: the distance between rows
     may be larger than a row (a slice of a wider tensor). Returns it, in elements."""
-    shape = t.shape
     if t.get_device() != dev:
         raise ValueError(f"{name}: expected a tensor on cuda:{dev}, got one on {t.device}")
     if t.dtype not in BF16_BITS:
         raise TypeError(f"{name}: element type {t.dtype} is not accepted here")
-    if shape[1:] != inner:
+    shape, stride = t.shape, t.stride()
+    if len(inner) == 2 and len(shape) == 3:   # the usual heads of tokens, without more tuples
+        T, n, last = shape
+        row, fits = n * last, n == inner[0] and last == inner[1]
+        dense = (stride[2] == 1 or last == 1) and (stride[1] == last or n == 1)
+    else:
+        T, row, last = shape[0] if shape else 0, inner[-1], inner[-1]
+        fits = len(inner) == 1 and shape[1:] == inner
+        dense = fits and (stride[1] == 1 or last == 1)
+    if not fits:
         raise ValueError(f"{name}: shape {tuple(shape)}, expected [T, {', '.join(map(str, inner))}]")
-    stride, last = t.stride(), inner[-1]
-    row = last if len(inner) == 1 else inner[0] * last
-    if (stride[-1] != 1 and last != 1) or (len(inner) == 2 and stride[1] != last and inner[0] != 1):
+    if not dense:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    if shape[0] <= 1:
+    if T <= 1:
         return row
     if stride[0] < row:
         raise ValueError(f"{name}: the rows must not overlap")
@@ -942,14 +948,15 @@ class RopeAxes:
         return RopeAxes(tuple(axes))
 
 
-def _tokens(cache, block_table, positions, seq_ids, T, dev):
+def _tokens(block_table, positions, seq_ids, T, dev):
     """The places of T tokens in a cache: block_table [B,width], positions [T], seq_ids [T] or None.
     Returns (B, width)."""
-    if block_table.dim() != 2:
+    shape = block_table.shape
+    if len(shape) != 2:
         raise ValueError("block_table: [B, width] expected")
     _need(block_table, "block_table", dev, _I32, None)
     _need(positions, "positions", dev, _I32, (T,))
-    B, width = block_table.shape
+    B, width = shape
     if T > _MAX_I32 or B > _MAX_I32 or width > _MAX_I32:
         raise ValueError(f"{T} tokens, block_table [{B}, {width}]: too large")
     if seq_ids is not None:
@@ -985,14 +992,14 @@ def kv_append(k, v, cache, block_table, positions, seq_ids=None, q=None, rope=No
     dev, inner = cache.device_index, cache.heads
     if k.dim() != 3 or block_table.dim() != 2:
         raise ValueError("k [T, Hkv, D] and block_table [B, width] expected")
-    T, D = k.shape[0], inner[1]
+    T, D = len(k), inner[1]
     ks, vs = _need_rows(k, "k", dev, inner), _need_rows(v, "v", dev, inner)
-    if v.shape[0] != T:
+    if len(v) != T:
         raise ValueError("v: as many tokens as k expected")
-    B, width = _tokens(cache, block_table, positions, seq_ids, T, dev)
+    B, width = _tokens(block_table, positions, seq_ids, T, dev)
     Hq = qs = qp = qo = 0
     if q is not None:
-        if q.dim() != 3 or q.shape[0] != T:
+        if q.dim() != 3 or len(q) != T:
             raise ValueError("q: [T, Hq, D] expected")
         Hq = q.shape[1]
         qs = _need_rows(q, "q", dev, (Hq, D))
@@ -1023,23 +1030,20 @@ def kv_append(k, v, cache, block_table, positions, seq_ids=None, q=None, rope=No
     elif rope_positions is not None:
         raise ValueError("rope_positions: rope_axes is required with them")
     workspace = _flags(workspace, T, dev)
-    where = (block_table.data_ptr(), B, width, 0 if seq_ids is None else seq_ids.data_ptr(),
-             positions.data_ptr(), rp, rows, dim)
     ws = 0 if workspace is None else workspace.data_ptr()
-    if type(cache) is NvFP4KVCache:
-        name = "ft_nvfp4_kv_append"
-        st = _LIB.ft_nvfp4_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, qo, T, Hq, cache._ref, *where,
-                                     axes, ws, _stream(None, dev))
-    elif axes is not None:
-        name = "ft_kv_append_axes"
-        st = _LIB.ft_kv_append_axes(k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, qo, T, Hq, cache._ref, *where,
-                                    axes, ws, _stream(None, dev))
+    four = type(cache) is NvFP4KVCache
+    if four or axes is not None:
+        st = (_LIB.ft_nvfp4_kv_append if four else _LIB.ft_kv_append_axes)(
+            k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, qo, T, Hq, cache._ref, block_table.data_ptr(), B, width,
+            0 if seq_ids is None else seq_ids.data_ptr(), positions.data_ptr(), rp, rows, dim, axes, ws,
+            _stream(None, dev))
     else:
-        name = "ft_kv_append"
-        st = _LIB.ft_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, qo, T, Hq, cache._ref, *where, ws,
-                               _stream(None, dev))
+        st = _LIB.ft_kv_append(
+            k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, qo, T, Hq, cache._ref, block_table.data_ptr(), B, width,
+            0 if seq_ids is None else seq_ids.data_ptr(), positions.data_ptr(), rp, rows, dim, ws,
+            _stream(None, dev))
     if st != FT_OK:
-        _check(st, name)
+        _check(st, "ft_nvfp4_kv_append" if four else "ft_kv_append" if axes is None else "ft_kv_append_axes")
     return q_out if q is not None else None
 
 
@@ -1056,7 +1060,7 @@ def kv_gather(cache, block_table, positions, seq_ids=None, k_out=None, v_out=Non
     if positions.dim() != 1:
         raise ValueError("positions: [T] expected")
     T = positions.shape[0]
-    B, width = _tokens(cache, block_table, positions, seq_ids, T, dev)
+    B, width = _tokens(block_table, positions, seq_ids, T, dev)
     shape = (T, *inner)
     if k_out is None:
         k_out = torch.empty(shape, dtype=torch.bfloat16, device=positions.device)
