@@ -372,7 +372,7 @@ __device__ __forceinline__ void attend_piece4(const AttendArgs& a, char* ring, i
           t = __fsub_ru(t, kSet4);   // upwards: no weight above 2^kSet4 at any size of t
           n[e] = none ? t : fmaxf(old, t);
           f[e] = none ? 0.f : exp2_fast(old - n[e]);
-          bar[g][e] = n[e] + kTop4;
+          bar[g][e] = __fadd_rd(n[e], kTop4);   // downwards: no weight above 2^kTop4 either
           if (n[e] == -INFINITY) n[e] = 0.f;   // no key yet: every weight is 0
         }
         less[g] = pair(-n[0], -n[1]);

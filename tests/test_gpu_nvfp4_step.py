@@ -190,3 +190,31 @@ def test_a_scale_below_zero_and_large_scores():
         assert np.all(np.abs(f64(lse)[0] - rlse) <= 2.0 ** -18 * np.abs(rlse) + 4e-5)
         if scale != 3.0:                                  # scores of hundreds: float32 moves them by more than a weight's step
             close(out[0], ref, mag, 2.0 ** -10, scale)
+
+
+def test_scores_whose_steps_are_larger_than_a_weights_range():
+    """Scores of 2^27 in units of log 2, where neighbouring float32 lie 16 apart: a weight is 1 or at least 2^16 times
+    another's, and no sum may overflow on the way from one to the other."""
+    m = ftmoe()
+    for ahead in (1, 2, 3):
+        n, D2 = 96, 64
+        codes = np.zeros((6, 16, 1, D2 // 2), np.uint8)
+        scales = np.full((6, 16, 1, D2 // 16), 0x38, np.uint8)   # 1
+        scales[..., 0] = 0x70                                    # 128
+        codes[..., 0] = 6                                        # 4 * 128 = 512 in element 0
+        late = codes.reshape(n, D2 // 2)
+        late[40:80, 8] = 2 * 1                                   # 1 in element 16 of keys 40 to 79
+        late[80:, 8] = (0, 2, 4, 5)[ahead]                       # 1, 2 or 3 in that of keys 80 on
+        vals = np.random.default_rng(ahead).integers(0, 256, codes.shape).astype(np.uint8)
+        q = torch.zeros((1, 1, D2))
+        q[0, 0, 0], q[0, 0, 16] = 2.0 ** 14, 1.0                 # products of 2^23 and 1, 2 or 3
+        cache = m.NvFP4KVCache(*(torch.from_numpy(a).cuda() for a in (codes, vals, scales, np.full_like(scales, 0x38))))
+        table = torch.arange(6, dtype=torch.int32)[None].cuda()
+        out, lse = m.paged_decode_attention(q.bfloat16().cuda(), cache, table, torch.tensor([n], dtype=torch.int32).cuda(),
+                                            scale=16 * float(np.log(2)))
+        vs = ob.nvfp4_values(vals, np.full_like(scales, 0x38), 1.0).reshape(n, 1, D2).astype(np.float64)
+        # the keys with the largest product, all alike: the others' weights are 2^-16 of theirs at most
+        best = slice(40, n) if ahead == 1 else slice(80, n)
+        want, mag = vs[best, 0].mean(0), np.abs(vs[best, 0]).mean(0)
+        close(out[0], want[None], np.maximum(mag, 6.0)[None], 2.0 ** -10 + 40 * 2.0 ** -16)
+        assert torch.isfinite(lse).all()
