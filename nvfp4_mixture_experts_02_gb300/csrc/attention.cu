@@ -36,7 +36,7 @@
 // length, page, keys, scores, sums, join.
 // NVFP4: the three 56 us (270 MB, 71 %), the 48 56 us (239 MB, 63 %), 64 of 6500 91.5 us with pages head by head and 97
 // slot by slot (481 MB, 78 and 73 %): the products' own part runs at 93 % of the copy rate (870 of the 806 cycles that
-// a step's bytes take, of which 604 issue an instruction); the first data arrive after 4.5 us and the join takes 7.
+// a step's bytes take, of which 548 issue an instruction); the first data arrive after 4.5 us and the join takes 7.
 // Without any arithmetic those take 83 and 92 us. With heads of 64 (200 sequences, a window of 1023: 30 us for 7.4)
 // rows of 32 bytes copy at 77 % and a step has as many instructions for half the bytes; with 16 heads a key head the
 // warp products' rate bounds the steps (64 products of 16 cycles in 1225; heads of 256: 46 us for 14.6).
@@ -126,10 +126,13 @@ __device__ __forceinline__ void store_row(const AttendArgs& a, int64_t at, float
 // A sequence's length, cut to what its row of the block table can hold.
 __device__ __forceinline__ int length_of(const AttendArgs& a, int b) { return min(a.seq_lens[b], a.max_len); }
 
-// First key and number of units of a sequence.
-__device__ __forceinline__ void span(int len, int window, int unit, int& first, int& units) {
+// First key, number of units of a sequence and the first unit's first key: a multiple of the unit, or (NVFP4, whose
+// copies find each key's page) the first key itself, which saves a window up to a unit of steps.
+template <int DT>
+__device__ __forceinline__ void span(int len, int window, int unit, int& first, int& units, int& base) {
   first = window > 0 && len > window ? len - window : 0;
-  units = len > 0 ? (len + unit - 1) / unit - first / unit : 0;
+  base = DT == kKvNvfp4 ? first : first / unit * unit;
+  units = len > 0 ? (len - base + unit - 1) / unit : 0;
 }
 
 template <int D, int DT, int NG>
@@ -169,10 +172,10 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
   int inc = 0;       // B <= 32: units up to and with sequence `lane`
   int all;
   if (a.B <= 32) {
-    int first, n = 0;
+    int first, base, n = 0;
     if (lane < a.B) {
       const int len = length_of(a, lane);
-      span(len, a.window, S::kUnit, first, n);
+      span<DT>(len, a.window, S::kUnit, first, n, base);
       if (block == 0 && warp == 0 && a.seq_lens[lane] > len) atomicOr(a.err, kErrBadPage);
     }
     inc = n;
@@ -193,9 +196,9 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
     const int b0 = threadIdx.x * per;
     int mine = 0, some = 0;   // units, sequences with any
     for (int b = b0; b < min(b0 + per, a.B); ++b) {
-      int first, n;
+      int first, base, n;
       const int len = length_of(a, b);
-      span(len, a.window, S::kUnit, first, n);
+      span<DT>(len, a.window, S::kUnit, first, n, base);
       mine += n;
       some += n > 0;
       if (blockIdx.x == 0 && a.seq_lens[b] > len) atomicOr(a.err, kErrBadPage);
@@ -233,8 +236,8 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
       for (int w = 0; w < (int)(threadIdx.x >> 5); ++w) at += scan[w];
     }
     for (int b = b0; b < min(b0 + per, a.B); ++b) {
-      int first, n;
-      span(length_of(a, b), a.window, S::kUnit, first, n);
+      int first, base, n;
+      span<DT>(length_of(a, b), a.window, S::kUnit, first, n, base);
       cum[b] = at;
       at += n + (n > 0 ? charge : 0);
     }
@@ -276,8 +279,8 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
       before = cum[b];
     }
     const int len = length_of(a, b);
-    int first, units;
-    span(len, a.window, S::kUnit, first, units);
+    int first, units, base;
+    span<DT>(len, a.window, S::kUnit, first, units, base);
     const int64_t local = u - (int64_t)before * HS;
     const int cost = (units + charge) << hl;   // of HW heads
     const int hg = (int)(local / cost);
@@ -295,8 +298,8 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
     }
     // this warp's keys of the piece: key0 + i * unit .. + KT - 1 in step i, up to key1
     const int at0 = max(u0 - (charge << hl), 0), at1 = max(u0 + n_units - (charge << hl), 0);
-    const int piece0 = first / S::kUnit * S::kUnit + at0 * unit;
-    const int key1 = min(len, first / S::kUnit * S::kUnit + at1 * unit), key0 = piece0 + stripe * KT;
+    const int piece0 = base + at0 * unit;
+    const int key1 = min(len, base + at1 * unit), key0 = piece0 + stripe * KT;
     const int n_sub = key1 > key0 ? (key1 - key0 + unit - 1) >> (kUnitLog2 - hl) : 0;
     float o[NG][MT][4], m[NG][2], l[NG][2];
 #pragma unroll

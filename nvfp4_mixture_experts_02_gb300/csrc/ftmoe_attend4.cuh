@@ -6,7 +6,7 @@
 // element is which column (q is laid out to match), nor which key is which row.
 //
 // A code becomes f16 by one conversion for two and one multiplication by its scale (e2m1 * e4m3 has six significant
-// bits), so a step of 32 keys of 128 elements issues 604 instructions (256 of them these), which the 12 warps of an SM
+// bits), so a step of 32 keys of 128 elements issues 548 instructions (256 of them these), which the 12 warps of an SM
 // overlap with the copies: products of the next step and values of this one are independent and stand side by side.
 // A weight is one f16: 11 bits, a relative error of 2^-12 where the outputs are rounded to 2^-9 and the values hold four
 // bits. The rest as a second f16, as for E4M3 caches, costs 8 % (48 ragged sequences 57.3 -> 62.2 us) to 13 % (three
