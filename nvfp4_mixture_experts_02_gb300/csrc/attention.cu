@@ -94,6 +94,10 @@ constexpr int kLongRun = 4;
 // 57.2 and 58.6 us, 100 up to 4000 51.2, 48.0, 50.3 and 52.9, 19 of 22272 89.5, 92.5, 91.6 and 93.3; with heads of 256
 // (units half as long) 13 up to 24001 50.2, 47.8, 47.4 and 45.9, 16 of 8192 43.1, 40.7, 39.9 and 39.9.
 constexpr int kChargeFrom = 12;
+// NVFP4: no segment is cut, and none is left to the join, where the longest is no more than this many units longer than
+// a run; a run then takes the segments that begin in it. 32 sequences with a window of 512 17.3 -> 13.2 us, 60 ragged
+// ones up to 300 9.0 -> 8.2; with eight units 128 of 512 would take 31.7 us for 28.3, one of 777 10.8 for 6.8.
+constexpr int kUncut = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // log2 of the largest weight. f16 holds 11 bits of weights down to 2^-14 and nothing under 2^-25: with
@@ -149,7 +153,7 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
   extern __shared__ __align__(1024) unsigned char smem[];
   constexpr int GR = S::kGroups;
   __shared__ float all_wm[GR * W][16], all_wl[GR * W][16], all_share[GR * W][16];
-  __shared__ int scan[GR * W], scan_some[F4 ? GR * W : 1];
+  __shared__ int scan[GR * W], scan_some[F4 ? GR * W : 1], scan_most[F4 ? GR * W : 1];
   int* cum = reinterpret_cast<int*>(smem + GR * S::kRing);   // [B + 1] units before each sequence (B > 32)
   griddep_launch_dependents();
   griddep_wait();
@@ -169,6 +173,7 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
   // joined, `charge` of them
   auto charge_of = [&](int units) { return (int64_t)units * HS >= (int64_t)kChargeFrom * blocks ? S::kCharge : 0; };
   int charge = 0;
+  int longest = 0;   // units of a sequence at most
   int inc = 0;       // B <= 32: units up to and with sequence `lane`
   int all;
   if (a.B <= 32) {
@@ -187,6 +192,7 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
     all = __shfl_sync(0xffffffffu, inc, 31);
     if constexpr (F4) {
       const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
+      longest = __reduce_max_sync(0xffffffffu, n);
       charge = charge_of(all);
       inc += charge * __popc(some & (0xffffffffu >> (31 - lane)));
       all += charge * __popc(some);
@@ -194,13 +200,14 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
   } else {
     const int per = (a.B + GR * W * 32 - 1) / (GR * W * 32);
     const int b0 = threadIdx.x * per;
-    int mine = 0, some = 0;   // units, sequences with any
+    int mine = 0, some = 0, most = 0;   // units, sequences with any, units of one
     for (int b = b0; b < min(b0 + per, a.B); ++b) {
       int first, base, n;
       const int len = length_of(a, b);
       span<DT>(len, a.window, S::kUnit, first, n, base);
       mine += n;
       some += n > 0;
+      most = max(most, n);
       if (blockIdx.x == 0 && a.seq_lens[b] > len) atomicOr(a.err, kErrBadPage);
     }
     int upto = mine;
@@ -217,7 +224,11 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
         const int v = __shfl_up_sync(0xffffffffu, some_upto, o);
         if (lane >= o) some_upto += v;
       }
-      if (lane == 31) scan_some[threadIdx.x >> 5] = some_upto;
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (lane == 31) {
+        scan_some[threadIdx.x >> 5] = some_upto;
+        scan_most[threadIdx.x >> 5] = most;
+      }
     }
     __syncthreads();
     int at = upto - mine;
@@ -229,6 +240,7 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
         units += scan[w];
         at += ahead ? scan[w] : 0;
         before += ahead ? scan_some[w] : 0;
+        longest = max(longest, scan_most[w]);
       }
       charge = charge_of(units);
       at += charge * before;
@@ -259,7 +271,8 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
     else if constexpr (GR == 1) __syncthreads();
     else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(W * 32) : "memory");
   };
-  if (u >= u_end && tid == 0) a.shared_segs[block] = make_int4(-1, 0, 0, 0);
+  const bool uncut = F4 && (int64_t)((longest + charge) << hl) <= quota + kUncut;
+  if ((uncut || u >= u_end) && tid == 0) a.shared_segs[block] = make_int4(-1, 0, 0, 0);
 
   while (u < u_end) {
     // the piece that begins at u: sequence b, with `before` units ahead of it
@@ -285,11 +298,15 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
     const int cost = (units + charge) << hl;   // of HW heads
     const int hg = (int)(local / cost);
     const int u0 = (int)(local - (int64_t)hg * cost);
-    const int n_units = (int)min((int64_t)(cost - u0), u_end - u);
+    if (uncut && u0 > 0) {   // the run's that the segment begins in
+      u += cost - u0;
+      continue;
+    }
+    const int n_units = uncut ? cost : (int)min((int64_t)(cost - u0), u_end - u);
     const int hs = hg * HW + hw;
     const int kvh = hs / a.gt, g0 = (hs - kvh * a.gt) * 16;
     const int G = min(a.group - g0, 16);
-    if (u == quota * block && tid == 0) {
+    if (!uncut && u == quota * block && tid == 0) {
       // for k_join: the segment that this run goes on with, if it does not begin here
       const int64_t s0 = u - u0, s1 = s0 + cost;
       a.shared_segs[block] =
