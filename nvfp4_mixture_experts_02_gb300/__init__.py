@@ -6,8 +6,8 @@
     y = ftmoe.decode(x, idx, w, experts, shared)      # T <= 64
     y = ftmoe.prefill(x, idx, w, experts, shared)     # any T
 
-and the operators between two such layers: nvfp4_linear, kv_append, paged_decode_attention,
-residual_norm and residual_norm_backward.
+and the operators between two such layers: nvfp4_linear, kv_append, kv_gather and paged_decode_attention (over
+caches in bf16, E4M3 or NVFP4), residual_norm and residual_norm_backward.
 
 Importing ``ftmoe`` needs the built library; build it with ``build.build()``.
 """

@@ -1031,7 +1031,7 @@ def kv_append(k, v, cache, block_table, positions, seq_ids=None, q=None, rope=No
         raise ValueError("rope_positions: rope_axes is required with them")
     workspace = _flags(workspace, T, dev)
     ws = 0 if workspace is None else workspace.data_ptr()
-    four = type(cache) is NvFP4KVCache
+    four = isinstance(cache, NvFP4KVCache)
     if four or axes is not None:
         st = (_LIB.ft_nvfp4_kv_append if four else _LIB.ft_kv_append_axes)(
             k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, qo, T, Hq, cache._ref, block_table.data_ptr(), B, width,
@@ -1071,7 +1071,7 @@ def kv_gather(cache, block_table, positions, seq_ids=None, k_out=None, v_out=Non
     else:
         _need(v_out, "v_out", dev, BF16_BITS, shape)
     workspace = _flags(workspace, T, dev)
-    four = type(cache) is NvFP4KVCache
+    four = isinstance(cache, NvFP4KVCache)
     st = (_LIB.ft_nvfp4_kv_gather if four else _LIB.ft_kv_gather)(
         cache._ref, block_table.data_ptr(), B, width, 0 if seq_ids is None else seq_ids.data_ptr(),
         positions.data_ptr(), T, k_out.data_ptr(), v_out.data_ptr(),
@@ -1096,8 +1096,9 @@ def _attention_bytes(B, D, dev) -> int:   # a size of the device's, asked for on
 def paged_decode_attention(q, cache, block_table, seq_lens, scale=None, window=0,
                            out=None, lse=None, workspace=None, stream=None):
     """ft_paged_decode_attention: q bf16 [B,Hq,D], one new token per sequence, over the first
-    seq_lens int32 [B] slots of each in the cache (PagedKVCache or NvFP4KVCache) (the last `window` of them if window > 0) through block_table
-    int32 [B,width]. scale: 1/sqrt(D) by default. Returns (out bf16 [B,Hq,D], lse f32 [B,Hq])."""
+    seq_lens int32 [B] slots of each (the last `window` of them if window > 0) in the cache (a PagedKVCache
+    or NvFP4KVCache) through block_table int32 [B,width]. scale: 1/sqrt(D) by default. Returns (out bf16
+    [B,Hq,D], lse f32 [B,Hq])."""
     if stream is not None:
         with torch.cuda.stream(stream):   # what the call makes belongs to the stream that it runs on
             return paged_decode_attention(q, cache, block_table, seq_lens, scale, window, out, lse,
@@ -1126,7 +1127,7 @@ def paged_decode_attention(q, cache, block_table, seq_lens, scale=None, window=0
         _need(workspace, "workspace", dev, None, None)
     elif B > 0:
         workspace = _scratch(_attention_bytes(B, D, dev), dev)
-    four = type(cache) is NvFP4KVCache
+    four = isinstance(cache, NvFP4KVCache)
     st = (_LIB.ft_nvfp4_paged_decode_attention if four else _LIB.ft_paged_decode_attention)(
         q.data_ptr(), qs, B, Hq, cache._ref, block_table.data_ptr(), width, seq_lens.data_ptr(),
         D ** -0.5 if scale is None else scale, window, out.data_ptr(), lse.data_ptr(),
