@@ -37,8 +37,8 @@
 // NVFP4: the three 56 us (270 MB, 71 %), the 48 56 us (239 MB, 63 %), 64 of 6500 91.5 us with pages head by head and 97
 // slot by slot (481 MB, 78 and 73 %): the products' own part runs at 93 % of the copy rate (870 of the 806 cycles that
 // a step's bytes take, of which 548 issue an instruction); the first data arrive after 4.5 us and the join takes 7.
-// Without any arithmetic those take 83 and 92 us. With heads of 64 (200 sequences, a window of 1023: 30 us for 7.4)
-// rows of 32 bytes copy at 77 % and a step has as many instructions for half the bytes; with 16 heads a key head the
+// Without any arithmetic those take 83 and 92 us. With heads of 64 (200 sequences, a window of 1023: 27 us for 7.4)
+// rows of 32 bytes copy at 77 % and as many bytes take a third more instructions; with 16 heads a key head the
 // warp products' rate bounds the steps (64 products of 16 cycles in 1225; heads of 256: 46 us for 14.6).
 #include <cmath>
 #include <cuda_runtime.h>
@@ -58,16 +58,17 @@ struct AttnShape {
   static constexpr int kRow = DT == kKvNvfp4 ? D / 2 : DT == FT_KV_E4M3 ? D : 2 * D;   // bytes of a key or value
   static constexpr int kCpr = kRow / 16;              // 16-byte pieces of it
   static constexpr int kScaleRow = DT == kKvNvfp4 ? D / 16 : 0;   // bytes of its block scales
-  static constexpr int kKeys = DT == kKvNvfp4 ? (D == 256 ? 16 : 32) : kRow <= 128 ? 32 : 16;   // keys of a warp's step
+  static constexpr int kKeys = DT == kKvNvfp4 ? 4096 / D : kRow <= 128 ? 32 : 16;   // keys of a warp's step
   static constexpr int kStageBytes = 2 * kKeys * (kRow + kScaleRow);   // those keys and values
   // blocks an SM: the others stream while one joins a piece's warps. Three of two stages each, not two of
   // three, where the registers allow it: 256 sequences up to 1024 with 8-bit keys of 128: 68 us for 79.
   // (Past some 2600 sequences their running sums in shared memory leave room for two.)
   static constexpr int kBlocks =
       kRow >= 512 || DT == kKvNvfp4 ? 1 : kRow == 128 && NG == 1 ? kAttendBlocks : 2;
-  // NVFP4: one block an SM, whose groups of warps each do what a block does otherwise
-  static constexpr int kGroups = DT != kKvNvfp4 ? 1 : D == 128 && NG == 1 ? kAttendBlocks : 2;
-  static constexpr int kWarps = (DT == kKvNvfp4 ? D >= 128 : kRow >= 128) ? 4 : 8;   // of a group
+  // NVFP4: one block an SM, whose groups of warps each do what a block does otherwise. With heads of 64 three groups of
+  // four warps at 64 keys a step, not two of eight at 32: 200 sequences with a window of 1023 27.2 us for 29.2.
+  static constexpr int kGroups = DT != kKvNvfp4 ? 1 : D == 64 || (D == 128 && NG == 1) ? kAttendBlocks : 2;
+  static constexpr int kWarps = DT == kKvNvfp4 || kRow >= 128 ? 4 : 8;   // of a group
   static constexpr int kQShared = DT != kKvNvfp4 || NG == 1 ? 0 : D == 256 ? 2 : D == 64 ? 1 : 0;   // groups of q in shared memory
   static constexpr int kQBytes = kQShared * (D / 16) * 256;
   static constexpr int kStages =

@@ -149,18 +149,23 @@ __device__ __forceinline__ void attend_piece4(const AttendArgs& a, char* ring, i
   const int lane = threadIdx.x & 31, c = lane & 3, r = lane >> 2;
   const int32_t* table = a.block_table + (int64_t)b * a.table_width;
 
-  // ---- copies: lane l looks after key l of a step
+  // ---- copies: lane l looks after keys l and, with 64 a step, l + 32 of it
   // offsets of rows in 16-byte pieces, of scales in rows of them: 32 bits (checked on the host)
-  int page = -1, slot = 0;
-  bool live = false;
+  constexpr int KL = KT > 32 ? KT / 32 : 1, KR = KT / KL;   // keys of a lane, keys between them
+  int page[KL], slot[KL];
+  bool live[KL];
   auto look_up = [&](int i) {
-    const int j = key0 + i * unit + lane;
-    live = i < n_sub && lane < KT && j >= first && j < key1;
-    page = -1;
-    if (live) {
-      const int col = (int)((__umulhi((uint32_t)a.div_mul, (uint32_t)j) + (uint32_t)j) >> a.div_shift);
-      slot = j - col * a.kv.page_size;
-      page = table[col];   // col < table_width: the length is cut to the table
+#pragma unroll
+    for (int z = 0; z < KL; ++z) {
+      const int j = key0 + i * unit + 32 * z + lane;
+      live[z] = i < n_sub && lane < KR && j >= first && j < key1;
+      page[z] = -1;
+      slot[z] = 0;
+      if (live[z]) {
+        const int col = (int)((__umulhi((uint32_t)a.div_mul, (uint32_t)j) + (uint32_t)j) >> a.div_shift);
+        slot[z] = j - col * a.kv.page_size;
+        page[z] = table[col];   // col < table_width: the length is cut to the table
+      }
     }
   };
   constexpr int CPR = ROW / 16, RPI = 32 / CPR;   // 16-byte pieces of a row, rows of one warp-wide copy
@@ -171,39 +176,42 @@ __device__ __forceinline__ void attend_piece4(const AttendArgs& a, char* ring, i
   const uint32_t to0 = smem_addr(ring);
   auto fetch = [&](int i, uint32_t stage) {   // the copies of step i, whose pages look_up has found
     if (i < n_sub) {
-      const bool in = (uint32_t)page < (uint32_t)a.kv.num_pages;
-      if (live && !in) atomicOr(a.err, kErrBadPage);   // no such page: read as zeros
-      // A key that is not there has codes and scales of zero.
-      const uint32_t p = in ? (uint32_t)page : 0u, s = in ? (uint32_t)slot : 0u;
-      const uint32_t st = to0 + stage;
-      const uint32_t ko = p * (uint32_t)(a.kv.k_page_stride >> 4) + s * (uint32_t)(a.kv.k_slot_stride >> 4);
-      const uint32_t kso = p * (uint32_t)(a.sc.k_page / SROW) + s * (uint32_t)(a.sc.k_slot / SROW);
-      uint32_t vo = ko, vso = kso;
-      if (!a.same_strides) {
-        vo = p * (uint32_t)(a.kv.v_page_stride >> 4) + s * (uint32_t)(a.kv.v_slot_stride >> 4);
-        vso = p * (uint32_t)(a.sc.v_page / SROW) + s * (uint32_t)(a.sc.v_slot / SROW);
-      }
-      if (KT == 32 || lane < KT) {
-        cp_async_scales<SROW>(st + KSC + lane * SROW, ksb + (uint64_t)kso * SROW, in);
-        cp_async_scales<SROW>(st + VSC + lane * SROW, vsb + (uint64_t)vso * SROW, in);
-      }
-      const uint32_t rows = __ballot_sync(0xffffffffu, in);
-      if (rows == 0xffffffffu >> (32 - KT) && a.same_strides) {   // as a rule
 #pragma unroll
-        for (int x = 0; x < KT / RPI; ++x) {
-          const uint32_t at = __shfl_sync(0xffffffffu, ko, x * RPI + lane / CPR);
-          const uint32_t to = st + piece4<D>(x * RPI + lane / CPR, ch);
-          copy16(to, kb + (uint64_t)at * 16);
-          copy16(to + V, vb + (uint64_t)at * 16);
+      for (int z = 0; z < KL; ++z) {
+        const bool in = (uint32_t)page[z] < (uint32_t)a.kv.num_pages;
+        if (live[z] && !in) atomicOr(a.err, kErrBadPage);   // no such page: read as zeros
+        // A key that is not there has codes and scales of zero.
+        const uint32_t p = in ? (uint32_t)page[z] : 0u, s = in ? (uint32_t)slot[z] : 0u;
+        const uint32_t st = to0 + stage + 32 * z * ROW, sc = to0 + stage + (32 * z + lane) * SROW;
+        const uint32_t ko = p * (uint32_t)(a.kv.k_page_stride >> 4) + s * (uint32_t)(a.kv.k_slot_stride >> 4);
+        const uint32_t kso = p * (uint32_t)(a.sc.k_page / SROW) + s * (uint32_t)(a.sc.k_slot / SROW);
+        uint32_t vo = ko, vso = kso;
+        if (!a.same_strides) {
+          vo = p * (uint32_t)(a.kv.v_page_stride >> 4) + s * (uint32_t)(a.kv.v_slot_stride >> 4);
+          vso = p * (uint32_t)(a.sc.v_page / SROW) + s * (uint32_t)(a.sc.v_slot / SROW);
         }
-      } else {
+        if (KR == 32 || lane < KR) {
+          cp_async_scales<SROW>(sc + KSC, ksb + (uint64_t)kso * SROW, in);
+          cp_async_scales<SROW>(sc + VSC, vsb + (uint64_t)vso * SROW, in);
+        }
+        const uint32_t rows = __ballot_sync(0xffffffffu, in);
+        if (rows == 0xffffffffu >> (32 - KR) && a.same_strides) {   // as a rule
 #pragma unroll
-        for (int x = 0; x < KT / RPI; ++x) {
-          const int row = x * RPI + lane / CPR;
-          const bool on = rows >> row & 1;
-          const uint32_t to = st + piece4<D>(row, ch);
-          cp_async16(to, kb + (uint64_t)__shfl_sync(0xffffffffu, ko, row) * 16, on);
-          cp_async16(to + V, vb + (uint64_t)__shfl_sync(0xffffffffu, vo, row) * 16, on);
+          for (int x = 0; x < KR / RPI; ++x) {
+            const uint32_t at = __shfl_sync(0xffffffffu, ko, x * RPI + lane / CPR);
+            const uint32_t to = st + piece4<D>(x * RPI + lane / CPR, ch);
+            copy16(to, kb + (uint64_t)at * 16);
+            copy16(to + V, vb + (uint64_t)at * 16);
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < KR / RPI; ++x) {
+            const int row = x * RPI + lane / CPR;
+            const bool on = rows >> row & 1;
+            const uint32_t to = st + piece4<D>(row, ch);
+            cp_async16(to, kb + (uint64_t)__shfl_sync(0xffffffffu, ko, row) * 16, on);
+            cp_async16(to + V, vb + (uint64_t)__shfl_sync(0xffffffffu, vo, row) * 16, on);
+          }
         }
       }
     }
