@@ -94,7 +94,9 @@ constexpr int kLongRun = 4;
 // begin anew and the results that are joined. With 0, 1, 2 and 4 of them 48 ragged sequences up to 8192 take 57.0, 56.1,
 // 57.2 and 58.6 us, 100 up to 4000 51.2, 48.0, 50.3 and 52.9, 19 of 22272 89.5, 92.5, 91.6 and 93.3; with heads of 256
 // (units half as long) 13 up to 24001 50.2, 47.8, 47.4 and 45.9, 16 of 8192 43.1, 40.7, 39.9 and 39.9.
-constexpr int kChargeFrom = 12;
+// From runs of 12, 8, 6 and 4 units on: 100 ragged sequences up to 2000 28.8, 28.7, 25.2 and 25.3 us, 200 up to 700 with
+// heads of 64 28.9, 28.8, 26.2 and 26.1, 64 of 1000 30.4, 31.7, 31.6 and 31.6.
+constexpr int kChargeFrom = 6;
 // NVFP4: no segment is cut, and none is left to the join, where the longest is no more than this many units longer than
 // a run; a run then takes the segments that begin in it. 32 sequences with a window of 512 17.3 -> 13.2 us, 60 ragged
 // ones up to 300 9.0 -> 8.2; with eight units 128 of 512 would take 31.7 us for 28.3, one of 777 10.8 for 6.8.
