@@ -34,8 +34,8 @@
 // 48 ragged ones up to 8192, E4M3, 423 MB: 85 us (73 %), of which some 10 us are launches, fill and
 // join, and the runs' pieces differ in cost. One sequence of 777: 7.8 us, two launches and the chain
 // length, page, keys, scores, sums, join.
-// NVFP4: the three 56 us (270 MB, 71 %), the 48 56 us (239 MB, 63 %), 64 of 6500 91.5 us with pages head by head and 97
-// slot by slot (481 MB, 78 and 73 %): the products' own part runs at 93 % of the copy rate (870 of the 806 cycles that
+// NVFP4: the three 56.5 us (270 MB, 71 %), the 48 56.7 us (239 MB, 62 %), 64 of 6500 92.5 us with pages head by head and 98.5
+// slot by slot (481 MB, 77 and 72 %): the products' own part runs at 93 % of the copy rate (870 of the 806 cycles that
 // a step's bytes take, of which 548 issue an instruction); the first data arrive after 4.5 us and the join takes 7.
 // Without any arithmetic those take 83 and 92 us. With heads of 64 (200 sequences, a window of 1023: 27 us for 7.4)
 // rows of 32 bytes copy at 77 % and as many bytes take a third more instructions; with 16 heads a key head the
@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
     else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(W * 32) : "memory");
   };
   const bool uncut = F4 && (int64_t)((longest + charge) << hl) <= quota + kUncut;
+  const int64_t cap = uncut ? max(total, u_end + 1) : u_end;   // where its last piece ends at the latest
   if ((uncut || u >= u_end) && tid == 0) a.shared_segs[block] = make_int4(-1, 0, 0, 0);
 
   while (u < u_end) {
@@ -301,11 +302,11 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
     const int cost = (units + charge) << hl;   // of HW heads
     const int hg = (int)(local / cost);
     const int u0 = (int)(local - (int64_t)hg * cost);
-    if (uncut && u0 > 0) {   // the run's that the segment begins in
+    if (u0 > 0 && cap > u_end) {   // the run's that the segment begins in
       u += cost - u0;
       continue;
     }
-    const int n_units = uncut ? cost : (int)min((int64_t)(cost - u0), u_end - u);
+    const int n_units = (int)min((int64_t)(cost - u0), cap - u);
     const int hs = hg * HW + hw;
     const int kvh = hs / a.gt, g0 = (hs - kvh * a.gt) * 16;
     const int G = min(a.group - g0, 16);
