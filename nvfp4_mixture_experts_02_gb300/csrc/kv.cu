@@ -19,8 +19,8 @@
 // k_kv_append_many: the blocks that the device holds at once share the tokens. A block looks up the places of all of
 // its tokens and lays their cosines and sines out in shared memory, where all heads of a token read them and each
 // pair's axis has been chosen; then a thread keeps its piece of a head and goes through the tokens with the next one's
-// values on their way. 4093 tokens into NVFP4 20.7 us, 9001 with three axes 41 us (65 % and 70 % of the copy rate);
-// what is left are the loads' latency at 2 blocks of 64 registers and the conversions.
+// values on their way. 4093 tokens into NVFP4 19.7 us, 9001 with three axes 38 us (66 and 75 % of the copy rate); what is
+// left are the instructions, some 200 a thread and token, at the warps that 56 registers allow.
 // k_kv_gather: a thread takes 16 elements of a key and of its value. Bound by memory: 115 thousand tokens of 8 heads
 // of 128 from NVFP4 122 us (90 %), most of it for the results.
 #include <algorithm>
@@ -34,12 +34,15 @@ namespace ftmoe {
 namespace {
 
 constexpr int kAppendThreads = 256;   // of a block, or as many as one token needs up to 512
-// From this many tokens a block (of those that the device holds at once) on, rotated ones go through
-// k_kv_append_many: 1200 tokens of 32 + 16 heads of 128 into NVFP4 8.5 us for 9.7, 4093 20.7 for 25.9 (into E4M3 20.4
-// for 23.3); 20000 of 2 + 2 heads of 64, three a block, would take 10.6 for 9.3. Without rotation k_kv_append is the
-// faster (16000 tokens 71 us for 77). Several axes always take k_kv_append_many: 37 tokens 2.7 us, 3.2 with the
-// choice of rows in each thread, 9001 41 us for 110.
-constexpr int kManyTokens = 4;
+// k_kv_append_many: threads of a block at most, blocks that an SM holds (384 x 56 registers; 4093 tokens of 32 + 16 heads
+// of 128 into NVFP4 19.7 us, 20.6 with two blocks of 72, 25.7 with four of 40; two tokens ahead 21.3 for 20.7).
+constexpr int kManyThreads = 384, kManyBlocks = 3;
+// From this many tokens a block (of those that the device holds at once) on, rotated ones of more than a few heads go
+// through it: 1200 of those tokens (three a block) 8.7 us for 9.6, 4093 19.7 for 26.1 (into E4M3 18.8 for 23.3), 800 (two) 7.0
+// for 6.8. Not tokens that share a block: 40000 of 2 + 2 heads of 64 would take 16.0 for 14.7. Without rotation
+// k_kv_append is the faster (16000 tokens 71 us for 77). Several axes always take it: 37 tokens 2.7 us, 3.2 with the
+// choice of rows in each thread, 9001 38 us for 110.
+constexpr int kManyTokens = 3;
 constexpr int kAppendTokens = 32, kAppendBytes = 40 * 1024;   // most tokens of a group, most shared memory
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -247,7 +250,7 @@ struct Pieces {
 };
 
 template <int D, int DT, bool AXES>
-__global__ void __launch_bounds__(512, 2)
+__global__ void __launch_bounds__(kManyThreads, kManyBlocks)
     k_kv_append_many(const AppendArgs a, int items, int groups, int per) {
   constexpr int PER_HEAD = D / 16;
   constexpr bool F8 = DT == FT_KV_E4M3, F4 = DT == kKvNvfp4;
@@ -459,11 +462,11 @@ template <int D, int DT>
 cudaError_t launch_t(cudaLaunchConfig_t cfg, const AppendArgs& a, int num_sms) {
   const int items = (a.Hq + 2 * a.kv.Hkv) * (D / 16);   // of a token
   const int groups = items < kAppendThreads ? kAppendThreads / items : 1;
-  const int turns = (items + 511) / 512;
+  const int turns = (items + kManyThreads - 1) / kManyThreads;
   const int threads = ((turns > 1 ? (items + turns - 1) / turns : items * groups) + 31) / 32 * 32;
-  const int resident = num_sms * (1024 / threads);   // blocks of k_kv_append_many at once
+  const int resident = num_sms * (kManyBlocks * kManyThreads / threads);   // blocks of k_kv_append_many at once
   int per = (int)(((int64_t)a.T + (int64_t)resident * groups - 1) / ((int64_t)resident * groups));
-  if (!a.axis_pos && (per < kManyTokens || a.rope_dim == 0)) {
+  if (!a.axis_pos && (groups > 1 || per < kManyTokens || a.rope_dim == 0)) {
     const int need = (items * groups + 31) / 32 * 32;
     cfg.gridDim = dim3((unsigned)((a.T + groups - 1) / groups));
     cfg.blockDim = dim3((unsigned)(need < 512 ? need : 512));

@@ -41,7 +41,7 @@ class Case:
         self.pos[[T // 9, T // 2]] = -1
         P = B * width + 3
         self.table = rng.permutation(P)[:B * width].reshape(B, width).astype(np.int32)
-        self.rope = rope_table(64, R) if R else None
+        self.rope = rope_table(max(64, T), R) if R else None
         wide = bf16(3 * rng.standard_normal((T, Hq + 2 * Hkv, D)) * 2.0 ** rng.integers(-20, 3, (T, Hq + 2 * Hkv, 1)))
         wide[0, Hq] = 1e5                                # saturates E4M3 and the block scales
         wide[1, Hq] = 0
@@ -137,7 +137,36 @@ def test_one_token_and_none():
     assert k.shape == v.shape == (0, 1, 64)
 
 
-AXES = [(0, 0), (1, 0), (2, 0), (4, 0), (0, 1), (3, 1)]
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "nvfp4"])
+@pytest.mark.parametrize("T,D,R,Hq,Hkv", [(1003, 128, 128, 32, 8), (1601, 256, 128, 20, 3), (2003, 64, 64, 50, 9), (1301, 128, 96, 64, 1)])
+def test_prompts_of_many_tokens_a_block(kind, T, D, R, Hq, Hkv):
+    c = Case(D, R, Hq, Hkv, 24, "head" if D == 256 else "slot", kind, T=T)
+    at = np.maximum(c.pos, 0)
+    c.run(ftmoe(), rotate32(c.k, c.rope, at), rotate32(c.q, c.rope, at))
+
+
+def test_prompts_of_many_tokens_that_lie_outside():
+    """Tokens without a place among many of a block: their neighbours are as ever."""
+    m = ftmoe()
+    c = Case(128, 128, 32, 8, 16, "slot", "nvfp4", T=1201)
+    at = np.maximum(c.pos, 0)
+    cache = c.run(m, rotate32(c.k, c.rope, at), rotate32(c.q, c.rope, at))
+    before = cache.k.clone(), cache.k_scales.clone()
+    wd = c.wide.cuda()
+    args = (wd[:, 32:40], wd[:, 40:], cache, i32(c.table))
+    kw = dict(seq_ids=i32(c.seq), q=wd[:, :32], rope=torch.from_numpy(c.rope).cuda())
+    whole = m.kv_append(*args, i32(c.pos), **kw)
+    assert m.get_error() == 0
+    pos = c.pos.copy()
+    pos[7] = c.rope.shape[0] + 5                           # past the table of angles
+    pos[1100] = 1 << 30
+    got = m.kv_append(*args, i32(pos), **kw)
+    assert m.get_error() == 6
+    assert not got[7].any() and not got[1100].any()
+    keep = torch.ones(c.T, dtype=torch.bool)
+    keep[[7, 1100]] = False
+    assert torch.equal(got[keep.cuda()], whole[keep.cuda()])
+    assert torch.equal(cache.k, before[0]) and torch.equal(cache.k_scales.view(torch.uint8), before[1].view(torch.uint8))
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "nvfp4"])
