@@ -334,256 +334,256 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
       attend_piece4<D, NG, S>(a, reinterpret_cast<char*>(rings) + warp * S::kWarpBytes, b, kvh, g0, G, first, key0, key1,
                               unit, n_sub, o, m, l);
     } else {
-    const int32_t* table = a.block_table + (int64_t)b * a.table_width;
-    int page = -1, slot = 0;
-    auto look_up = [&](int i) {   // lane l < KT: the page and slot of key l of step i
-      const int j = key0 + i * unit + lane % KT;
-      page = -1;
-      if (i < n_sub && j >= first && j < key1) {
-        const int col = (int)((__umulhi((uint32_t)a.div_mul, (uint32_t)j) + (uint32_t)j) >> a.div_shift);
-        slot = j - col * a.kv.page_size;
-        page = table[col];   // col < table_width: the length is cut to the table
-      }
-    };
-    auto fetch = [&](int i) {     // the copies of step i, whose pages look_up has found
-      if (i < n_sub) {
-        int64_t ko = -1, vo = -1;
-        if (page >= 0 && page < a.kv.num_pages) {
-          ko = ((int64_t)page * a.kv.k_page_stride + (int64_t)slot * a.kv.k_slot_stride +
-                (int64_t)kvh * a.kv.k_head_stride) * (F16 ? 1 : 2);
-          if (!a.same_strides)
-            vo = ((int64_t)page * a.kv.v_page_stride + (int64_t)slot * a.kv.v_slot_stride +
-                  (int64_t)kvh * a.kv.v_head_stride) * (F16 ? 1 : 2);
-        } else if (lane < KT) {
-          const int j = key0 + i * unit + lane;
-          if (j >= first && j < key1) atomicOr(a.err, kErrBadPage);   // no such page: read as zeros
+      const int32_t* table = a.block_table + (int64_t)b * a.table_width;
+      int page = -1, slot = 0;
+      auto look_up = [&](int i) {   // lane l < KT: the page and slot of key l of step i
+        const int j = key0 + i * unit + lane % KT;
+        page = -1;
+        if (i < n_sub && j >= first && j < key1) {
+          const int col = (int)((__umulhi((uint32_t)a.div_mul, (uint32_t)j) + (uint32_t)j) >> a.div_shift);
+          slot = j - col * a.kv.page_size;
+          page = table[col];   // col < table_width: the length is cut to the table
         }
-        const uint32_t st = ring + (uint32_t)((i % ST) * S::kStageBytes);
-        constexpr int RPI = 32 / CPR;   // rows of one warp-wide copy
+      };
+      auto fetch = [&](int i) {     // the copies of step i, whose pages look_up has found
+        if (i < n_sub) {
+          int64_t ko = -1, vo = -1;
+          if (page >= 0 && page < a.kv.num_pages) {
+            ko = ((int64_t)page * a.kv.k_page_stride + (int64_t)slot * a.kv.k_slot_stride +
+                  (int64_t)kvh * a.kv.k_head_stride) * (F16 ? 1 : 2);
+            if (!a.same_strides)
+              vo = ((int64_t)page * a.kv.v_page_stride + (int64_t)slot * a.kv.v_slot_stride +
+                    (int64_t)kvh * a.kv.v_head_stride) * (F16 ? 1 : 2);
+          } else if (lane < KT) {
+            const int j = key0 + i * unit + lane;
+            if (j >= first && j < key1) atomicOr(a.err, kErrBadPage);   // no such page: read as zeros
+          }
+          const uint32_t st = ring + (uint32_t)((i % ST) * S::kStageBytes);
+          constexpr int RPI = 32 / CPR;   // rows of one warp-wide copy
 #pragma unroll
-        for (int p = 0; p < KT / RPI; ++p) {
-          const int row = p * RPI + lane / CPR, ch = lane % CPR;
-          const int64_t k_at = __shfl_sync(0xffffffffu, ko, row);
-          const int64_t v_at = a.same_strides ? k_at : __shfl_sync(0xffffffffu, vo, row);
-          const bool on = k_at >= 0;
-          const uint32_t to = st + swz<CPR>(row, ch);
-          cp_async16(to, static_cast<const char*>(a.kv.k) + (on ? k_at + ch * 16 : 0), on);
-          cp_async16(to + KT * S::kRow, static_cast<const char*>(a.kv.v) + (on ? v_at + ch * 16 : 0), on);
+          for (int p = 0; p < KT / RPI; ++p) {
+            const int row = p * RPI + lane / CPR, ch = lane % CPR;
+            const int64_t k_at = __shfl_sync(0xffffffffu, ko, row);
+            const int64_t v_at = a.same_strides ? k_at : __shfl_sync(0xffffffffu, vo, row);
+            const bool on = k_at >= 0;
+            const uint32_t to = st + swz<CPR>(row, ch);
+            cp_async16(to, static_cast<const char*>(a.kv.k) + (on ? k_at + ch * 16 : 0), on);
+            cp_async16(to + KT * S::kRow, static_cast<const char*>(a.kv.v) + (on ? v_at + ch * 16 : 0), on);
+          }
         }
-      }
-      cp_async_commit();
-    };
-    look_up(0);
+        cp_async_commit();
+      };
+      look_up(0);
 #pragma unroll
-    for (int i = 0; i < ST - 1; ++i) {
-      fetch(i);
-      look_up(i + 1);
-    }
+      for (int i = 0; i < ST - 1; ++i) {
+        fetch(i);
+        look_up(i + 1);
+      }
 
-    // ---- q as the column operand: column l / 4 of group g is head 8 g + l / 4
-    uint32_t q[NG][KS][2];
-    float sl[NG][2];   // log2 units per unit of the raw product, heads 8 g + 2 c, + 1
-    {
-      const uint16_t* qb = a.q + (int64_t)b * a.q_stride + (int64_t)(kvh * a.group + g0) * D;
+      // ---- q as the column operand: column l / 4 of group g is head 8 g + l / 4
+      uint32_t q[NG][KS][2];
+      float sl[NG][2];   // log2 units per unit of the raw product, heads 8 g + 2 c, + 1
+      {
+        const uint16_t* qb = a.q + (int64_t)b * a.q_stride + (int64_t)(kvh * a.group + g0) * D;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const bool on = 8 * g + r < G;
-        const uint16_t* qh = qb + (8 * g + r) * D;
-        sl[g][0] = sl[g][1] = a.scale * a.kv.k_scale * kLog2e;
+        for (int g = 0; g < NG; ++g) {
+          const bool on = 8 * g + r < G;
+          const uint16_t* qh = qb + (8 * g + r) * D;
+          sl[g][0] = sl[g][1] = a.scale * a.kv.k_scale * kLog2e;
+          if constexpr (!F16) {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+              q[g][ks][0] = on ? *reinterpret_cast<const uint32_t*>(qh + 16 * ks + 2 * c) : 0u;
+              q[g][ks][1] = on ? *reinterpret_cast<const uint32_t*>(qh + 16 * ks + 2 * c + 8) : 0u;
+            }
+          } else {
+            float top = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {   // E4M3 keys come four elements to a lane
+              uint2 v = make_uint2(0, 0);
+              if (on) v = *reinterpret_cast<const uint2*>(qh + 16 * ks + 4 * c);
+              q[g][ks][0] = v.x;
+              q[g][ks][1] = v.y;
+              top = fmaxf(top, finite_top(v.x, v.y));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            float up, down;
+            f16_scale(top, up, down);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                q[g][ks][e] = pack_f16(bf16_lo(q[g][ks][e]) * up, bf16_hi(q[g][ks][e]) * up);
+            sl[g][0] *= __shfl_sync(0xffffffffu, down, 8 * c);       // head 2 c: lanes 8 c ..
+            sl[g][1] *= __shfl_sync(0xffffffffu, down, 8 * c + 4);
+          }
+        }
+      }
+
+      const int krow = ((lane >> 3) & 1) * 8 + (lane & 7), half = lane >> 4;
+
+      for (int i = 0; i < n_sub; ++i) {
+        cp_async_wait<ST - 2>();
+        __syncwarp();
+        // the next copies go into the stage that the previous step has left
+        fetch(i + ST - 1);
+        look_up(i + ST);
+        const uint32_t st = ring + (uint32_t)((i % ST) * S::kStageBytes);
+        // s^T = k q^T: 16 keys a tile
+        float s[NG][NH][4];
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int h = 0; h < NH; ++h) s[g][h][0] = s[g][h][1] = s[g][h][2] = s[g][h][3] = 0.f;
         if constexpr (!F16) {
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            q[g][ks][0] = on ? *reinterpret_cast<const uint32_t*>(qh + 16 * ks + 2 * c) : 0u;
-            q[g][ks][1] = on ? *reinterpret_cast<const uint32_t*>(qh + 16 * ks + 2 * c + 8) : 0u;
-          }
-        } else {
-          float top = 0.f;
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {   // E4M3 keys come four elements to a lane
-            uint2 v = make_uint2(0, 0);
-            if (on) v = *reinterpret_cast<const uint2*>(qh + 16 * ks + 4 * c);
-            q[g][ks][0] = v.x;
-            q[g][ks][1] = v.y;
-            top = fmaxf(top, finite_top(v.x, v.y));
-          }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          float up, down;
-          f16_scale(top, up, down);
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              q[g][ks][e] = pack_f16(bf16_lo(q[g][ks][e]) * up, bf16_hi(q[g][ks][e]) * up);
-          sl[g][0] *= __shfl_sync(0xffffffffu, down, 8 * c);       // head 2 c: lanes 8 c ..
-          sl[g][1] *= __shfl_sync(0xffffffffu, down, 8 * c + 4);
-        }
-      }
-    }
-
-    const int krow = ((lane >> 3) & 1) * 8 + (lane & 7), half = lane >> 4;
-
-    for (int i = 0; i < n_sub; ++i) {
-      cp_async_wait<ST - 2>();
-      __syncwarp();
-      // the next copies go into the stage that the previous step has left
-      fetch(i + ST - 1);
-      look_up(i + ST);
-      const uint32_t st = ring + (uint32_t)((i % ST) * S::kStageBytes);
-      // s^T = k q^T: 16 keys a tile
-      float s[NG][NH][4];
-#pragma unroll
-      for (int g = 0; g < NG; ++g)
-#pragma unroll
-        for (int h = 0; h < NH; ++h) s[g][h][0] = s[g][h][1] = s[g][h][2] = s[g][h][3] = 0.f;
-      if constexpr (!F16) {
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            uint32_t k[4];   // keys 0-7 and 8-15 of dims 0-7, then of dims 8-15
-            ldmatrix4(k, st + swz<CPR>(16 * h + krow, 2 * ks + half));
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-              mma_bf16(s[g][h], k[0], k[1], k[2], k[3], q[g][ks][0], q[g][ks][1]);
-          }
-      } else {
-#pragma unroll
-        for (int ks = 0; ks < KS; ks += 2)
-#pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            uint32_t k[4];   // keys 0-7 and 8-15 of 16 dims, then of the next 16
-            ldmatrix4(k, st + swz<CPR>(16 * h + krow, ks + half));
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              uint32_t a0, a1, a2, a3;
-              e4m3x4_to_f16(k[2 * e], a0, a2);
-              e4m3x4_to_f16(k[2 * e + 1], a1, a3);
+            for (int h = 0; h < NH; ++h) {
+              uint32_t k[4];   // keys 0-7 and 8-15 of dims 0-7, then of dims 8-15
+              ldmatrix4(k, st + swz<CPR>(16 * h + krow, 2 * ks + half));
 #pragma unroll
               for (int g = 0; g < NG; ++g)
-                mma_f16(s[g][h], a0, a1, a2, a3, q[g][ks + e][0], q[g][ks + e][1]);
+                mma_bf16(s[g][h], k[0], k[1], k[2], k[3], q[g][ks][0], q[g][ks][1]);
             }
-          }
-      }
-      // scores in log2 units: key j0 + 16 h + r (elements 0, 1) and + 8; keys outside [first, key1)
-      // do not count
-      const int j0 = key0 + i * unit;
-      bool up = false;
-      float top[NG][2];
+        } else {
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
+          for (int ks = 0; ks < KS; ks += 2)
 #pragma unroll
-        for (int h = 0; h < NH; ++h)
+            for (int h = 0; h < NH; ++h) {
+              uint32_t k[4];   // keys 0-7 and 8-15 of 16 dims, then of the next 16
+              ldmatrix4(k, st + swz<CPR>(16 * h + krow, ks + half));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[g][h][e] *= sl[g][e & 1];
-        if (j0 < first || j0 + KT > key1) {
+              for (int e = 0; e < 2; ++e) {
+                uint32_t a0, a1, a2, a3;
+                e4m3x4_to_f16(k[2 * e], a0, a2);
+                e4m3x4_to_f16(k[2 * e + 1], a1, a3);
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+                  mma_f16(s[g][h], a0, a1, a2, a3, q[g][ks + e][0], q[g][ks + e][1]);
+              }
+            }
+        }
+        // scores in log2 units: key j0 + 16 h + r (elements 0, 1) and + 8; keys outside [first, key1)
+        // do not count
+        const int j0 = key0 + i * unit;
+        bool up = false;
+        float top[NG][2];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
 #pragma unroll
           for (int h = 0; h < NH; ++h)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = j0 + 16 * h + r + (e >> 1) * 8;
-              if (j < first || j >= key1) s[g][h][e] = -INFINITY;
-            }
-        }
+            for (int e = 0; e < 4; ++e) s[g][h][e] *= sl[g][e & 1];
+          if (j0 < first || j0 + KT > key1) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float t = fmaxf(s[g][0][e], s[g][0][2 + e]);
+            for (int h = 0; h < NH; ++h)
 #pragma unroll
-          for (int h = 1; h < NH; ++h) t = fmaxf(t, fmaxf(s[g][h][e], s[g][h][2 + e]));
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
-          if constexpr (F16) t = __fsub_ru(t, kLift);   // upwards: no weight above 2^15 at any size of t
-          top[g][e] = t;
-          up |= t > m[g][e];
-        }
-      }
-      if (__any_sync(0xffffffffu, up)) {   // a new maximum: what is summed shrinks
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          float f[2];
+              for (int e = 0; e < 4; ++e) {
+                const int j = j0 + 16 * h + r + (e >> 1) * 8;
+                if (j < first || j >= key1) s[g][h][e] = -INFINITY;
+              }
+          }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float n = fmaxf(m[g][e], top[g][e]);
-            f[e] = m[g][e] == -INFINITY ? 0.f : exp2_fast(m[g][e] - n);
-            m[g][e] = n;
-            l[g][e] *= f[e];
-          }
+            float t = fmaxf(s[g][0][e], s[g][0][2 + e]);
 #pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            o[g][t][0] *= f[0]; o[g][t][1] *= f[1];
-            o[g][t][2] *= f[0]; o[g][t][3] *= f[1];
-          }
-        }
-      }
-      uint32_t p[NG][NH][2], rest[NG][NH][2];   // p^T: columns heads, rows keys 0-7 and 8-15 of a tile
+            for (int h = 1; h < NH; ++h) t = fmaxf(t, fmaxf(s[g][h][e], s[g][h][2 + e]));
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float base = m[g][e] == -INFINITY ? 0.f : m[g][e];   // no key yet: every p is 0
-#pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            s[g][h][e] = exp2_fast(s[g][h][e] - base);
-            s[g][h][2 + e] = exp2_fast(s[g][h][2 + e] - base);
-            l[g][e] += s[g][h][e] + s[g][h][2 + e];
+            for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
+            if constexpr (F16) t = __fsub_ru(t, kLift);   // upwards: no weight above 2^15 at any size of t
+            top[g][e] = t;
+            up |= t > m[g][e];
           }
         }
+        if (__any_sync(0xffffffffu, up)) {   // a new maximum: what is summed shrinks
 #pragma unroll
-        for (int h = 0; h < NH; ++h)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float p0 = s[g][h][2 * x], p1 = s[g][h][2 * x + 1];
-            if constexpr (F16) {
-              const uint32_t v = pack_f16(p0, p1);
-              p[g][h][x] = transpose8(v);
-              rest[g][h][x] = transpose8(pack_f16(p0 - f16_lo(v), p1 - f16_hi(v)));
-            } else {
-              const uint32_t v = pack_bf16(p0, p1);
-              p[g][h][x] = transpose8(v);
-              rest[g][h][x] = transpose8(pack_bf16(p0 - bf16_lo(v), p1 - bf16_hi(v)));
-            }
-          }
-      }
-      // o^T += v^T p^T: 16 dims at a time
-      const uint32_t vs = st + KT * S::kRow;
-      if constexpr (!F16) {
-        const int vrow = half * 8 + (lane & 7), vch = (lane >> 3) & 1;
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            uint32_t v[4];   // dims 0-7 and 8-15 of keys 0-7, then of keys 8-15
-            ldmatrix4_trans(v, vs + swz<CPR>(16 * h + vrow, 2 * t + vch));
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-              mma_bf16(o[g][t], v[0], v[1], v[2], v[3], p[g][h][0], p[g][h][1]);
-              mma_bf16(o[g][t], v[0], v[1], v[2], v[3], rest[g][h][0], rest[g][h][1]);
-            }
-          }
-      } else {
-#pragma unroll
-        for (int t = 0; t < MT; t += 2)
-#pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            uint32_t v[4];   // keys 0-7 and 8-15 of 16 dims, then of the next 16
-            ldmatrix4_trans(v, vs + swz<CPR>(16 * h + krow, t + half));
+          for (int g = 0; g < NG; ++g) {
+            float f[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              // (key, dim d), (key, d + 1), (key + 1, d), (key + 1, d + 1): rows 0-7 take the even dims
-              uint32_t a0, a1, a2, a3;
-              e4m3x4_to_f16(__byte_perm(v[2 * e], 0, 0x3120), a0, a1);
-              e4m3x4_to_f16(__byte_perm(v[2 * e + 1], 0, 0x3120), a2, a3);
+              const float n = fmaxf(m[g][e], top[g][e]);
+              f[e] = m[g][e] == -INFINITY ? 0.f : exp2_fast(m[g][e] - n);
+              m[g][e] = n;
+              l[g][e] *= f[e];
+            }
 #pragma unroll
-              for (int g = 0; g < NG; ++g) {
-                mma_f16(o[g][t + e], a0, a1, a2, a3, p[g][h][0], p[g][h][1]);
-                mma_f16(o[g][t + e], a0, a1, a2, a3, rest[g][h][0], rest[g][h][1]);
-              }
+            for (int t = 0; t < MT; ++t) {
+              o[g][t][0] *= f[0]; o[g][t][1] *= f[1];
+              o[g][t][2] *= f[0]; o[g][t][3] *= f[1];
             }
           }
+        }
+        uint32_t p[NG][NH][2], rest[NG][NH][2];   // p^T: columns heads, rows keys 0-7 and 8-15 of a tile
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float base = m[g][e] == -INFINITY ? 0.f : m[g][e];   // no key yet: every p is 0
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+              s[g][h][e] = exp2_fast(s[g][h][e] - base);
+              s[g][h][2 + e] = exp2_fast(s[g][h][2 + e] - base);
+              l[g][e] += s[g][h][e] + s[g][h][2 + e];
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < NH; ++h)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float p0 = s[g][h][2 * x], p1 = s[g][h][2 * x + 1];
+              if constexpr (F16) {
+                const uint32_t v = pack_f16(p0, p1);
+                p[g][h][x] = transpose8(v);
+                rest[g][h][x] = transpose8(pack_f16(p0 - f16_lo(v), p1 - f16_hi(v)));
+              } else {
+                const uint32_t v = pack_bf16(p0, p1);
+                p[g][h][x] = transpose8(v);
+                rest[g][h][x] = transpose8(pack_bf16(p0 - bf16_lo(v), p1 - bf16_hi(v)));
+              }
+            }
+        }
+        // o^T += v^T p^T: 16 dims at a time
+        const uint32_t vs = st + KT * S::kRow;
+        if constexpr (!F16) {
+          const int vrow = half * 8 + (lane & 7), vch = (lane >> 3) & 1;
+#pragma unroll
+          for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+              uint32_t v[4];   // dims 0-7 and 8-15 of keys 0-7, then of keys 8-15
+              ldmatrix4_trans(v, vs + swz<CPR>(16 * h + vrow, 2 * t + vch));
+#pragma unroll
+              for (int g = 0; g < NG; ++g) {
+                mma_bf16(o[g][t], v[0], v[1], v[2], v[3], p[g][h][0], p[g][h][1]);
+                mma_bf16(o[g][t], v[0], v[1], v[2], v[3], rest[g][h][0], rest[g][h][1]);
+              }
+            }
+        } else {
+#pragma unroll
+          for (int t = 0; t < MT; t += 2)
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+              uint32_t v[4];   // keys 0-7 and 8-15 of 16 dims, then of the next 16
+              ldmatrix4_trans(v, vs + swz<CPR>(16 * h + krow, t + half));
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                // (key, dim d), (key, d + 1), (key + 1, d), (key + 1, d + 1): rows 0-7 take the even dims
+                uint32_t a0, a1, a2, a3;
+                e4m3x4_to_f16(__byte_perm(v[2 * e], 0, 0x3120), a0, a1);
+                e4m3x4_to_f16(__byte_perm(v[2 * e + 1], 0, 0x3120), a2, a3);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                  mma_f16(o[g][t + e], a0, a1, a2, a3, p[g][h][0], p[g][h][1]);
+                  mma_f16(o[g][t + e], a0, a1, a2, a3, rest[g][h][0], rest[g][h][1]);
+                }
+              }
+            }
+        }
+        __syncwarp();   // every lane has read the stage before it is filled again
       }
-      __syncwarp();   // every lane has read the stage before it is filled again
-    }
-    cp_async_wait<0>();
+      cp_async_wait<0>();
     }
 
     // ---- join the warps of a head: sums [head][LD] in each one's ring
