@@ -505,7 +505,7 @@ ft_status ft_paged_decode_attention(const uint16_t* q, int64_t q_stride, int32_t
 /*
  * ft_nvfp4_paged_decode_attention — ft_paged_decode_attention over an NVFP4 cache: the same arguments,
  * workspace, flags and errors. Keys and values enter their products exactly (e2m1 * e4m3 is an f16);
- * before a weight meets its value it is rounded to 11 bits, or to within 2^-35 of the largest key's
+ * before a weight meets its value it is rounded to 22 bits, or to within 2^-35 of the largest key's
  * weight. A NaN block scale gives NaN. From the first element of a cache's codes to its last there may be
  * 64 GiB, from the first of its scales to the last 2^28 * D bytes (FT_ERR_UNSUPPORTED_SHAPE beyond).
  */

@@ -28,7 +28,7 @@
 // weight, see kLift). One f16 for p moves outputs over their bf16 rounding: 48 ragged sequences are 8.1e-4 off the
 // rounded exact result with one, 0.8e-4 with two (bf16 caches 0.6e-4), at 0 to 1 % of the time, 4 to 5 % with heads
 // of 64 (200 ragged sequences up to 700, 26.3 and 27.5 us) or 16 heads a key head (16 x 8192, 40.9 and 43.2 us).
-// NVFP4 caches (ftmoe_attend4.cuh): f16 products as for E4M3, a weight in one f16. Statistics and sums are float32.
+// NVFP4 caches (ftmoe_attend4.cuh): f16 products and weights in two f16 as for E4M3. Statistics and sums are float32.
 //
 // Measured (of the copy rate of 6786 GB/s): three sequences up to 131072, bf16, 962 MB: 155 us (91 %).
 // 48 ragged ones up to 8192, E4M3, 423 MB: 85 us (73 %), of which some 10 us are launches, fill and

@@ -8,9 +8,10 @@
 // A code becomes f16 by one conversion for two and one multiplication by its scale (e2m1 * e4m3 has six significant
 // bits), so a step of 32 keys of 128 elements issues 548 instructions (256 of them these), which the 12 warps of an SM
 // overlap with the copies: products of the next step and values of this one are independent and stand side by side.
-// A weight is one f16: 11 bits, a relative error of 2^-12 where the outputs are rounded to 2^-9 and the values hold four
-// bits. The rest as a second f16, as for E4M3 caches, costs 8 % (48 ragged sequences 57.3 -> 62.2 us) to 13 % (three
-// long ones 57.1 -> 64.3): twice the products.
+// A weight is two f16, as for E4M3 caches. One alone, 11 bits, puts one output in some thirty on the neighbouring bf16
+// (8e-4 off the rounded exact result for 1e-4) and takes 56.9 us for 60.7 (48 ragged sequences), 56.6 for 63.1 (three
+// long ones), 27.1 for 28.4 (heads of 64, a window of 1023): half of the value products. The second product of a pair
+// right behind the first: 60.7 us, 62.1 behind all four first ones of a word.
 // Measured and not kept: 16 warps of 128 registers (spills and two stages: 123 us for 103 at 64 x 6500, with three
 // stages 109), four stages for three (no change), groups held to the slowest one's pace (2 to 5 % slower), copies of
 // whole tiles by the tensor memory accelerator (rows of 64 bytes at 6.5 TB/s for 6.7, of 32 at 4.6 for 5.2 in a copy
@@ -135,7 +136,7 @@ __device__ __forceinline__ void value_scales(uint32_t (&s)[D == 256 ? 2 : 1], co
 
 // A weight is at most 2^kTop4, and the largest of a head's is set to 2^kSet4 where the running maximum is set anew,
 // which is when one would pass 2^kTop4: few steps after the first do, and the others need no maximum over the
-// lanes. One f16 holds 11 bits of weights down to 2^-14, 2^-24 of the largest, and nothing under 2^-25.
+// lanes. Two f16 hold 22 bits of weights down to 2^-3 and all but 2^-25 of smaller ones: 2^-35 of the largest.
 constexpr float kTop4 = 15.f, kSet4 = 10.f;
 
 // Steps of S::kKeys keys, key0 + i * unit on, up to key1 (and from `first` on). Leaves the warp's o^T, running
@@ -273,7 +274,7 @@ __device__ __forceinline__ void attend_piece4(const AttendArgs& a, char* ring, i
     bar[g][0] = bar[g][1] = -INFINITY;
   }
   float s[NG][NH][4];
-  uint32_t p[NG][NH][2];   // p^T: columns heads, rows keys 0-7 and 8-15 of a tile
+  uint32_t p[NG][NH][2], rest[NG][NH][2];   // p^T: columns heads, rows keys 0-7 and 8-15 of a tile
 
   // s^T = k q^T of a stage
   const int krow = key_of_row<D>(r);
@@ -401,7 +402,9 @@ __device__ __forceinline__ void attend_piece4(const AttendArgs& a, char* ring, i
           const float2 v = unpair(pair_add(x[g][h][e], less[g]));
           const float w0 = exp2_fast(v.x), w1 = exp2_fast(v.y);
           sum[g] = pair_add(sum[g], pair(w0, w1));
-          p[g][h][e] = transpose8(pack_f16(w0, w1));
+          const uint32_t v16 = pack_f16(w0, w1);
+          p[g][h][e] = transpose8(v16);
+          rest[g][h][e] = transpose8(pack_f16(w0 - f16_lo(v16), w1 - f16_hi(v16)));
         }
   };
 
@@ -433,7 +436,10 @@ __device__ __forceinline__ void attend_piece4(const AttendArgs& a, char* ring, i
           const uint32_t b0 = hmul2(a0[e], s01[j / 2]), b1 = hmul2(a1[e], s01[j / 2]);
           const uint32_t b2 = hmul2(a2[e], s89[j / 2]), b3 = hmul2(a3[e], s89[j / 2]);
 #pragma unroll
-          for (int g = 0; g < NG; ++g) mma_f16(o[g][4 * j + e], b0, b1, b2, b3, p[g][h][0], p[g][h][1]);
+          for (int g = 0; g < NG; ++g) {
+            mma_f16(o[g][4 * j + e], b0, b1, b2, b3, p[g][h][0], p[g][h][1]);
+            mma_f16(o[g][4 * j + e], b0, b1, b2, b3, rest[g][h][0], rest[g][h][1]);
+          }
         }
       }
     }
