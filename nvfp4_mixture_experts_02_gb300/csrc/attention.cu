@@ -693,8 +693,9 @@ __device__ __forceinline__ void add_pieces(const float2* ml, const float (*y)[E]
   }
 }
 
-template <int D, int W, int kJoinWarps, int kFlight>   // kFlight: pieces of a warp in flight
-__global__ void __launch_bounds__(kJoinWarps * 32, kJoinWarps == 8 ? 3 : 1) k_join(const AttendArgs a) {
+// kFlight: pieces of a warp in flight; kJoinBlocks: blocks that an SM holds
+template <int D, int W, int kJoinWarps, int kJoinBlocks, int kFlight>
+__global__ void __launch_bounds__(kJoinWarps * 32, kJoinBlocks) k_join(const AttendArgs a) {
   constexpr int E = D / 32;
   static_assert(kJoinWarps % kTeam == 0);   // whole teams
   __shared__ float sums[kJoinWarps][D], wm[kJoinWarps], wl[kJoinWarps];
@@ -856,10 +857,15 @@ cudaError_t launch_d(AttendArgs a, int num_sms, cudaStream_t stream) {
   // Warps of a block of k_join. NVFP4: eight, so that all blocks run at once (48 ragged sequences 58.2 us, 60.5 with
   // sixteen of as many registers, 57.2 for 56.3 with sixteen of 40; one of 777 keys 6.7, 6.8 and 7.8).
   constexpr int kJoinWarps = DT == kKvNvfp4 ? 8 : 16;
-  cfg.gridDim = dim3((unsigned)(S::kBlocks * S::kGroups * num_sms));   // a block for every run
+  // Blocks of k_join that an SM holds: as many as there are runs, but not more than two of sixteen warps, which leaves
+  // each thread 64 registers. One would take 36.1 us for 34.4 (64 sequences of 1000, E4M3), 51.2 for 49.9 (bf16), 63.3
+  // for 61.7 (13 up to 24001 with heads of 256, E4M3).
+  constexpr int kRuns = S::kBlocks * S::kGroups;   // an SM
+  constexpr int kJoinBlocks = DT == kKvNvfp4 ? 3 : kRuns < 2 ? kRuns : 2;
+  cfg.gridDim = dim3((unsigned)(kRuns * num_sms));   // a block for every run
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, k_join<D, S::kWarps, kJoinWarps, DT == kKvNvfp4 && D <= 128 ? 8 : 4>, a);
+  return cudaLaunchKernelEx(&cfg, k_join<D, S::kWarps, kJoinWarps, kJoinBlocks, DT == kKvNvfp4 && D <= 128 ? 8 : 4>, a);
 }
 
 template <int D, int DT>
