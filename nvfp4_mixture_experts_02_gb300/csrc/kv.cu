@@ -473,7 +473,11 @@ cudaError_t launch_t(cudaLaunchConfig_t cfg, const AppendArgs& a, int num_sms) {
     return cudaLaunchKernelEx(&cfg, k_kv_append<D, DT>, a, items, groups);
   }
   const int bytes = groups * (a.rope_dim * (int)sizeof(float) + (int)sizeof(TokenPlace));   // for one token each
-  per = std::min(per, std::min(kAppendBytes / bytes, kAppendTokens));
+  // Tokens that do not fit the blocks at once go in rounds. A last one of less than half of the blocks takes as long as
+  // any other: all blocks then take fewer tokens instead (16000 tokens of 32 + 16 heads of 128 into bf16, half of each
+  // head rotated, 85.4 -> 68.4 us). Fuller ones are left: 40000 with a quarter rotated 158 us, 174 in equal rounds.
+  const int most = std::min(kAppendBytes / bytes, kAppendTokens), rounds = (per + most - 1) / most;
+  per = per > most && 2 * (per % most) < most ? (per + rounds - 1) / rounds : std::min(per, most);
   cfg.gridDim = dim3((unsigned)((a.T + groups * per - 1) / (groups * per)));
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)(per * bytes);
