@@ -389,8 +389,8 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
         for (int g = 0; g < NG; ++g) {
           const bool on = 8 * g + r < G;
           const uint16_t* qh = qb + (8 * g + r) * D;
-          sl[g][0] = sl[g][1] = a.scale * a.kv.k_scale * kLog2e;
           if constexpr (!F16) {
+            sl[g][0] = sl[g][1] = a.scale * a.kv.k_scale * kLog2e;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
               q[g][ks][0] = on ? *reinterpret_cast<const uint32_t*>(qh + 16 * ks + 2 * c) : 0u;
@@ -415,8 +415,9 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
 #pragma unroll
               for (int e = 0; e < 2; ++e)
                 q[g][ks][e] = pack_f16(bf16_lo(q[g][ks][e]) * up, bf16_hi(q[g][ks][e]) * up);
-            sl[g][0] *= __shfl_sync(0xffffffffu, down, 8 * c);       // head 2 c: lanes 8 c ..
-            sl[g][1] *= __shfl_sync(0xffffffffu, down, 8 * c + 4);
+            const float unit_s = copysignf(product3(fabsf(a.scale), a.kv.k_scale, down), a.scale) * kLog2e;
+            sl[g][0] = __shfl_sync(0xffffffffu, unit_s, 8 * c);       // head 2 c: lanes 8 c ..
+            sl[g][1] = __shfl_sync(0xffffffffu, unit_s, 8 * c + 4);
           }
         }
       }

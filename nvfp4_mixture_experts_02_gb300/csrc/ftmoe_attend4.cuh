@@ -235,7 +235,6 @@ __device__ __forceinline__ void attend_piece4(const AttendArgs& a, char* ring, i
   uint64_t sl[NG];   // log2 units per unit of the raw product, heads 8 g + 2 c, + 1
   {
     const uint16_t* qb = a.q + (int64_t)b * a.q_stride + (int64_t)(kvh * a.group + g0) * D;
-    const float unit_s = fabsf(a.scale) * a.kv.k_scale * 1.4426950408889634f;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       const bool on = 8 * g + r < G;
@@ -257,8 +256,9 @@ __device__ __forceinline__ void attend_piece4(const AttendArgs& a, char* ring, i
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
         for (int e = 0; e < 2; ++e) q[g][ks][e] = pack_f16(bf16_lo(q[g][ks][e]) * up, bf16_hi(q[g][ks][e]) * up);
-      sl[g] = pair(unit_s * __shfl_sync(0xffffffffu, down, 8 * c),   // head 2 c: lanes 8 c ..
-                   unit_s * __shfl_sync(0xffffffffu, down, 8 * c + 4));
+      const float unit_s = product3(fabsf(a.scale), a.kv.k_scale, down) * 1.4426950408889634f;
+      sl[g] = pair(__shfl_sync(0xffffffffu, unit_s, 8 * c),   // head 2 c: lanes 8 c ..
+                   __shfl_sync(0xffffffffu, unit_s, 8 * c + 4));
     }
 #pragma unroll
     for (int g = 0; g < QS; ++g)

@@ -143,4 +143,11 @@ __device__ __forceinline__ void f16_scale(float top, float& up, float& down) {
   down = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
 }
 
+// a b c of positive factors, where the product of two may lie outside the floats although all three's does not: the
+// largest and the smallest are multiplied first.
+__device__ __forceinline__ float product3(float a, float b, float c) {
+  const float lo = fminf(a, b), hi = fmaxf(a, b);
+  return fmaxf(hi, c) * fminf(lo, c) * fmaxf(lo, fminf(hi, c));
+}
+
 }  // namespace ftmoe

@@ -62,3 +62,43 @@ SCALES = [(2.0 ** -100, 2.0 ** 100), (2.0 ** 100, 2.0 ** -100), (2.0 ** -60, 2.0
 def test_tensor_scales_that_the_softmax_scale_undoes(g, D, Hq, Hkv):
     check(D, Hq, Hkv, g, (400.0, 400.0), 1.0)
     check(D, Hq, Hkv, g, (1.0, 900.0), 1.0, -1.0, seed=1)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 8, 2), (128, 32, 2), (256, 16, 1)])
+@pytest.mark.parametrize("g,top,q_size", [
+    (2.0 ** -100, 400.0, 2.0 ** 100), (2.0 ** -100, 2000.0, 2.0 ** 124),   # the latter: scale * g under 2^-126
+    (2.0 ** 100, 0.1, 2.0 ** -120), (2.0 ** 100, 0.1, 2.0 ** -127)])       # past 2^128
+def test_queries_that_the_scales_undo(g, top, q_size, D, Hq, Hkv):
+    check(D, Hq, Hkv, (g, 1.0), (top, 400.0), q_size)
+
+
+FACTORS = [(16, 128, 64.0, 122, -90), (8, 256, 64.0, 110, -10), (8, 64, 2.0 ** -6, -126, 99), (16, 128, 2.0 ** -6, -126, 90)]
+
+
+@pytest.mark.parametrize("kind,Hq,D,codes,power,k_power", [("nvfp4", *f) for f in FACTORS] + [("e4m3", *f) for f in FACTORS] +
+                         [("e4m3", 8, 64, 64.0, 122, -110)])   # a tensor scale of NVFP4 is 2^-100 at least
+def test_powers_of_two_cancel(kind, Hq, D, codes, power, k_power):
+    """q 2^power, keys 2^k_power and the softmax scale over both: the bits of q, keys and scale themselves."""
+    m = ftmoe()
+    rng = np.random.default_rng(Hq)
+    n, page = 150, 16
+    x = np.clip(np.round(8 * rng.standard_normal((2, 10 * page, 1, D))) / 8, -3, 3).astype(np.float32)
+    x[0] *= codes
+    if kind == "nvfp4":
+        (kc, ks), (vc, vs) = (ob.nvfp4_rows(a.reshape(10, page, 1, D), 1.0) for a in x)
+        t = [torch.from_numpy(a).cuda() for a in (kc, vc, ks, vs)]
+        cache = lambda g: m.NvFP4KVCache(*t, g, 1.0)  # noqa: E731
+    else:
+        t = [torch.from_numpy(a.reshape(10, page, 1, D)).to(torch.float8_e4m3fn).cuda() for a in x]
+        cache = lambda g: m.PagedKVCache(*t, g, 1.0)  # noqa: E731
+    q = bf16(np.clip(np.round(4 * rng.standard_normal((1, Hq, D))) / 4, -3, 3))
+    table = torch.arange(10, dtype=torch.int32, device="cuda")[None]
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    scale = float(np.float32(1 / (codes * np.sqrt(D))))
+    want = m.paged_decode_attention(q.cuda(), cache(1.0), table, lens, scale=scale)
+    far = (q.double() * 2.0 ** power).bfloat16()
+    assert torch.equal(far.double(), q.double() * 2.0 ** power)
+    got = m.paged_decode_attention(far.cuda(), cache(2.0 ** k_power), table, lens, scale=scale * 2.0 ** (-power - k_power))
+    assert torch.isfinite(want[1]).all()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
