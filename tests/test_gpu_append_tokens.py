@@ -1,4 +1,4 @@
-"""The cache append of one token, bit-exact against float32 arithmetic."""
+"""The cache append of one token, and of many tokens with several rotary axes, bit-exact against float32 arithmetic."""
 import numpy as np
 import pytest
 import torch
@@ -40,3 +40,20 @@ def test_one_token(kind, D, R, Hq, Hkv):
         axes, pos = axes_of(m, R), c.rng.integers(0, 64, (3, 1)).astype(np.int32)
         c.run(m, rotate_axes32(c.k, c.rope, pos, axes.axes), rotate_axes32(c.q, c.rope, pos, axes.axes),
               rope_positions=i32(pos), rope_axes=axes)
+
+
+# tokens of a block on 152 SMs: 3, 3, 8 times 2, 3 (two heads a thread), 21 times 6
+MANY = [(1003, 128, 128, 32, 8), (1201, 128, 96, 32, 8), (6001, 64, 64, 4, 2), (2003, 128, 128, 40, 8), (64001, 64, 32, 1, 1)]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T,D,R,Hq,Hkv", MANY[:4])
+def test_axes_of_many_tokens_a_block(kind, T, D, R, Hq, Hkv):
+    m = ftmoe()
+    c = Case(D, R, Hq, Hkv, 24, "head" if T % 2003 == 0 else "slot", kind, T=T)
+    axes = axes_of(m, R)
+    pos = c.rng.integers(0, len(c.rope), (3, T)).astype(np.int32)
+    pos[:, c.pos < 0] = 1 << 30                          # not looked at for padding
+    at = np.where(c.pos < 0, 0, pos)
+    c.run(m, rotate_axes32(c.k, c.rope, at, axes.axes), rotate_axes32(c.q, c.rope, at, axes.axes),
+          rope_positions=i32(pos), rope_axes=axes)
