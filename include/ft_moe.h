@@ -380,7 +380,9 @@ typedef struct {
  *   What is stored is value * (1 / scale), rounded to nearest (E4M3: saturated at +-448).
  *   workspace  at least FT_MOE_WORKSPACE_HEAD_BYTES, its error word collects
  *              FT_ERR_DEVICE_FLAG, or NULL. A page, sequence or position outside its table stores
- *              nothing and flags. No two tokens of a call may share a slot.
+ *              nothing and flags. The query of a position outside the table of angles is zero; that of
+ *              a token whose page, sequence or place in block_table lies outside is rotated as ever. No
+ *              two tokens of a call may share a slot.
  *   T <= 1048576, Hq and Hkv <= 1024.
  */
 ft_status ft_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
@@ -395,8 +397,8 @@ ft_status ft_kv_append(const uint16_t* k, int64_t k_stride, const uint16_t* v, i
  * pair i of a head, elements i and i + rope_dim / 2, turns by row positions[axis[i]][token] of the
  * table. A host struct that a call copies; only `positions` is device memory.
  *   positions  int32 [axes, T], axis a at positions + a * stride (4-byte aligned). A position outside
- *              the table flags, and its token is treated like one whose place is outside; those of
- *              padding tokens are not looked at
+ *              the table, on any of the axes, flags: its token stores nothing and has a zero query.
+ *              Those of padding tokens are not looked at
  *   axis       the axis of each of the rope_dim / 2 pairs, below `axes`
  */
 typedef struct {

@@ -984,7 +984,9 @@ def kv_append(k, v, cache, block_table, positions, seq_ids=None, q=None, rope=No
     rope f32 [rows, R] (cos | sin; None: not at all). With rope_axes (a RopeAxes of R/2 pairs), each pair turns by
     the row that rope_positions int32 [axes,T] gives its axis. Returns the rotated q bf16 [T,Hq,D], or None
     without q. Rows of k, v and q may be slices of one projection's output. A token whose page,
-    sequence or position lies outside its table stores nothing and flags it (get_error)."""
+    sequence or position lies outside its table stores nothing and flags it (get_error); its query is zero
+    where the position lies outside rope, and rotated as ever otherwise. Padding (a negative place) stores
+    nothing and has a zero query."""
     if stream is not None:
         with torch.cuda.stream(stream):   # what the call makes belongs to the stream that it runs on
             return kv_append(k, v, cache, block_table, positions, seq_ids, q, rope, q_out, workspace, None,
