@@ -917,13 +917,21 @@ class NvFP4KVCache:
     page_size, Hkv, D = PagedKVCache.page_size, PagedKVCache.Hkv, PagedKVCache.D
 
 
+def _whole(numbers, name):
+    numbers = tuple(numbers)
+    whole = tuple(int(n) for n in numbers)
+    if any(w != n for w, n in zip(whole, numbers)):
+        raise ValueError(f"RopeAxes: {name} are whole numbers")
+    return whole
+
+
 @dataclass(frozen=True)
 class RopeAxes:
     """Which of up to four axes (time, height, width, ..) turns each rotary pair: axes, R/2 numbers from 0 on."""
     axes: tuple
 
     def __post_init__(self):
-        axes = tuple(int(a) for a in self.axes)
+        axes = _whole(self.axes, "axes")
         if not 0 < len(axes) <= 128 or min(axes) < 0 or max(axes) > 3:
             raise ValueError("RopeAxes: the axis, 0 to 3, of each of 1 to 128 pairs")
         object.__setattr__(self, "axes", axes)
@@ -934,7 +942,7 @@ class RopeAxes:
     def of_sections(sections, interleaved=False) -> RopeAxes:
         """sections: the number of pairs of each axis. They follow one another, or, interleaved, pair i goes
         to axis i mod len(sections) while that one has pairs left, then to the first that has."""
-        left, axes = [int(n) for n in sections], []
+        left, axes = list(_whole(sections, "sections")), []
         if not left or min(left) < 0:
             raise ValueError("RopeAxes: the number of pairs of each axis")
         if not interleaved:
