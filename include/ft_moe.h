@@ -486,8 +486,8 @@ size_t ft_paged_attention_workspace_bytes(int32_t B, int32_t D);
  *                out = 0 and lse = -inf, as does a row whose scores are all -inf
  *   block_table  int32 [B, table_width] as for ft_kv_append; entries past a sequence's last page
  *                are not read. A page outside [0, num_pages) flags FT_ERR_DEVICE_FLAG in the
- *                workspace, and its keys and values read as zeros; a length past the table (or 2^30)
- *                flags it too and is cut to it.
+ *                workspace, and its keys and values read as zeros; a length past the table (or 2^30,
+ *                or 2^37 / B - 512 unless a window is shorter) flags it too and is cut to it.
  *   out          bf16 [B, Hq, D], lse float [B, Hq] or NULL, fully overwritten
  *   workspace    ft_paged_attention_workspace_bytes(B, D) bytes, 256-byte aligned, its first
  *                FT_MOE_WORKSPACE_HEAD_BYTES zeroed once (ft_moe_workspace_init); calls that

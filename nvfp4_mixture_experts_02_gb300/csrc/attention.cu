@@ -130,7 +130,7 @@ __device__ __forceinline__ void store_row(const AttendArgs& a, int64_t at, float
   *reinterpret_cast<uint2*>(a.out + at) = y;
 }
 
-// A sequence's length, cut to what its row of the block table can hold.
+// A sequence's length, cut to what its row of the block table can hold (and the call can count).
 __device__ __forceinline__ int length_of(const AttendArgs& a, int b) { return min(a.seq_lens[b], a.max_len); }
 
 // First key, number of units of a sequence and the first unit's first key: a multiple of the unit, or (NVFP4, whose
@@ -896,6 +896,10 @@ cudaError_t launch_attend(const AttendArgs& args, int num_sms, cudaStream_t stre
   page_division(a.kv.page_size, a.div_mul, a.div_shift);
   const int64_t slots = (int64_t)a.table_width * a.kv.page_size;
   a.max_len = (int)(slots < (1 << 30) ? slots : 1 << 30);
+  // The kernels number the units of all sequences (64 keys at least, up to six more of a sequence for its ends and its
+  // charge) in 32 bits: 4096 sequences may have 2^25 - 512 keys each inside the window, 128 of them 2^30 - 512.
+  const int64_t most = ((1ll << 31) / a.B - 8) * 64;
+  if (a.max_len > most && (a.window == 0 || a.window > most)) a.max_len = (int)most;
   switch (a.kv.dtype) {
     case FT_KV_BF16: return launch_t<FT_KV_BF16>(a, num_sms, stream);
     case FT_KV_E4M3: return launch_t<FT_KV_E4M3>(a, num_sms, stream);

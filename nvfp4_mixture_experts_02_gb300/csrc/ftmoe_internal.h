@@ -195,7 +195,7 @@ struct AttendArgs {
   int group, gt;           // query heads per key head, 16-head parts of them (set by the launch)
   int same_strides;        // keys and values lie alike (set by the launch)
   int div_mul, div_shift;  // division by the page size (set by the launch)
-  int max_len;             // slots of a row of the block table (set by the launch)
+  int max_len;             // slots of a row of the block table, or what the call can count (set by the launch)
   int heads_log2;          // log2 of the key heads that a block may take at once (set by the launch)
   KvScales sc;             // NVFP4
 };
