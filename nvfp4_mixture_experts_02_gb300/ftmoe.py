@@ -1002,14 +1002,14 @@ def kv_append(k, v, cache, block_table, positions, seq_ids=None, q=None, rope=No
     dev, inner = cache.device_index, cache.heads
     if k.dim() != 3 or block_table.dim() != 2:
         raise ValueError("k [T, Hkv, D] and block_table [B, width] expected")
-    T, D = len(k), inner[1]
+    T, D = k.shape[0], inner[1]
     ks, vs = _need_rows(k, "k", dev, inner), _need_rows(v, "v", dev, inner)
-    if len(v) != T:
+    if v.shape[0] != T:
         raise ValueError("v: as many tokens as k expected")
     B, width = _tokens(block_table, positions, seq_ids, T, dev)
     Hq = qs = qp = qo = 0
     if q is not None:
-        if q.dim() != 3 or len(q) != T:
+        if q.dim() != 3 or q.shape[0] != T:
             raise ValueError("q: [T, Hq, D] expected")
         Hq = q.shape[1]
         qs = _need_rows(q, "q", dev, (Hq, D))
