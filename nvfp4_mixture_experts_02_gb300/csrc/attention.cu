@@ -30,16 +30,19 @@
 // of 64 (200 ragged sequences up to 700, 26.3 and 27.5 us) or 16 heads a key head (16 x 8192, 40.9 and 43.2 us).
 // NVFP4 caches (ftmoe_attend4.cuh): f16 products and weights in two f16 as for E4M3. Statistics and sums are float32.
 //
-// Measured (of the copy rate of 6786 GB/s): three sequences up to 131072, bf16, 962 MB: 155 us (91 %).
-// 48 ragged ones up to 8192, E4M3, 423 MB: 85 us (73 %), of which some 10 us are launches, fill and
-// join, and the runs' pieces differ in cost. One sequence of 777: 7.8 us, two launches and the chain
+// Measured (of the copy rate of 6786 GB/s): three sequences up to 131072, bf16, 962 MB: 147 us (96 %).
+// 48 ragged ones up to 8192, E4M3, 423 MB: 80 us (78 %), of which some 10 us are launches, fill and
+// join, and the runs' pieces differ in cost. One sequence of 777: 7.6 us, two launches and the chain
 // length, page, keys, scores, sums, join.
-// NVFP4: the three 56.5 us (270 MB, 71 %), the 48 56.7 us (239 MB, 62 %), 64 of 6500 92.5 us with pages head by head and 98.5
-// slot by slot (481 MB, 77 and 72 %): the products' own part runs at 93 % of the copy rate (870 of the 806 cycles that
-// a step's bytes take, of which 548 issue an instruction); the first data arrive after 4.5 us and the join takes 7.
-// Without any arithmetic those take 83 and 92 us. With heads of 64 (200 sequences, a window of 1023: 27 us for 7.4)
-// rows of 32 bytes copy at 77 % and as many bytes take a third more instructions; with 16 heads a key head the
-// warp products' rate bounds the steps (64 products of 16 cycles in 1225; heads of 256: 46 us for 14.6).
+// NVFP4: the three 63.4 us (270 MB, 63 %), the 48 60.8 us (239 MB, 58 %), 64 of 6500 104 us with pages head by head or slot
+// by slot (481 MB, 68 %). The SM's twelve warps take a step of 55 KB in 1.46 us, of which the copy rate would take 1.24,
+// the instructions (some 620 a warp) 0.95 and the tensor pipe (48 products of 8 cycles) 0.59. Outside the steps of the 48:
+// 5 us until data flow, 3 for the pieces' results, 5 (in the mean) until the last run ends, 5 of join.
+// With heads of 64 (200 sequences, a window of 1023: 28.5 us for 7.4) rows of 32 bytes copy at 77 % and as many bytes take
+// a third more instructions; 18 of the 28.5 us are the runs, 8.7 of them steps; the last one ends 4.4 us later, the join
+// takes 4.6. Heads of 256 with 16 heads a key head (49.3 us for 14.6): 27 us are steps, 1.52 each for 37 KB, where the copy
+// rate would take 0.83, the tensor pipe 0.79 (96 products) and the instructions 0.70; two warps a scheduler do not hide
+// one's latencies behind the other. The rest: 6 us until data flow, 5 for the results, 5 until the last run ends, 5 of join.
 #include <cmath>
 #include <cuda_runtime.h>
 
@@ -66,7 +69,8 @@ struct AttnShape {
   static constexpr int kBlocks =
       kRow >= 512 || DT == kKvNvfp4 ? 1 : kRow == 128 && NG == 1 ? kAttendBlocks : 2;
   // NVFP4: one block an SM, whose groups of warps each do what a block does otherwise. With heads of 64 three groups of
-  // four warps at 64 keys a step, not two of eight at 32: 200 sequences with a window of 1023 27.2 us for 29.2.
+  // four warps at 64 keys a step, not two of eight at 32: 200 sequences with a window of 1023 27.2 us for 29.2 (with
+  // weights in one f16).
   static constexpr int kGroups = DT != kKvNvfp4 ? 1 : D == 64 || (D == 128 && NG == 1) ? kAttendBlocks : 2;
   static constexpr int kWarps = DT == kKvNvfp4 || kRow >= 128 ? 4 : 8;   // of a group
   static constexpr int kQShared = DT != kKvNvfp4 || NG == 1 ? 0 : D == 256 ? 2 : D == 64 ? 1 : 0;   // groups of q in shared memory
@@ -91,15 +95,17 @@ struct AttnShape {
 // 17.0 when runs of two units are long; 8 up to 2048 take 14.0 us, and 15.5 when only runs of eight are.
 constexpr int kLongRun = 4;
 // NVFP4, runs of at least this many units: a segment begins with kCharge units without keys, for the copies that
-// begin anew and the results that are joined. With 0, 1, 2 and 4 of them 48 ragged sequences up to 8192 take 57.0, 56.1,
-// 57.2 and 58.6 us, 100 up to 4000 51.2, 48.0, 50.3 and 52.9, 19 of 22272 89.5, 92.5, 91.6 and 93.3; with heads of 256
-// (units half as long) 13 up to 24001 50.2, 47.8, 47.4 and 45.9, 16 of 8192 43.1, 40.7, 39.9 and 39.9.
-// From runs of 12, 8, 6 and 4 units on: 100 ragged sequences up to 2000 28.8, 28.7, 25.2 and 25.3 us, 200 up to 700 with
-// heads of 64 28.9, 28.8, 26.2 and 26.1, 64 of 1000 30.4, 31.7, 31.6 and 31.6.
+// begin anew and the results that are joined. It helps ragged lengths and costs 2 to 5 % of even ones whose runs cut every
+// segment: with 0, 1, 2 and 4 of them 48 ragged sequences up to 8192 take 61.6, 60.8, 62.2 and 63.6 us, 100 up to 4000
+// 55.6, 52.5, 55.3 and 58.0, 19 of 22272 100.3, 102.5, 102.2 and 103.3, 64 of 1000 31.8, 33.4, 32.3 and 32.4; with heads of
+// 256 (units half as long) 13 up to 24001 53.8, 51.0, 50.7 and 49.3, 16 of 8192 48.2, 45.6, 45.0 and 44.8.
+// From runs of 12, 8, 6 and 4 units on: 100 ragged sequences up to 2000 29.7, 29.8, 26.7 and 26.7 us, 200 up to 700 with
+// heads of 64 30.5, 30.5, 27.9 and 27.9, 200 with a window of 1023 28.5, 28.4, 28.5 and 30.1, 64 of 1000 31.8 and 33.4
+// from eight units or fewer on.
 constexpr int kChargeFrom = 6;
 // NVFP4: no segment is cut, and none is left to the join, where the longest is no more than this many units longer than
-// a run; a run then takes the segments that begin in it. 32 sequences with a window of 512 17.3 -> 13.2 us, 60 ragged
-// ones up to 300 9.0 -> 8.2; with eight units 128 of 512 would take 31.7 us for 28.3, one of 777 10.8 for 6.8.
+// a run; a run then takes the segments that begin in it. 32 sequences with a window of 512 18.0 -> 14.0 us, 60 ragged
+// ones up to 300 15.9 -> 14.2; with eight units 128 of 512 would take 34.4 us for 30.3, one of 777 11.3 for 7.0.
 constexpr int kUncut = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -855,8 +861,8 @@ cudaError_t launch_d(AttendArgs a, int num_sms, cudaStream_t stream) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, k_attend<D, DT, NG>, a)) != cudaSuccess) return e;
-  // Warps of a block of k_join. NVFP4: eight, so that all blocks run at once (48 ragged sequences 58.2 us, 60.5 with
-  // sixteen of as many registers, 57.2 for 56.3 with sixteen of 40; one of 777 keys 6.7, 6.8 and 7.8).
+  // Warps of a block of k_join. NVFP4: eight, so that all blocks run at once (48 ragged sequences, weights still in one
+  // f16, 58.2 us, 60.5 with sixteen of as many registers, 57.2 for 56.3 with sixteen of 40; one of 777 keys 6.7, 6.8 and 7.8).
   constexpr int kJoinWarps = DT == kKvNvfp4 ? 8 : 16;
   // Blocks of k_join that an SM holds: as many as there are runs, but not more than two of sixteen warps, which leaves
   // each thread 64 registers. One would take 36.1 us for 34.4 (64 sequences of 1000, E4M3), 51.2 for 49.9 (bf16), 63.3

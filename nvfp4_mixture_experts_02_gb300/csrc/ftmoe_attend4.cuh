@@ -6,13 +6,13 @@
 // element is which column (q is laid out to match), nor which key is which row.
 //
 // A code becomes f16 by one conversion for two and one multiplication by its scale (e2m1 * e4m3 has six significant
-// bits), so a step of 32 keys of 128 elements issues 548 instructions (256 of them these), which the 12 warps of an SM
-// overlap with the copies: products of the next step and values of this one are independent and stand side by side.
+// bits), so a step of 32 keys of 128 elements issues some 620 instructions (256 of them these), which the 12 warps of an
+// SM overlap with the copies: products of the next step and values of this one are independent and stand side by side.
 // A weight is two f16, as for E4M3 caches. One alone, 11 bits, puts one output in some thirty on the neighbouring bf16
 // (8e-4 off the rounded exact result for 1e-4) and takes 56.9 us for 60.7 (48 ragged sequences), 56.6 for 63.1 (three
 // long ones), 27.1 for 28.4 (heads of 64, a window of 1023): half of the value products. The second product of a pair
 // right behind the first: 60.7 us, 62.1 behind all four first ones of a word.
-// Measured and not kept: 16 warps of 128 registers (spills and two stages: 123 us for 103 at 64 x 6500, with three
+// Measured and not kept, with weights still in one f16: 16 warps of 128 registers (spills and two stages: 123 us for 103 at 64 x 6500, with three
 // stages 109), four stages for three (no change), groups held to the slowest one's pace (2 to 5 % slower), copies of
 // whole tiles by the tensor memory accelerator (rows of 64 bytes at 6.5 TB/s for 6.7, of 32 at 4.6 for 5.2 in a copy
 // of the same pattern), hints that fetch 128 or 256 bytes into L2 (no change).

@@ -19,10 +19,11 @@
 // k_kv_append_many: the blocks that the device holds at once share the tokens. A block looks up the places of all of
 // its tokens and lays their cosines and sines out in shared memory, where all heads of a token read them and each
 // pair's axis has been chosen; then a thread keeps its piece of a head and goes through the tokens with the next one's
-// values on their way. 4093 tokens into NVFP4 19.7 us, 9001 with three axes 38 us (66 and 75 % of the copy rate); what is
-// left are the instructions, some 200 a thread and token, at the warps that 56 registers allow.
+// values on their way. 4093 tokens into NVFP4 19.7 us, into E4M3 18.8, into bf16 19.9, 9001 with three axes 38.1, 37.6
+// and 40.2 (66 to 83 % of the copy rate): the loads' latency at the 36 warps that 56 registers allow, whose instructions, some
+// 200 a thread and token, fill 63 % of the issue slots.
 // k_kv_gather: a thread takes 16 elements of a key and of its value. Bound by memory: 115 thousand tokens of 8 heads
-// of 128 from NVFP4 122 us (90 %), most of it for the results.
+// of 128 from NVFP4 123 us (90 %), from E4M3 134 (96 %), from bf16 173 (99 %), most of it for the results.
 #include <algorithm>
 #include <cuda_runtime.h>
 
@@ -38,10 +39,11 @@ constexpr int kAppendThreads = 256;   // of a block, or as many as one token nee
 // of 128 into NVFP4 19.7 us, 20.6 with two blocks of 72, 25.7 with four of 40; two tokens ahead 21.3 for 20.7).
 constexpr int kManyThreads = 384, kManyBlocks = 3;
 // From this many tokens a block (of those that the device holds at once) on, rotated ones of more than a few heads go
-// through it: 1200 of those tokens (three a block) 8.7 us for 9.6, 4093 19.7 for 26.1 (into E4M3 18.8 for 23.3), 800 (two) 7.0
-// for 6.8. Not tokens that share a block: 40000 of 2 + 2 heads of 64 would take 16.0 for 14.7. Without rotation
-// k_kv_append is the faster (16000 tokens 71 us for 77). Several axes always take it: 37 tokens 2.7 us, 3.2 with the
-// choice of rows in each thread, 9001 38 us for 110.
+// through it: 1200 of those tokens (three a block) 8.7 us for 9.6, 4093 19.7 for 26.1 (into E4M3 18.8 for 23.3, into bf16 19.9
+// for 24.2), 800 (two) 7.0 for 6.8. Not tokens that share a block: 40000 of 2 + 2 heads of 64 would take 16.0 for 14.7. Not
+// without rotation: into bf16 k_kv_append is the faster there up to 16000 tokens or so (8000 36.8 us for 41.4, 16000 70.4 for
+// 74.5, but 40000 172 for 161); into E4M3 and NVFP4 it is not (8000 34.3 for 31.9 and 40.3 for 32.4). Several axes always
+// take it: 37 tokens 2.7 us, 3.2 with the choice of rows in each thread, 9001 38 us for 110.
 constexpr int kManyTokens = 3;
 constexpr int kAppendTokens = 32, kAppendBytes = 40 * 1024;   // most tokens of a group, most shared memory
 
