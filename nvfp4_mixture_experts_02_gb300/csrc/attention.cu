@@ -372,9 +372,10 @@ __global__ void __launch_bounds__(AttnShape<D, DT, NG>::kGroups * AttnShape<D, D
             const int64_t k_at = __shfl_sync(0xffffffffu, ko, row);
             const int64_t v_at = a.same_strides ? k_at : __shfl_sync(0xffffffffu, vo, row);
             const bool on = k_at >= 0;
-            const uint32_t to = st + swz<CPR>(row, ch);
-            cp_async16(to, static_cast<const char*>(a.kv.k) + (on ? k_at + ch * 16 : 0), on);
-            cp_async16(to + KT * S::kRow, static_cast<const char*>(a.kv.v) + (on ? v_at + ch * 16 : 0), on);
+            // the place written out twice: kept in a register, it costs three more spilled ones with heads of 256
+            cp_async16(st + swz<CPR>(row, ch), static_cast<const char*>(a.kv.k) + (on ? k_at + ch * 16 : 0), on);
+            cp_async16(st + KT * S::kRow + swz<CPR>(row, ch),
+                       static_cast<const char*>(a.kv.v) + (on ? v_at + ch * 16 : 0), on);
           }
         }
         cp_async_commit();
@@ -863,11 +864,12 @@ cudaError_t launch_d(AttendArgs a, int num_sms, cudaStream_t stream) {
   if ((e = cudaLaunchKernelEx(&cfg, k_attend<D, DT, NG>, a)) != cudaSuccess) return e;
   // Warps of a block of k_join. NVFP4: eight, so that all blocks run at once (48 ragged sequences, weights still in one
   // f16, 58.2 us, 60.5 with sixteen of as many registers, 57.2 for 56.3 with sixteen of 40; one of 777 keys 6.7, 6.8 and 7.8).
-  constexpr int kJoinWarps = DT == kKvNvfp4 ? 8 : 16;
-  // Blocks of k_join that an SM holds: as many as there are runs, but not more than two of sixteen warps, which leaves
-  // each thread 64 registers. One would take 36.1 us for 34.4 (64 sequences of 1000, E4M3), 51.2 for 49.9 (bf16), 63.3
-  // for 61.7 (13 up to 24001 with heads of 256, E4M3).
+  // Heads of 256 where an SM has two runs (E4M3): eight as well, because two blocks of sixteen leave 64 registers, too
+  // few for four rows of 256 in flight: two sequences of 62648 51.7 -> 50.0 us, 13 up to 24001 60.8 -> 59.9, one of 777 9.4 -> 8.8.
   constexpr int kRuns = S::kBlocks * S::kGroups;   // an SM
+  constexpr int kJoinWarps = DT == kKvNvfp4 || (D == 256 && kRuns > 1) ? 8 : 16;
+  // Blocks of k_join that an SM holds: as many as there are runs, but not more than two of sixteen warps, which leaves
+  // each thread 64 registers. One would take 36.1 us for 34.4 (64 sequences of 1000, E4M3), 51.2 for 49.9 (bf16).
   constexpr int kJoinBlocks = DT == kKvNvfp4 ? 3 : kRuns < 2 ? kRuns : 2;
   cfg.gridDim = dim3((unsigned)(kRuns * num_sms));   // a block for every run
   cfg.blockDim = dim3(kJoinWarps * 32);
